@@ -130,6 +130,35 @@ int k3mla_absorb_q_append(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* q
                           const uint16_t* k_rope, int64_t r_stride, int B,
                           int32_t* dev_err, void* stream);
 
+/* ---- from the projections to the cache: norms, rotation, append ----------------
+ * For every packed token row r < R at position p of slot b, in one pass:
+ *   q_out[r][h] = rot_p( q[r][h] * q_weight / sqrt(mean(q[r][h]^2) + eps) )   every head h, 192 entries
+ *   c           = c_kv[r] * c_weight / sqrt(mean(c_kv[r]^2) + eps)            512 entries
+ *   k           = rot_p( k_rope[r] * k_weight / sqrt(mean(k_rope[r]^2) + eps) ) 64 entries
+ *   the cache row of position p (k3mla_append_latent's address) = c | k
+ * each in f32, rounded once.  A NULL weight leaves that norm out (weight and division).  rot_p turns the
+ * pairs of the 64 rope entries (the last 64 of a head's 192) by the angles p * inv_freq[i], i < 32: pair i
+ * is entries (i, i + 32), or (2i, 2i + 1) with interleaved != 0; (x, y) becomes (x cos - y sin,
+ * x sin + y cos).  NULL inv_freq: no rotation.  The angle is reduced in 64 bits, so far positions keep
+ * their accuracy (positions below 2^29).
+ * row_start [B + 1] (non-decreasing): rows row_start[b] .. row_start[b + 1] - 1 are slot b's, at positions
+ *            pos0[b], pos0[b] + 1, ...; NULL (R == B): row b is slot b's only one, at pos0[b].  Rows outside
+ *            every slot and rows at negative positions are left as they are, in q_out and in the cache.
+ * q          device [R][96][192] bf16; q_out the same shape, q itself or no overlap with it
+ * c_kv, k_rope device bf16, row r at c_kv + r * c_stride, k_rope + r * r_stride (elements)
+ * q_weight [192], c_weight [512], k_weight [64] device bf16 or NULL; inv_freq [32] device f32 or NULL
+ * eps        >= 0
+ * slab, block_table, dev_err: as for k3mla_append_latent_rows (K3MLA_DEV_UNMAPPED: that cache row is
+ *            skipped, its queries are not)
+ * bf16 pointers 16-byte aligned, strides multiples of 8.  One kernel on `stream`; it reads nothing before
+ * the kernel ahead of it has completed. */
+int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
+                           int n_pages, int n_layers, int layer, const int32_t* block_table,
+                           int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                           const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
+                           const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
+                           const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err, void* stream);
+
 /* ---- exact-chain decode (PR #869, M2 commit: the certified rounding chain) ----
  * The same result as k3mla_absorb_q + k3mla_paged_decode, computed landing for
  * landing as the chain states it: q absorption summed over d ascending, score
@@ -397,6 +426,36 @@ int k3mla_pool_page_refs(const k3mla_pool* pool, int page);
 int k3mla_copy_pages(uint16_t* dst_slab, int dst_n_pages, const uint16_t* src_slab, int src_n_pages,
                      int n_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
                      int32_t* dev_err, void* stream);
+
+/* ---- giving cache memory back while a slot lives ---------------------------------
+ * k3mla_pool_trim: with n_tokens tokens in the slot and windowed attention (window, n_sink: see
+ * k3mla_window_decode), unmaps every page that no token from position n_tokens on can see -- wholly
+ * behind the next token's window and past the sinks; its table entries become -1, its references
+ * drop by one.  Returns the number of pages unmapped (>= 0).  K3MLA_E_INVALID for window < 1 or a
+ * negative n_tokens / n_sink, K3MLA_E_CTX for n_tokens > max_ctx.  A trimmed position cannot be written
+ * again (k3mla_pool_cow gives K3MLA_E_CTX), and k3mla_pool_share_prefix shares the hole as it is.
+ * k3mla_pool_truncate: unmaps the pages past the first new_len tokens (nothing if the slot maps no
+ * more than those), e.g. after k3mla_compact_rows. */
+int k3mla_pool_trim(k3mla_pool* pool, int slot, int n_tokens, int window, int n_sink);
+int k3mla_pool_truncate(k3mla_pool* pool, int slot, int new_len);
+
+/* ---- row compaction: the kept tokens of each slot move to the front of its pages --
+ * For every slot b < B, layer l < n_layers and i < n_b = keep_start[b + 1] - keep_start[b], in place:
+ *   cache row of position i <- cache row of position keep[l * keep_layer_stride + keep_start[b] + i]
+ * The slot then holds n_b tokens (rows from n_b on keep what they held; k3mla_pool_truncate gives their
+ * pages back).  Rotated keys keep the angles of their old positions.
+ * keep       device int32 [n_keep], or [n_layers] lists of n_keep entries keep_layer_stride apart: per
+ *            slot strictly ascending positions (>= 0).  keep_layer_stride 0: one list for every layer.
+ * keep_start device int32 [B + 1], non-decreasing, within [0, n_keep]
+ * slab, block_table: as for k3mla_append_latent; a source entry -1 reads as a zero row
+ * dev_err    device int32 or NULL: K3MLA_DEV_UNMAPPED where position i has no page (that row is skipped),
+ *            K3MLA_DEV_BAD_PAGE for a source page outside [-1, n_pages) and K3MLA_DEV_CTX for a kept position
+ *            outside the table (read as zero rows)
+ * A page that receives rows must be mapped by one slot of the call only (k3mla_pool_cow un-shares it).
+ * One kernel on `stream`; it reads nothing before the kernel ahead of it has completed. */
+int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, const int32_t* block_table,
+                       int max_pages_per_slot, const int32_t* keep, int64_t keep_layer_stride, int n_keep,
+                       const int32_t* keep_start, int B, int32_t* dev_err, void* stream);
 
 /* ---- paged decode with built-in scratch ---------------------------------------
  * The pegainfer PR #869 page has no counterpart to this call.  It is k3mla_paged_decode without the

@@ -8,6 +8,16 @@
 // is one contiguous block copy.  The copy is HBM-bound (read + write of
 // n_layers * 73,728 bytes per page); each CTA moves 16-byte vectors, eight in
 // flight per thread, over one page of one (src, dst) pair.
+//
+// Row compaction (k3mla_compact_rows): the kept tokens of a slot move to the front of its pages, in
+// place.  Entry i of a slot's ascending list of kept positions goes to position i, and i <= keep[i], so
+// a walk over i in ascending order never writes a row that a later step still has to read: rows up to i
+// are written only after entries up to i have been read.  Within one 128-byte column of the rows (a
+// layer's 576 entries are nine of them) this order is one CTA's: it reads CR_ROWS rows, waits at a
+// barrier, and writes them while the next ones are on their way -- reading ahead is always safe.  The
+// columns, the layers and the slots are independent, so even a lone slot of 24 layers fills the GPU (216
+// CTAs).  Bound: HBM, 2,304 bytes a moved row and layer; rows that stay in place are neither read nor
+// written.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -54,6 +64,91 @@ __global__ void __launch_bounds__(CP_THREADS) k3mla_copy_pages_kernel(uint16_t* 
     }
 }
 
+constexpr int CR_VECS = 8;                            // 16-byte vectors of a row's 128-byte column
+constexpr int CR_COLS = ROW * 2 / (16 * CR_VECS);     // nine columns
+constexpr int CR_THREADS = 256;
+constexpr int CR_GROUP = CR_THREADS / CR_VECS;        // rows that the CTA's threads cover at once
+constexpr int CR_UNROLL = 4;                          // ... and groups of them on their way at once
+constexpr int CR_ROWS = CR_GROUP * CR_UNROLL;         // 128 rows a step
+static_assert(CR_COLS * CR_VECS * 16 == ROW * 2, "whole columns");
+
+// The rows of one step of one thread: where each goes and what it holds.
+struct CompactStep {
+    uint4 v[CR_UNROLL];
+    int64_t dst[CR_UNROLL];  // the slab's row, -1: nothing to write
+};
+
+struct CompactParams {
+    uint16_t* slab;
+    const int32_t *table, *keep, *keep_start;
+    int64_t keep_stride;  // entries from a layer's list to the next layer's, 0: one list for all
+    int32_t* dev_err;
+    int n_pages, n_layers, max_pages, n_keep, layer0, slot0;
+};
+
+__device__ __forceinline__ void compact_load(const CompactParams& p, CompactStep& st, const int32_t* keep,
+                                             const int32_t* table, int i0, int n, int layer, int vec)
+{
+#pragma unroll
+    for (int u = 0; u < CR_UNROLL; ++u) {
+        const int i = i0 + u * CR_GROUP + (int)threadIdx.x / CR_VECS;
+        st.dst[u] = -1;
+        st.v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (i >= n) continue;
+        const int32_t t = keep[i];
+        if (t == i) continue;  // the row stays where it is
+        const int dp = i / PAGE;
+        const int32_t d = dp < p.max_pages ? table[dp] : -1;
+        uint32_t bits = 0;
+        if (d < 0 || d >= p.n_pages)
+            bits = K3MLA_DEV_UNMAPPED;  // nowhere to write it
+        else
+            st.dst[u] = ((int64_t)d * p.n_layers + layer) * PAGE + i % PAGE;
+        if (t < 0 || t / PAGE >= p.max_pages) {
+            bits |= K3MLA_DEV_CTX;
+        } else {
+            const int32_t s = table[t / PAGE];
+            if (s < -1 || s >= p.n_pages)
+                bits |= K3MLA_DEV_BAD_PAGE;
+            else if (s >= 0)  // -1: a zero row
+                st.v[u] = reinterpret_cast<const uint4*>(
+                    p.slab + (((int64_t)s * p.n_layers + layer) * PAGE + t % PAGE) * ROW)[vec];
+        }
+        if (bits && p.dev_err) atomicOr(p.dev_err, (int)bits);
+    }
+}
+
+__device__ __forceinline__ void compact_store(const CompactParams& p, const CompactStep& st, int vec)
+{
+#pragma unroll
+    for (int u = 0; u < CR_UNROLL; ++u)
+        if (st.dst[u] >= 0) reinterpret_cast<uint4*>(p.slab + st.dst[u] * ROW)[vec] = st.v[u];
+}
+
+// grid (columns, layers, slots); block CR_THREADS.
+__global__ void __launch_bounds__(CR_THREADS) k3mla_compact_rows_kernel(const CompactParams p)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int b = p.slot0 + (int)blockIdx.z, layer = p.layer0 + (int)blockIdx.y;
+    const int first = max(0, p.keep_start[b]);
+    const int n = min(p.n_keep, p.keep_start[b + 1]) - first;
+    const int32_t* keep = p.keep + (int64_t)layer * p.keep_stride + first;
+    const int32_t* table = p.table + (int64_t)b * p.max_pages;
+    const int vec = (int)blockIdx.x * CR_VECS + (int)threadIdx.x % CR_VECS;
+    if (n <= 0) return;
+    CompactStep a, c;  // a: the step being written, c: the next one
+    compact_load(p, a, keep, table, 0, n, layer, vec);
+    for (int i = 0; i < n; i += 2 * CR_ROWS) {
+        compact_load(p, c, keep, table, i + CR_ROWS, n, layer, vec);
+        __syncthreads();  // every thread holds its rows of step a: they may be overwritten
+        compact_store(p, a, vec);
+        compact_load(p, a, keep, table, i + 2 * CR_ROWS, n, layer, vec);
+        __syncthreads();
+        compact_store(p, c, vec);
+    }
+}
+
 }  // namespace k3
 
 using namespace k3;
@@ -79,4 +174,34 @@ extern "C" int k3mla_copy_pages(uint16_t* dst_slab, int dst_n_pages, const uint1
     return launch_pdl(k3mla_copy_pages_kernel, dim3((unsigned)chunks, (unsigned)n), dim3(CP_THREADS), 0,
                       reinterpret_cast<cudaStream_t>(stream), "k3mla_copy_pages_kernel", dst_slab, dst_n_pages,
                       src_slab, src_n_pages, src_ids, dst_ids, page_vecs, dev_err);
+}
+
+extern "C" int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, const int32_t* block_table,
+                                  int max_pages_per_slot, const int32_t* keep, int64_t keep_layer_stride, int n_keep,
+                                  const int32_t* keep_start, int B, int32_t* dev_err, void* stream)
+{
+    if (B < 0 || n_pages <= 0 || n_layers <= 0 || max_pages_per_slot <= 0 || n_keep < 0 ||
+        (keep_layer_stride != 0 && keep_layer_stride < n_keep)) {
+        set_error("k3mla_compact_rows: invalid sizes");
+        return K3MLA_E_INVALID;
+    }
+    if (B == 0 || n_keep == 0) return K3MLA_OK;
+    if (!slab || !block_table || !keep || !keep_start || !aligned(slab, 16)) {
+        set_error("k3mla_compact_rows: null or misaligned pointer");
+        return K3MLA_E_INVALID;
+    }
+    if (!device_ok()) return K3MLA_E_DEVICE;
+    CompactParams p;
+    p.slab = slab, p.table = block_table, p.keep = keep, p.keep_start = keep_start, p.keep_stride = keep_layer_stride;
+    p.dev_err = dev_err, p.n_pages = n_pages, p.n_layers = n_layers, p.max_pages = max_pages_per_slot, p.n_keep = n_keep;
+    constexpr int MOST = 65535;  // a grid's extent in y and z
+    for (p.slot0 = 0; p.slot0 < B; p.slot0 += MOST)
+        for (p.layer0 = 0; p.layer0 < n_layers; p.layer0 += MOST) {
+            const int ny = n_layers - p.layer0 < MOST ? n_layers - p.layer0 : MOST;
+            const int nz = B - p.slot0 < MOST ? B - p.slot0 : MOST;
+            const int rc = launch_pdl(k3mla_compact_rows_kernel, dim3(CR_COLS, ny, nz), dim3(CR_THREADS), 0,
+                                      reinterpret_cast<cudaStream_t>(stream), "k3mla_compact_rows_kernel", p);
+            if (rc) return rc;
+        }
+    return K3MLA_OK;
 }

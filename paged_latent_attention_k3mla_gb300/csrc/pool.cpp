@@ -13,6 +13,10 @@
 // first takes a private copy (k3mla_pool_cow names the copy; the device moves
 // the bytes with k3mla_copy_pages); a page returns to the free list when its
 // last slot releases it.
+//
+// Windowed attention and eviction give pages back while a slot lives: k3mla_pool_trim unmaps the pages
+// that no later token can see (holes, -1, inside the slot's mapped range), k3mla_pool_truncate those past
+// a shorter length.
 #include <cstdint>
 #include <cstdlib>
 #include <new>
@@ -105,6 +109,15 @@ extern "C" int k3mla_pool_ensure_all(k3mla_pool* p, const int32_t* new_len, int 
     return K3MLA_OK;
 }
 
+// Takes one slot's mapping of a page away (nothing for a hole); 1 when there was one.
+static int unmap(k3mla_pool* p, int32_t* entry)
+{
+    if (*entry < 0) return 0;
+    if (--p->refs[*entry] == 0) p->free.push_back(*entry);
+    *entry = -1;
+    return 1;
+}
+
 extern "C" int k3mla_pool_release_slot(k3mla_pool* p, int slot)
 {
     if (!p) return K3MLA_E_INVALID;
@@ -112,12 +125,35 @@ extern "C" int k3mla_pool_release_slot(k3mla_pool* p, int slot)
     int32_t* row = p->table.data() + (size_t)slot * p->max_pages;
     // Push back in reverse so that a re-claim of the same count takes the same ids; a page another
     // slot still maps stays out of the free list.
-    for (int lp = p->mapped[slot] - 1; lp >= 0; --lp) {
-        if (--p->refs[row[lp]] == 0) p->free.push_back(row[lp]);
-        row[lp] = -1;
-    }
+    for (int lp = p->mapped[slot] - 1; lp >= 0; --lp) unmap(p, row + lp);
     p->mapped[slot] = 0;
     return K3MLA_OK;
+}
+
+extern "C" int k3mla_pool_truncate(k3mla_pool* p, int slot, int new_len)
+{
+    if (!p || new_len < 0) return K3MLA_E_INVALID;
+    if (slot < 0 || slot >= p->n_slots) return K3MLA_E_SLOT;
+    const int keep = (int)(((long long)new_len + K3MLA_PAGE - 1) / K3MLA_PAGE);
+    int32_t* row = p->table.data() + (size_t)slot * p->max_pages;
+    for (int lp = p->mapped[slot] - 1; lp >= keep; --lp) unmap(p, row + lp);
+    if (p->mapped[slot] > keep) p->mapped[slot] = keep;
+    return K3MLA_OK;
+}
+
+extern "C" int k3mla_pool_trim(k3mla_pool* p, int slot, int n_tokens, int window, int n_sink)
+{
+    if (!p || n_tokens < 0 || window < 1 || n_sink < 0) return K3MLA_E_INVALID;
+    if (slot < 0 || slot >= p->n_slots) return K3MLA_E_SLOT;
+    if (n_tokens > p->max_ctx) return K3MLA_E_CTX;
+    // the next token, at position n_tokens, sees tokens n_tokens - window + 1 .. n_tokens and the sinks
+    const long long first = (long long)n_tokens - window + 1;
+    int32_t* row = p->table.data() + (size_t)slot * p->max_pages;
+    int given = 0;
+    for (long long lp = ((long long)n_sink + K3MLA_PAGE - 1) / K3MLA_PAGE;
+         lp < p->mapped[slot] && (lp + 1) * K3MLA_PAGE <= first; ++lp)
+        given += unmap(p, row + lp);
+    return given;
 }
 
 extern "C" int k3mla_pool_share_prefix(k3mla_pool* p, int dst_slot, int src_slot, int n_tokens)
@@ -131,7 +167,7 @@ extern "C" int k3mla_pool_share_prefix(k3mla_pool* p, int dst_slot, int src_slot
     int32_t* dst = p->table.data() + (size_t)dst_slot * p->max_pages;
     for (int lp = 0; lp < need; ++lp) {
         dst[lp] = src[lp];
-        ++p->refs[src[lp]];
+        if (src[lp] >= 0) ++p->refs[src[lp]];  // a trimmed page stays a hole
     }
     p->mapped[dst_slot] = need;
     return K3MLA_OK;
@@ -145,6 +181,7 @@ extern "C" int k3mla_pool_cow(k3mla_pool* p, int slot, int pos, int32_t* src_pag
     if (lp >= p->mapped[slot]) return K3MLA_E_CTX;  // map the position first (k3mla_pool_ensure)
     int32_t* row = p->table.data() + (size_t)slot * p->max_pages;
     const int32_t old = row[lp];
+    if (old < 0) return K3MLA_E_CTX;  // trimmed away: no token of that page can be written any more
     if (p->refs[old] == 1) return 0;  // the slot owns the page alone: write in place
     if (p->free.empty()) return K3MLA_E_NO_PAGES;
     const int32_t fresh = p->free.back();

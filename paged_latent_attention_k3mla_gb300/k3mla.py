@@ -31,7 +31,8 @@ EXPORTS = (
     "k3mla_decode_exact_workspace_bytes", "k3mla_pool_ensure_all", "k3mla_batch_planned_split_tokens",
     "k3mla_decode_layer_workspace_bytes", "k3mla_decode_layer", "k3mla_diag_decode_timeout",
     "k3mla_expanded_cache_bytes", "k3mla_expand_latent_cache", "k3mla_expanded_decode", "k3mla_diag_exact_exp",
-    "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode",
+    "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_pool_trim",
+    "k3mla_pool_truncate", "k3mla_compact_rows",
 )
 
 # Size of the library's built-in decode scratch (K3MLA_NOALLOC_SCRATCH_BYTES).
@@ -93,6 +94,11 @@ def load(build_if_needed: bool = True):
             "k3mla_decode_layer_workspace_bytes": ([I, I], SZ),
             "k3mla_decode_layer": ([P, P, P, I, I, I, P, I, P, P, I64, P, I64, ctypes.c_uint16, P, P, P, SZ, I, I, P, P],
                                    I),
+            "k3mla_norm_rope_append": ([P, P, P, P, I, I, I, P, I, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I, I, I,
+                                        P, P], I),
+            "k3mla_pool_trim": ([P, I, I, I, I], I),
+            "k3mla_pool_truncate": ([P, I, I], I),
+            "k3mla_compact_rows": ([P, I, I, P, I, P, I64, I, P, I, P, P], I),
             "k3mla_decode_exact": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, P, SZ, I, I, P, P], I),
         }
         for name, (args, res) in sig.items():
@@ -131,6 +137,18 @@ def _opt(t, dtype, shape, name):
     return None if t is None else _dev(t, dtype, shape, name)
 
 
+def _table(t: torch.Tensor, B: int):
+    if t.dim() != 2 or t.shape[0] != B:
+        raise K3mlaError(f"block_table has shape {tuple(t.shape)}, expected [{B}, max_pages]")
+    return _dev(t, torch.int32, None, "block_table")
+
+
+def _here(t: torch.Tensor, name: str):
+    """The call runs on the current device: its tensors have to be there too."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise K3mlaError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def absorb_q(q: torch.Tensor, w_kv_b: torch.Tensor, q_abs: torch.Tensor, stream=None) -> None:
     """q [B,96,192] bf16, w_kv_b [24576,512] bf16 -> q_abs [B,96,576] bf16 (written)."""
     B = q.shape[0]
@@ -160,9 +178,11 @@ def append_latent(slab: torch.Tensor, layer: int, block_table: torch.Tensor, pos
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_append_latent")
 
 
-def _rows(t: torch.Tensor, B: int, name: str):
+def _rows(t: torch.Tensor, B: int, name: str, width: int = 0):
     if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != B:
         raise K3mlaError(f"{name} must be a CUDA bf16 [B, n] tensor with unit inner stride")
+    if t.shape[1] < width:
+        raise K3mlaError(f"{name} has {t.shape[1]} columns, at least {width} are read")
     return ctypes.c_void_p(t.data_ptr())
 
 
@@ -216,6 +236,49 @@ def append_latent_rows(slab: torch.Tensor, layer: int, block_table: torch.Tensor
         _dev(pos0, torch.int32, (B,), "pos0"), _dev(row_start, torch.int32, (B + 1,), "row_start"),
         _rows(c_kv, R, "c_kv"), c_kv.stride(0), _rows(k_rope, R, "k_rope"), k_rope.stride(0), B, int(max_rows),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_append_latent_rows")
+
+
+def norm_rope_append(q: torch.Tensor, q_out: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                     pos0: torch.Tensor, row_start: torch.Tensor | None, c_kv: torch.Tensor, k_rope: torch.Tensor,
+                     q_weight: torch.Tensor | None = None, c_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                     interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Norms of q [R, 96, 192] per head (weight [192]), of the latent c_kv [R, >=512] ([512]) and of the rope
+    key k_rope [R, >=64] ([64]), rotation of the rope entries by pos * inv_freq [32] (f32), queries to q_out
+    (may be q), keys into the cache rows of their positions; see k3mla_norm_rope_append.  A weight of None
+    leaves that norm out, inv_freq None the rotation; row_start None: one row per slot, at pos0."""
+    R = q.shape[0]
+    B = pos0.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    _here(slab, "slab")
+    _check(load().k3mla_norm_rope_append(
+        _dev(q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _dev(q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
+        _opt(q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _table(block_table, B), block_table.shape[1], _dev(pos0, torch.int32, (B,), "pos0"),
+        _opt(row_start, torch.int32, (B + 1,), "row_start"), _rows(c_kv, R, "c_kv", LORA), c_kv.stride(0),
+        _opt(c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE), k_rope.stride(0),
+        _opt(k_weight, torch.bfloat16, (ROPE,), "k_weight"), float(eps), _opt(inv_freq, torch.float32, (ROPE // 2,), "inv_freq"),
+        int(bool(interleaved)), B, R, _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
+        "k3mla_norm_rope_append")
+
+
+def compact_rows(slab: torch.Tensor, block_table: torch.Tensor, keep: torch.Tensor, keep_start: torch.Tensor,
+                 dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Eviction, in place: entry i of slot b's ascending list keep[.., keep_start[b] + i] of kept positions
+    moves to position i, in every layer; see k3mla_compact_rows.  keep [n] or [1, n] (one list for every
+    layer) or [L, n] int32, keep_start [B + 1] int32."""
+    n_pages, L = slab.shape[0], slab.shape[1]
+    B = keep_start.shape[0] - 1
+    n = keep.shape[-1]
+    if keep.dim() not in (1, 2) or (keep.dim() == 2 and keep.shape[0] not in (1, L)):
+        raise K3mlaError(f"keep has shape {tuple(keep.shape)}, expected [n], [1, n] or [{L}, n]")
+    _here(slab, "slab")
+    _check(load().k3mla_compact_rows(
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _table(block_table, B), block_table.shape[1],
+        _dev(keep, torch.int32, None, "keep"), n if keep.dim() == 2 and keep.shape[0] == L and L > 1 else 0, n,
+        _dev(keep_start, torch.int32, (B + 1,), "keep_start"), B, _opt(dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream)), "k3mla_compact_rows")
 
 
 def chunk_views(block_table: torch.Tensor, pos0: torch.Tensor, row_start: torch.Tensor,
@@ -492,6 +555,15 @@ class Pool:
         if rc == 1:
             return s.value, d.value
         return None if rc == 0 else rc
+
+    def trim(self, slot: int, n_tokens: int, window: int, n_sink: int = 0) -> int:
+        """Give back the pages of `slot` that no token from position n_tokens on can see (their number, or
+        a negative status code)."""
+        return int(load().k3mla_pool_trim(self._h, slot, n_tokens, window, n_sink))
+
+    def truncate(self, slot: int, new_len: int) -> int:
+        """Give back the pages past the first new_len tokens (status code)."""
+        return int(load().k3mla_pool_truncate(self._h, slot, new_len))
 
     def refs(self, page: int) -> int:
         return int(load().k3mla_pool_page_refs(self._h, page))

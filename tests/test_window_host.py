@@ -1,0 +1,133 @@
+"""Host-side tests of the windowed latent-cache operators that need no GPU: the pool's trim and truncate, and
+argument errors that come back before anything is launched."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from paged_latent_attention_k3mla_gb300 import k3mla
+
+
+def test_trim_unmaps_what_no_later_token_sees():
+    pool = k3mla.Pool(n_slots=2, max_ctx=1024, n_pages=16)
+    assert pool.ensure(0, 600) == 0                              # ten pages
+    before = pool.table()[0].copy()
+    assert pool.trim(0, 600, 1024, 0) == 0                       # the window reaches the first token
+    # the next token (position 600) sees 600 - 200 + 1 = 401 and later; with 65 sinks pages 0, 1 stay
+    assert pool.trim(0, 600, 200, 65) == 4                       # pages 2..5 hold tokens 128..383
+    t = pool.table()[0]
+    assert np.all(t[2:6] == -1) and np.array_equal(t[[0, 1, 6, 7, 8, 9]], before[[0, 1, 6, 7, 8, 9]])
+    assert pool.stats() == (16, 6)
+    assert pool.trim(0, 600, 200, 65) == 0                       # nothing left to give
+    assert pool.trim(0, 600, 153, 65) == 1                       # first seen: 448, page 6 ends there
+    assert pool.trim(0, 600, 1, 0) == 4                          # pages 0, 1, 7, 8; the next token's page stays
+    assert pool.table()[0, 9] == before[9] and pool.stats() == (16, 1)
+    assert pool.ensure(0, 641) == 0 and pool.table()[0, 10] >= 0  # growth goes on behind the holes
+    assert pool.cow(0, 100) == -4 and pool.cow(0, 640) is None
+    assert pool.release(0) == 0 and pool.stats() == (16, 0)
+    assert all(pool.refs(p) == 0 for p in range(16))
+    pool.close()
+
+
+def test_every_page_trimmed_is_behind_every_later_window():
+    for n in (1, 63, 64, 65, 127, 128, 129, 500, 511, 512):
+        for w in (1, 2, 63, 64, 65, 66, 128, 129, 600):
+            for s in (0, 1, 64, 65, 130, 10 ** 9):
+                pool = k3mla.Pool(n_slots=1, max_ctx=512)
+                pool.ensure(0, n)
+                full = pool.table()[0].copy()
+                given = pool.trim(0, n, w, s)
+                t = pool.table()[0]
+                seen = {p // 64 for p in range(n) if p < s or p > n - w}     # by the next token, at position n
+                for lp in range((n + 63) // 64):
+                    assert (t[lp] == full[lp]) == (lp in seen or (n % 64 and lp == n // 64)), (n, w, s, lp)
+                assert given == int((t != full).sum())
+                pool.close()
+
+
+def test_trim_of_shared_pages_and_sharing_of_holes():
+    pool = k3mla.Pool(n_slots=3, max_ctx=512, n_pages=12)
+    assert pool.ensure(0, 320) == 0 and pool.share_prefix(1, 0, 320) == 0
+    shared = pool.table()[0, :5].copy()
+    assert pool.trim(0, 320, 64, 0) == 4                         # slot 1 still holds them: first seen token 257
+    assert pool.stats() == (12, 5) and all(pool.refs(int(p)) == 1 for p in shared[:4])
+    assert pool.share_prefix(2, 0, 320) == 0                     # the holes come along
+    assert np.all(pool.table()[2, :4] == -1) and pool.table()[2, 4] == shared[4] and pool.refs(int(shared[4])) == 3
+    for s in (0, 1, 2):
+        assert pool.release(s) == 0
+    assert pool.stats() == (12, 0)
+    assert pool.ensure(0, 512) == 0 and len(set(pool.table()[0].tolist())) == 8   # no page twice in the free list
+    pool.close()
+
+
+def test_truncate_gives_back_the_pages_behind():
+    pool = k3mla.Pool(n_slots=2, max_ctx=512)
+    assert pool.ensure(0, 512) == 0
+    before = pool.table()[0].copy()
+    assert pool.truncate(0, 512) == 0 and pool.stats()[1] == 8
+    assert pool.truncate(0, 65) == 0 and pool.stats()[1] == 2
+    assert np.array_equal(pool.table()[0, :2], before[:2]) and np.all(pool.table()[0, 2:] == -1)
+    assert pool.truncate(0, 2 ** 31 - 1) == 0 and pool.stats()[1] == 2
+    assert pool.ensure(0, 512) == 0 and pool.stats()[1] == 8
+    assert pool.truncate(0, 0) == 0 and pool.stats()[1] == 0
+    pool.close()
+
+
+def test_pool_refusals():
+    pool = k3mla.Pool(n_slots=1, max_ctx=128)
+    assert pool.trim(1, 0, 1, 0) == -3 and pool.trim(0, 129, 1, 0) == -4
+    assert pool.trim(0, -1, 1, 0) == -1 and pool.trim(0, 1, 0, 0) == -1 and pool.trim(0, 1, 1, -1) == -1
+    assert pool.truncate(1, 0) == -3 and pool.truncate(0, -1) == -1
+    lib = k3mla.load()
+    assert lib.k3mla_pool_trim(None, 0, 0, 1, 0) == -1 and lib.k3mla_pool_truncate(None, 0, 0) == -1
+    pool.close()
+
+
+P = ctypes.c_void_p(256)          # never dereferenced: every call below is refused on the host
+ODD = ctypes.c_void_p(264)        # 8-byte aligned only
+
+
+def norm_rope(lib, **change):
+    a = dict(q=P, q_out=P, qw=None, slab=P, n_pages=4, n_layers=2, layer=1, table=P, cols=2, pos0=P, start=P, c=P, cs=576,
+             cw=None, k=P, ks=576, kw=None, eps=1e-6, inv=None, inter=0, B=2, R=3, err=None, stream=None)
+    a.update(change)
+    return lib.k3mla_norm_rope_append(*a.values())
+
+
+@pytest.mark.parametrize("change", [
+    dict(layer=2), dict(layer=-1), dict(n_pages=0), dict(cols=0), dict(cs=511), dict(cs=580), dict(ks=63), dict(ks=68),
+    dict(eps=-1.0), dict(eps=float("nan")), dict(B=-1), dict(R=-1), dict(start=None), dict(q=None), dict(q_out=None),
+    dict(slab=None), dict(table=None), dict(pos0=None), dict(c=None), dict(k=None), dict(q=ODD), dict(q_out=ODD),
+    dict(slab=ODD), dict(c=ODD), dict(k=ODD), dict(qw=ODD), dict(cw=ODD), dict(kw=ODD), dict(inv=ctypes.c_void_p(257)),
+    dict(R=2 ** 31 - 1)])
+def test_norm_rope_refusals(change):
+    lib = k3mla.load()
+    assert norm_rope(lib, **change) == -1
+    assert b"k3mla_norm_rope_append" in lib.k3mla_last_error()
+
+
+def test_norm_rope_without_rows_does_nothing():
+    lib = k3mla.load()
+    assert norm_rope(lib, R=0) == 0 and norm_rope(lib, B=0, R=0, start=None) == 0
+
+
+def compact(lib, **change):
+    a = dict(slab=P, n_pages=4, n_layers=2, table=P, cols=2, keep=P, stride=0, n=5, start=P, B=2, err=None, stream=None)
+    a.update(change)
+    return lib.k3mla_compact_rows(*a.values())
+
+
+@pytest.mark.parametrize("change", [dict(n_pages=0), dict(n_layers=0), dict(cols=0), dict(n=-1), dict(B=-1), dict(stride=4),
+                                    dict(stride=-1), dict(slab=None), dict(slab=ODD), dict(table=None), dict(keep=None),
+                                    dict(start=None)])
+def test_compact_refusals(change):
+    lib = k3mla.load()
+    assert compact(lib, **change) == -1
+    assert b"k3mla_compact_rows" in lib.k3mla_last_error()
+
+
+def test_compact_without_rows_does_nothing():
+    lib = k3mla.load()
+    assert compact(lib, n=0) == 0 and compact(lib, B=0) == 0
