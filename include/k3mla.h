@@ -331,6 +331,53 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
                        uint16_t scale_bf16, uint16_t* out, int32_t* argmax_t, void* workspace, size_t ws_bytes,
                        int B, int max_ctx, int32_t* dev_err, void* stream);
 
+/* ---- attention over a sliding window and the first tokens ----------------------------
+ * A token row with a context of n tokens (its own the last of them, at position n - 1) sees
+ *   t < min(n_sink, n)   and   max(0, n - window) <= t < n
+ * and nothing in between:
+ *   s_t = scale * (q_abs[h] . row_t),  p = softmax over the seen t,
+ *   o_lat = sum_t p_t row_t[0:512],    out[h] = W_UV[h] o_lat
+ * with a -1 table entry read as zero rows that take part in the softmax, as in k3mla_paged_decode.
+ * Scores, maxima and sums are f32 (there is no bf16 landing of the scores here); p goes to the tensor
+ * cores in bf16, o_lat as the sum of two bf16.  Pages that hold no seen token are neither read nor
+ * looked up in the table (k3mla_pool_trim frees them), and what they or the unseen tokens of other pages
+ * hold, NaN and infinities included, never reaches a result.  window >= n gives full attention.
+ *
+ * k3mla_window_decode: one token row per slot, n = ctx_len[b].
+ * k3mla_window_chunk_decode: the token rows of prefill chunks (as for k3mla_chunk_decode): row j of slot
+ * b has n = pos0[b] + j + 1, so its window moves along with it; the chunk's cache rows are appended first.
+ *
+ * What a slot sees is cut into splits as for k3mla_paged_decode, but in its list of seen pages: split_tokens
+ * (a multiple of K3MLA_TILE) counts 64 tokens a page of that list; K3MLA_SPLIT_AUTO cuts by the slot's own
+ * list.  Either way a slot's result does not depend on the rest of the batch.  k3mla_window_split_tokens plans
+ * a length that keeps the current device busy with B slots of up to max_ctx tokens (a host-side helper); a
+ * result then depends on B, max_ctx and the device.  A chunk's rows are not split.
+ *
+ * q_abs       device [B][96][576] (decode), [R][96][576] (chunk) bf16 from k3mla_absorb_q
+ * out         device [B][96][128], [R][96][128] bf16, 16-byte aligned; zeros for n <= 0 and for rows outside
+ *             every slot
+ * window      >= 1;  n_sink >= 0
+ * scale_bf16  the softmax scale as a bf16 bit pattern, positive and finite
+ * max_ctx     upper bound of n; a larger one is clamped, as one past the table is (K3MLA_DEV_CTX)
+ * workspace   device, 256-byte aligned, at least the bytes that the sizing call gives; scratch
+ * others      as for k3mla_paged_decode and k3mla_chunk_decode
+ * Two kernels on `stream` (three when max_ctx, window and split_tokens allow several splits), each reading
+ * nothing but w_kv_b before the kernel ahead of it has completed: w_kv_b must not be written by the kernel
+ * immediately before this call. */
+size_t k3mla_window_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);
+int k3mla_window_split_tokens(int B, int max_ctx, int window, int n_sink);
+int k3mla_window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                        const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                        const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                        size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
+                        int32_t* dev_err, void* stream);
+size_t k3mla_window_chunk_decode_workspace_bytes(int B, int R, int max_ctx);
+int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                              const int32_t* block_table, int max_pages_per_slot, const int32_t* pos0,
+                              const int32_t* row_start, int B, int R, const uint16_t* w_kv_b, uint16_t scale_bf16,
+                              uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx, int window, int n_sink,
+                              int32_t* dev_err, void* stream);
+
 /* The split length a slot of context ctx gets from k3mla_paged_decode:
  * split_tokens when it is positive, else the default rule's length (at most
  * K3MLA_SPLIT_MAX; K3MLA_TILE for ctx <= 0).  The slot then has

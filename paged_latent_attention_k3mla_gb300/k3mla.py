@@ -32,7 +32,8 @@ EXPORTS = (
     "k3mla_decode_layer_workspace_bytes", "k3mla_decode_layer", "k3mla_diag_decode_timeout",
     "k3mla_expanded_cache_bytes", "k3mla_expand_latent_cache", "k3mla_expanded_decode", "k3mla_diag_exact_exp",
     "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_pool_trim",
-    "k3mla_pool_truncate", "k3mla_compact_rows",
+    "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
+    "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
 )
 
 # Size of the library's built-in decode scratch (K3MLA_NOALLOC_SCRATCH_BYTES).
@@ -96,6 +97,11 @@ def load(build_if_needed: bool = True):
                                    I),
             "k3mla_norm_rope_append": ([P, P, P, P, I, I, I, P, I, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I, I, I,
                                         P, P], I),
+            "k3mla_window_decode_workspace_bytes": ([I, I, I, I, I], SZ),
+            "k3mla_window_split_tokens": ([I, I, I, I], I),
+            "k3mla_window_decode": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
+            "k3mla_window_chunk_decode_workspace_bytes": ([I, I, I], SZ),
+            "k3mla_window_chunk_decode": ([P, P, I, I, I, P, I, P, P, I, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, P, P], I),
             "k3mla_pool_trim": ([P, I, I, I, I], I),
             "k3mla_pool_truncate": ([P, I, I], I),
             "k3mla_compact_rows": ([P, I, I, P, I, P, I64, I, P, I, P, P], I),
@@ -318,6 +324,60 @@ def chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tabl
         _dev(out, torch.bfloat16, (R, H, V), "out"), _opt(argmax, torch.int32, (R, H), "argmax"),
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), int(max_ctx),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_chunk_decode")
+
+
+def window_decode_workspace_bytes(B: int, max_ctx: int, window: int, n_sink: int = 0,
+                                  split_tokens: int = SPLIT_AUTO) -> int:
+    return int(load().k3mla_window_decode_workspace_bytes(B, max_ctx, window, n_sink, split_tokens))
+
+
+def window_split_tokens(B: int, max_ctx: int, window: int, n_sink: int = 0) -> int:
+    """A split length for window_decode that keeps the current device busy with B slots; a slot's result
+    bits then depend on it (see k3mla_window_split_tokens)."""
+    return int(load().k3mla_window_split_tokens(int(B), int(max_ctx), int(window), int(n_sink)))
+
+
+def window_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor, ctx_len: torch.Tensor,
+                  w_kv_b: torch.Tensor, scale_bf16: int, out: torch.Tensor, workspace: torch.Tensor, max_ctx: int,
+                  window: int, n_sink: int = 0, split_tokens: int = SPLIT_AUTO, dev_err: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Decode over the last `window` tokens and the first `n_sink` tokens of each slot: q_abs [B, 96, 576] ->
+    out [B, 96, 128]; see k3mla_window_decode.  `workspace`: uint8, >= window_decode_workspace_bytes."""
+    B = q_abs.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    _here(slab, "slab")
+    _check(load().k3mla_window_decode(
+        _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(block_table, B), block_table.shape[1], _dev(ctx_len, torch.int32, (B,), "ctx_len"),
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _dev(out, torch.bfloat16, (B, H, V), "out"), _dev(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+        B, int(max_ctx), int(window), int(n_sink), int(split_tokens), _opt(dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream)), "k3mla_window_decode")
+
+
+def window_chunk_decode_workspace_bytes(B: int, R: int, max_ctx: int) -> int:
+    return int(load().k3mla_window_chunk_decode_workspace_bytes(B, R, max_ctx))
+
+
+def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                        pos0: torch.Tensor, row_start: torch.Tensor, w_kv_b: torch.Tensor, scale_bf16: int,
+                        out: torch.Tensor, workspace: torch.Tensor, max_ctx: int, window: int, n_sink: int = 0,
+                        dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """The token rows of prefill chunks, each over its own last `window` tokens and the slot's first `n_sink`:
+    q_abs [R, 96, 576] -> out [R, 96, 128] (slot b's rows row_start[b] .. row_start[b+1]-1, row j at position
+    pos0[b] + j); see k3mla_window_chunk_decode."""
+    R = q_abs.shape[0]
+    B = pos0.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    _here(slab, "slab")
+    _check(load().k3mla_window_chunk_decode(
+        _dev(q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(block_table, B), block_table.shape[1], _dev(pos0, torch.int32, (B,), "pos0"),
+        _dev(row_start, torch.int32, (B + 1,), "row_start"), B, R,
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _dev(out, torch.bfloat16, (R, H, V), "out"), _dev(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+        int(max_ctx), int(window), int(n_sink), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
+        "k3mla_window_chunk_decode")
 
 
 def decode_exact_workspace_bytes(B: int, max_ctx: int) -> int:

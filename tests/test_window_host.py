@@ -131,3 +131,65 @@ def test_compact_refusals(change):
 def test_compact_without_rows_does_nothing():
     lib = k3mla.load()
     assert compact(lib, n=0) == 0 and compact(lib, B=0) == 0
+
+
+def decode(lib, **change):
+    a = dict(q=P, slab=P, n_pages=4, n_layers=2, layer=1, table=P, cols=2, ctx=P, w=P, scale=0x3D94, out=P, ws=P,
+             ws_bytes=1 << 40, B=2, max_ctx=128, window=100, sink=4, split=0, err=None, stream=None)
+    a.update(change)
+    return lib.k3mla_window_decode(*a.values())
+
+
+def chunk(lib, **change):
+    a = dict(q=P, slab=P, n_pages=4, n_layers=2, layer=1, table=P, cols=2, pos0=P, start=P, B=2, R=3, w=P, scale=0x3D94,
+             out=P, ws=P, ws_bytes=1 << 40, max_ctx=128, window=100, sink=4, err=None, stream=None)
+    a.update(change)
+    return lib.k3mla_window_chunk_decode(*a.values())
+
+
+COMMON = [dict(layer=2), dict(layer=-1), dict(n_pages=0), dict(n_layers=0), dict(cols=0), dict(max_ctx=0), dict(window=0),
+          dict(window=-1), dict(sink=-1), dict(scale=0), dict(scale=0x8000), dict(scale=0xBD94), dict(scale=0x7F80),
+          dict(scale=0x7FC0), dict(B=-1), dict(n_pages=1 << 24, n_layers=4), dict(q=None), dict(q=ODD), dict(slab=None),
+          dict(slab=ODD), dict(table=None), dict(w=None), dict(w=ODD), dict(out=None), dict(out=ODD), dict(ws=None), dict(ws=ODD)]
+
+
+@pytest.mark.parametrize("change", COMMON + [dict(ctx=None), dict(split=-128), dict(split=100), dict(B=70000)])
+def test_window_decode_refusals(change):
+    lib = k3mla.load()
+    assert decode(lib, **change) == -1
+    assert b"k3mla_window_decode" in lib.k3mla_last_error()
+
+
+@pytest.mark.parametrize("change", COMMON + [dict(pos0=None), dict(start=None), dict(R=-1), dict(B=0)])
+def test_window_chunk_refusals(change):
+    lib = k3mla.load()
+    assert chunk(lib, **change) == -1
+    assert b"k3mla_window_chunk_decode" in lib.k3mla_last_error()
+
+
+def test_window_workspaces():
+    lib = k3mla.load()
+    assert decode(lib, ws_bytes=k3mla.window_decode_workspace_bytes(2, 128, 100, 4) - 1) == -6
+    assert chunk(lib, ws_bytes=k3mla.window_chunk_decode_workspace_bytes(2, 3, 128) - 1) == -6
+    assert decode(lib, B=0) == 0 and chunk(lib, R=0) == 0 and chunk(lib, R=0, B=0) == 0
+    r256 = lambda x: (x + 255) // 256 * 256
+    for B, max_ctx, w, s, split in ((1, 128, 100, 4, 0), (64, 4096, 1024, 64, 0), (3, 5000, 1000, 100, 128), (2, 10 ** 6, 9000, 0, 0)):
+        # a window covers at most (w + 62) / 64 + 1 pages, the sinks (s + 63) / 64, the context all of its own
+        pages = min(-(-max_ctx // 64), -(-min(s, max_ctx) // 64) + (min(w, max_ctx) + 62) // 64 + 1)
+        ns = -(-pages * 64 // (split or 4096))
+        o_lat = r256(2 * 96 * B * 512 * 2)
+        partial = 0 if ns == 1 else r256(B * ns * 96 * 512 * 4) + r256(B * ns * 96 * 8)
+        assert k3mla.window_decode_workspace_bytes(B, max_ctx, w, s, split) == o_lat + partial
+    assert k3mla.window_chunk_decode_workspace_bytes(2, 37, 1000) == r256(2 * 96 * 37 * 512 * 2)
+    for bad in ((0, 1, 1, 0, 0), (1, 0, 1, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1, -1, 0), (1, 1, 1, 0, 64)):
+        assert k3mla.window_decode_workspace_bytes(*bad) == 0
+
+
+def test_window_split_plan():
+    for B, max_ctx, w, s in ((1, 32768, 4096, 4), (16, 4096, 1000, 4), (64, 4096, 1024, 64), (500, 4096, 1024, 0), (1, 1, 1, 0),
+                             (3, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1)):
+        split = k3mla.window_split_tokens(B, max_ctx, w, s)
+        assert split >= 128 and split % 128 == 0
+    assert k3mla.window_split_tokens(500, 4096, 1024, 0) >= 1024      # more slots than SM pairs: a split a slot
+    assert k3mla.window_split_tokens(1, 32768, 4096, 4) < k3mla.window_split_tokens(16, 32768, 4096, 4)
+    assert k3mla.window_split_tokens(0, 1, 1, 0) == 128
