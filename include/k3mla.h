@@ -339,7 +339,7 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  *   o_lat = sum_t p_t row_t[0:512],    out[h] = W_UV[h] o_lat
  * with a -1 table entry read as zero rows that take part in the softmax, as in k3mla_paged_decode.
  * Scores, maxima and sums are f32 (there is no bf16 landing of the scores here); p goes to the tensor
- * cores in bf16, o_lat as the sum of two bf16.  Pages that hold no seen token are neither read nor
+ * cores in bf16, o_lat in f16 with a power of two per row.  Pages that hold no seen token are neither read nor
  * looked up in the table (k3mla_pool_trim frees them), and what they or the unseen tokens of other pages
  * hold, NaN and infinities included, never reaches a result.  window >= n gives full attention.
  *

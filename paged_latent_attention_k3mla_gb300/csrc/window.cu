@@ -9,8 +9,9 @@
 //
 // Numerics.  Scores, maxima, sums and o_lat are f32.  Three roundings go below that: the p of the second
 // contraction to bf16 (the tensor core's operand type; both operands have one type and the cache is bf16),
-// o_lat to a pair of bf16 (hi + lo, 2^-17: a single bf16 here would add as much error again as the output's
-// own rounding does), and the output to bf16.
+// o_lat to f16 with a power of two per row (2^-12 of an entry; bf16 here would add as much error again as
+// the output's own rounding does), and the output to bf16.  W_UV, bf16, takes part as f16 with a power of
+// two per row of its own: exact, but for entries below 2^-29 of their row's largest.
 //
 // Structure.  A unit of work is 96 heads of one slot and one split of what it sees (decode), or 32 heads of
 // up to four consecutive token rows (chunk): a row in each of the 128 (96) TMEM lanes.  Clusters of two
@@ -23,14 +24,13 @@
 //   * A unit's pages are the logical pages that hold a seen token, in ascending order: those of the sinks,
 //     then those of the window.  Pages in between are neither read nor looked up, so they may have been
 //     freed (k3mla_pool_trim).
-//   * Score CTA: three producer threads stream Q and then the page thirds through one ring of 24 KB units;
-//     four warps copy Q into TMEM once the last MMA of the unit before has read the old one; three threads
-//     issue the score MMAs (A = Q from TMEM, B = the page); eight softmax warps mask, keep a lazily moved
-//     reference max, and pass bf16 p to the PV CTA by bulk DSMEM copies.
-//   * PV CTA: four producer threads stream the pages' latents again (mostly from L2) as half pages; one
+//   * Score CTA: a producer streams Q and then the page thirds through one ring of 24 KB units; three
+//     threads issue the score MMAs (A = Q from TMEM, B = the page); the softmax warps of each quarter take a page
+//     each in turn, mask, keep a lazily moved reference max, and pass bf16 p to the PV CTA by bulk DSMEM copies
+//     (the first of them copies Q into TMEM when the last MMA of the unit before has read the old one).
+//   * PV CTA: a producer streams the pages' latents again (mostly from L2) as half pages; one
 //     thread issues O[rows x 512] += P . C; four warps rescale O when a reference moved and, at a unit's
-//     end, take O out of TMEM through two staged boxes while the next unit's MMAs already run; four warps
-//     clear what a page holds of unseen tokens.
+//     end, take O out of TMEM through staged boxes and bulk tensor stores; four warps clear what a page holds of unseen tokens.
 //   * Unseen tokens.  Their scores are replaced (never multiplied), and in the pages that hold some their
 //     latents are cleared in shared memory, because p = 0 times a NaN or infinity there would still be
 //     NaN.  In a chunk a token may be seen by some rows of the unit only; then just its NaNs and
@@ -59,54 +59,57 @@ template <bool MQ> struct WCfg {
     static constexpr int NQ = (9 + QPU - 1) / QPU;       // ring uses that a unit's Q takes
     static constexpr int QCHUNK = ROWS * 128;            // one chunk of Q, [rows][128 B]
     static constexpr int NPBUF = MQ ? 3 : 4;             // PV CTA: P buffers
+    static constexpr int NPAR = MQ ? 3 : 2;              // score CTA: softmax warps of a quarter, a page each in turn
+    static constexpr int W_PROD = 4 * NPAR;              // ... behind them the producer ...
+    static constexpr int W_MMA0 = W_PROD + 1;            // ... and three MMA issuers
+    static constexpr int THREADS = 32 * (W_MMA0 + 3);
+    static constexpr int REGS = 65536 / THREADS / 8 * 8 < 168 ? 65536 / THREADS / 8 * 8 : 168;
     static constexpr int PSTAGE = RPQ * 128;             // score CTA: one softmax warp's P rows (x 64 tokens)
     static constexpr int PT_BYTES = ROWS * 128;          // P [rows][64 tokens] bf16, K-major, 128-byte swizzle
     static constexpr int META_ALPHA = PT_BYTES;          // f32 alpha[rows]
     static constexpr int META_FLAGS = PT_BYTES + 4 * ROWS;     // u32 flags[4]: "some row of quarter w rescaled"
     static constexpr int PCOPY = PT_BYTES + 4 * ROWS + 16;     // bytes sent per page
     static constexpr int PBUF = (PCOPY + 1023) / 1024 * 1024;  // buffer pitch
-    static constexpr int BOX = ROWS * 128;               // PV CTA: one write-out box
 };
 constexpr int WN_S = 3;        // S buffers, one MMA issuer each
-constexpr int WN_HALF = 4;     // PV CTA: half-page slots, one producer each
-// rank 0: warps 0-7 softmax, 8-10 producers, 11-13 MMA issuers, 11-14 copy Q; rank 1: warps 0-3 epilogue,
-// 4-7 producers, 9 MMA issuer, 10-13 clear unseen tokens.  Warp 8 allocates TMEM in both.
-constexpr int W_THREADS = 480;
-constexpr int WW_PROD0 = 8, WW_MMA0 = 11, WW_COPY0 = 11, WW_ALLOC = 8;
-constexpr int WW_HPROD0 = 4, WW_PV = 9, WW_CLEAR0 = 10;
-// named barriers (0 is __syncthreads): score CTA, the decision hand-off of a quarter's two softmax warps, their
-// final combine, the four copy warps; PV CTA, the epilogue warps
-constexpr uint32_t WB_HAND = 1, WB_FIN = 9, WB_COPY = 13, WB_OUT = 1;
+constexpr int WN_HALF = 4;     // PV CTA: half-page slots
+constexpr int W_BOX = 32 * 128;  // PV CTA: one write-out box of a warp, 32 rows of 128 bytes
+constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6;  // PV CTA: warps 0-3 epilogue, the producer, the MMA issuer,
+                                                        // four warps that clear unseen tokens
+// named barriers (0 is __syncthreads): score CTA, a quarter's decision hand-offs by turn; PV CTA, the
+// epilogue warps
+constexpr uint32_t WB_HAND = 1, WB_OUT = 1;
 
 template <bool MQ> struct __align__(1024) WSmem {
     using C = WCfg<MQ>;
     union {
         struct {
             uint8_t ring[C::NUNIT][THIRD];
-            uint8_t pstage[8][C::PSTAGE];
+            uint8_t pstage[4 * C::NPAR][C::PSTAGE];
         } c0;
         struct {
             uint8_t ring[WN_HALF][SLOT1];
             uint8_t recv[C::NPBUF][C::PBUF];
-            uint8_t box[2][C::BOX];
+            uint8_t box[C::ROWS / 32][2][W_BOX];
         } c1;
     } u;
     uint64_t full[8], empty[8];          // the ring of this CTA
     uint64_t s_full[WN_S], s_empty[WN_S];
     uint64_t q_free, q_ready;            // Q of the unit before is no longer read / Q of this unit is in TMEM
     uint64_t p_full[C::NPBUF], p_empty[C::NPBUF];
-    uint64_t o_done, epi_req, epi_done, clear_req, clear_done;
+    uint64_t o_done, epi_req, epi_done, clear_done[2];
     uint64_t l_full[2], rl_free[2];      // 1 / l of every row, by parity of the unit
+    uint64_t fin_full[2][4], fin_free[2][4];  // a quarter's sums of exp, by parity of the unit
     float rl[2][C::ROWS];
-    float xm[2][4][32], xa[2][4][32];    // reference max after a page and its rescale factor, by page parity
-    float fin_l[2][4][32];               // the odd pages' sum of exp, by unit parity
-    int32_t unit_loaded[C::NUNIT];       // uses of a ring unit whose load has been issued ...
-    int32_t unit_taken[C::NUNIT];        // ... and whose consumer has taken it
+    float xm[2][4][32];                  // reference max after a page, by parity of the page
+    float fin_l[2][C::NPAR][4][32];      // a unit's sums of exp by softmax warp, by parity of the unit
+    float fin_m[2][C::NPAR][4][32];      // ... and the reference each is held to
+    int32_t unit_taken[C::NUNIT];        // uses of a ring unit that their consumer has taken
+    int32_t copied[C::NUNIT];            // quarters that have copied their rows of the Q chunk in a ring unit
+    int32_t pv_seen;                     // PV CTA: pages whose latents the MMA issuer has seen arrive and cleared
     uint32_t tmem_base;
     uint32_t epi_cmd, epi_stage;         // to the epilogue warps: bit 0 rescale O, bit 1 write it out
     int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_single;
-    uint32_t clear_cmd, clear_slot[2];   // to the clearing warps (0: leave): the page's two half slots, ...
-    uint32_t clear_none[2], clear_some[2];  // ... its tokens that no row sees, and those that some rows see
     int32_t abort_flag;
     uint64_t wait_ns;
 };
@@ -114,11 +117,10 @@ template <bool MQ> struct __align__(1024) WSmem {
 template <bool MQ> constexpr bool wsmem_fits()
 {
     using C = WCfg<MQ>;
-    static_assert(C::QPU * C::QCHUNK <= THIRD && C::QCHUNK % 1024 == 0 && SLOT1 % 1024 == 0 && C::PBUF % 1024 == 0 &&
-                      C::BOX % 1024 == 0,
-                  "operand tiles and boxes fit and start 1024-byte aligned");
+    static_assert(C::QPU * C::QCHUNK <= THIRD && C::QCHUNK % 1024 == 0 && SLOT1 % 1024 == 0 && C::PBUF % 1024 == 0,
+                  "operand tiles fit and start 1024-byte aligned");
     static_assert(C::NUNIT <= 8 && WN_HALF <= 8, "barrier arrays");
-    static_assert(C::NPBUF * C::PBUF + 2 * C::BOX >= (C::NPBUF - 1) * C::PBUF + 128 * 128,
+    static_assert(WN_HALF * SLOT1 + (C::NPBUF - 1) * C::PBUF + 128 * 128 <= sizeof(WSmem<MQ>::u),
                   "all 128 rows of the last P buffer, read as the A operand, lie in this CTA's tile area");
     static_assert(sizeof(WSmem<MQ>) + 1024 <= 227 * 1024, "shared memory of one CTA (with alignment slack)");
     return true;
@@ -129,6 +131,8 @@ struct WinParams {
     const int32_t* table;
     const int32_t* ctx_len;              // decode
     const int32_t *pos0, *row_start;     // chunk
+    uint16_t* olat;                      // [96][R][512] f16: o_lat times a power of two per row
+    float* oscale;                       // [96][R]: what undoes it
     float* ws_o;                         // [B][nsplit][96][512] f32 partials (decode, nsplit > 1)
     float2* ws_ml;                       // [B][nsplit][96]: reference max (in log2 units), sum of exp
     int32_t* dev_err;
@@ -164,9 +168,9 @@ __host__ __device__ inline int w_pages(int n_lo, int n_hi, int window, int n_sin
 }
 
 // Unit u (a whole warp, every lane the same answer).
-template <bool MQ> __device__ __forceinline__ WUnit w_unit(const WinParams& p, int u, bool report)
+// Out of line: every role calls it, once a unit.
+template <bool MQ> __device__ __noinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report)
 {
-    WUnit g;
     g.npg = 0;
     g.first = 0;
     g.s = 0;
@@ -206,7 +210,7 @@ template <bool MQ> __device__ __forceinline__ WUnit w_unit(const WinParams& p, i
             }
             before += __shfl_sync(0xFFFFFFFFu, upto, 31);
         }
-        if (!found) return g;
+        if (!found) return;
         const int64_t n0 = (int64_t)p.pos0[g.b] + (g.row0 - p.row_start[g.b]) + 1;
         const int64_t n1 = n0 + g.rows - 1;
         if (report && n1 > p.cap && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
@@ -228,7 +232,6 @@ template <bool MQ> __device__ __forceinline__ WUnit w_unit(const WinParams& p, i
         g.first = g.s * per;
         g.npg = min(per, max(0, all - g.first));
     }
-    return g;
 }
 
 __device__ __forceinline__ int w_logical(const WUnit& g, int i)
@@ -244,6 +247,12 @@ __device__ __forceinline__ uint64_t w_seen(const WinParams& p, int n, int t0)
 {
     const uint64_t before_n = w_low(n - t0);
     return before_n & (w_low(min(p.n_sink, n) - t0) | ~w_low(max(0, n - p.window) - t0));
+}
+
+// Whether rows with contexts n_lo .. n_hi all see the whole page at t0 (most pages: no masks to work out).
+__device__ __forceinline__ bool w_whole(const WinParams& p, int n_lo, int n_hi, int t0)
+{
+    return t0 + PAGE <= n_lo && (t0 >= n_hi - p.window || t0 + PAGE <= p.n_sink);
 }
 
 // The slab row of logical page lp of slot b, or one past the end (read as zeros).
@@ -280,7 +289,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
         mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.s_empty[i], 4);
     }
-    mbar_init(&sm.q_free, 3);
+    mbar_init(&sm.q_free, WN_S);
     mbar_init(&sm.q_ready, 4);
     for (int i = 0; i < C::NPBUF; ++i) {
         mbar_init(&sm.p_full[i], 1);
@@ -289,13 +298,17 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.epi_req, 1);
     mbar_init(&sm.epi_done, 4);
-    mbar_init(&sm.clear_req, 1);
-    mbar_init(&sm.clear_done, 4);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.clear_done[i], 4);
     for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.l_full[i], 1);
         mbar_init(&sm.rl_free[i], 1);
+        for (int q = 0; q < 4; ++q) {
+            mbar_init(&sm.fin_full[i][q], C::NPAR - 1);
+            mbar_init(&sm.fin_free[i][q], 1);
+        }
     }
-    for (int i = 0; i < C::NUNIT; ++i) sm.unit_loaded[i] = sm.unit_taken[i] = 0;
+    for (int i = 0; i < C::NUNIT; ++i) sm.unit_taken[i] = sm.copied[i] = 0;
+    sm.pv_seen = 0;
     if (rank == 1) {  // expected before anything is sent
         for (int i = 0; i < C::NPBUF; ++i) mbar_arrive_expect_tx(&sm.p_full[i], C::PCOPY);
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.l_full[i], 4 * C::ROWS);
@@ -306,121 +319,71 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
 
 // ---- score CTA ----------------------------------------------------------------------------
 
-// Producer t: Q uses t, t + 3, ... of a unit, then third t of each of its pages.  The uses of the ring are
-// numbered on from unit to unit; use g lies in ring unit g % NUNIT.
+// Producer: a unit's Q, then its pages in thirds.  The uses of the ring are numbered on from unit to unit; use g
+// lies in ring unit g % NUNIT.
 template <bool MQ>
 __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_page, const CUtensorMap& tm_q,
-                                          const WinParams& p, int t)
+                                          const WinParams& p)
 {
     using C = WCfg<MQ>;
     const bool me = lane_id() == 0;
     bool ok = true;
-    int base = 0;
-    auto take = [&](int g, uint32_t bytes) -> int {  // the ring unit, ready to be loaded; -1 after an abort
-        const int u = g % C::NUNIT, k = g / C::NUNIT;
-        if (!wait_count(&sm.unit_loaded[u], k, sm, p.dev_err) ||
-            !wait_bar(&sm.empty[u], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err))
-            return -1;
-        *reinterpret_cast<volatile int32_t*>(&sm.unit_loaded[u]) = k + 1;
-        mbar_arrive_expect_tx(&sm.full[u], bytes);
+    int use = 0;
+    auto take = [&](uint32_t bytes) -> int {  // the next ring unit, ready to be loaded
+        const int u = use % C::NUNIT, k = use / C::NUNIT;
+        ++use;
+        ok = ok && wait_bar(&sm.empty[u], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
+        if (ok) mbar_arrive_expect_tx(&sm.full[u], bytes);
         return u;
     };
     W_FOR_UNITS(un)
     {
-        const WUnit g = w_unit<MQ>(p, un, false);
+        WUnit g;
+        w_unit<MQ>(g, p, un, false);
         if (g.npg == 0) continue;
-        for (int j = t; j < C::NQ && me && ok; j += 3) {
-            const int u = take(base + j, C::QPU * C::QCHUNK);
-            if (u < 0) {
-                ok = false;
-            } else if constexpr (MQ) {
-                // heads 32 hb .. of four consecutive token rows (those past the group land in lanes nobody reads)
-                tma_load_4d(sm.u.c0.ring[u], &tm_q, 0, 32 * g.hb, g.row0, j, &sm.full[u]);
-            } else {
-                tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
-            }
+        for (int j = 0; j < C::NQ && me && ok; ++j) {
+            const int u = take(C::QPU * C::QCHUNK);
+            if (!ok) break;
+            // (chunk: heads 32 hb .. of four consecutive token rows; those past the group land in lanes nobody reads)
+            if constexpr (MQ) tma_load_4d(sm.u.c0.ring[u], &tm_q, 0, 32 * g.hb, g.row0, j, &sm.full[u]);
+            else tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
         }
-        base += C::NQ;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
-            if (me && ok) {
-                const int u = take(base + 3 * i + t, THIRD);
-                if (u < 0) ok = false;
-                else tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * t, &sm.full[u]);
+            for (int t = 0; t < 3 && me && ok; ++t) {
+                const int u = take(THIRD);
+                if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * t, &sm.full[u]);
             }
         }
-        base += 3 * g.npg;
     }
     if (!ok) drain_inflight();
 }
 
-// Warps WW_COPY0 .. +3: Q of the unit from the ring into TMEM, lane 32 w + l <- row RPQ w + l; then, in the
-// first three of them, the score MMAs of the pages i = r (mod 3, counted on from unit to unit).
-template <bool MQ>
-__device__ __forceinline__ void w_copy_and_score(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
+// Issuer r: the score MMAs of the pages a = r (mod 3), counted on from unit to unit, into S buffer r.  (One
+// thread alone issues these MMAs at 50 clocks each, the tensor core retires one every 32.)
+template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int r)
 {
     using C = WCfg<MQ>;
-    const int lane = (int)lane_id(), qd = (int)(warp & 3u), r = (int)warp - WW_MMA0;
-    const int row = C::RPQ * qd + lane;
-    const uint32_t taddr = tbase + ((32u * (uint32_t)qd) << 16) + Q_COL;
     bool ok = true;
     int base = 0, gp = 0, done = 0;  // ring uses, pages and units before this unit
     W_FOR_UNITS(un)
     {
-        const WUnit g = w_unit<MQ>(p, un, false);
+        WUnit g;
+        w_unit<MQ>(g, p, un, false);
         if (g.npg == 0) continue;
-        // the score MMAs of the unit before have read the old Q
-        if (ok && done > 0) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.q_free, (uint32_t)(done - 1) & 1u, sm, p.dev_err));
-        tc_fence_after();
-        for (int j = 0; j < C::NQ; ++j) {
-            const int u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
-            if (ok)
-                ok = __all_sync(0xFFFFFFFFu, wait_count(&sm.unit_taken[u], k, sm, p.dev_err) &&
-                                                 wait_bar(&sm.full[u], (uint32_t)(k & 1), sm, p.dev_err));
-            if (ok)
-#pragma unroll
-                for (int cc = 0; cc < C::QPU; ++cc) {
-                    const int c = C::QPU * j + cc;
-                    if (c >= 9) break;
-                    uint32_t v[32];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                        if (lane < C::RPQ)
-                            w = *reinterpret_cast<const uint4*>(sm.u.c0.ring[u] + cc * C::QCHUNK + row * 128 +
-                                                                ((x ^ (row & 7)) << 4));
-                        v[4 * x] = w.x, v[4 * x + 1] = w.y, v[4 * x + 2] = w.z, v[4 * x + 3] = w.w;
-                    }
-                    tmem_st32(taddr + 32u * (uint32_t)c, v);
-                }
-            tmem_wait_st();
-            named_bar(WB_COPY, 128);  // all four quarters have read the ring unit
-            if (warp == WW_COPY0 && lane == 0) {
-                *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = k + 1;
-                mbar_arrive(&sm.empty[u]);
-            }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_ready);
         base += C::NQ;
-        if (r < WN_S && lane == 0 && ok) {
+        if (lane_id() == 0 && ok) {
             ok = wait_bar(&sm.q_ready, (uint32_t)done & 1u, sm, p.dev_err);
             tc_fence_after();
             for (int i = (r + WN_S - gp % WN_S) % WN_S; i < g.npg && ok; i += WN_S) {
                 const int k = (gp + i) / WN_S;
-                if (!wait_bar(&sm.s_empty[r], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait_bar(&sm.s_empty[r], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
-                    if (!wait_count(&sm.unit_taken[u], ku, sm, p.dev_err) ||
-                        !wait_bar(&sm.full[u], (uint32_t)(ku & 1), sm, p.dev_err)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = wait_count(&sm.unit_taken[u], ku, sm, p.dev_err) &&
+                         wait_bar(&sm.full[u], (uint32_t)(ku & 1), sm, p.dev_err);
+                    if (!ok) break;
                     *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = ku + 1;
                     tc_fence_after();
                     issue_score_third(tbase, S_COL + 64u * (uint32_t)r, smem_u32(sm.u.c0.ring[u]), t);
@@ -430,7 +393,6 @@ __device__ __forceinline__ void w_copy_and_score(WSmem<MQ>& sm, const WinParams&
             }
             if (ok) umma_commit(&sm.q_free);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
         base += 3 * g.npg;
         gp += g.npg;
         ++done;
@@ -438,9 +400,51 @@ __device__ __forceinline__ void w_copy_and_score(WSmem<MQ>& sm, const WinParams&
     if (!ok) drain_inflight();
 }
 
-// Softmax warp (quarter qd, page parity par): thread l = row RPQ qd + l of the pages of its parity.  The
-// reference max is a chain through a unit's pages: each warp hands its page's decision (new reference,
-// rescale factor) to the other warp of the quarter.  All in log2 units.
+// A warp of each quarter copies its rows of Q from the ring into TMEM (lane 32 w + l <- row RPQ w + l), once the
+// score MMAs of the unit before have read the old Q.
+template <bool MQ>
+__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int base, int done,
+                                         bool ok)
+{
+    using C = WCfg<MQ>;
+    const int lane = (int)lane_id(), row = C::RPQ * qd + lane;
+    const uint32_t taddr = tbase + ((32u * (uint32_t)qd) << 16) + Q_COL;
+    if (ok && done > 0) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.q_free, (uint32_t)(done - 1) & 1u, sm, p.dev_err));
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < 9 && ok; ++c) {
+        const int j = c / C::QPU, u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
+        if (c % C::QPU == 0)
+            ok = __all_sync(0xFFFFFFFFu, wait_count(&sm.unit_taken[u], k, sm, p.dev_err) &&
+                                             wait_bar(&sm.full[u], (uint32_t)(k & 1), sm, p.dev_err));
+        if (!ok) break;
+        uint32_t v[32];
+        const uint8_t* src = sm.u.c0.ring[u] + (c % C::QPU) * C::QCHUNK + row * 128;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (lane < C::RPQ) w = *reinterpret_cast<const uint4*>(src + ((x ^ (row & 7)) << 4));
+            v[4 * x] = w.x, v[4 * x + 1] = w.y, v[4 * x + 2] = w.z, v[4 * x + 3] = w.w;
+        }
+        tmem_st32(taddr + 32u * (uint32_t)c, v);
+        __syncwarp();
+        if ((c + 1) % C::QPU == 0 || c == 8)
+            if (lane == 0 && atomicAdd(&sm.copied[u], 1) == 3) {  // the last of the four quarters: the ring unit is read
+                sm.copied[u] = 0;
+                *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = k + 1;
+                mbar_arrive(&sm.empty[u]);
+            }
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.q_ready);
+    return ok;
+}
+
+// Softmax warp (quarter qd, turn par): thread l = row RPQ qd + l of every NPAR-th page.  The reference max is a
+// chain through a unit's pages: the warp of each page hands its decision on to the warp of the next one; a
+// warp's sum of exp follows the reference when it comes to its own next page.  All in log2 units.
 template <bool MQ>
 __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
 {
@@ -448,22 +452,26 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     const int qd = (int)(warp & 3u), par = (int)(warp >> 2), l = (int)lane_id();
     const int h = C::RPQ * qd + l;
     const bool has_row = l < C::RPQ;
-    const uint32_t bar_in = WB_HAND + 2u * (uint32_t)qd + (uint32_t)(par ^ 1);
-    const uint32_t bar_out = WB_HAND + 2u * (uint32_t)qd + (uint32_t)par;
+    // barrier x of a quarter: the warp of turn x arrives, the next one's waits, and neither ever does the other
+    const uint32_t hand = WB_HAND + (uint32_t)(C::NPAR * qd);
     const uint32_t t_lane = tbase + ((32u * (uint32_t)qd) << 16) + S_COL;
     const uint32_t recv0 = mapa(smem_u32(sm.u.c1.recv[0]), 1);
     const uint32_t pfull0 = mapa(smem_u32(&sm.p_full[0]), 1);
     const float TAU2 = TAU * 1.4426950408889634f;
     uint8_t* stage = sm.u.c0.pstage[warp];
     bool ok = true;
-    int gp = 0, done = 0, singles = 0;
+    int base = 0, gp = 0, done = 0, singles = 0;
     W_FOR_UNITS(un)
     {
-        const WUnit g = w_unit<MQ>(p, un, warp == 0 && l == 0);
+        WUnit g;
+        w_unit<MQ>(g, p, un, warp == 0 && l == 0);
         if (g.npg == 0) continue;
+        if (par == 0) ok = w_copy_q<MQ>(sm, p, tbase, qd, base, done, ok);
+        base += C::NQ + 3 * g.npg;
         const int n = MQ ? (qd < g.rows ? w_clamp(g.n0 + qd, p.cap) : 0) : g.n0;  // this quarter's context
         float m_ref = -INFINITY, lsum = 0.f;
-        for (int i = (gp & 1) == par ? 0 : 1; i < g.npg; i += 2) {
+        const int rel = (par + C::NPAR - gp % C::NPAR) % C::NPAR;  // this warp's first page of the unit
+        for (int i = rel; i < g.npg; i += C::NPAR) {
             const int a = gp + i, r = a % WN_S, k = a / WN_S;
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.s_full[r], (uint32_t)(k & 1), sm, p.dev_err));
             uint32_t x[2][32];
@@ -479,8 +487,9 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
 #pragma unroll
                 for (int q = 0; q < 32; ++q) x[0][q] = x[1][q] = 0xFF800000u;
             }
-            const uint64_t seen = w_seen(p, n, PAGE * w_logical(g, i));
-            if (seen != ~0ull) {
+            const int t0 = PAGE * w_logical(g, i);
+            if (!w_whole(p, n, n, t0)) {
+                const uint64_t seen = w_seen(p, n, t0);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const uint32_t bits = (uint32_t)(seen >> (32 * e));
@@ -496,40 +505,42 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
                 m4[q & 3] = fmaxf(m4[q & 3], __uint_as_float(x[1][q]));
             }
             const float pmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.kscale;
-            float m_prev = -INFINITY;
-            if (i > 0) {  // the decision of the page before, from the other warp
-                named_bar(bar_in, 64);
-                m_prev = sm.xm[(a - 1) & 1][qd][l];
-                lsum *= sm.xa[(a - 1) & 1][qd][l];
-            }
+            const float m_own = m_ref;
             float alpha = 1.f;
             bool resc = false;
             if (i == 0) {
                 m_ref = pmax;
-            } else if (pmax > m_prev + TAU2) {
-                alpha = ex2_approx(m_prev - pmax);
-                lsum *= alpha;
-                m_ref = pmax;
-                resc = true;
-            } else {
-                m_ref = m_prev;
+            } else {  // the decision of the page before
+                named_bar(hand + (uint32_t)((a - 1) % C::NPAR), 64);
+                m_ref = sm.xm[(a - 1) & 1][qd][l];
+                if (pmax > m_ref + TAU2) {
+                    alpha = ex2_approx(m_ref - pmax);
+                    m_ref = pmax;
+                    resc = true;
+                }
             }
             sm.xm[a & 1][qd][l] = m_ref;
-            sm.xa[a & 1][qd][l] = alpha;
-            named_bar_arrive(bar_out, 64);
+            named_bar_arrive(hand + (uint32_t)par, 64);
+            if (m_own != m_ref) lsum *= ex2_approx(m_own - m_ref);  // (nothing summed yet: 0)
             const float mb = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: every p is 0
             uint32_t sp[32];
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t part[2] = {0ull, 0ull};
+            const uint64_t k2 = f32x2(p.kscale, p.kscale), mb2 = f32x2(-mb, -mb);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
                 for (int q = 0; q < 16; ++q) {  // p~ = bf16(2^(s - m_ref)); l sums the f32 values
-                    const float e0 = ex2_approx(fmaf(__uint_as_float(x[e][2 * q]), p.kscale, -mb));
-                    const float e1 = ex2_approx(fmaf(__uint_as_float(x[e][2 * q + 1]), p.kscale, -mb));
-                    part[q & 3] += e0 + e1;
+                    float e0, e1;
+                    f32x2_parts(fma_f32x2(f32x2(__uint_as_float(x[e][2 * q]), __uint_as_float(x[e][2 * q + 1])), k2, mb2),
+                                e0, e1);
+                    e0 = ex2_approx(e0);
+                    e1 = ex2_approx(e1);
+                    part[q & 1] = add_f32x2(part[q & 1], f32x2(e0, e1));
                     sp[16 * e + q] = pack_bf16x2(e0, e1);
                 }
-            lsum += (part[0] + part[1]) + (part[2] + part[3]);
+            float l0, l1;
+            f32x2_parts(add_f32x2(part[0], part[1]), l0, l1);
+            lsum += l0 + l1;
             // this warp's P rows, once the bulk copy of its page before has read the staging rows
             if (l == 0) bulk_wait_read<0>();
             __syncwarp();
@@ -555,15 +566,24 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             if (freed && l == 0) st_async_b32(dst + C::META_FLAGS + 4 * qd, any ? 1u : 0u, bar);
         }
         const int last = gp + g.npg - 1;
-        if ((last & 1) != par) {  // the last page's decision, when that page was the other warp's
-            named_bar(bar_in, 64);
-            m_ref = sm.xm[last & 1][qd][l];
-            lsum *= sm.xa[last & 1][qd][l];
-        }
-        if (par == 1) sm.fin_l[done & 1][qd][l] = lsum;
-        named_bar(WB_FIN + (uint32_t)qd, 64);
-        if (par == 0 && ok && !aborted(sm)) {
-            const float ltot = lsum + sm.fin_l[done & 1][qd][l];
+        if ((last + 1) % C::NPAR == par) named_bar(hand + (uint32_t)(last % C::NPAR), 64);  // nobody's page follows the last
+        // the quarter's sums meet in the warp of turn 1; the others go on at once
+        if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.fin_free[done & 1][qd], (uint32_t)((done >> 1) & 1) ^ 1u, sm, p.dev_err));
+        sm.fin_l[done & 1][rel][qd][l] = lsum;
+        sm.fin_m[done & 1][rel][qd][l] = m_ref;
+        __syncwarp();
+        if (par != 1) {
+            if (l == 0) mbar_arrive(&sm.fin_full[done & 1][qd]);
+        } else if (ok && __all_sync(0xFFFFFFFFu, wait_bar(&sm.fin_full[done & 1][qd], (uint32_t)(done >> 1) & 1u, sm, p.dev_err))) {
+            m_ref = sm.fin_m[done & 1][(g.npg - 1) % C::NPAR][qd][l];  // the last page's warp
+            float ltot = 0.f;  // by the unit's own count of pages: the order does not depend on the units before
+#pragma unroll
+            for (int w = 0; w < C::NPAR; ++w) {
+                const float m_w = sm.fin_m[done & 1][w][qd][l], l_w = sm.fin_l[done & 1][w][qd][l];
+                ltot += m_w == m_ref ? l_w : l_w * ex2_approx(m_w - m_ref);
+            }
+            __syncwarp();
+            if (l == 0) mbar_arrive(&sm.fin_free[done & 1][qd]);
             if (g.single) {  // the PV CTA lands o_lat itself
                 const int sl = singles & 1;
                 // (a row that sees nothing has l = 0; its o_lat is not used)
@@ -588,30 +608,30 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
 
 // ---- PV CTA -------------------------------------------------------------------------------
 
-// Producer q: the half pages u = q (mod WN_HALF), counted on from unit to unit.
+// Producer: the units' pages again, their latents only, as half pages.
 template <bool MQ>
-__device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMap& tm_page8, const WinParams& p, int q)
+__device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMap& tm_page8, const WinParams& p)
 {
     const uint64_t pol = policy_evict_first();  // the last reader of the latent in this unit
     const bool me = lane_id() == 0;
     bool ok = true;
-    int gp = 0;
+    int e = 0;
     W_FOR_UNITS(un)
     {
-        const WUnit g = w_unit<MQ>(p, un, false);
+        WUnit g;
+        w_unit<MQ>(g, p, un, false);
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
-            const int e = 2 * (gp + i) + (q & 1), k = e / WN_HALF;
-            if (!me || !ok || e % WN_HALF != q) continue;
-            if (!wait_bar(&sm.empty[q], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err)) {
-                ok = false;
-                continue;
+            for (int x = 0; x < 2; ++x, ++e) {
+                const int q = e % WN_HALF;
+                if (!me || !ok) continue;
+                ok = wait_bar(&sm.empty[q], (uint32_t)((e / WN_HALF) & 1) ^ 1u, sm, p.dev_err);
+                if (!ok) continue;
+                mbar_arrive_expect_tx(&sm.full[q], SLOT1);
+                tma_load_3d_hint(sm.u.c1.ring[q], &tm_page8, 0, y + HALF * x, 0, &sm.full[q], pol);
             }
-            mbar_arrive_expect_tx(&sm.full[q], SLOT1);
-            tma_load_3d_hint(sm.u.c1.ring[q], &tm_page8, 0, y + HALF * (q & 1), 0, &sm.full[q], pol);
         }
-        gp += g.npg;
     }
     if (!ok) drain_inflight();
 }
@@ -640,30 +660,26 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
     int gp = 0;
     W_FOR_UNITS(un)
     {
-        const WUnit g = w_unit<MQ>(p, un, false);
+        WUnit g;
+        w_unit<MQ>(g, p, un, false);
         if (g.npg == 0) continue;
+        const int n_lo = w_clamp(g.n0, p.cap), n_hi = MQ ? w_clamp(g.n0 + g.rows - 1, p.cap) : n_lo;
         for (int i = 0; i < g.npg && me && ok; ++i) {
             const int a = gp + i, st = a % C::NPBUF;
-            const int q0 = (2 * a) % WN_HALF, q1 = q0 + 1;
-            const uint32_t ph = (uint32_t)((2 * a / WN_HALF) & 1);
-            if (!wait_bar(&sm.full[q0], ph, sm, p.dev_err) || !wait_bar(&sm.full[q1], ph, sm, p.dev_err)) {
+            const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
+            if (!wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) ||
+                !wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err)) {
                 ok = false;
                 break;
             }
-            uint64_t none, some;
-            w_unseen<MQ>(p, g, PAGE * w_logical(g, i), none, some);
-            if (none | some || i == 0) {  // (with a unit's first page always: the clearing warps' waits stay short)
-                sm.clear_cmd = 1u;
-                sm.clear_slot[0] = (uint32_t)q0;
-                sm.clear_slot[1] = (uint32_t)q1;
-                sm.clear_none[0] = (uint32_t)none;
-                sm.clear_none[1] = (uint32_t)(none >> 32);
-                sm.clear_some[0] = (uint32_t)some;
-                sm.clear_some[1] = (uint32_t)(some >> 32);
-                mbar_arrive(&sm.clear_req);
-                ok = wait_bar(&sm.clear_done, clear_k++ & 1u, sm, p.dev_err);
-                if (!ok) break;
+            if (!w_whole(p, n_lo, n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
+                if (!wait_bar(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u, sm, p.dev_err)) {
+                    ok = false;
+                    break;
+                }
+                ++clear_k;
             }
+            *reinterpret_cast<volatile int32_t*>(&sm.pv_seen) = a + 1;
             if (!wait_bar(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1), sm, p.dev_err, true)) {
                 ok = false;
                 break;
@@ -709,138 +725,170 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
     if (!ok) {
         drain_inflight();
         *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
-    } else if (me) {  // the clearing and epilogue warps leave
+    } else if (me) {  // the epilogue warps leave
         if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
         sm.epi_cmd = 0u;
         mbar_arrive(&sm.epi_req);
-        sm.clear_cmd = 0u;
-        mbar_arrive(&sm.clear_req);
     }
 }
 
-// Warps WW_CLEAR0 .. +3: in the two half-page slots named, the latents of tokens that no row sees become
-// zero, and the NaNs and infinities of those that some rows see.
+// Warps WW_CLEAR0 .. +3: in every page that not all rows of the unit see whole, the latents of tokens that no
+// row sees become zero, and so do the NaNs and infinities of those that only some rows see.  They run ahead of
+// the MMA issuer by up to two pages: page a is taken up once the issuer is past the waits of page a - 2, so
+// that neither the parity of a half-page slot's barrier (used again every two to three pages) nor that of the
+// two barriers they answer on in turn can be mistaken.
 template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, uint32_t warp)
 {
-    const int tid = ((int)warp - WW_CLEAR0) * 32 + (int)lane_id();
-    for (uint32_t k = 0;; ++k) {
-        const bool got = wait_bar(&sm.clear_req, k & 1u, sm, p.dev_err);
-        if (!__all_sync(0xFFFFFFFFu, got)) break;
-        const volatile uint32_t *vn = sm.clear_none, *vs = sm.clear_some;
-        const uint64_t none = (uint64_t)vn[1] << 32 | vn[0], some = (uint64_t)vs[1] << 32 | vs[0];
-        if (!*reinterpret_cast<const volatile uint32_t*>(&sm.clear_cmd)) break;
-        // 64 tokens x 64 pieces of 16 bytes: a warp takes half a token's pieces at a time
-        for (int e = tid; (none | some) && e < PAGE * 64; e += 128) {
-            const int t = e >> 6, piece = e & 63;
-            if (!((none | some) >> t & 1ull)) continue;
-            const uint32_t slot = reinterpret_cast<const volatile uint32_t*>(sm.clear_slot)[t >> 5];
-            uint4* at = reinterpret_cast<uint4*>(sm.u.c1.ring[slot] + (piece >> 3) * HCHUNK + (t & 31) * 128 + (piece & 7) * 16);
-            if (none >> t & 1ull) {
-                *at = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                uint4 v = *at;
-                auto finite = [](uint32_t w) {  // bf16 with all exponent bits set: NaN or infinity
-                    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
-                    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
-                    return w;
-                };
-                v.x = finite(v.x), v.y = finite(v.y), v.z = finite(v.z), v.w = finite(v.w);
-                *at = v;
+    const int lane = (int)lane_id(), w = (int)warp - WW_CLEAR0;
+    bool ok = true;
+    int gp = 0, done = 0;
+    W_FOR_UNITS(un)
+    {
+        WUnit g;
+        w_unit<MQ>(g, p, un, false);
+        const int n_lo = w_clamp(g.n0, p.cap), n_hi = MQ ? w_clamp(g.n0 + g.rows - 1, p.cap) : n_lo;
+        for (int i = 0; i < g.npg && ok; ++i) {
+            const int a = gp + i, t0 = PAGE * w_logical(g, i);
+            if (w_whole(p, n_lo, n_hi, t0)) continue;
+            uint64_t none, some;
+            w_unseen<MQ>(p, g, t0, none, some);
+            const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
+            if (lane == 0)
+                ok = wait_count(&sm.pv_seen, a - 1, sm, p.dev_err) &&
+                     wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) &&
+                     wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+#pragma unroll 1
+            for (int t = w; t < PAGE; t += 4) {  // a warp a token: 64 pieces of 16 bytes, two a lane
+                const bool no = none >> t & 1ull;
+                if (!no && !(some >> t & 1ull)) continue;
+                uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
+                    if (no) {
+                        *piece = make_uint4(0u, 0u, 0u, 0u);
+                    } else {
+                        uint4 v = *piece;
+                        auto finite = [](uint32_t b) {  // bf16 with all exponent bits set: NaN or infinity
+                            if ((b & 0x7F80u) == 0x7F80u) b &= 0xFFFF0000u;
+                            if ((b & 0x7F800000u) == 0x7F800000u) b &= 0x0000FFFFu;
+                            return b;
+                        };
+                        v.x = finite(v.x), v.y = finite(v.y), v.z = finite(v.z), v.w = finite(v.w);
+                        *piece = v;
+                    }
+                }
             }
+            fence_proxy_async_cta();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.clear_done[done & 1]);
+            ++done;
         }
-        fence_proxy_async_cta();
-        __syncwarp();
-        if (lane_id() == 0) mbar_arrive(&sm.clear_done);
+        gp += g.npg;
     }
 }
 
-// O [rows x 512] f32 leaves TMEM, 64 dims at a time, through two staged boxes of 128-byte rows and bulk
-// tensor stores: bf16 hi and lo of o_lat = O / l when the unit is all its rows see, else two 32-dim boxes
-// of the f32 partial.  The TMEM is handed back after its last load; the stores run on behind.
+// The power of two that brings a row with largest magnitude m into f16's range (to [2^14, 2^15)), and its
+// inverse; 1 for rows of zeros, infinities or NaN.
+__device__ __forceinline__ float w_row_scale(float m, float& inverse)
+{
+    const int e = (int)(__float_as_uint(m) >> 23) & 255;  // m >= 0; (f32 subnormals count as zero)
+    const bool plain = e > 0 && e < 255;
+    const int up = plain ? min(max(141 - e, -126), 126) : 0;  // 2^up m in [2^14, 2^15), or as near as f32 allows
+    inverse = __uint_as_float((uint32_t)(127 - up) << 23);
+    return __uint_as_float((uint32_t)(127 + up) << 23);
+}
+
+// O [rows x 512] f32 leaves TMEM, a row a thread: f16 o_lat = O / l with a power of two per row when the unit is
+// all its rows see, else the f32 partial.  Each warp stages its 32 rows in two boxes of its own in turn (128
+// bytes a row, 128-byte swizzle; 64 dims f16 or 32 dims f32) and sends them by bulk tensor stores; no warp waits
+// for another.  What leaves the SM sets the time: as bf16 hi + lo a chunk's unit took 8.2 us to write 256 KB, by
+// bulk stores and by 32-byte stores from the registers alike.
 template <bool MQ>
-__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_row,
-                                            const WinParams& p, uint32_t t_lane, int row, int singles)
+__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
+                                            const WinParams& p, uint32_t t_lane, int warp, int singles)
 {
     using C = WCfg<MQ>;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
-    const bool single = sm.epi_single != 0, has_row = row < C::ROWS;
+    const bool single = sm.epi_single != 0;
+    const int lane = (int)lane_id(), row = 32 * warp + lane;
+    // a chunk's warp holds 32 heads of token row row0 + warp; decode's the heads 32 warp .. of slot b
+    const bool mine = MQ ? warp < rows : row < C::ROWS;
+    const int tok = MQ ? row0 + warp : b, head0 = MQ ? 32 * hb : 32 * warp;
     float r = 1.f;
     if (single) {
-        if (has_row) r = sm.rl[singles & 1][row];
+        if (mine) r = sm.rl[singles & 1][row];
         named_bar(WB_OUT, 128);
         if (threadIdx.x == 0) {  // the slot of 1 / l is free again
             mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
             mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
         }
-    }
-    const uint32_t sw = (uint32_t)(row & 7);
+        __syncwarp();
+        if (mine) {
+            float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-        uint32_t v[2][32];
-        tmem_ld32(t_lane + 64u * (uint32_t)k, v[0]);
-        tmem_ld32(t_lane + 64u * (uint32_t)k + 32u, v[1]);
-        tmem_wait_ld();
-        if (k == 7) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane_id() == 0) mbar_arrive(&sm.epi_done);
-        }
+            for (int k = 0; k < 16; ++k) {
+                uint32_t v[32];
+                tmem_ld32(t_lane + 32u * (uint32_t)k, v);
+                tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            uint4 q[8];
-            if (single) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t* at = &v[i >> 2][8 * (i & 3) + 2 * e];
-                        float f0 = __uint_as_float(at[0]), f1 = __uint_as_float(at[1]);
-                        if (x == 0) {  // hi; what it leaves stays for lo
-                            f0 *= r, f1 *= r;
-                            w[e] = pack_bf16x2(f0, f1);
-                            at[0] = __float_as_uint(f0 - bf16lo_to_f32(w[e]));
-                            at[1] = __float_as_uint(f1 - bf16hi_to_f32(w[e]));
-                        } else {
-                            w[e] = pack_bf16x2(f0, f1);
-                        }
-                    }
-                    q[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q[i] = make_uint4(v[x][4 * i], v[x][4 * i + 1], v[x][4 * i + 2], v[x][4 * i + 3]);
+                for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], fabsf(__uint_as_float(v[e])));
             }
-            if (threadIdx.x == 0) bulk_wait_read<1>();  // the box's store before has read it
-            __syncwarp();
-            named_bar(WB_OUT, 128);
-            uint8_t* box = sm.u.c1.box[x];
-            if (has_row)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(box + row * 128 + (((uint32_t)i ^ sw) << 4)) = q[i];
-            fence_proxy_async_cta();
-            __syncwarp();
-            named_bar(WB_OUT, 128);
-            if (threadIdx.x == 0) {
-                if constexpr (MQ) {  // o_lat [2][96][R][512] as (512 dims, 96 heads, R rows, 2)
-                    if (rows == 4)
-                        tma_store_4d(&tm_out, box, 64 * k, 32 * hb, row0, x);
-                    else
-                        for (int w = 0; w < rows; ++w) tma_store_4d(&tm_row, box + 32 * w * 128, 64 * k, 32 * hb, row0 + w, x);
-                } else if (single) {  // o_lat [2][96][B][512] as (512 dims, B slots, 96 heads, 2)
-                    tma_store_4d(&tm_out, box, 64 * k, b, 0, x);
-                } else {  // partials [B][nsplit][96][512] f32 as (512 dims, rows)
-                    tma_store_2d(&tm_row, box, 64 * k + 32 * x, (b * p.nsplit + s) * H);
-                }
-                bulk_commit();
-            }
+            float inverse;
+            r *= w_row_scale(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * r, inverse);
+            p.oscale[(size_t)(head0 + lane) * p.R + tok] = inverse;
         }
     }
+    const uint32_t sw = (uint32_t)(lane & 7);
+    int x = 0;
+#pragma unroll 1
+    for (int k = 0; k < 16 && mine; ++k) {
+        uint32_t v[32];
+        tmem_ld32(t_lane + 32u * (uint32_t)k, v);
+        tmem_wait_ld();
+        const bool send = !single || (k & 1);  // two loads fill a box of f16
+        uint8_t* at = sm.u.c1.box[MQ ? warp : min(warp, C::ROWS / 32 - 1)][x] + lane * 128;
+        if (!single || !(k & 1)) {
+            if (lane == 0) bulk_wait_read<1>();  // the box's store before has read it
+            __syncwarp();
+        }
+        if (single) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_f16x2(__uint_as_float(v[8 * i + 2 * e]) * r, __uint_as_float(v[8 * i + 2 * e + 1]) * r);
+                *reinterpret_cast<uint4*>(at + ((((uint32_t)(4 * (k & 1) + i)) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(at + (((uint32_t)i ^ sw) << 4)) =
+                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+        if (!send) continue;
+        fence_proxy_async_cta();  // the bulk store reads the box through the async proxy
+        __syncwarp();
+        if (lane == 0) {
+            const uint8_t* box = at;
+            if (single)  // o_lat [96][R][512] as (512 dims, R rows, 96 heads)
+                tma_store_3d(&tm_out, box, 32 * (k - 1), tok, head0);
+            else  // partials [B][nsplit][96][512] f32 as (512 dims, rows)
+                tma_store_2d(&tm_part, box, 32 * k, (b * p.nsplit + s) * H + head0);
+            bulk_commit();
+        }
+        x ^= 1;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.epi_done);
 }
 
 template <bool MQ>
-__device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_row,
+__device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
                                            const WinParams& p, uint32_t tbase, uint32_t warp)
 {
     using C = WCfg<MQ>;
@@ -863,7 +911,7 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_
         tc_fence_after();
         if (cmd & 2u) {
             const bool single = sm.epi_single != 0;
-            w_write_out<MQ>(sm, tm_out, tm_row, p, t_lane, row, singles);
+            w_write_out<MQ>(sm, tm_out, tm_part, p, t_lane, (int)warp, singles);
             singles += single;
             continue;
         }
@@ -885,17 +933,18 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.epi_done);
     }
-    if (threadIdx.x == 0) bulk_wait<0>();
+    if (lane == 0) bulk_wait_read<0>();
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
 
 template <bool MQ>
-__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(WCfg<MQ>::REGS)
     k3mla_window_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
                         const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
-                        const __grid_constant__ CUtensorMap tm_row, const WinParams p)
+                        const __grid_constant__ CUtensorMap tm_part, const WinParams p)
 {
+    using C = WCfg<MQ>;
     extern __shared__ uint8_t smem_raw[];
     WSmem<MQ>& sm = *reinterpret_cast<WSmem<MQ>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = lane_id();
@@ -903,11 +952,11 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
         w_init(sm, rank);
         fence_mbarrier_init_cluster();
     }
-    if (warp == WW_ALLOC) {
+    if (warp == 4) {
         tmem_alloc(&sm.tmem_base, TMEM_COLS);
         tmem_relinquish();
     }
-    if (warp == 4 && lane == 0) {
+    if (warp == 5 && lane == 0) {
         tma_prefetch_desc(rank == 0 ? &tm_page : &tm_page8);
         tma_prefetch_desc(rank == 0 ? &tm_q : &tm_out);
     }
@@ -918,12 +967,12 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     griddep_wait();
     griddep_launch_dependents();
     if (rank == 0) {
-        if (warp < 8) w_softmax<MQ>(sm, p, tbase, warp);
-        else if (warp < WW_MMA0) w_produce<MQ>(sm, tm_page, tm_q, p, (int)warp - WW_PROD0);
-        else w_copy_and_score<MQ>(sm, p, tbase, warp);
+        if (warp < C::W_PROD) w_softmax<MQ>(sm, p, tbase, warp);
+        else if (warp == C::W_PROD) w_produce<MQ>(sm, tm_page, tm_q, p);
+        else w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
     } else {
-        if (warp < 4) w_epilogue<MQ>(sm, tm_out, tm_row, p, tbase, warp);
-        else if (warp < WW_HPROD0 + WN_HALF) w_produce_halves<MQ>(sm, tm_page8, p, (int)warp - WW_HPROD0);
+        if (warp < 4) w_epilogue<MQ>(sm, tm_out, tm_part, p, tbase, warp);
+        else if (warp == WW_HALVES) w_produce_halves<MQ>(sm, tm_page8, p);
         else if (warp == WW_PV) w_issue_pv<MQ>(sm, p, tbase);
         else if (warp >= WW_CLEAR0 && warp < WW_CLEAR0 + 4) w_clear<MQ>(sm, p, warp);
     }
@@ -931,18 +980,22 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    if (warp == WW_ALLOC) tmem_dealloc(tbase, TMEM_COLS);
+    if (warp == 4) tmem_dealloc(tbase, TMEM_COLS);
 }
 
 // ---- merge of splits (decode) ---------------------------------------------------------------
 
-constexpr int WM_THREADS = 128;
+constexpr int WM_GROUPS = 4;
+constexpr int WM_THREADS = 128 * WM_GROUPS;
 
-// A row (slot, head) per CTA, four dims a thread: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max),
-// i ascending, landed as bf16 hi + lo.  The order depends on the slot's own splits only.
-__global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const WinParams p, uint16_t* olat)
+// A row (slot, head) per CTA: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max), four dims a thread and
+// every fourth split a group of 128 threads, so that a long list of splits is a few loads deep; the groups
+// are added as (g0 + g1) + (g2 + g3).  The order depends on the slot's own splits only.
+__global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const WinParams p)
 {
-    const int h = blockIdx.x, b = blockIdx.y, d = 4 * (int)threadIdx.x;
+    __shared__ float4 sum[WM_GROUPS][128];
+    __shared__ float sl[WM_GROUPS], smax[4];
+    const int h = blockIdx.x, b = blockIdx.y, d = 4 * ((int)threadIdx.x & 127), g = (int)threadIdx.x >> 7;
     griddep_wait();
     griddep_launch_dependents();
     int nsp, wp0;
@@ -953,11 +1006,13 @@ __global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const Wi
     const float2* ml = p.ws_ml + (size_t)b * p.nsplit * H + h;
     const float* o = p.ws_o + ((size_t)b * p.nsplit * H + h) * LORA + d;
     float m = -INFINITY;
-    for (int i = 0; i < ns; ++i) m = fmaxf(m, ml[(size_t)i * H].x);
+    for (int i = (int)lane_id(); i < ns; i += 32) m = fmaxf(m, ml[(size_t)i * H].x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
     float l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < ns; ++i) {
+#pragma unroll 8
+    for (int i = g; i < ns; i += WM_GROUPS) {
         const float2 rec = ml[(size_t)i * H];
         const float4 v = *reinterpret_cast<const float4*>(o + (size_t)i * H * LORA);
         const float w = ex2_approx(rec.x - m);
@@ -967,42 +1022,57 @@ __global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const Wi
         acc.z = fmaf(w, v.z, acc.z);
         acc.w = fmaf(w, v.w, acc.w);
     }
-    const float r = 1.f / l;
-    acc.x *= r, acc.y *= r, acc.z *= r, acc.w *= r;
-    const uint2 hi = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-    const uint2 lo = make_uint2(pack_bf16x2(acc.x - bf16lo_to_f32(hi.x), acc.y - bf16hi_to_f32(hi.x)),
-                                pack_bf16x2(acc.z - bf16lo_to_f32(hi.y), acc.w - bf16hi_to_f32(hi.y)));
-    uint16_t* out = olat + ((size_t)h * p.B + b) * LORA + d;
-    *reinterpret_cast<uint2*>(out) = hi;
-    *reinterpret_cast<uint2*>(out + (size_t)H * p.B * LORA) = lo;
+    sum[g][threadIdx.x & 127] = acc;
+    if (d == 0) sl[g] = l;
+    __syncthreads();
+    if (g > 0) return;
+    const float r = 1.f / ((sl[0] + sl[1]) + (sl[2] + sl[3]));
+    const float4 s1 = sum[1][threadIdx.x], s2 = sum[2][threadIdx.x], s3 = sum[3][threadIdx.x];
+    acc.x = ((acc.x + s1.x) + (s2.x + s3.x)) * r;
+    acc.y = ((acc.y + s1.y) + (s2.y + s3.y)) * r;
+    acc.z = ((acc.z + s1.z) + (s2.z + s3.z)) * r;
+    acc.w = ((acc.w + s1.w) + (s2.w + s3.w)) * r;
+    float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
+    if (lane_id() == 0) smax[threadIdx.x >> 5] = big;
+    named_bar(1, 128);
+    float inverse;
+    const float up = w_row_scale(fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3])), inverse);
+    *reinterpret_cast<uint2*>(p.olat + ((size_t)h * p.B + b) * LORA + d) =
+        make_uint2(pack_f16x2(acc.x * up, acc.y * up), pack_f16x2(acc.z * up, acc.w * up));
+    if (d == 0) p.oscale[(size_t)h * p.B + b] = inverse;
 }
 
 // ---- W_UV expansion ---------------------------------------------------------------------------
 
-// OUT_h^T [128 v x 64 rows] = W_UV[h] [128 x 512] . (hi + lo)^T [512 x 64], a CTA per head taking tiles of 64
-// rows in turn with W_UV[h] resident (128 KB, read before the grid wait: a weight).  o_lat streams through
-// a ring of 64-dim chunks, hi and lo beside each other; two accumulators, so that a tile's outputs leave while
-// the next one's MMAs run.
+// OUT_h^T [128 v x 64 rows] = W_UV[h] [128 x 512] . o_lat^T [512 x 64], a CTA per head taking tiles of 64 rows in
+// turn with W_UV[h] resident: read once (before the grid wait: a weight) and turned into f16 where it lies, each
+// of its rows times a power of two.  o_lat streams through a ring of 64-dim chunks; two accumulators, so that
+// a tile's outputs leave while the next one's MMAs run.  The powers of two come off on the way out, W_UV's by TMEM
+// lane, o_lat's by column.
 constexpr int WX_TILE = 64;
-constexpr int WX_RING = 4;
-constexpr int WX_CHUNK = WX_TILE * 128;               // one plane of a chunk
+constexpr int WX_RING = 8;
+constexpr int WX_CHUNK = WX_TILE * 128;
 constexpr int WX_A = 8 * VH * 128;                    // W_UV[h]
 constexpr int WX_OUT = WX_TILE * VH * 2;              // a tile's bf16 outputs
-constexpr int WX_SMEM = WX_A + WX_RING * 2 * WX_CHUNK + WX_OUT + 1024;
-constexpr int WX_EPI = 8;                             // epilogue warps 2..9
-constexpr int WX_THREADS = 32 * (2 + WX_EPI);
-static_assert(WX_SMEM <= 227 * 1024, "shared memory");
+constexpr int WX_SMEM = WX_A + WX_RING * WX_CHUNK + WX_OUT + 1024;
+constexpr int WX_EPI = 16;                            // warps 0..15 convert W_UV, then take the outputs
+constexpr int WX_THREADS = 32 * (WX_EPI + 2);         // ... one loads, one issues
+static_assert(WX_SMEM <= 225 * 1024, "shared memory, beside a few hundred static bytes");
 
 struct WxSmem {
-    uint64_t w_full, b_full[WX_RING], b_empty[WX_RING], d_full[2], d_empty[2];
+    uint64_t w_full, w_ready, b_full[WX_RING], b_empty[WX_RING], d_full[2], d_empty[2];
     uint32_t tmem_base;
     int32_t abort_flag;
     uint64_t wait_ns;
-    int32_t valid[WX_TILE];
+    float wscale[VH];         // what undoes W_UV's powers of two
+    float rscale[2][WX_TILE]; // ... and o_lat's, by tile parity; 0: the row sees nothing
 };
 
 struct WxParams {
     const int32_t *ctx_len, *pos0, *row_start;  // decode: ctx_len; chunk: pos0 and row_start
+    const float* oscale;
     uint16_t* out;
     int32_t* dev_err;
     int B, R, cap;  // R: the rows of o_lat and out (decode: B)
@@ -1022,6 +1092,36 @@ __device__ __forceinline__ bool wx_valid(const WxParams& p, int r)
     return r >= p.row_start[lo] && r < p.row_start[lo + 1] && (int64_t)p.pos0[lo] + (r - p.row_start[lo]) >= 0;
 }
 
+// W_UV[h] in shared memory ([8 chunks][128 rows][128 B], 128-byte swizzle), bf16 -> f16 in place, every row times
+// the power of two that brings its largest entry to [2^14, 2^15).  Four threads a row, sixteen 16-byte pieces each,
+// held in registers between the row's maximum and the conversion.
+__device__ __forceinline__ void wx_convert(uint8_t* sa, float* wscale)
+{
+    const int row = (int)threadIdx.x >> 2, j = threadIdx.x & 3;
+    uint4 v[16];
+    uint32_t m = 0;  // the largest magnitude: bf16 bit patterns of magnitudes order like the magnitudes
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int piece = 2 * j + (i & 1);
+        v[i] = *reinterpret_cast<const uint4*>(sa + (i >> 1) * (VH * 128) + row * 128 + ((piece ^ (row & 7)) << 4));
+        m = __vmaxu2(__vmaxu2(m, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu);
+        m = __vmaxu2(__vmaxu2(m, v[i].z & 0x7FFF7FFFu), v[i].w & 0x7FFF7FFFu);
+    }
+    m = max(m & 0xFFFFu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    float inverse;
+    const float up = w_row_scale(__uint_as_float(m << 16), inverse);
+    auto half2 = [&](uint32_t w) { return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up); };
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int piece = 2 * j + (i & 1);
+        *reinterpret_cast<uint4*>(sa + (i >> 1) * (VH * 128) + row * 128 + ((piece ^ (row & 7)) << 4)) =
+            make_uint4(half2(v[i].x), half2(v[i].y), half2(v[i].z), half2(v[i].w));
+    }
+    if (j == 0) wscale[row] = inverse;
+}
+
 __global__ void __launch_bounds__(WX_THREADS, 1)
     k3mla_window_expand_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_o,
                                const WxParams p)
@@ -1030,13 +1130,14 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
     __shared__ WxSmem sm;
     uint8_t* sa = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sb = sa + WX_A;
-    uint16_t* so = reinterpret_cast<uint16_t*>(sb + WX_RING * 2 * WX_CHUNK);
+    uint16_t* so = reinterpret_cast<uint16_t*>(sb + WX_RING * WX_CHUNK);
     const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = (int)lane_id();
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 32 * WX_EPI) {
         sm.abort_flag = 0;
         sm.wait_ns = WAIT_NS;
         mbar_init(&sm.w_full, 1);
+        mbar_init(&sm.w_ready, WX_EPI);
         for (int i = 0; i < WX_RING; ++i) {
             mbar_init(&sm.b_full[i], 1);
             mbar_init(&sm.b_empty[i], 1);
@@ -1046,8 +1147,11 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
             mbar_init(&sm.d_empty[i], WX_EPI);
         }
         fence_mbarrier_init_cluster();
+        mbar_arrive_expect_tx(&sm.w_full, WX_A);
+        for (int c = 0; c < 8; ++c)
+            tma_load_3d_hint(sa + c * (VH * 128), &tm_w, 0, h * WROWS_PER_HEAD + NOPE, c, &sm.w_full, policy_evict_first());
     }
-    if (warp == 1) {
+    if (warp == 0) {
         tmem_alloc(&sm.tmem_base, 2 * WX_TILE);
         tmem_relinquish();
     }
@@ -1056,12 +1160,8 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
     tc_fence_after();
     const uint32_t tbase = sm.tmem_base;
     bool ok = true;
-    if (warp == 0) {
+    if (warp == WX_EPI) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.w_full, WX_A);
-            for (int c = 0; c < 8; ++c)
-                tma_load_3d_hint(sa + c * (VH * 128), &tm_w, 0, h * WROWS_PER_HEAD + NOPE, c, &sm.w_full,
-                                 policy_evict_first());
             griddep_wait();
             int g = 0;
             for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y)
@@ -1069,17 +1169,17 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
                     const int s = g % WX_RING;
                     ok = wait_bar(&sm.b_empty[s], (uint32_t)((g / WX_RING) & 1) ^ 1u, sm, p.dev_err);
                     if (!ok) break;
-                    mbar_arrive_expect_tx(&sm.b_full[s], 2 * WX_CHUNK);
-                    for (int x = 0; x < 2; ++x)  // rows past the batch are the next head's, or zeros: not stored
-                        tma_load_3d(sb + (2 * s + x) * WX_CHUNK, &tm_o, 0, (x * H + h) * p.R + t * WX_TILE, c, &sm.b_full[s]);
+                    mbar_arrive_expect_tx(&sm.b_full[s], WX_CHUNK);
+                    // (rows past the batch are the next head's, or zeros: not stored)
+                    tma_load_3d(sb + s * WX_CHUNK, &tm_o, 0, h * p.R + t * WX_TILE, c, &sm.b_full[s]);
                 }
             if (!ok) drain_inflight();
         }
-    } else if (warp == 1) {
+    } else if (warp == WX_EPI + 1) {
         if (lane == 0) {
-            const uint32_t idesc = make_idesc_bf16(128, WX_TILE, 0, 0);
+            const uint32_t idesc = make_idesc_f16(128, WX_TILE);
             griddep_wait();  // (the bounded waits below start when o_lat is there)
-            ok = wait_bar(&sm.w_full, 0, sm, p.dev_err);
+            ok = wait_bar(&sm.w_ready, 0, sm, p.dev_err);
             int g = 0, it = 0;
             for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y, ++it) {
                 ok = wait_bar(&sm.d_empty[it & 1], (uint32_t)((it >> 1) & 1) ^ 1u, sm, p.dev_err);
@@ -1089,12 +1189,10 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = make_sdesc(smem_u32(sa + c * (VH * 128)), 16, 1024);
-                    for (int x = 0; x < 2; ++x) {
-                        const uint64_t bd = make_sdesc(smem_u32(sb + (2 * s + x) * WX_CHUNK), 16, 1024);
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_ss(tbase + (uint32_t)(WX_TILE * (it & 1)), ad + 2u * ks, bd + 2u * ks, idesc,
-                                    (c | x | ks) != 0);
-                    }
+                    const uint64_t bd = make_sdesc(smem_u32(sb + s * WX_CHUNK), 16, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        umma_ss(tbase + (uint32_t)(WX_TILE * (it & 1)), ad + 2u * ks, bd + 2u * ks, idesc, (c | ks) != 0);
                     umma_commit(&sm.b_empty[s]);
                 }
                 if (ok) umma_commit(&sm.d_full[it & 1]);
@@ -1102,44 +1200,54 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
             if (!ok) drain_inflight();
         }
     } else {
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.w_full, 0, sm, p.dev_err));
+        if (ok) wx_convert(sa, sm.wscale);
+        fence_proxy_async_cta();  // the MMAs read it through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.w_ready);
         griddep_wait();
         griddep_launch_dependents();
-        const int q = warp & 3, cg = (warp - 2) >> 2, tid = (int)threadIdx.x - 64, v = 32 * q + lane;
+        const int q = warp & 3, cg = warp >> 2, tid = (int)threadIdx.x, v = 32 * q + lane;
+        named_bar(1, 32 * WX_EPI);  // wscale is complete
+        const float ws = sm.wscale[v];
         int it = 0;
         for (int t = blockIdx.y; t < tiles; t += gridDim.y, ++it) {
             const int r0 = t * WX_TILE;
-            if (tid < WX_TILE) sm.valid[tid] = wx_valid(p, r0 + tid);
+            if (tid < WX_TILE) sm.rscale[it & 1][tid] = wx_valid(p, r0 + tid) ? p.oscale[(size_t)h * p.R + r0 + tid] : 0.f;
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.d_full[it & 1], (uint32_t)(it >> 1) & 1u, sm, p.dev_err));
             if (ok) {
                 tc_fence_after();
-                uint32_t acc[32];
-                tmem_ld32(tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(WX_TILE * (it & 1) + 32 * cg), acc);
+                uint32_t acc[16];
+                tmem_ld16(tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(WX_TILE * (it & 1) + 16 * cg), acc);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.d_empty[it & 1]);
+                named_bar(1, 32 * WX_EPI);  // rscale is there, and the outputs of the tile before have left
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    so[(32 * cg + j) * VH + v] = (uint16_t)(pack_bf16x2(__uint_as_float(acc[j]), 0.f) & 0xFFFFu);
+                for (int j = 0; j < 16; ++j) {
+                    const float rs = sm.rscale[it & 1][16 * cg + j];
+                    const float x = rs == 0.f ? 0.f : __uint_as_float(acc[j]) * ws * rs;
+                    so[(16 * cg + j) * VH + v] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
+                }
+            } else {
+                named_bar(1, 32 * WX_EPI);
             }
             named_bar(1, 32 * WX_EPI);
             if (ok)
                 for (int e = tid; e < WX_TILE * (VH / 8); e += 32 * WX_EPI) {
                     const int r = e / (VH / 8), k = e % (VH / 8);
-                    if (r0 + r < p.R) {
-                        const uint4 x = reinterpret_cast<const uint4*>(so + r * VH)[k];
+                    if (r0 + r < p.R)
                         reinterpret_cast<uint4*>(p.out + ((size_t)(r0 + r) * H + h) * VH)[k] =
-                            sm.valid[r] ? x : make_uint4(0u, 0u, 0u, 0u);
-                    }
+                            reinterpret_cast<const uint4*>(so + r * VH)[k];
                 }
-            named_bar(1, 32 * WX_EPI);
         }
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tbase, 2 * WX_TILE);
+    if (warp == 0) tmem_dealloc(tbase, 2 * WX_TILE);
 }
 
 // ---- host --------------------------------------------------------------------------------------
@@ -1161,13 +1269,14 @@ static int w_nsplit(int cap, int window, int n_sink, int split_tokens)
 }
 
 struct WinWs {
-    size_t olat, o, ml, total;
+    size_t olat, scale, o, ml, total;
 };
 static WinWs w_layout(long long rows, int nsplit)
 {
     WinWs w;
     w.olat = 0;
-    w.o = w_up((size_t)rows * H * LORA * 2 * 2);
+    w.scale = w_up((size_t)rows * H * LORA * 2);
+    w.o = w.scale + w_up((size_t)rows * H * 4);
     w.ml = w.o + (nsplit > 1 ? w_up((size_t)rows * nsplit * H * LORA * 4) : 0);
     w.total = w.ml + (nsplit > 1 ? w_up((size_t)rows * nsplit * H * 8) : 0);
     return w;
@@ -1195,54 +1304,50 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                     const WinWs& wl, WinParams& p, cudaStream_t st)
 {
     using C = WCfg<MQ>;
-    uint16_t* olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
+    p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
+    p.oscale = reinterpret_cast<float*>(ws + wl.scale);
     p.ws_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.o) : nullptr;
     p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
-    CUtensorMap tm_page, tm_page8, tm_q, tm_out, tm_row, tm_w, tm_o;
+    CUtensorMap tm_page, tm_page8, tm_q, tm_out, tm_part, tm_w, tm_o;
     const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
     int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
     if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
     if (rc) return rc;
     if (MQ) {
-        {   // q_abs as (64 elements, 96 heads, R rows, 9 chunks): a chunk of 32 heads of four token rows
-            const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
-            const uint32_t box[4] = {64, 32, 4, 1};
-            rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
-        }
-        const uint64_t dims[4] = {LORA, H, R, 2}, strides[3] = {R * LORA * 2, LORA * 2, (uint64_t)H * R * LORA * 2};
-        const uint32_t box4[4] = {64, 32, 4, 1}, box1[4] = {64, 32, 1, 1};
-        if (!rc) rc = make_tmap_store(&tm_out, false, 4, olat, dims, strides, box4, true);
-        if (!rc) rc = make_tmap_store(&tm_row, false, 4, olat, dims, strides, box1, true);
+        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): a chunk of 32 heads of four token rows
+        const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
+        const uint32_t box[4] = {64, 32, 4, 1};
+        rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
     } else {
         rc = make_tmap_slab_3d(&tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
-        const uint64_t dims[4] = {LORA, R, H, 2}, strides[3] = {LORA * 2, R * LORA * 2, (uint64_t)H * R * LORA * 2};
-        const uint32_t box[4] = {64, 1, H, 1};
-        if (!rc) rc = make_tmap_store(&tm_out, false, 4, olat, dims, strides, box, true);
-        tm_row = tm_out;
-        if (!rc && p.nsplit > 1) {
-            const uint64_t d2[2] = {LORA, R * p.nsplit * H}, s2[1] = {LORA * 4};
-            const uint32_t b2[2] = {32, H};
-            rc = make_tmap_store(&tm_row, true, 2, p.ws_o, d2, s2, b2, true);
-        }
+    }
+    // o_lat [96][R][512] as (512 dims, R rows, 96 heads): a box is 64 dims of 32 heads of one row
+    const uint64_t od[3] = {LORA, R, H}, os[2] = {LORA * 2, R * LORA * 2};
+    const uint32_t ob[3] = {64, 1, 32};
+    if (!rc) rc = make_tmap_store(&tm_out, false, 3, p.olat, od, os, ob, true);
+    tm_part = tm_out;
+    if (!rc && p.nsplit > 1) {  // partials [B][nsplit][96][512] f32: 32 dims of 32 rows
+        const uint64_t pd[2] = {LORA, R * p.nsplit * H}, ps[1] = {LORA * 4};
+        const uint32_t pb[2] = {32, 32};
+        rc = make_tmap_store(&tm_part, true, 2, p.ws_o, pd, ps, pb, true);
     }
     if (!rc) rc = make_tmap_slab_3d(&tm_w, w_kv_b, (uint64_t)H * WROWS_PER_HEAD, LORA, 8, VH, 1);
-    if (!rc) rc = make_tmap_slab_3d(&tm_o, olat, 2ull * H * R, LORA, 8, WX_TILE, 1);
+    if (!rc) rc = make_tmap_slab_3d(&tm_o, p.olat, (uint64_t)H * R, LORA, 8, WX_TILE, 1);
     if (rc) return rc;
     static bool attr_done[64] = {}, attr_expand[64] = {};
     const size_t smem = sizeof(WSmem<MQ>) + 1024;
     set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
     set_smem_attr(reinterpret_cast<const void*>(k3mla_window_expand_kernel), WX_SMEM, attr_expand);
     const int clusters = std::min(p.n_units, sm_count() / 2);
-    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
-                    tm_page8, tm_q, tm_out, tm_row, p);
+    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(C::THREADS), smem, st, "k3mla_window_kernel", tm_page,
+                    tm_page8, tm_q, tm_out, tm_part, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
-        rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(WM_THREADS), 0, st, "k3mla_window_merge_kernel", p,
-                        olat);
+        rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(WM_THREADS), 0, st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
     }
     WxParams x;
-    x.ctx_len = p.ctx_len, x.pos0 = p.pos0, x.row_start = p.row_start, x.out = out, x.dev_err = p.dev_err;
+    x.ctx_len = p.ctx_len, x.pos0 = p.pos0, x.row_start = p.row_start, x.oscale = p.oscale, x.out = out, x.dev_err = p.dev_err;
     x.B = p.B, x.R = p.R, x.cap = p.cap;
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
     return launch_pdl(k3mla_window_expand_kernel, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st,
@@ -1366,7 +1471,7 @@ extern "C" int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* 
         return K3MLA_E_WORKSPACE;
     }
     const long long units = 3ll * (((long long)R + 3ll * B) / 4);  // sum over slots of ceil(n_b / 4), at most
-    if (units > 0x3FFFFFFFll || 2ll * R * H > 0x7FFFFFFFll) {
+    if (units > 0x3FFFFFFFll || (long long)R * H > 0x7FFFFFFFll) {
         set_error("k3mla_window_chunk_decode: too many rows");
         return K3MLA_E_INVALID;
     }
