@@ -24,13 +24,14 @@
 //   * A unit's pages are the logical pages that hold a seen token, in ascending order: those of the sinks,
 //     then those of the window.  Pages in between are neither read nor looked up, so they may have been
 //     freed (k3mla_pool_trim).
-//   * Score CTA: a producer streams Q and then the page thirds through one ring of 24 KB units; three
+//   * Score CTA: the producers stream Q and then the page thirds through one ring of 24 KB units; three
 //     threads issue the score MMAs (A = Q from TMEM, B = the page); the softmax warps of each quarter take a page
 //     each in turn, mask, keep a lazily moved reference max, and pass bf16 p to the PV CTA by bulk DSMEM copies
 //     (the first of them copies Q into TMEM when the last MMA of the unit before has read the old one).
-//   * PV CTA: a producer streams the pages' latents again (mostly from L2) as half pages; one
-//     thread issues O[rows x 512] += P . C; four warps rescale O when a reference moved and, at a unit's
-//     end, take O out of TMEM through staged boxes and bulk tensor stores; four warps clear what a page holds of unseen tokens.
+//   * PV CTA: a producer streams the pages' latents again (mostly from L2) as half pages; one thread issues
+//     O[rows x 512] += P . C; eight warps rescale O when a reference moved and, at a unit's end, take O out of
+//     TMEM; four warps clear what a page holds of unseen tokens;
+//     one plans the units of both CTAs ahead.
 //   * Unseen tokens.  Their scores are replaced (never multiplied), and in the pages that hold some their
 //     latents are cleared in shared memory, because p = 0 times a NaN or infinity there would still be
 //     NaN.  In a chunk a token may be seen by some rows of the unit only; then just its NaNs and
@@ -55,15 +56,18 @@ template <bool MQ> struct WCfg {
     static constexpr int RPQ = MQ ? 32 : 24;             // rows per 32-lane quarter
     static constexpr int ROWS = 4 * RPQ;                 // rows of a unit
     static constexpr int NUNIT = MQ ? 7 : 8;             // score CTA: ring of 24 KB units
-    static constexpr int QPU = MQ ? 1 : 2;               // 64-column chunks of Q in one ring unit
-    static constexpr int NQ = (9 + QPU - 1) / QPU;       // ring uses that a unit's Q takes
-    static constexpr int QCHUNK = ROWS * 128;            // one chunk of Q, [rows][128 B]
+    // Q in the ring: pieces of 64 columns, of all 96 rows (decode) or of two token rows' 64 (chunk)
+    static constexpr int QROWS = MQ ? 64 : 96;
+    static constexpr int QPIECE = QROWS * 128;           // [rows][128 B]
+    static constexpr int QPU = THIRD / QPIECE;           // pieces of one ring unit: 3 or 2
+    static constexpr int NPIECE = 9 * ROWS / QROWS;      // 18 or 9
+    static constexpr int NQ = (NPIECE + QPU - 1) / QPU;  // ring uses that a unit's Q takes: 6 or 5
+    static constexpr int NPROD = MQ ? 1 : 3;             // score CTA: producers
     static constexpr int NPBUF = MQ ? 3 : 4;             // PV CTA: P buffers
     static constexpr int NPAR = MQ ? 3 : 2;              // score CTA: softmax warps of a quarter, a page each in turn
-    static constexpr int W_PROD = 4 * NPAR;              // ... behind them the producer ...
-    static constexpr int W_MMA0 = W_PROD + 1;            // ... and three MMA issuers
-    static constexpr int THREADS = 32 * (W_MMA0 + 3);
-    static constexpr int REGS = 65536 / THREADS / 8 * 8 < 168 ? 65536 / THREADS / 8 * 8 : 168;
+    static constexpr int W_PROD = 4 * NPAR;              // ... behind them the producers ...
+    static constexpr int W_MMA0 = W_PROD + NPROD;        // ... and three MMA issuers
+    static_assert(W_MMA0 + 3 <= 16, "the warps of a CTA");
     static constexpr int PSTAGE = RPQ * 128;             // score CTA: one softmax warp's P rows (x 64 tokens)
     static constexpr int PT_BYTES = ROWS * 128;          // P [rows][64 tokens] bf16, K-major, 128-byte swizzle
     static constexpr int META_ALPHA = PT_BYTES;          // f32 alpha[rows]
@@ -74,11 +78,25 @@ template <bool MQ> struct WCfg {
 constexpr int WN_S = 3;        // S buffers, one MMA issuer each
 constexpr int WN_HALF = 4;     // PV CTA: half-page slots
 constexpr int W_BOX = 32 * 128;  // PV CTA: one write-out box of a warp, 32 rows of 128 bytes
-constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6;  // PV CTA: warps 0-3 epilogue, the producer, the MMA issuer,
-                                                        // four warps that clear unseen tokens
-// named barriers (0 is __syncthreads): score CTA, a quarter's decision hand-offs by turn; PV CTA, the
-// epilogue warps
-constexpr uint32_t WB_HAND = 1, WB_OUT = 1;
+constexpr int W_THREADS = 512;  // 128 registers a thread
+// PV CTA: the producer, the MMA issuer, four warps that clear unseen tokens, eight of the epilogue (0-3 and 10-13: a
+// warp reads the TMEM lanes of its own quarter), one that plans the units of both CTAs
+constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6, WW_EPI1 = 10, WW_PLAN = 14;
+constexpr int W_PLANS = 8;         // planned units kept
+constexpr uint32_t WB_OUT = 1;     // named barrier of the epilogue warps
+constexpr int W_EPI = 8;
+
+// A unit: which rows, which pages.
+struct __align__(16) WUnit {
+    int b, s, hb;
+    int row0, rows;  // chunk: the first token row and how many; decode: 0, 1
+    int n0;          // context of the first row (the next rows': one more each, all clamped to the table)
+    int npg;         // pages of the unit, at least one; -1: there are no more units
+    int first;       // the first of them in the list of the pages seen
+    int nsp, wp0;    // entry g of that list is logical page g for g < nsp, else g - nsp + wp0
+    int single;      // the unit holds all its rows see: final o_lat
+    int n_hi;        // the last row's context
+};
 
 template <bool MQ> struct __align__(1024) WSmem {
     using C = WCfg<MQ>;
@@ -90,7 +108,9 @@ template <bool MQ> struct __align__(1024) WSmem {
         struct {
             uint8_t ring[WN_HALF][SLOT1];
             uint8_t recv[C::NPBUF][C::PBUF];
-            uint8_t box[C::ROWS / 32][2][W_BOX];
+            uint8_t box[C::ROWS / 32][2][W_BOX];  // one of each epilogue warp
+            float rl[2][C::ROWS];          // 1 / l of every row, by parity of the unit; written by the score CTA
+            float half_max[2][C::ROWS];    // the rows' largest |O| in each half of the dims
         } c1;
     } u;
     uint64_t full[8], empty[8];          // the ring of this CTA
@@ -98,14 +118,18 @@ template <bool MQ> struct __align__(1024) WSmem {
     uint64_t q_free, q_ready;            // Q of the unit before is no longer read / Q of this unit is in TMEM
     uint64_t p_full[C::NPBUF], p_empty[C::NPBUF];
     uint64_t o_done, epi_req, epi_done, clear_done[2];
-    uint64_t l_full[2], rl_free[2];      // 1 / l of every row, by parity of the unit
+    uint64_t l_full[2], rl_free[2];      // PV CTA's rl, by parity of the unit
+    uint64_t hand[4][C::NPAR];           // a quarter's decision on a page, by turn
     uint64_t fin_full[2][4], fin_free[2][4];  // a quarter's sums of exp, by parity of the unit
-    float rl[2][C::ROWS];
     float xm[2][4][32];                  // reference max after a page, by parity of the page
     float fin_l[2][C::NPAR][4][32];      // a unit's sums of exp by softmax warp, by parity of the unit
     float fin_m[2][C::NPAR][4][32];      // ... and the reference each is held to
+    int32_t unit_loaded[C::NUNIT];       // uses of a ring unit whose load has been issued
     int32_t unit_taken[C::NUNIT];        // uses of a ring unit that their consumer has taken
     int32_t copied[C::NUNIT];            // quarters that have copied their rows of the Q chunk in a ring unit
+    WUnit plan[W_PLANS];                 // the units, in order
+    uint64_t plan_full[W_PLANS];
+    int32_t pv_units, clear_units;       // PV CTA: units whose MMAs have been issued / that a clearing warp has left
     int32_t pv_seen;                     // PV CTA: pages whose latents the MMA issuer has seen arrive and cleared
     uint32_t tmem_base;
     uint32_t epi_cmd, epi_stage;         // to the epilogue warps: bit 0 rescale O, bit 1 write it out
@@ -117,7 +141,7 @@ template <bool MQ> struct __align__(1024) WSmem {
 template <bool MQ> constexpr bool wsmem_fits()
 {
     using C = WCfg<MQ>;
-    static_assert(C::QPU * C::QCHUNK <= THIRD && C::QCHUNK % 1024 == 0 && SLOT1 % 1024 == 0 && C::PBUF % 1024 == 0,
+    static_assert(C::QPIECE % 1024 == 0 && SLOT1 % 1024 == 0 && C::PBUF % 1024 == 0,
                   "operand tiles fit and start 1024-byte aligned");
     static_assert(C::NUNIT <= 8 && WN_HALF <= 8, "barrier arrays");
     static_assert(WN_HALF * SLOT1 + (C::NPBUF - 1) * C::PBUF + 128 * 128 <= sizeof(WSmem<MQ>::u),
@@ -141,17 +165,6 @@ struct WinParams {
     float kscale;                        // scale * log2(e) > 0
 };
 
-// A unit: which rows, which pages.
-struct WUnit {
-    int b, s, hb;
-    int row0, rows;  // chunk: the first token row and how many; decode: 0, 1
-    int n0;          // context of the first row (the next rows': one more each, all clamped to the table)
-    int npg;         // pages of the unit, 0: nothing to do
-    int first;       // the first of them in the list of the pages seen
-    int nsp, wp0;    // entry g of that list is logical page g for g < nsp, else g - nsp + wp0
-    bool single;     // the unit holds all its rows see: final o_lat
-};
-
 __host__ __device__ inline int w_clamp(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
 
 // The pages that the rows with contexts n_lo .. n_hi see: how many, and the two numbers of WUnit.
@@ -168,8 +181,7 @@ __host__ __device__ inline int w_pages(int n_lo, int n_hi, int window, int n_sin
 }
 
 // Unit u (a whole warp, every lane the same answer).
-// Out of line: every role calls it, once a unit.
-template <bool MQ> __device__ __noinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report)
+template <bool MQ> __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report)
 {
     g.npg = 0;
     g.first = 0;
@@ -177,7 +189,7 @@ template <bool MQ> __device__ __noinline__ void w_unit(WUnit& g, const WinParams
     g.hb = 0;
     g.row0 = 0;
     g.rows = 1;
-    g.single = true;
+    g.single = 1;
     int last;
     if constexpr (MQ) {
         // group u / 3 of up to four rows, counted slot by slot: 32 slots a step
@@ -214,7 +226,7 @@ template <bool MQ> __device__ __noinline__ void w_unit(WUnit& g, const WinParams
         const int64_t n0 = (int64_t)p.pos0[g.b] + (g.row0 - p.row_start[g.b]) + 1;
         const int64_t n1 = n0 + g.rows - 1;
         if (report && n1 > p.cap && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
-        g.n0 = (int)max((int64_t)-4, min(n0, (int64_t)p.cap));
+        g.n0 = (int)max((int64_t)-4, min(n0, (int64_t)p.cap));  // (the rows' own contexts are clamped again)
         last = (int)max((int64_t)0, min(n1, (int64_t)p.cap));
     } else {
         g.b = u / p.nsplit;
@@ -223,6 +235,7 @@ template <bool MQ> __device__ __noinline__ void w_unit(WUnit& g, const WinParams
         if (report && n > p.cap && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
         g.n0 = last = w_clamp(n, p.cap);
     }
+    g.n_hi = last;
     const int all = w_pages(max(g.n0, 0), last, p.window, p.n_sink, g.nsp, g.wp0);
     if constexpr (MQ) {
         g.npg = all;
@@ -289,6 +302,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
         mbar_init(&sm.s_full[i], 1);
         mbar_init(&sm.s_empty[i], 4);
     }
+    for (int i = 0; i < 4 * C::NPAR; ++i) mbar_init(&sm.hand[i / C::NPAR][i % C::NPAR], 1);
     mbar_init(&sm.q_free, WN_S);
     mbar_init(&sm.q_ready, 4);
     for (int i = 0; i < C::NPBUF; ++i) {
@@ -297,7 +311,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
     }
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.epi_req, 1);
-    mbar_init(&sm.epi_done, 4);
+    mbar_init(&sm.epi_done, W_EPI);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.clear_done[i], 4);
     for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.l_full[i], 1);
@@ -307,55 +321,110 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
             mbar_init(&sm.fin_free[i][q], 1);
         }
     }
-    for (int i = 0; i < C::NUNIT; ++i) sm.unit_taken[i] = sm.copied[i] = 0;
-    sm.pv_seen = 0;
+    for (int i = 0; i < C::NUNIT; ++i) sm.unit_loaded[i] = sm.unit_taken[i] = sm.copied[i] = 0;
+    for (int i = 0; i < W_PLANS; ++i) mbar_init(&sm.plan_full[i], 1);
+    sm.pv_seen = sm.pv_units = sm.clear_units = 0;
     if (rank == 1) {  // expected before anything is sent
         for (int i = 0; i < C::NPBUF; ++i) mbar_arrive_expect_tx(&sm.p_full[i], C::PCOPY);
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.l_full[i], 4 * C::ROWS);
     }
 }
 
-#define W_FOR_UNITS(u) for (int u = (int)blockIdx.x >> 1; u < p.n_units; u += (int)gridDim.x >> 1)
+// The planner (a warp of the PV CTA) works the cluster's units out ahead of both CTAs' roles and leaves each in
+// the shared memory of both.  At most three units ahead of the PV CTA's MMAs: the softmax warps are then no more
+// than two further units behind (their sums of exp meet in two slots), so W_PLANS = 8 slots never run over.
+template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const WinParams& p)
+{
+    const int lane = (int)lane_id();
+    bool ok = true;
+    int n = 0;
+    auto publish = [&](const WUnit& g) {
+        if (n >= 4 && lane == 0)
+            ok = wait_count(&sm.pv_units, n - 3, sm, p.dev_err) && wait_count(&sm.clear_units, 4 * (n - 6), sm, p.dev_err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        const int slot = n % W_PLANS;
+        if (lane < 2) {  // one lane a CTA
+            const uint32_t at = mapa(smem_u32(&sm.plan[slot]), (uint32_t)lane);
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&g);
+#pragma unroll
+            for (int i = 0; i < (int)(sizeof(WUnit) / 4); ++i) st_cluster_u32(at + 4 * i, w[i]);
+            mbar_arrive_remote(mapa(smem_u32(&sm.plan_full[slot]), (uint32_t)lane));
+        }
+        ++n;
+    };
+    for (int u = (int)blockIdx.x >> 1; u < p.n_units && ok; u += (int)gridDim.x >> 1) {
+        WUnit g;
+        w_unit<MQ>(g, p, u, lane == 0);
+        if (g.npg > 0) publish(g);
+    }
+    WUnit end = {};
+    end.npg = -1;
+    publish(end);
+}
+
+// The n-th unit; npg is -1 behind the last one, and after an abort.
+template <bool MQ> __device__ __forceinline__ WUnit w_next(WSmem<MQ>& sm, const WinParams& p, int n)
+{
+    WUnit g;
+    if (__all_sync(0xFFFFFFFFu, wait_bar(&sm.plan_full[n % W_PLANS], (uint32_t)(n / W_PLANS) & 1u, sm, p.dev_err, true)))
+        g = sm.plan[n % W_PLANS];
+    else
+        g.npg = -1;
+    return g;
+}
 
 // ---- score CTA ----------------------------------------------------------------------------
 
-// Producer: a unit's Q, then its pages in thirds.  The uses of the ring are numbered on from unit to unit; use g
-// lies in ring unit g % NUNIT.
+// Producer t of NPROD: a unit's Q, then its pages in thirds, every NPROD-th use of the ring.  The uses are
+// numbered on from unit to unit; use g lies in ring unit g % NUNIT.
 template <bool MQ>
 __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_page, const CUtensorMap& tm_q,
-                                          const WinParams& p)
+                                          const WinParams& p, int t)
 {
     using C = WCfg<MQ>;
     const bool me = lane_id() == 0;
     bool ok = true;
-    int use = 0;
-    auto take = [&](uint32_t bytes) -> int {  // the next ring unit, ready to be loaded
+    int base = 0;
+    auto take = [&](int use, uint32_t bytes) -> int {  // the use's ring unit, ready to be loaded
         const int u = use % C::NUNIT, k = use / C::NUNIT;
-        ++use;
+        if (C::NPROD > 1) ok = ok && wait_count(&sm.unit_loaded[u], k, sm, p.dev_err);
         ok = ok && wait_bar(&sm.empty[u], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
-        if (ok) mbar_arrive_expect_tx(&sm.full[u], bytes);
+        if (ok) {
+            if (C::NPROD > 1) *reinterpret_cast<volatile int32_t*>(&sm.unit_loaded[u]) = k + 1;
+            mbar_arrive_expect_tx(&sm.full[u], bytes);
+        }
         return u;
     };
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, false);
-        if (g.npg == 0) continue;
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
         for (int j = 0; j < C::NQ && me && ok; ++j) {
-            const int u = take(C::QPU * C::QCHUNK);
+            if ((base + j) % C::NPROD != t) continue;
+            const int u = take(base + j, C::QPU * C::QPIECE);
             if (!ok) break;
-            // (chunk: heads 32 hb .. of four consecutive token rows; those past the group land in lanes nobody reads)
-            if constexpr (MQ) tma_load_4d(sm.u.c0.ring[u], &tm_q, 0, 32 * g.hb, g.row0, j, &sm.full[u]);
-            else tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
+            if constexpr (MQ) {
+                // piece: heads 32 hb .. of two consecutive token rows (those past the group land in lanes nobody reads)
+                for (int x = 0; x < C::QPU; ++x) {
+                    const int pc = C::QPU * j + x;
+                    tma_load_4d(sm.u.c0.ring[u] + x * C::QPIECE, &tm_q, 0, 32 * g.hb, g.row0 + 2 * (pc & 1), pc >> 1,
+                                &sm.full[u]);
+                }
+            } else {
+                tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
+            }
         }
+        base += C::NQ;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
-            for (int t = 0; t < 3 && me && ok; ++t) {
-                const int u = take(THIRD);
-                if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * t, &sm.full[u]);
+            for (int x = 0; x < 3 && me && ok; ++x) {
+                if ((base + 3 * i + x) % C::NPROD != t) continue;
+                const int u = take(base + 3 * i + x, THIRD);
+                if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
             }
         }
+        base += 3 * g.npg;
     }
     if (!ok) drain_inflight();
 }
@@ -366,19 +435,18 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
 {
     using C = WCfg<MQ>;
     bool ok = true;
-    int base = 0, gp = 0, done = 0;  // ring uses, pages and units before this unit
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, false);
-        if (g.npg == 0) continue;
+    int base = 0, gp = 0;  // ring uses and pages before this unit
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
         base += C::NQ;
         if (lane_id() == 0 && ok) {
-            ok = wait_bar(&sm.q_ready, (uint32_t)done & 1u, sm, p.dev_err);
+            ok = wait_bar(&sm.q_ready, (uint32_t)un & 1u, sm, p.dev_err);
             tc_fence_after();
             for (int i = (r + WN_S - gp % WN_S) % WN_S; i < g.npg && ok; i += WN_S) {
                 const int k = (gp + i) / WN_S;
                 ok = wait_bar(&sm.s_empty[r], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
+#pragma unroll 1
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
                     ok = wait_count(&sm.unit_taken[u], ku, sm, p.dev_err) &&
@@ -395,7 +463,6 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
         }
         base += 3 * g.npg;
         gp += g.npg;
-        ++done;
     }
     if (!ok) drain_inflight();
 }
@@ -403,48 +470,54 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
 // A warp of each quarter copies its rows of Q from the ring into TMEM (lane 32 w + l <- row RPQ w + l), once the
 // score MMAs of the unit before have read the old Q.
 template <bool MQ>
-__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int base, int done,
-                                         bool ok)
+__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int base, int un)
 {
     using C = WCfg<MQ>;
-    const int lane = (int)lane_id(), row = C::RPQ * qd + lane;
+    const int lane = (int)lane_id();
+    const int row = MQ ? 32 * (qd & 1) + lane : C::RPQ * qd + lane;  // of a piece
     const uint32_t taddr = tbase + ((32u * (uint32_t)qd) << 16) + Q_COL;
-    if (ok && done > 0) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.q_free, (uint32_t)(done - 1) & 1u, sm, p.dev_err));
+    if (!__all_sync(0xFFFFFFFFu, un == 0 || wait_bar(&sm.q_free, (uint32_t)(un - 1) & 1u, sm, p.dev_err))) return false;
     tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < 9 && ok; ++c) {
-        const int j = c / C::QPU, u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
-        if (c % C::QPU == 0)
-            ok = __all_sync(0xFFFFFFFFu, wait_count(&sm.unit_taken[u], k, sm, p.dev_err) &&
-                                             wait_bar(&sm.full[u], (uint32_t)(k & 1), sm, p.dev_err));
-        if (!ok) break;
-        uint32_t v[32];
-        const uint8_t* src = sm.u.c0.ring[u] + (c % C::QPU) * C::QCHUNK + row * 128;
+    for (int j = 0; j < C::NQ; ++j) {
+        const int u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
+        if (!__all_sync(0xFFFFFFFFu, wait_count(&sm.unit_taken[u], k, sm, p.dev_err) &&
+                                         wait_bar(&sm.full[u], (uint32_t)(k & 1), sm, p.dev_err)))
+            return false;
+#pragma unroll 1
+        for (int x = 0; x < C::QPU; ++x) {
+            const int pc = C::QPU * j + x, c = MQ ? pc >> 1 : pc;
+            if (pc >= C::NPIECE || (MQ && (pc & 1) != qd >> 1)) continue;
+            uint32_t v[32];
+            const uint8_t* src = sm.u.c0.ring[u] + x * C::QPIECE + row * 128;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            if (lane < C::RPQ) w = *reinterpret_cast<const uint4*>(src + ((x ^ (row & 7)) << 4));
-            v[4 * x] = w.x, v[4 * x + 1] = w.y, v[4 * x + 2] = w.z, v[4 * x + 3] = w.w;
-        }
-        tmem_st32(taddr + 32u * (uint32_t)c, v);
-        __syncwarp();
-        if ((c + 1) % C::QPU == 0 || c == 8)
-            if (lane == 0 && atomicAdd(&sm.copied[u], 1) == 3) {  // the last of the four quarters: the ring unit is read
-                sm.copied[u] = 0;
-                *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = k + 1;
-                mbar_arrive(&sm.empty[u]);
+            for (int y = 0; y < 8; ++y) {
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (lane < C::RPQ) w = *reinterpret_cast<const uint4*>(src + ((y ^ (row & 7)) << 4));
+                v[4 * y] = w.x, v[4 * y + 1] = w.y, v[4 * y + 2] = w.z, v[4 * y + 3] = w.w;
             }
+            tmem_st32(taddr + 32u * (uint32_t)c, v);
+        }
+        __syncwarp();
+        if (lane == 0 && atomicAdd(&sm.copied[u], 1) == 3) {  // the last of the four quarters: the ring unit is read
+            sm.copied[u] = 0;
+            *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = k + 1;
+            mbar_arrive(&sm.empty[u]);
+        }
     }
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.q_ready);
-    return ok;
+    return true;
 }
 
 // Softmax warp (quarter qd, turn par): thread l = row RPQ qd + l of every NPAR-th page.  The reference max is a
 // chain through a unit's pages: the warp of each page hands its decision on to the warp of the next one; a
-// warp's sum of exp follows the reference when it comes to its own next page.  All in log2 units.
+// warp's sum of exp follows the reference when it comes to its own next page.  All in log2 units.  The chain of
+// turns runs on through all units, so a turn's barrier is never a phase ahead of who waits on it.
+// (The page's code is written to be short: the SM's instruction fetch is what these kernels run short of first.
+// The scores' issue loop unrolled three times, 9 KB more, took the 16 x 64-token chunk from 328 to 358 us.)
 template <bool MQ>
 __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
 {
@@ -452,41 +525,36 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     const int qd = (int)(warp & 3u), par = (int)(warp >> 2), l = (int)lane_id();
     const int h = C::RPQ * qd + l;
     const bool has_row = l < C::RPQ;
-    // barrier x of a quarter: the warp of turn x arrives, the next one's waits, and neither ever does the other
-    const uint32_t hand = WB_HAND + (uint32_t)(C::NPAR * qd);
     const uint32_t t_lane = tbase + ((32u * (uint32_t)qd) << 16) + S_COL;
     const uint32_t recv0 = mapa(smem_u32(sm.u.c1.recv[0]), 1);
     const uint32_t pfull0 = mapa(smem_u32(&sm.p_full[0]), 1);
     const float TAU2 = TAU * 1.4426950408889634f;
     uint8_t* stage = sm.u.c0.pstage[warp];
-    bool ok = true;
-    int base = 0, gp = 0, done = 0, singles = 0;
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, warp == 0 && l == 0);
-        if (g.npg == 0) continue;
-        if (par == 0) ok = w_copy_q<MQ>(sm, p, tbase, qd, base, done, ok);
+    auto wait = [&](uint64_t* bar, int phase, bool cluster = false) {
+        return __all_sync(0xFFFFFFFFu, wait_bar(bar, (uint32_t)phase & 1u, sm, p.dev_err, cluster));
+    };
+    int base = 0, gp = 0, singles = 0;
+#pragma unroll 1
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
+        if (par == 0 && !w_copy_q<MQ>(sm, p, tbase, qd, base, un)) return;
         base += C::NQ + 3 * g.npg;
         const int n = MQ ? (qd < g.rows ? w_clamp(g.n0 + qd, p.cap) : 0) : g.n0;  // this quarter's context
         float m_ref = -INFINITY, lsum = 0.f;
         const int rel = (par + C::NPAR - gp % C::NPAR) % C::NPAR;  // this warp's first page of the unit
+#pragma unroll 1
         for (int i = rel; i < g.npg; i += C::NPAR) {
-            const int a = gp + i, r = a % WN_S, k = a / WN_S;
-            if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.s_full[r], (uint32_t)(k & 1), sm, p.dev_err));
+            const int a = gp + i, r = a % WN_S;
+            if (!wait(&sm.s_full[r], a / WN_S)) return;
+            tc_fence_after();
             uint32_t x[2][32];
-            if (ok) {
-                tc_fence_after();
-                tmem_ld32(t_lane + 64u * (uint32_t)r, x[0]);
-                tmem_ld32(t_lane + 64u * (uint32_t)r + 32u, x[1]);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (l == 0) mbar_arrive(&sm.s_empty[r]);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 32; ++q) x[0][q] = x[1][q] = 0xFF800000u;
-            }
+            tmem_ld32(t_lane + 64u * (uint32_t)r, x[0]);
+            tmem_ld32(t_lane + 64u * (uint32_t)r + 32u, x[1]);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (l == 0) mbar_arrive(&sm.s_empty[r]);
             const int t0 = PAGE * w_logical(g, i);
             if (!w_whole(p, n, n, t0)) {
                 const uint64_t seen = w_seen(p, n, t0);
@@ -500,95 +568,88 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-                m4[q & 3] = fmaxf(m4[q & 3], __uint_as_float(x[0][q]));
-                m4[q & 3] = fmaxf(m4[q & 3], __uint_as_float(x[1][q]));
-            }
+            for (int q = 0; q < 32; ++q)
+                m4[q & 3] = fmaxf(m4[q & 3], fmaxf(__uint_as_float(x[0][q]), __uint_as_float(x[1][q])));
             const float pmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.kscale;
             const float m_own = m_ref;
-            float alpha = 1.f;
-            bool resc = false;
-            if (i == 0) {
-                m_ref = pmax;
-            } else {  // the decision of the page before
-                named_bar(hand + (uint32_t)((a - 1) % C::NPAR), 64);
-                m_ref = sm.xm[(a - 1) & 1][qd][l];
-                if (pmax > m_ref + TAU2) {
-                    alpha = ex2_approx(m_ref - pmax);
-                    m_ref = pmax;
-                    resc = true;
-                }
+            float m_prev = pmax;  // the decision of the page before; a unit's first page sets the reference
+            if (i > 0) {
+                if (!wait(&sm.hand[qd][(a - 1) % C::NPAR], (a - 1) / C::NPAR)) return;
+                m_prev = sm.xm[(a - 1) & 1][qd][l];
             }
+            const bool resc = pmax > m_prev + TAU2;
+            const float alpha = resc ? ex2_approx(m_prev - pmax) : 1.f;
+            m_ref = resc ? pmax : m_prev;
             sm.xm[a & 1][qd][l] = m_ref;
-            named_bar_arrive(hand + (uint32_t)par, 64);
-            if (m_own != m_ref) lsum *= ex2_approx(m_own - m_ref);  // (nothing summed yet: 0)
+            __syncwarp();
+            if (l == 0) mbar_arrive(&sm.hand[qd][par]);
+            lsum *= m_own == m_ref ? 1.f : ex2_approx(m_own - m_ref);  // (nothing summed yet: 0)
             const float mb = m_ref == -INFINITY ? 0.f : m_ref;  // nothing seen yet: every p is 0
-            uint32_t sp[32];
             uint64_t part[2] = {0ull, 0ull};
             const uint64_t k2 = f32x2(p.kscale, p.kscale), mb2 = f32x2(-mb, -mb);
+            // the bulk copy of this warp's page before has read its staging rows
+            if (l == 0) bulk_wait_read<0>();
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int j = 0; j < 8; ++j) {  // tokens 8 j .. 8 j + 7: p~ = bf16(2^(s - m_ref)); l sums the f32 values
+                uint32_t w[4];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {  // p~ = bf16(2^(s - m_ref)); l sums the f32 values
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t* at = &x[j >> 2][8 * (j & 3) + 2 * q];
                     float e0, e1;
-                    f32x2_parts(fma_f32x2(f32x2(__uint_as_float(x[e][2 * q]), __uint_as_float(x[e][2 * q + 1])), k2, mb2),
-                                e0, e1);
+                    f32x2_parts(fma_f32x2(f32x2(__uint_as_float(at[0]), __uint_as_float(at[1])), k2, mb2), e0, e1);
                     e0 = ex2_approx(e0);
                     e1 = ex2_approx(e1);
                     part[q & 1] = add_f32x2(part[q & 1], f32x2(e0, e1));
-                    sp[16 * e + q] = pack_bf16x2(e0, e1);
+                    w[q] = pack_bf16x2(e0, e1);
                 }
+                if (has_row)
+                    *reinterpret_cast<uint4*>(stage + pt_chunk_off(h, j) - qd * C::PSTAGE) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
             float l0, l1;
             f32x2_parts(add_f32x2(part[0], part[1]), l0, l1);
             lsum += l0 + l1;
-            // this warp's P rows, once the bulk copy of its page before has read the staging rows
-            if (l == 0) bulk_wait_read<0>();
-            __syncwarp();
-            if (has_row) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(stage + pt_chunk_off(h, j) - qd * C::PSTAGE) =
-                        make_uint4(sp[4 * j], sp[4 * j + 1], sp[4 * j + 2], sp[4 * j + 3]);
-            }
             fence_proxy_async_cta();  // the bulk copy reads the rows through the async proxy
             __syncwarp();
             const int st = a % C::NPBUF;
-            bool freed = false;  // the PV CTA has finished with the buffer's page before
-            if (ok) freed = wait_bar(&sm.p_empty[st], (uint32_t)((a / C::NPBUF) & 1) ^ 1u, sm, p.dev_err);
+            // the PV CTA has finished with the buffer's page before
+            if (!wait(&sm.p_empty[st], a / C::NPBUF + 1)) return;
             const uint32_t dst = recv0 + (uint32_t)(st * C::PBUF);
             const uint32_t bar = pfull0 + (uint32_t)(st * sizeof(uint64_t));
-            if (freed && l == 0) {
+            const uint32_t any = __ballot_sync(0xFFFFFFFFu, resc && has_row);
+            if (l == 0) {
                 bulk_copy_to_cluster(dst + (uint32_t)(qd * C::PSTAGE), stage, C::PSTAGE, bar);
                 bulk_commit();
+                st_async_b32(dst + C::META_FLAGS + 4 * qd, any ? 1u : 0u, bar);
             }
-            if (freed && has_row) st_async_b32(dst + C::META_ALPHA + 4 * h, __float_as_uint(alpha), bar);
-            const uint32_t any = __ballot_sync(0xFFFFFFFFu, resc && has_row);
-            if (freed && l == 0) st_async_b32(dst + C::META_FLAGS + 4 * qd, any ? 1u : 0u, bar);
+            if (has_row) st_async_b32(dst + C::META_ALPHA + 4 * h, __float_as_uint(alpha), bar);
         }
         const int last = gp + g.npg - 1;
-        if ((last + 1) % C::NPAR == par) named_bar(hand + (uint32_t)(last % C::NPAR), 64);  // nobody's page follows the last
+        // (the turn after the last page's waits for its decision all the same)
+        if ((last + 1) % C::NPAR == par && !wait(&sm.hand[qd][last % C::NPAR], last / C::NPAR)) return;
         // the quarter's sums meet in the warp of turn 1; the others go on at once
-        if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.fin_free[done & 1][qd], (uint32_t)((done >> 1) & 1) ^ 1u, sm, p.dev_err));
-        sm.fin_l[done & 1][rel][qd][l] = lsum;
-        sm.fin_m[done & 1][rel][qd][l] = m_ref;
+        if (!wait(&sm.fin_free[un & 1][qd], (un >> 1) + 1)) return;
+        sm.fin_l[un & 1][rel][qd][l] = lsum;
+        sm.fin_m[un & 1][rel][qd][l] = m_ref;
         __syncwarp();
         if (par != 1) {
-            if (l == 0) mbar_arrive(&sm.fin_full[done & 1][qd]);
-        } else if (ok && __all_sync(0xFFFFFFFFu, wait_bar(&sm.fin_full[done & 1][qd], (uint32_t)(done >> 1) & 1u, sm, p.dev_err))) {
-            m_ref = sm.fin_m[done & 1][(g.npg - 1) % C::NPAR][qd][l];  // the last page's warp
+            if (l == 0) mbar_arrive(&sm.fin_full[un & 1][qd]);
+        } else {
+            if (!wait(&sm.fin_full[un & 1][qd], un >> 1)) return;
+            m_ref = sm.fin_m[un & 1][(g.npg - 1) % C::NPAR][qd][l];  // the last page's warp
             float ltot = 0.f;  // by the unit's own count of pages: the order does not depend on the units before
 #pragma unroll
             for (int w = 0; w < C::NPAR; ++w) {
-                const float m_w = sm.fin_m[done & 1][w][qd][l], l_w = sm.fin_l[done & 1][w][qd][l];
+                const float m_w = sm.fin_m[un & 1][w][qd][l], l_w = sm.fin_l[un & 1][w][qd][l];
                 ltot += m_w == m_ref ? l_w : l_w * ex2_approx(m_w - m_ref);
             }
             __syncwarp();
-            if (l == 0) mbar_arrive(&sm.fin_free[done & 1][qd]);
-            if (g.single) {  // the PV CTA lands o_lat itself
+            if (l == 0) mbar_arrive(&sm.fin_free[un & 1][qd]);
+            if (g.single) {  // the PV CTA lands o_lat itself (a row that sees nothing has l = 0; its o_lat is not used)
                 const int sl = singles & 1;
-                // (a row that sees nothing has l = 0; its o_lat is not used)
-                if (wait_bar(&sm.rl_free[sl], (uint32_t)((singles >> 1) & 1) ^ 1u, sm, p.dev_err, true) && has_row)
-                    st_async_b32(mapa(smem_u32(&sm.rl[sl][h]), 1), __float_as_uint(1.f / ltot),
+                if (!wait(&sm.rl_free[sl], (singles >> 1) + 1, true)) return;
+                if (has_row)
+                    st_async_b32(mapa(smem_u32(&sm.u.c1.rl[sl][h]), 1), __float_as_uint(1.f / ltot),
                                  mapa(smem_u32(&sm.l_full[sl]), 1));
             } else if (has_row) {
                 p.ws_ml[((size_t)g.b * p.nsplit + g.s) * H + h] = make_float2(m_ref, ltot);
@@ -596,7 +657,6 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
         }
         singles += g.single;
         gp += g.npg;
-        ++done;
     }
     // this warp's bulk copies have landed, and so have the PV CTA's last releases of its P buffers
     if (l == 0) {
@@ -616,10 +676,9 @@ __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMa
     const bool me = lane_id() == 0;
     bool ok = true;
     int e = 0;
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, false);
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
@@ -658,12 +717,10 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
     bool ok = true, pending = false;  // pending: the epilogue has not yet taken the unit before out of TMEM
     uint32_t epi_k = 0, clear_k = 0;
     int gp = 0;
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, false);
-        if (g.npg == 0) continue;
-        const int n_lo = w_clamp(g.n0, p.cap), n_hi = MQ ? w_clamp(g.n0 + g.rows - 1, p.cap) : n_lo;
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
+        const int n_lo = w_clamp(g.n0, p.cap);
         for (int i = 0; i < g.npg && me && ok; ++i) {
             const int a = gp + i, st = a % C::NPBUF;
             const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
@@ -672,7 +729,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                 ok = false;
                 break;
             }
-            if (!w_whole(p, n_lo, n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
+            if (!w_whole(p, n_lo, g.n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
                 if (!wait_bar(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u, sm, p.dev_err)) {
                     ok = false;
                     break;
@@ -701,10 +758,12 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
             }
             tc_fence_after();
             // each half-page slot goes back to its producer once the MMAs that read it are done
-            issue_pv_half(tbase, smem_u32(sm.u.c1.ring[q0]), smem_u32(sm.u.c1.recv[st]), 0, i > 0);
-            umma_commit(&sm.empty[q0]);
-            issue_pv_half(tbase, smem_u32(sm.u.c1.ring[q1]), smem_u32(sm.u.c1.recv[st]), 1, i > 0);
-            umma_commit(&sm.empty[q1]);
+#pragma unroll 1
+            for (int x = 0; x < 2; ++x) {
+                const int q = x ? q1 : q0;
+                issue_pv_half(tbase, smem_u32(sm.u.c1.ring[q]), smem_u32(sm.u.c1.recv[st]), x, i > 0);
+                umma_commit(&sm.empty[q]);
+            }
             mbar_arrive_expect_tx(&sm.p_full[st], C::PCOPY);
             umma_commit_mc(&sm.p_empty[st], (uint16_t)0x1);
         }
@@ -716,9 +775,10 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
             sm.epi_hb = g.hb;
             sm.epi_row0 = g.row0;
             sm.epi_rows = g.rows;
-            sm.epi_single = g.single ? 1 : 0;
+            sm.epi_single = g.single;
             mbar_arrive(&sm.epi_req);
             pending = true;
+            *reinterpret_cast<volatile int32_t*>(&sm.pv_units) = un + 1;
         }
         gp += g.npg;
     }
@@ -742,14 +802,13 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
     const int lane = (int)lane_id(), w = (int)warp - WW_CLEAR0;
     bool ok = true;
     int gp = 0, done = 0;
-    W_FOR_UNITS(un)
-    {
-        WUnit g;
-        w_unit<MQ>(g, p, un, false);
-        const int n_lo = w_clamp(g.n0, p.cap), n_hi = MQ ? w_clamp(g.n0 + g.rows - 1, p.cap) : n_lo;
+    for (int un = 0;; ++un) {
+        const WUnit g = w_next<MQ>(sm, p, un);
+        if (g.npg < 0) break;
+        const int n_lo = w_clamp(g.n0, p.cap);
         for (int i = 0; i < g.npg && ok; ++i) {
             const int a = gp + i, t0 = PAGE * w_logical(g, i);
-            if (w_whole(p, n_lo, n_hi, t0)) continue;
+            if (w_whole(p, n_lo, g.n_hi, t0)) continue;
             uint64_t none, some;
             w_unseen<MQ>(p, g, t0, none, some);
             const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
@@ -787,6 +846,7 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
             ++done;
         }
         gp += g.npg;
+        if (lane == 0) atomicAdd(&sm.clear_units, 1);
     }
 }
 
@@ -801,59 +861,67 @@ __device__ __forceinline__ float w_row_scale(float m, float& inverse)
     return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
-// O [rows x 512] f32 leaves TMEM, a row a thread: f16 o_lat = O / l with a power of two per row when the unit is
-// all its rows see, else the f32 partial.  Each warp stages its 32 rows in two boxes of its own in turn (128
-// bytes a row, 128-byte swizzle; 64 dims f16 or 32 dims f32) and sends them by bulk tensor stores; no warp waits
-// for another.  What leaves the SM sets the time: as bf16 hi + lo a chunk's unit took 8.2 us to write 256 KB, by
-// bulk stores and by 32-byte stores from the registers alike.
+// O [rows x 512] f32 leaves TMEM, a row a thread and half the dims a warp: f16 o_lat = O / l with a power of two
+// per row when the unit is all its rows see, else the f32 partial.  Each warp turns 32 rows of 128 bytes (64
+// dims f16 or 32 dims f32) around in a box of shared memory of its own, so that eight lanes store a whole line
+// of a row.  (A chunk's unit as bf16 hi + lo, 256 KB, took 8.2 us by bulk tensor stores from the boxes, whose
+// reads each have to be waited for, and as long by 32-byte stores straight from the registers.)
 template <bool MQ>
-__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                            const WinParams& p, uint32_t t_lane, int warp, int singles)
+__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, uint32_t t_lane, int quarter, int half,
+                                            int singles)
 {
     using C = WCfg<MQ>;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
     const bool single = sm.epi_single != 0;
-    const int lane = (int)lane_id(), row = 32 * warp + lane;
-    // a chunk's warp holds 32 heads of token row row0 + warp; decode's the heads 32 warp .. of slot b
-    const bool mine = MQ ? warp < rows : row < C::ROWS;
-    const int tok = MQ ? row0 + warp : b, head0 = MQ ? 32 * hb : 32 * warp;
+    const int lane = (int)lane_id(), row = 32 * quarter + lane;
+    // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
+    const bool mine = MQ ? quarter < rows : row < C::ROWS;
+    const int tok = MQ ? row0 + quarter : b, head0 = MQ ? 32 * hb : 32 * quarter;
     float r = 1.f;
     if (single) {
-        if (mine) r = sm.rl[singles & 1][row];
-        named_bar(WB_OUT, 128);
-        if (threadIdx.x == 0) {  // the slot of 1 / l is free again
-            mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
-            mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
-        }
-        __syncwarp();
         if (mine) {
+            r = sm.u.c1.rl[singles & 1][row];
             float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < 8; ++k) {
                 uint32_t v[32];
                 tmem_ld32(t_lane + 32u * (uint32_t)k, v);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], fabsf(__uint_as_float(v[e])));
             }
-            float inverse;
-            r *= w_row_scale(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * r, inverse);
-            p.oscale[(size_t)(head0 + lane) * p.R + tok] = inverse;
+            sm.u.c1.half_max[half][row] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
         }
+        named_bar(WB_OUT, 32 * W_EPI);
+        if (threadIdx.x == 0) {  // the slot of 1 / l is free again
+            mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
+            mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
+        }
+        if (mine) {
+            float inverse;
+            r *= w_row_scale(fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r, inverse);
+            if (half == 0) p.oscale[(size_t)(head0 + lane) * p.R + tok] = inverse;
+        }
+        __syncwarp();
     }
     const uint32_t sw = (uint32_t)(lane & 7);
-    int x = 0;
+    uint8_t* box = sm.u.c1.box[MQ ? quarter : min(quarter, C::ROWS / 32 - 1)][half];
+    // o_lat [96][R][512] f16, or partials [B][nsplit][96][512] f32: this lane's piece of rows 4 j + lane / 8
+    uint8_t* out;
+    size_t pitch;
+    if (single) {
+        out = reinterpret_cast<uint8_t*>(p.olat + ((size_t)head0 * p.R + tok) * LORA + 256 * half);
+        pitch = (size_t)p.R * LORA * 2;
+    } else {
+        out = reinterpret_cast<uint8_t*>(p.ws_o + (((size_t)b * p.nsplit + s) * H + head0) * LORA + 256 * half);
+        pitch = LORA * 4;
+    }
+    out += (lane >> 3) * pitch + 16 * (lane & 7);
 #pragma unroll 1
-    for (int k = 0; k < 16 && mine; ++k) {
+    for (int k = 0; k < 8 && mine; ++k) {
         uint32_t v[32];
         tmem_ld32(t_lane + 32u * (uint32_t)k, v);
         tmem_wait_ld();
-        const bool send = !single || (k & 1);  // two loads fill a box of f16
-        uint8_t* at = sm.u.c1.box[MQ ? warp : min(warp, C::ROWS / 32 - 1)][x] + lane * 128;
-        if (!single || !(k & 1)) {
-            if (lane == 0) bulk_wait_read<1>();  // the box's store before has read it
-            __syncwarp();
-        }
         if (single) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -861,57 +929,56 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const CUtensorMap& tm
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w[e] = pack_f16x2(__uint_as_float(v[8 * i + 2 * e]) * r, __uint_as_float(v[8 * i + 2 * e + 1]) * r);
-                *reinterpret_cast<uint4*>(at + ((((uint32_t)(4 * (k & 1) + i)) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(box + lane * 128 + ((((uint32_t)(4 * (k & 1) + i)) ^ sw) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
             }
+            if (!(k & 1)) continue;  // two loads fill a box of f16
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(at + (((uint32_t)i ^ sw) << 4)) =
+                *reinterpret_cast<uint4*>(box + lane * 128 + (((uint32_t)i ^ sw) << 4)) =
                     make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
-        if (!send) continue;
-        fence_proxy_async_cta();  // the bulk store reads the box through the async proxy
         __syncwarp();
-        if (lane == 0) {
-            const uint8_t* box = at;
-            if (single)  // o_lat [96][R][512] as (512 dims, R rows, 96 heads)
-                tma_store_3d(&tm_out, box, 32 * (k - 1), tok, head0);
-            else  // partials [B][nsplit][96][512] f32 as (512 dims, rows)
-                tma_store_2d(&tm_part, box, 32 * k, (b * p.nsplit + s) * H + head0);
-            bulk_commit();
+        uint8_t* to = out + 128 * (single ? k >> 1 : k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = 4 * j + (lane >> 3);
+            *reinterpret_cast<uint4*>(to + (size_t)(4 * j) * pitch) =
+                *reinterpret_cast<const uint4*>(box + i * 128 + (((uint32_t)(lane & 7) ^ (uint32_t)(i & 7)) << 4));
         }
-        x ^= 1;
+        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.epi_done);
 }
 
+// Epilogue warp: the TMEM lanes of its quarter, the dims of its half.
 template <bool MQ>
-__device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_out, const CUtensorMap& tm_part,
-                                           const WinParams& p, uint32_t tbase, uint32_t warp)
+__device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int quarter, int half)
 {
     using C = WCfg<MQ>;
-    const int lane = (int)lane_id(), row = 32 * (int)warp + lane;
-    const uint32_t t_lane = tbase + ((32u * warp) << 16);
+    const int lane = (int)lane_id(), row = 32 * quarter + lane;
+    const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16) + 256u * (uint32_t)half;
     uint32_t od = 0;
     int singles = 0;
     for (uint32_t k = 0;; ++k) {
         // (an abort may reach one warp and not another: they agree on it, so that all or none pass the
         // write-out's barriers)
         bool got = __all_sync(0xFFFFFFFFu, wait_bar(&sm.epi_req, k & 1u, sm, p.dev_err));
-        if (named_bar_any(WB_OUT, 128, !got)) break;
+        if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         const uint32_t cmd = *reinterpret_cast<volatile uint32_t*>(&sm.epi_cmd);
         if (!cmd) break;
         got = wait_bar(&sm.o_done, od++ & 1u, sm, p.dev_err);
         if ((cmd & 2u) && sm.epi_single)
             got = got && wait_bar(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u, sm, p.dev_err, true);
         got = __all_sync(0xFFFFFFFFu, got);
-        if (named_bar_any(WB_OUT, 128, !got)) break;
+        if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         tc_fence_after();
         if (cmd & 2u) {
             const bool single = sm.epi_single != 0;
-            w_write_out<MQ>(sm, tm_out, tm_part, p, t_lane, (int)warp, singles);
+            w_write_out<MQ>(sm, p, t_lane, quarter, half, singles);
             singles += single;
             continue;
         }
@@ -919,7 +986,7 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_
         const float f = row < C::ROWS ? al[row] : 1.f;
         if (__any_sync(0xFFFFFFFFu, f != 1.f)) {  // some row of this warp moved its reference
 #pragma unroll 1
-            for (int cb = 0; cb < LORA / 32; ++cb) {
+            for (int cb = 0; cb < LORA / 64; ++cb) {
                 uint32_t v[32];
                 tmem_ld32(t_lane + 32u * (uint32_t)cb, v);
                 tmem_wait_ld();
@@ -933,16 +1000,14 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const CUtensorMap& tm_
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.epi_done);
     }
-    if (lane == 0) bulk_wait_read<0>();
 }
 
 // ---- the kernel ---------------------------------------------------------------------------
 
 template <bool MQ>
-__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(WCfg<MQ>::REGS)
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     k3mla_window_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
-                        const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
-                        const __grid_constant__ CUtensorMap tm_part, const WinParams p)
+                        const __grid_constant__ CUtensorMap tm_q, const WinParams p)
 {
     using C = WCfg<MQ>;
     extern __shared__ uint8_t smem_raw[];
@@ -958,7 +1023,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(WCfg<MQ>::REGS)
     }
     if (warp == 5 && lane == 0) {
         tma_prefetch_desc(rank == 0 ? &tm_page : &tm_page8);
-        tma_prefetch_desc(rank == 0 ? &tm_q : &tm_out);
+        if (rank == 0) tma_prefetch_desc(&tm_q);
     }
     tc_fence_before();
     cluster_sync();
@@ -968,13 +1033,15 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(WCfg<MQ>::REGS)
     griddep_launch_dependents();
     if (rank == 0) {
         if (warp < C::W_PROD) w_softmax<MQ>(sm, p, tbase, warp);
-        else if (warp == C::W_PROD) w_produce<MQ>(sm, tm_page, tm_q, p);
-        else w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
+        else if (warp < C::W_MMA0) w_produce<MQ>(sm, tm_page, tm_q, p, (int)warp - C::W_PROD);
+        else if (warp < C::W_MMA0 + WN_S) w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
     } else {
-        if (warp < 4) w_epilogue<MQ>(sm, tm_out, tm_part, p, tbase, warp);
+        if (warp < 4 || (warp >= WW_EPI1 && warp < WW_EPI1 + 4))
+            w_epilogue<MQ>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
         else if (warp == WW_HALVES) w_produce_halves<MQ>(sm, tm_page8, p);
         else if (warp == WW_PV) w_issue_pv<MQ>(sm, p, tbase);
-        else if (warp >= WW_CLEAR0 && warp < WW_CLEAR0 + 4) w_clear<MQ>(sm, p, warp);
+        else if (warp < WW_CLEAR0 + 4) w_clear<MQ>(sm, p, warp);
+        else if (warp == WW_PLAN) w_plan<MQ>(sm, p);
     }
     __syncwarp();
     tc_fence_before();
@@ -1308,28 +1375,18 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     p.oscale = reinterpret_cast<float*>(ws + wl.scale);
     p.ws_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.o) : nullptr;
     p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
-    CUtensorMap tm_page, tm_page8, tm_q, tm_out, tm_part, tm_w, tm_o;
+    CUtensorMap tm_page, tm_page8, tm_q, tm_w, tm_o;
     const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
     int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
     if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
     if (rc) return rc;
     if (MQ) {
-        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): a chunk of 32 heads of four token rows
+        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
         const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
-        const uint32_t box[4] = {64, 32, 4, 1};
+        const uint32_t box[4] = {64, 32, 2, 1};
         rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
     } else {
         rc = make_tmap_slab_3d(&tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
-    }
-    // o_lat [96][R][512] as (512 dims, R rows, 96 heads): a box is 64 dims of 32 heads of one row
-    const uint64_t od[3] = {LORA, R, H}, os[2] = {LORA * 2, R * LORA * 2};
-    const uint32_t ob[3] = {64, 1, 32};
-    if (!rc) rc = make_tmap_store(&tm_out, false, 3, p.olat, od, os, ob, true);
-    tm_part = tm_out;
-    if (!rc && p.nsplit > 1) {  // partials [B][nsplit][96][512] f32: 32 dims of 32 rows
-        const uint64_t pd[2] = {LORA, R * p.nsplit * H}, ps[1] = {LORA * 4};
-        const uint32_t pb[2] = {32, 32};
-        rc = make_tmap_store(&tm_part, true, 2, p.ws_o, pd, ps, pb, true);
     }
     if (!rc) rc = make_tmap_slab_3d(&tm_w, w_kv_b, (uint64_t)H * WROWS_PER_HEAD, LORA, 8, VH, 1);
     if (!rc) rc = make_tmap_slab_3d(&tm_o, p.olat, (uint64_t)H * R, LORA, 8, WX_TILE, 1);
@@ -1339,8 +1396,8 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
     set_smem_attr(reinterpret_cast<const void*>(k3mla_window_expand_kernel), WX_SMEM, attr_expand);
     const int clusters = std::min(p.n_units, sm_count() / 2);
-    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(C::THREADS), smem, st, "k3mla_window_kernel", tm_page,
-                    tm_page8, tm_q, tm_out, tm_part, p);
+    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
+                    tm_page8, tm_q, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
         rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(WM_THREADS), 0, st, "k3mla_window_merge_kernel", p);
