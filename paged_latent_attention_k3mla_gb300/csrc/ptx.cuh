@@ -32,6 +32,15 @@ __device__ __forceinline__ uint64_t globaltimer()
     return t;
 }
 
+// One lane of a warp in step: the compiler keeps what that lane then computes in uniform registers, which the
+// tensor core's and the TMA's instructions take their operands from.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count)

@@ -67,7 +67,8 @@ template <bool MQ> struct WCfg {
     static constexpr int NPAR = MQ ? 3 : 2;              // score CTA: softmax warps of a quarter, a page each in turn
     static constexpr int W_PROD = 4 * NPAR;              // ... behind them the producers ...
     static constexpr int W_MMA0 = W_PROD + NPROD;        // ... and three MMA issuers
-    static_assert(W_MMA0 + 3 <= 16, "the warps of a CTA");
+    static constexpr int NISS = MQ ? 3 : 3;
+    static_assert(W_MMA0 + NISS <= 16, "the warps of a CTA");
     static constexpr int PSTAGE = RPQ * 128;             // score CTA: one softmax warp's P rows (x 64 tokens)
     static constexpr int PT_BYTES = ROWS * 128;          // P [rows][64 tokens] bf16, K-major, 128-byte swizzle
     static constexpr int META_ALPHA = PT_BYTES;          // f32 alpha[rows]
@@ -303,7 +304,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
         mbar_init(&sm.s_empty[i], 4);
     }
     for (int i = 0; i < 4 * C::NPAR; ++i) mbar_init(&sm.hand[i / C::NPAR][i % C::NPAR], 1);
-    mbar_init(&sm.q_free, WN_S);
+    mbar_init(&sm.q_free, C::NISS);
     mbar_init(&sm.q_ready, 4);
     for (int i = 0; i < C::NPBUF; ++i) {
         mbar_init(&sm.p_full[i], 1);
@@ -383,8 +384,7 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
                                           const WinParams& p, int t)
 {
     using C = WCfg<MQ>;
-    const bool me = lane_id() == 0;
-    bool ok = true;
+    bool ok = true;  // (the elected lane's)
     int base = 0;
     auto take = [&](int use, uint32_t bytes) -> int {  // the use's ring unit, ready to be loaded
         const int u = use % C::NUNIT, k = use / C::NUNIT;
@@ -399,30 +399,37 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
     for (int un = 0;; ++un) {
         const WUnit g = w_next<MQ>(sm, p, un);
         if (g.npg < 0) break;
-        for (int j = 0; j < C::NQ && me && ok; ++j) {
-            if ((base + j) % C::NPROD != t) continue;
-            const int u = take(base + j, C::QPU * C::QPIECE);
-            if (!ok) break;
-            if constexpr (MQ) {
-                // piece: heads 32 hb .. of two consecutive token rows (those past the group land in lanes nobody reads)
-                for (int x = 0; x < C::QPU; ++x) {
-                    const int pc = C::QPU * j + x;
-                    tma_load_4d(sm.u.c0.ring[u] + x * C::QPIECE, &tm_q, 0, 32 * g.hb, g.row0 + 2 * (pc & 1), pc >> 1,
-                                &sm.full[u]);
+        if (elect_one()) {
+            for (int j = 0; j < C::NQ && ok; ++j) {
+                if ((base + j) % C::NPROD != t) continue;
+                const int u = take(base + j, C::QPU * C::QPIECE);
+                if (!ok) break;
+                if constexpr (MQ) {
+                    // piece: heads 32 hb .. of two consecutive token rows (those past the group land in lanes nobody reads)
+                    for (int x = 0; x < C::QPU; ++x) {
+                        const int pc = C::QPU * j + x;
+                        tma_load_4d(sm.u.c0.ring[u] + x * C::QPIECE, &tm_q, 0, 32 * g.hb, g.row0 + 2 * (pc & 1), pc >> 1,
+                                    &sm.full[u]);
+                    }
+                } else {
+                    tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
                 }
-            } else {
-                tma_load_3d(sm.u.c0.ring[u], &tm_q, 0, g.b * H, C::QPU * j, &sm.full[u]);
             }
         }
+        __syncwarp();
         base += C::NQ;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
-            for (int x = 0; x < 3 && me && ok; ++x) {
-                if ((base + 3 * i + x) % C::NPROD != t) continue;
-                const int u = take(base + 3 * i + x, THIRD);
-                if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+            if (elect_one()) {
+#pragma unroll 1
+                for (int x = 0; x < 3 && ok; ++x) {
+                    if ((base + 3 * i + x) % C::NPROD != t) continue;
+                    const int u = take(base + 3 * i + x, THIRD);
+                    if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+                }
             }
+            __syncwarp();
         }
         base += 3 * g.npg;
     }
@@ -440,12 +447,13 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
         const WUnit g = w_next<MQ>(sm, p, un);
         if (g.npg < 0) break;
         base += C::NQ;
-        if (lane_id() == 0 && ok) {
+        if (elect_one() && ok) {
             ok = wait_bar(&sm.q_ready, (uint32_t)un & 1u, sm, p.dev_err);
             tc_fence_after();
-            for (int i = (r + WN_S - gp % WN_S) % WN_S; i < g.npg && ok; i += WN_S) {
-                const int k = (gp + i) / WN_S;
-                ok = wait_bar(&sm.s_empty[r], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
+#pragma unroll 1
+            for (int i = (r + C::NISS - gp % C::NISS) % C::NISS; i < g.npg && ok; i += C::NISS) {
+                const int sb = (gp + i) % WN_S, k = (gp + i) / WN_S;
+                ok = wait_bar(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
 #pragma unroll 1
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
@@ -454,13 +462,14 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
                     if (!ok) break;
                     *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = ku + 1;
                     tc_fence_after();
-                    issue_score_third(tbase, S_COL + 64u * (uint32_t)r, smem_u32(sm.u.c0.ring[u]), t);
+                    issue_score_third(tbase, S_COL + 64u * (uint32_t)sb, smem_u32(sm.u.c0.ring[u]), t);
                     umma_commit(&sm.empty[u]);
                 }
-                if (ok) umma_commit(&sm.s_full[r]);
+                if (ok) umma_commit(&sm.s_full[sb]);
             }
             if (ok) umma_commit(&sm.q_free);
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         base += 3 * g.npg;
         gp += g.npg;
     }
@@ -673,23 +682,25 @@ template <bool MQ>
 __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMap& tm_page8, const WinParams& p)
 {
     const uint64_t pol = policy_evict_first();  // the last reader of the latent in this unit
-    const bool me = lane_id() == 0;
-    bool ok = true;
+    bool ok = true;                             // (the elected lane's)
     int e = 0;
     for (int un = 0;; ++un) {
         const WUnit g = w_next<MQ>(sm, p, un);
         if (g.npg < 0) break;
         WLookup rows;
-        for (int i = 0; i < g.npg; ++i) {
+        for (int i = 0; i < g.npg; ++i, e += 2) {
             const int32_t y = rows(p, g, i);
-            for (int x = 0; x < 2; ++x, ++e) {
-                const int q = e % WN_HALF;
-                if (!me || !ok) continue;
-                ok = wait_bar(&sm.empty[q], (uint32_t)((e / WN_HALF) & 1) ^ 1u, sm, p.dev_err);
-                if (!ok) continue;
-                mbar_arrive_expect_tx(&sm.full[q], SLOT1);
-                tma_load_3d_hint(sm.u.c1.ring[q], &tm_page8, 0, y + HALF * x, 0, &sm.full[q], pol);
+            if (elect_one()) {
+#pragma unroll 1
+                for (int x = 0; x < 2 && ok; ++x) {
+                    const int q = (e + x) % WN_HALF;
+                    ok = wait_bar(&sm.empty[q], (uint32_t)(((e + x) / WN_HALF) & 1) ^ 1u, sm, p.dev_err);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&sm.full[q], SLOT1);
+                    tma_load_3d_hint(sm.u.c1.ring[q], &tm_page8, 0, y + HALF * x, 0, &sm.full[q], pol);
+                }
             }
+            __syncwarp();
         }
     }
     if (!ok) drain_inflight();
@@ -713,7 +724,7 @@ template <bool MQ>
 __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase)
 {
     using C = WCfg<MQ>;
-    const bool me = lane_id() == 0;
+    // (elect_one() names the same lane every time: pending and the two counters are that lane's)
     bool ok = true, pending = false;  // pending: the epilogue has not yet taken the unit before out of TMEM
     uint32_t epi_k = 0, clear_k = 0;
     int gp = 0;
@@ -721,71 +732,75 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
         const WUnit g = w_next<MQ>(sm, p, un);
         if (g.npg < 0) break;
         const int n_lo = w_clamp(g.n0, p.cap);
-        for (int i = 0; i < g.npg && me && ok; ++i) {
-            const int a = gp + i, st = a % C::NPBUF;
-            const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
-            if (!wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) ||
-                !wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err)) {
-                ok = false;
-                break;
-            }
-            if (!w_whole(p, n_lo, g.n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
-                if (!wait_bar(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u, sm, p.dev_err)) {
+        if (elect_one() && ok) {
+#pragma unroll 1
+            for (int i = 0; i < g.npg && ok; ++i) {
+                const int a = gp + i, st = a % C::NPBUF;
+                const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
+                if (!wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) ||
+                    !wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err)) {
                     ok = false;
                     break;
                 }
-                ++clear_k;
-            }
-            *reinterpret_cast<volatile int32_t*>(&sm.pv_seen) = a + 1;
-            if (!wait_bar(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1), sm, p.dev_err, true)) {
-                ok = false;
-                break;
-            }
-            fence_proxy_async_cta();  // the P tile came through DSMEM copies; the MMA reads it
-            const volatile uint32_t* rf = reinterpret_cast<const volatile uint32_t*>(sm.u.c1.recv[st] + C::META_FLAGS);
-            const bool resc = i > 0 && (rf[0] | rf[1] | rf[2] | rf[3]) != 0u;
-            if (pending || resc) {
-                if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
-                pending = false;
-                if (ok && resc) {
-                    umma_commit(&sm.o_done);
-                    sm.epi_cmd = 1u;
-                    sm.epi_stage = (uint32_t)st;
-                    mbar_arrive(&sm.epi_req);
-                    ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+                if (!w_whole(p, n_lo, g.n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
+                    if (!wait_bar(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u, sm, p.dev_err)) {
+                        ok = false;
+                        break;
+                    }
+                    ++clear_k;
                 }
-                if (!ok) break;
-            }
-            tc_fence_after();
-            // each half-page slot goes back to its producer once the MMAs that read it are done
+                *reinterpret_cast<volatile int32_t*>(&sm.pv_seen) = a + 1;
+                if (!wait_bar(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1), sm, p.dev_err, true)) {
+                    ok = false;
+                    break;
+                }
+                fence_proxy_async_cta();  // the P tile came through DSMEM copies; the MMA reads it
+                const volatile uint32_t* rf = reinterpret_cast<const volatile uint32_t*>(sm.u.c1.recv[st] + C::META_FLAGS);
+                const bool resc = i > 0 && (rf[0] | rf[1] | rf[2] | rf[3]) != 0u;
+                if (pending || resc) {
+                    if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+                    pending = false;
+                    if (ok && resc) {
+                        umma_commit(&sm.o_done);
+                        sm.epi_cmd = 1u;
+                        sm.epi_stage = (uint32_t)st;
+                        mbar_arrive(&sm.epi_req);
+                        ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+                    }
+                    if (!ok) break;
+                }
+                tc_fence_after();
+                // each half-page slot goes back to its producer once the MMAs that read it are done
 #pragma unroll 1
-            for (int x = 0; x < 2; ++x) {
-                const int q = x ? q1 : q0;
-                issue_pv_half(tbase, smem_u32(sm.u.c1.ring[q]), smem_u32(sm.u.c1.recv[st]), x, i > 0);
-                umma_commit(&sm.empty[q]);
+                for (int x = 0; x < 2; ++x) {
+                    const int q = x ? q1 : q0;
+                    issue_pv_half(tbase, smem_u32(sm.u.c1.ring[q]), smem_u32(sm.u.c1.recv[st]), x, i > 0);
+                    umma_commit(&sm.empty[q]);
+                }
+                mbar_arrive_expect_tx(&sm.p_full[st], C::PCOPY);
+                umma_commit_mc(&sm.p_empty[st], (uint16_t)0x1);
             }
-            mbar_arrive_expect_tx(&sm.p_full[st], C::PCOPY);
-            umma_commit_mc(&sm.p_empty[st], (uint16_t)0x1);
+            if (ok) {  // O of the unit is complete: to be written out
+                umma_commit(&sm.o_done);
+                sm.epi_cmd = 2u;
+                sm.epi_b = g.b;
+                sm.epi_s = g.s;
+                sm.epi_hb = g.hb;
+                sm.epi_row0 = g.row0;
+                sm.epi_rows = g.rows;
+                sm.epi_single = g.single;
+                mbar_arrive(&sm.epi_req);
+                pending = true;
+                *reinterpret_cast<volatile int32_t*>(&sm.pv_units) = un + 1;
+            }
         }
-        if (me && ok) {  // O of the unit is complete: to be written out
-            umma_commit(&sm.o_done);
-            sm.epi_cmd = 2u;
-            sm.epi_b = g.b;
-            sm.epi_s = g.s;
-            sm.epi_hb = g.hb;
-            sm.epi_row0 = g.row0;
-            sm.epi_rows = g.rows;
-            sm.epi_single = g.single;
-            mbar_arrive(&sm.epi_req);
-            pending = true;
-            *reinterpret_cast<volatile int32_t*>(&sm.pv_units) = un + 1;
-        }
+        ok = __all_sync(0xFFFFFFFFu, ok);
         gp += g.npg;
     }
     if (!ok) {
         drain_inflight();
         *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
-    } else if (me) {  // the epilogue warps leave
+    } else if (elect_one()) {  // the epilogue warps leave
         if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
         sm.epi_cmd = 0u;
         mbar_arrive(&sm.epi_req);
@@ -1034,7 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     if (rank == 0) {
         if (warp < C::W_PROD) w_softmax<MQ>(sm, p, tbase, warp);
         else if (warp < C::W_MMA0) w_produce<MQ>(sm, tm_page, tm_q, p, (int)warp - C::W_PROD);
-        else if (warp < C::W_MMA0 + WN_S) w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
+        else if (warp < C::W_MMA0 + C::NISS) w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
     } else {
         if (warp < 4 || (warp >= WW_EPI1 && warp < WW_EPI1 + 4))
             w_epilogue<MQ>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
