@@ -77,12 +77,12 @@ template <bool MQ> struct WCfg {
     static constexpr int PBUF = (PCOPY + 1023) / 1024 * 1024;  // buffer pitch
 };
 constexpr int WN_S = 3;        // S buffers, one MMA issuer each
-constexpr int WN_HALF = 4;     // PV CTA: half-page slots
-constexpr int W_BOX = 32 * 128;  // PV CTA: one write-out box of a warp, 32 rows of 128 bytes
+constexpr int WN_HALF = 5;     // PV CTA: half-page slots
 constexpr int W_THREADS = 512;  // 128 registers a thread
 // PV CTA: the producer, the MMA issuer, four warps that clear unseen tokens, eight of the epilogue (0-3 and 10-13: a
-// warp reads the TMEM lanes of its own quarter), one that plans the units of both CTAs
-constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6, WW_EPI1 = 10, WW_PLAN = 14;
+// warp reads the TMEM lanes of its own quarter), one that plans the units of both CTAs, one
+// for the rows that see nothing
+constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6, WW_EPI1 = 10, WW_PLAN = 14, WW_EMPTY = 15;
 constexpr int W_PLANS = 8;         // planned units kept
 constexpr uint32_t WB_OUT = 1;     // named barrier of the epilogue warps
 constexpr int W_EPI = 8;
@@ -109,7 +109,6 @@ template <bool MQ> struct __align__(1024) WSmem {
         struct {
             uint8_t ring[WN_HALF][SLOT1];
             uint8_t recv[C::NPBUF][C::PBUF];
-            uint8_t box[C::ROWS / 32][2][W_BOX];  // one of each epilogue warp
             float rl[2][C::ROWS];          // 1 / l of every row, by parity of the unit; written by the score CTA
             float half_max[2][C::ROWS];    // the rows' largest |O| in each half of the dims
         } c1;
@@ -134,7 +133,7 @@ template <bool MQ> struct __align__(1024) WSmem {
     int32_t pv_seen;                     // PV CTA: pages whose latents the MMA issuer has seen arrive and cleared
     uint32_t tmem_base;
     uint32_t epi_cmd, epi_stage;         // to the epilogue warps: bit 0 rescale O, bit 1 write it out
-    int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_single;
+    int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_n0, epi_single;
     int32_t abort_flag;
     uint64_t wait_ns;
 };
@@ -153,11 +152,12 @@ template <bool MQ> constexpr bool wsmem_fits()
 static_assert(wsmem_fits<false>() && wsmem_fits<true>(), "shared-memory layouts");
 
 struct WinParams {
+    const uint16_t* q_abs;
     const int32_t* table;
     const int32_t* ctx_len;              // decode
     const int32_t *pos0, *row_start;     // chunk
     uint16_t* olat;                      // [96][R][512] f16: o_lat times a power of two per row
-    float* oscale;                       // [96][R]: what undoes it
+    float* oscale;                       // [96][R]: what undoes it; 0 for rows that see nothing
     float* ws_o;                         // [B][nsplit][96][512] f32 partials (decode, nsplit > 1)
     float2* ws_ml;                       // [B][nsplit][96]: reference max (in log2 units), sum of exp
     int32_t* dev_err;
@@ -344,6 +344,8 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
             ok = wait_count(&sm.pv_units, n - 3, sm, p.dev_err) && wait_count(&sm.clear_units, 4 * (n - 6), sm, p.dev_err);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
+        if (n > 0 && g.npg > 0 && lane < g.rows)  // its queries, into L2 (the first unit's are loaded at once)
+            bulk_prefetch_l2(p.q_abs + ((size_t)(MQ ? g.row0 + lane : g.b) * H + 32 * g.hb) * ROW, (MQ ? 32 : H) * ROW * 2);
         const int slot = n % W_PLANS;
         if (lane < 2) {  // one lane a CTA
             const uint32_t at = mapa(smem_u32(&sm.plan[slot]), (uint32_t)lane);
@@ -788,6 +790,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                 sm.epi_hb = g.hb;
                 sm.epi_row0 = g.row0;
                 sm.epi_rows = g.rows;
+                sm.epi_n0 = g.n0;
                 sm.epi_single = g.single;
                 mbar_arrive(&sm.epi_req);
                 pending = true;
@@ -865,6 +868,32 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
     }
 }
 
+// The rows that see nothing, which no unit has: their o_lat counts as zero whatever the workspace holds.
+template <bool MQ> __device__ __forceinline__ void w_empty_rows(const WinParams& p)
+{
+    const int lane = (int)lane_id(), stride = 32 * ((int)gridDim.x >> 1);
+    for (int r0 = 32 * ((int)blockIdx.x >> 1); r0 < p.R; r0 += stride) {
+        const int r = r0 + lane;
+        bool sees = true;
+        if (r < p.R) {
+            if constexpr (MQ) {
+                int lo = 0, hi = p.B;  // the last slot with row_start[b] <= r
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (p.row_start[mid] <= r) lo = mid;
+                    else hi = mid;
+                }
+                const int first = p.row_start[lo];
+                sees = r >= first && r < p.row_start[lo + 1] && (int64_t)p.pos0[lo] + (r - first) >= 0;
+            } else {
+                sees = min(p.ctx_len[r], p.cap) > 0;
+            }
+        }
+        if (!sees)
+            for (int h = 0; h < H; ++h) p.oscale[(size_t)h * p.R + r] = 0.f;
+    }
+}
+
 // The power of two that brings a row with largest magnitude m into f16's range (to [2^14, 2^15)), and its
 // inverse; 1 for rows of zeros, infinities or NaN.
 __device__ __forceinline__ float w_row_scale(float m, float& inverse)
@@ -876,93 +905,85 @@ __device__ __forceinline__ float w_row_scale(float m, float& inverse)
     return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
-// O [rows x 512] f32 leaves TMEM, a row a thread and half the dims a warp: f16 o_lat = O / l with a power of two
-// per row when the unit is all its rows see, else the f32 partial.  Each warp turns 32 rows of 128 bytes (64
-// dims f16 or 32 dims f32) around in a box of shared memory of its own, so that eight lanes store a whole line
-// of a row.  (A chunk's unit as bf16 hi + lo, 256 KB, took 8.2 us by bulk tensor stores from the boxes, whose
-// reads each have to be waited for, and as long by 32-byte stores straight from the registers.)
+// O [rows x 512] f32 leaves TMEM, a row a thread and half the dims a warp, each lane storing whole 32-byte sectors
+// of its own row: f16 o_lat = O / l with a power of two per row when the unit is all its rows see, else the f32
+// partial.  Reading TMEM sets the pace (some 64 bytes a clock and SM: 2.1 us for a chunk's 256 KB; eight warps
+// are no faster than four, nor are bulk stores or stores of whole lines from staged boxes), so it is read once: the
+// power of two comes from the row's first 32 entries, with room for 2^8 times their largest, and the row's
+// largest entry is found on the way.  A row that it shows to have left the range, or to lie far below it, has its
+// warps go over their rows again with the power of two that fits.
 template <bool MQ>
-__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, uint32_t t_lane, int quarter, int half,
+__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, uint32_t t_row, int quarter, int half,
                                             int singles)
 {
     using C = WCfg<MQ>;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
     const bool single = sm.epi_single != 0;
     const int lane = (int)lane_id(), row = 32 * quarter + lane;
+    const uint32_t t_lane = t_row + 256u * (uint32_t)half;
     // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
-    const bool mine = MQ ? quarter < rows : row < C::ROWS;
-    const int tok = MQ ? row0 + quarter : b, head0 = MQ ? 32 * hb : 32 * quarter;
-    float r = 1.f;
-    if (single) {
-        if (mine) {
-            r = sm.u.c1.rl[singles & 1][row];
-            float m[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool mine = MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : row < C::ROWS;  // (and the row sees something)
+    const int tok = MQ ? row0 + quarter : b, head = (MQ ? 32 * hb : 32 * quarter) + lane;
+    if (!single) {
+        float* out = p.ws_o + (((size_t)b * p.nsplit + s) * H + head) * LORA + 256 * half;
 #pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-                uint32_t v[32];
-                tmem_ld32(t_lane + 32u * (uint32_t)k, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], fabsf(__uint_as_float(v[e])));
-            }
-            sm.u.c1.half_max[half][row] = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-        }
-        named_bar(WB_OUT, 32 * W_EPI);
-        if (threadIdx.x == 0) {  // the slot of 1 / l is free again
-            mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
-            mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
-        }
-        if (mine) {
-            float inverse;
-            r *= w_row_scale(fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r, inverse);
-            if (half == 0) p.oscale[(size_t)(head0 + lane) * p.R + tok] = inverse;
-        }
-        __syncwarp();
-    }
-    const uint32_t sw = (uint32_t)(lane & 7);
-    uint8_t* box = sm.u.c1.box[MQ ? quarter : min(quarter, C::ROWS / 32 - 1)][half];
-    // o_lat [96][R][512] f16, or partials [B][nsplit][96][512] f32: this lane's piece of rows 4 j + lane / 8
-    uint8_t* out;
-    size_t pitch;
-    if (single) {
-        out = reinterpret_cast<uint8_t*>(p.olat + ((size_t)head0 * p.R + tok) * LORA + 256 * half);
-        pitch = (size_t)p.R * LORA * 2;
-    } else {
-        out = reinterpret_cast<uint8_t*>(p.ws_o + (((size_t)b * p.nsplit + s) * H + head0) * LORA + 256 * half);
-        pitch = LORA * 4;
-    }
-    out += (lane >> 3) * pitch + 16 * (lane & 7);
-#pragma unroll 1
-    for (int k = 0; k < 8 && mine; ++k) {
-        uint32_t v[32];
-        tmem_ld32(t_lane + 32u * (uint32_t)k, v);
-        tmem_wait_ld();
-        if (single) {
+        for (int k = 0; k < 8 && mine; ++k) {
+            uint32_t v[32];
+            tmem_ld32(t_lane + 32u * (uint32_t)k, v);
+            tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
+                uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack_f16x2(__uint_as_float(v[8 * i + 2 * e]) * r, __uint_as_float(v[8 * i + 2 * e + 1]) * r);
-                *reinterpret_cast<uint4*>(box + lane * 128 + ((((uint32_t)(4 * (k & 1) + i)) ^ sw) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 8; ++e) w[e] = v[8 * i + e];
+                st_global_v8(out + 32 * k + 8 * i, w);
             }
-            if (!(k & 1)) continue;  // two loads fill a box of f16
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(box + lane * 128 + (((uint32_t)i ^ sw) << 4)) =
-                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         }
-        __syncwarp();
-        uint8_t* to = out + 128 * (single ? k >> 1 : k);
+    } else {
+        float r = 0.f, inverse = 1.f, up = 1.f;
+        uint16_t* out = p.olat + ((size_t)head * p.R + tok) * LORA + 256 * half;
+        if (mine) r = sm.u.c1.rl[singles & 1][row];
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {  // the second only for rows whose first power of two did not fit
+            float m = 0.f;
+#pragma unroll 1
+            for (int k = pass == 0 ? -1 : 0; k < 8 && mine; ++k) {
+                uint32_t v[32];
+                tmem_ld32(k < 0 ? t_row : t_lane + 32u * (uint32_t)k, v);
+                tmem_wait_ld();
+                float m2[2] = {0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int i = 4 * j + (lane >> 3);
-            *reinterpret_cast<uint4*>(to + (size_t)(4 * j) * pitch) =
-                *reinterpret_cast<const uint4*>(box + i * 128 + (((uint32_t)(lane & 7) ^ (uint32_t)(i & 7)) << 4));
+                for (int e = 0; e < 32; ++e) m2[e & 1] = fmaxf(m2[e & 1], fabsf(__uint_as_float(v[e])));
+                m = fmaxf(m, fmaxf(m2[0], m2[1]));
+                if (k < 0) {  // the row's first entries: their largest to [2^6, 2^7)
+                    up = w_row_scale(m * r * 256.f, inverse);
+                    m = 0.f;
+                    continue;
+                }
+                const float f = r * up;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
+                    st_global_v8(out + 32 * k + 16 * i, w);
+                }
+            }
+            if (pass) break;
+            if (mine) sm.u.c1.half_max[half][row] = m;
+            named_bar(WB_OUT, 32 * W_EPI);
+            if (threadIdx.x == 0) {  // the slot of 1 / l is free again
+                mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
+                mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
+            }
+            __syncwarp();
+            if (mine) m = fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r;
+            const bool fits = !mine || m == 0.f || (m * up >= 1.f && m * up < 65504.f);
+            if (__all_sync(0xFFFFFFFFu, fits)) break;
+            if (!fits) up = w_row_scale(m, inverse);
         }
-        __syncwarp();
+        if (mine && half == 0) p.oscale[(size_t)head * p.R + tok] = inverse;
     }
     tc_fence_before();
     __syncwarp();
@@ -975,7 +996,7 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
 {
     using C = WCfg<MQ>;
     const int lane = (int)lane_id(), row = 32 * quarter + lane;
-    const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16) + 256u * (uint32_t)half;
+    const uint32_t t_row = tbase + ((32u * (uint32_t)quarter) << 16), t_lane = t_row + 256u * (uint32_t)half;
     uint32_t od = 0;
     int singles = 0;
     for (uint32_t k = 0;; ++k) {
@@ -993,7 +1014,7 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
         tc_fence_after();
         if (cmd & 2u) {
             const bool single = sm.epi_single != 0;
-            w_write_out<MQ>(sm, p, t_lane, quarter, half, singles);
+            w_write_out<MQ>(sm, p, t_row, quarter, half, singles);
             singles += single;
             continue;
         }
@@ -1057,6 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
         else if (warp == WW_PV) w_issue_pv<MQ>(sm, p, tbase);
         else if (warp < WW_CLEAR0 + 4) w_clear<MQ>(sm, p, warp);
         else if (warp == WW_PLAN) w_plan<MQ>(sm, p);
+        else if (warp == WW_EMPTY) w_empty_rows<MQ>(p);
     }
     __syncwarp();
     tc_fence_before();
@@ -1149,30 +1171,15 @@ struct WxSmem {
     int32_t abort_flag;
     uint64_t wait_ns;
     float wscale[VH];         // what undoes W_UV's powers of two
-    float rscale[2][WX_TILE]; // ... and o_lat's, by tile parity; 0: the row sees nothing
+    float rscale[2][WX_TILE]; // ... and o_lat's, by tile parity; 0: the row sees nothing, its output is 0
 };
 
 struct WxParams {
-    const int32_t *ctx_len, *pos0, *row_start;  // decode: ctx_len; chunk: pos0 and row_start
     const float* oscale;
     uint16_t* out;
     int32_t* dev_err;
-    int B, R, cap;  // R: the rows of o_lat and out (decode: B)
+    int R;  // the rows of o_lat and out
 };
-
-// Whether row r sees any token.
-__device__ __forceinline__ bool wx_valid(const WxParams& p, int r)
-{
-    if (r >= p.R) return false;
-    if (p.ctx_len) return min(p.ctx_len[r], p.cap) > 0;
-    int lo = 0, hi = p.B;  // the last slot with row_start[b] <= r
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.row_start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    return r >= p.row_start[lo] && r < p.row_start[lo + 1] && (int64_t)p.pos0[lo] + (r - p.row_start[lo]) >= 0;
-}
 
 // W_UV[h] in shared memory ([8 chunks][128 rows][128 B], 128-byte swizzle), bf16 -> f16 in place, every row times
 // the power of two that brings its largest entry to [2^14, 2^15).  Four threads a row, sixteen 16-byte pieces each,
@@ -1292,10 +1299,16 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         const int q = warp & 3, cg = warp >> 2, tid = (int)threadIdx.x, v = 32 * q + lane;
         named_bar(1, 32 * WX_EPI);  // wscale is complete
         const float ws = sm.wscale[v];
+        auto scale_of = [&](int t) {  // o_lat's power of two of row tid of tile t
+            const int r = t * WX_TILE + tid;
+            return tid < WX_TILE && r < p.R ? p.oscale[(size_t)h * p.R + r] : 0.f;
+        };
         int it = 0;
+        float next = scale_of(blockIdx.y);
         for (int t = blockIdx.y; t < tiles; t += gridDim.y, ++it) {
             const int r0 = t * WX_TILE;
-            if (tid < WX_TILE) sm.rscale[it & 1][tid] = wx_valid(p, r0 + tid) ? p.oscale[(size_t)h * p.R + r0 + tid] : 0.f;
+            if (tid < WX_TILE) sm.rscale[it & 1][tid] = next;
+            next = scale_of(t + gridDim.y);  // (a tile ahead: its latency stays off the path)
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.d_full[it & 1], (uint32_t)(it >> 1) & 1u, sm, p.dev_err));
             if (ok) {
                 tc_fence_after();
@@ -1419,8 +1432,7 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
         if (rc) return rc;
     }
     WxParams x;
-    x.ctx_len = p.ctx_len, x.pos0 = p.pos0, x.row_start = p.row_start, x.oscale = p.oscale, x.out = out, x.dev_err = p.dev_err;
-    x.B = p.B, x.R = p.R, x.cap = p.cap;
+    x.oscale = p.oscale, x.out = out, x.dev_err = p.dev_err, x.R = p.R;
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
     return launch_pdl(k3mla_window_expand_kernel, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st,
                       "k3mla_window_expand_kernel", tm_w, tm_o, x);
@@ -1446,7 +1458,7 @@ static int w_check(const char* who, const uint16_t* q_abs, const uint16_t* slab,
         set_error("%s: null or misaligned pointer", who);
         return K3MLA_E_INVALID;
     }
-    p.table = table;
+    p.q_abs = q_abs, p.table = table;
     p.n_pages = n_pages, p.n_layers = n_layers, p.layer = layer, p.max_pages = max_pages;
     p.cap = (int)std::min<long long>(std::min(max_ctx, 0x7FFFFF00), (long long)max_pages * PAGE);
     p.window = window, p.n_sink = n_sink, p.nsplit = 1;
