@@ -135,6 +135,7 @@ template <bool MQ> struct __align__(1024) WSmem {
     uint32_t epi_cmd, epi_stage;         // to the epilogue warps: bit 0 rescale O, bit 1 write it out
     int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_n0, epi_single;
     int32_t abort_flag;
+    int32_t* dev_err;
     uint64_t wait_ns;
 };
 
@@ -165,6 +166,49 @@ struct WinParams {
     int window, n_sink, split_tokens, nsplit, n_units;
     float kscale;                        // scale * log2(e) > 0
 };
+
+template <bool MQ> __device__ __forceinline__ WSmem<MQ>& w_smem()
+{
+    extern __shared__ uint8_t smem_raw[];
+    return *reinterpret_cast<WSmem<MQ>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+}
+
+// Bounded wait for a phase of one of this CTA's barriers; false after an abort or when the time runs out.  The
+// test is in line (a call where it succeeds cost a fifth of the whole kernel's time), what follows is not.
+template <bool MQ> __device__ __noinline__ bool w_wait_slow(uint32_t bar, uint32_t parity)
+{
+    WSmem<MQ>& sm = w_smem<MQ>();
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait_cluster_for(bar, parity, SUSPEND_NS)) {
+        if (aborted(sm)) return false;
+        if (globaltimer() - t0 > sm.wait_ns) {
+            *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
+            if (sm.dev_err) atomicOr(sm.dev_err, (int)K3MLA_DEV_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+template <bool MQ, bool CLUSTER = false> __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity)
+{
+    const uint32_t a = smem_u32(bar);
+    if (CLUSTER ? mbar_test_wait_cluster(a, parity) : mbar_test_wait(a, parity)) return true;
+    return w_wait_slow<MQ>(a, parity);
+}
+
+template <bool MQ> __device__ __noinline__ bool w_count_slow(const int32_t* counter, int32_t target)
+{
+    WSmem<MQ>& sm = w_smem<MQ>();
+    return wait_count(counter, target, sm, sm.dev_err);
+}
+
+// Bounded wait until a shared counter of this CTA reaches `target`.
+template <bool MQ> __device__ __forceinline__ bool w_count(const int32_t* counter, int32_t target)
+{
+    if (*reinterpret_cast<const volatile int32_t*>(counter) >= target) return true;
+    return w_count_slow<MQ>(counter, target);
+}
 
 __host__ __device__ inline int w_clamp(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
 
@@ -256,11 +300,10 @@ __device__ __forceinline__ int w_logical(const WUnit& g, int i)
 
 __device__ __forceinline__ uint64_t w_low(int k) { return k >= 64 ? ~0ull : (k <= 0 ? 0ull : (1ull << k) - 1ull); }
 
-// Which of the 64 tokens from t0 on a row with context n sees.
-__device__ __forceinline__ uint64_t w_seen(const WinParams& p, int n, int t0)
+// Which of the 64 tokens from t0 on lie below `end` and are sinks of it or not below `from`.
+__device__ __forceinline__ uint64_t w_between(const WinParams& p, int from, int end, int t0)
 {
-    const uint64_t before_n = w_low(n - t0);
-    return before_n & (w_low(min(p.n_sink, n) - t0) | ~w_low(max(0, n - p.window) - t0));
+    return w_low(end - t0) & (w_low(min(p.n_sink, end) - t0) | ~w_low(max(0, from) - t0));
 }
 
 // Whether rows with contexts n_lo .. n_hi all see the whole page at t0 (most pages: no masks to work out).
@@ -290,11 +333,13 @@ struct WLookup {
 };
 
 template <bool MQ>
-__device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank)
+__device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* dev_err)
 {
     using C = WCfg<MQ>;
     sm.wait_ns = WAIT_NS;
+    sm.dev_err = dev_err;
     sm.abort_flag = 0;
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
         mbar_init(&sm.full[i], 1);
         mbar_init(&sm.empty[i], 1);
@@ -339,9 +384,12 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
     const int lane = (int)lane_id();
     bool ok = true;
     int n = 0;
-    auto publish = [&](const WUnit& g) {
-        if (n >= 4 && lane == 0)
-            ok = wait_count(&sm.pv_units, n - 3, sm, p.dev_err) && wait_count(&sm.clear_units, 4 * (n - 6), sm, p.dev_err);
+    for (int u = (int)blockIdx.x >> 1; ok; u += (int)gridDim.x >> 1) {
+        WUnit g;
+        g.npg = -1;
+        if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0);
+        if (g.npg == 0) continue;
+        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3) && w_count<MQ>(&sm.clear_units, 4 * (n - 6));
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
         if (n > 0 && g.npg > 0 && lane < g.rows)  // its queries, into L2 (the first unit's are loaded at once)
@@ -349,28 +397,21 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
         const int slot = n % W_PLANS;
         if (lane < 2) {  // one lane a CTA
             const uint32_t at = mapa(smem_u32(&sm.plan[slot]), (uint32_t)lane);
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(&g);
+            const uint4* w = reinterpret_cast<const uint4*>(&g);
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(WUnit) / 4); ++i) st_cluster_u32(at + 4 * i, w[i]);
+            for (int i = 0; i < (int)(sizeof(WUnit) / 16); ++i) st_cluster_v4(at + 16 * i, w[i]);
             mbar_arrive_remote(mapa(smem_u32(&sm.plan_full[slot]), (uint32_t)lane));
         }
+        if (g.npg < 0) return;
         ++n;
-    };
-    for (int u = (int)blockIdx.x >> 1; u < p.n_units && ok; u += (int)gridDim.x >> 1) {
-        WUnit g;
-        w_unit<MQ>(g, p, u, lane == 0);
-        if (g.npg > 0) publish(g);
     }
-    WUnit end = {};
-    end.npg = -1;
-    publish(end);
 }
 
 // The n-th unit; npg is -1 behind the last one, and after an abort.
 template <bool MQ> __device__ __forceinline__ WUnit w_next(WSmem<MQ>& sm, const WinParams& p, int n)
 {
     WUnit g;
-    if (__all_sync(0xFFFFFFFFu, wait_bar(&sm.plan_full[n % W_PLANS], (uint32_t)(n / W_PLANS) & 1u, sm, p.dev_err, true)))
+    if (__all_sync(0xFFFFFFFFu, w_wait<MQ, true>(&sm.plan_full[n % W_PLANS], (uint32_t)(n / W_PLANS) & 1u)))
         g = sm.plan[n % W_PLANS];
     else
         g.npg = -1;
@@ -390,8 +431,8 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
     int base = 0;
     auto take = [&](int use, uint32_t bytes) -> int {  // the use's ring unit, ready to be loaded
         const int u = use % C::NUNIT, k = use / C::NUNIT;
-        if (C::NPROD > 1) ok = ok && wait_count(&sm.unit_loaded[u], k, sm, p.dev_err);
-        ok = ok && wait_bar(&sm.empty[u], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
+        if (C::NPROD > 1) ok = ok && w_count<MQ>(&sm.unit_loaded[u], k);
+        ok = ok && w_wait<MQ>(&sm.empty[u], (uint32_t)(k & 1) ^ 1u);
         if (ok) {
             if (C::NPROD > 1) *reinterpret_cast<volatile int32_t*>(&sm.unit_loaded[u]) = k + 1;
             mbar_arrive_expect_tx(&sm.full[u], bytes);
@@ -450,17 +491,17 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
         if (g.npg < 0) break;
         base += C::NQ;
         if (elect_one() && ok) {
-            ok = wait_bar(&sm.q_ready, (uint32_t)un & 1u, sm, p.dev_err);
+            ok = w_wait<MQ>(&sm.q_ready, (uint32_t)un & 1u);
             tc_fence_after();
 #pragma unroll 1
             for (int i = (r + C::NISS - gp % C::NISS) % C::NISS; i < g.npg && ok; i += C::NISS) {
                 const int sb = (gp + i) % WN_S, k = (gp + i) / WN_S;
-                ok = wait_bar(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u, sm, p.dev_err);
+                ok = w_wait<MQ>(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u);
 #pragma unroll 1
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
-                    ok = wait_count(&sm.unit_taken[u], ku, sm, p.dev_err) &&
-                         wait_bar(&sm.full[u], (uint32_t)(ku & 1), sm, p.dev_err);
+                    ok = w_count<MQ>(&sm.unit_taken[u], ku) &&
+                         w_wait<MQ>(&sm.full[u], (uint32_t)(ku & 1));
                     if (!ok) break;
                     *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = ku + 1;
                     tc_fence_after();
@@ -487,13 +528,13 @@ __device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint
     const int lane = (int)lane_id();
     const int row = MQ ? 32 * (qd & 1) + lane : C::RPQ * qd + lane;  // of a piece
     const uint32_t taddr = tbase + ((32u * (uint32_t)qd) << 16) + Q_COL;
-    if (!__all_sync(0xFFFFFFFFu, un == 0 || wait_bar(&sm.q_free, (uint32_t)(un - 1) & 1u, sm, p.dev_err))) return false;
+    if (!__all_sync(0xFFFFFFFFu, un == 0 || w_wait<MQ>(&sm.q_free, (uint32_t)(un - 1) & 1u))) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int j = 0; j < C::NQ; ++j) {
         const int u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
-        if (!__all_sync(0xFFFFFFFFu, wait_count(&sm.unit_taken[u], k, sm, p.dev_err) &&
-                                         wait_bar(&sm.full[u], (uint32_t)(k & 1), sm, p.dev_err)))
+        if (!__all_sync(0xFFFFFFFFu, w_count<MQ>(&sm.unit_taken[u], k) &&
+                                         w_wait<MQ>(&sm.full[u], (uint32_t)(k & 1))))
             return false;
 #pragma unroll 1
         for (int x = 0; x < C::QPU; ++x) {
@@ -541,9 +582,7 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     const uint32_t pfull0 = mapa(smem_u32(&sm.p_full[0]), 1);
     const float TAU2 = TAU * 1.4426950408889634f;
     uint8_t* stage = sm.u.c0.pstage[warp];
-    auto wait = [&](uint64_t* bar, int phase, bool cluster = false) {
-        return __all_sync(0xFFFFFFFFu, wait_bar(bar, (uint32_t)phase & 1u, sm, p.dev_err, cluster));
-    };
+    auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xFFFFFFFFu, w_wait<MQ>(bar, (uint32_t)phase & 1u)); };
     int base = 0, gp = 0, singles = 0;
 #pragma unroll 1
     for (int un = 0;; ++un) {
@@ -559,24 +598,29 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             const int a = gp + i, r = a % WN_S;
             if (!wait(&sm.s_full[r], a / WN_S)) return;
             tc_fence_after();
+            const uint32_t t_s = t_lane + 64u * (uint32_t)r;
+            const int t0 = PAGE * w_logical(g, i);
+            if (!w_whole(p, n, n, t0)) {  // unseen tokens' scores become -inf, in TMEM (a loop: short code, few pages)
+                const uint64_t seen = w_between(p, n - p.window, n, t0);
+#pragma unroll 1
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t y[16];
+                    tmem_ld16(t_s + 16u * (uint32_t)e, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 16; ++q)
+                        if (!((uint32_t)(seen >> (16 * e)) >> q & 1u)) y[q] = 0xFF800000u;
+                    tmem_st16(t_s + 16u * (uint32_t)e, y);
+                }
+                tmem_wait_st();
+            }
             uint32_t x[2][32];
-            tmem_ld32(t_lane + 64u * (uint32_t)r, x[0]);
-            tmem_ld32(t_lane + 64u * (uint32_t)r + 32u, x[1]);
+            tmem_ld32(t_s, x[0]);
+            tmem_ld32(t_s + 32u, x[1]);
             tmem_wait_ld();
             tc_fence_before();
             __syncwarp();
             if (l == 0) mbar_arrive(&sm.s_empty[r]);
-            const int t0 = PAGE * w_logical(g, i);
-            if (!w_whole(p, n, n, t0)) {
-                const uint64_t seen = w_seen(p, n, t0);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t bits = (uint32_t)(seen >> (32 * e));
-#pragma unroll
-                    for (int q = 0; q < 32; ++q)
-                        if (!((bits >> q) & 1u)) x[e][q] = 0xFF800000u;  // -inf
-                }
-            }
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int q = 0; q < 32; ++q)
@@ -658,11 +702,11 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             if (l == 0) mbar_arrive(&sm.fin_free[un & 1][qd]);
             if (g.single) {  // the PV CTA lands o_lat itself (a row that sees nothing has l = 0; its o_lat is not used)
                 const int sl = singles & 1;
-                if (!wait(&sm.rl_free[sl], (singles >> 1) + 1, true)) return;
+                if (!__all_sync(0xFFFFFFFFu, w_wait<MQ, true>(&sm.rl_free[sl], (uint32_t)((singles >> 1) + 1) & 1u))) return;
                 if (has_row)
                     st_async_b32(mapa(smem_u32(&sm.u.c1.rl[sl][h]), 1), __float_as_uint(1.f / ltot),
                                  mapa(smem_u32(&sm.l_full[sl]), 1));
-            } else if (has_row) {
+            } else if (!MQ && has_row) {
                 p.ws_ml[((size_t)g.b * p.nsplit + g.s) * H + h] = make_float2(m_ref, ltot);
             }
         }
@@ -673,7 +717,7 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     if (l == 0) {
         bulk_wait<0>();
         for (int a = max(0, gp - C::NPBUF); a < gp && !aborted(sm); ++a)
-            wait_bar(&sm.p_empty[a % C::NPBUF], (uint32_t)((a / C::NPBUF) & 1), sm, p.dev_err);
+            w_wait<MQ>(&sm.p_empty[a % C::NPBUF], (uint32_t)((a / C::NPBUF) & 1));
     }
 }
 
@@ -696,7 +740,7 @@ __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMa
 #pragma unroll 1
                 for (int x = 0; x < 2 && ok; ++x) {
                     const int q = (e + x) % WN_HALF;
-                    ok = wait_bar(&sm.empty[q], (uint32_t)(((e + x) / WN_HALF) & 1) ^ 1u, sm, p.dev_err);
+                    ok = w_wait<MQ>(&sm.empty[q], (uint32_t)(((e + x) / WN_HALF) & 1) ^ 1u);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&sm.full[q], SLOT1);
                     tma_load_3d_hint(sm.u.c1.ring[q], &tm_page8, 0, y + HALF * x, 0, &sm.full[q], pol);
@@ -706,20 +750,6 @@ __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMa
         }
     }
     if (!ok) drain_inflight();
-}
-
-// The tokens of a page that no row of the unit sees, and those that only some of its rows see.
-template <bool MQ>
-__device__ __forceinline__ void w_unseen(const WinParams& p, const WUnit& g, int t0, uint64_t& none, uint64_t& some)
-{
-    uint64_t any = 0, all = ~0ull;
-    for (int w = 0; w < (MQ ? g.rows : 1); ++w) {
-        const uint64_t s = w_seen(p, MQ ? w_clamp(g.n0 + w, p.cap) : g.n0, t0);
-        any |= s;
-        all &= s;
-    }
-    none = ~any;
-    some = any & ~all;
 }
 
 template <bool MQ>
@@ -739,20 +769,20 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
             for (int i = 0; i < g.npg && ok; ++i) {
                 const int a = gp + i, st = a % C::NPBUF;
                 const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
-                if (!wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) ||
-                    !wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err)) {
+                if (!w_wait<MQ>(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u) ||
+                    !w_wait<MQ>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u)) {
                     ok = false;
                     break;
                 }
                 if (!w_whole(p, n_lo, g.n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
-                    if (!wait_bar(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u, sm, p.dev_err)) {
+                    if (!w_wait<MQ>(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u)) {
                         ok = false;
                         break;
                     }
                     ++clear_k;
                 }
                 *reinterpret_cast<volatile int32_t*>(&sm.pv_seen) = a + 1;
-                if (!wait_bar(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1), sm, p.dev_err, true)) {
+                if (!w_wait<MQ, true>(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1))) {
                     ok = false;
                     break;
                 }
@@ -760,14 +790,14 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                 const volatile uint32_t* rf = reinterpret_cast<const volatile uint32_t*>(sm.u.c1.recv[st] + C::META_FLAGS);
                 const bool resc = i > 0 && (rf[0] | rf[1] | rf[2] | rf[3]) != 0u;
                 if (pending || resc) {
-                    if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+                    if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
                     pending = false;
                     if (ok && resc) {
                         umma_commit(&sm.o_done);
                         sm.epi_cmd = 1u;
                         sm.epi_stage = (uint32_t)st;
                         mbar_arrive(&sm.epi_req);
-                        ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+                        ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
                     }
                     if (!ok) break;
                 }
@@ -804,7 +834,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
         drain_inflight();
         *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
     } else if (elect_one()) {  // the epilogue warps leave
-        if (pending) ok = wait_bar(&sm.epi_done, epi_k++ & 1u, sm, p.dev_err);
+        if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
         sm.epi_cmd = 0u;
         mbar_arrive(&sm.epi_req);
     }
@@ -827,13 +857,14 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
         for (int i = 0; i < g.npg && ok; ++i) {
             const int a = gp + i, t0 = PAGE * w_logical(g, i);
             if (w_whole(p, n_lo, g.n_hi, t0)) continue;
-            uint64_t none, some;
-            w_unseen<MQ>(p, g, t0, none, some);
+            // the rows' contexts are consecutive, n_lo .. n_hi: what any and what all of them see
+            const uint64_t any = w_between(p, n_lo - p.window, g.n_hi, t0), all = w_between(p, g.n_hi - p.window, n_lo, t0);
+            const uint64_t none = ~any, some = any & ~all;
             const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
             if (lane == 0)
-                ok = wait_count(&sm.pv_seen, a - 1, sm, p.dev_err) &&
-                     wait_bar(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u, sm, p.dev_err) &&
-                     wait_bar(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u, sm, p.dev_err);
+                ok = w_count<MQ>(&sm.pv_seen, a - 1) &&
+                     w_wait<MQ>(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u) &&
+                     w_wait<MQ>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
 #pragma unroll 1
@@ -918,7 +949,7 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
 {
     using C = WCfg<MQ>;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
-    const bool single = sm.epi_single != 0;
+    const bool single = MQ || sm.epi_single != 0;
     const int lane = (int)lane_id(), row = 32 * quarter + lane;
     const uint32_t t_lane = t_row + 256u * (uint32_t)half;
     // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
@@ -1002,13 +1033,13 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
     for (uint32_t k = 0;; ++k) {
         // (an abort may reach one warp and not another: they agree on it, so that all or none pass the
         // write-out's barriers)
-        bool got = __all_sync(0xFFFFFFFFu, wait_bar(&sm.epi_req, k & 1u, sm, p.dev_err));
+        bool got = __all_sync(0xFFFFFFFFu, w_wait<MQ>(&sm.epi_req, k & 1u));
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         const uint32_t cmd = *reinterpret_cast<volatile uint32_t*>(&sm.epi_cmd);
         if (!cmd) break;
-        got = wait_bar(&sm.o_done, od++ & 1u, sm, p.dev_err);
+        got = w_wait<MQ>(&sm.o_done, od++ & 1u);
         if ((cmd & 2u) && sm.epi_single)
-            got = got && wait_bar(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u, sm, p.dev_err, true);
+            got = got && w_wait<MQ, true>(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u);
         got = __all_sync(0xFFFFFFFFu, got);
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         tc_fence_after();
@@ -1046,11 +1077,10 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
                         const __grid_constant__ CUtensorMap tm_q, const WinParams p)
 {
     using C = WCfg<MQ>;
-    extern __shared__ uint8_t smem_raw[];
-    WSmem<MQ>& sm = *reinterpret_cast<WSmem<MQ>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    WSmem<MQ>& sm = w_smem<MQ>();
     const uint32_t rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = lane_id();
     if (threadIdx.x == 0) {
-        w_init(sm, rank);
+        w_init(sm, rank, p.dev_err);
         fence_mbarrier_init_cluster();
     }
     if (warp == 4) {
