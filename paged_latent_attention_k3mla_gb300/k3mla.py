@@ -50,6 +50,8 @@ class K3mlaError(RuntimeError):
 def load(build_if_needed: bool = True):
     """Load libk3mla.so (building it first when it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -121,22 +123,33 @@ def _check(rc: int, what: str):
         raise K3mlaError(f"{what} failed with status {rc}: {msg}")
 
 
+# The current stream's handle without a Stream object (3 us a call on the GPU machine's host), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    return stream.cuda_stream
 
 
 def _dev(t: torch.Tensor, dtype, shape=None, name="tensor"):
+    """The address of a dense CUDA tensor of this dtype (and shape, a tuple).  Every call checks a dozen of them, so
+    the good case is one expression; what is wrong is worked out only when something is."""
+    try:
+        if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise K3mlaError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise K3mlaError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise K3mlaError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise K3mlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return ctypes.c_void_p(t.data_ptr())
+    raise K3mlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _opt(t, dtype, shape, name):
@@ -151,7 +164,7 @@ def _table(t: torch.Tensor, B: int):
 
 def _here(t: torch.Tensor, name: str):
     """The call runs on the current device: its tensors have to be there too."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
         raise K3mlaError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
@@ -185,11 +198,11 @@ def append_latent(slab: torch.Tensor, layer: int, block_table: torch.Tensor, pos
 
 
 def _rows(t: torch.Tensor, B: int, name: str, width: int = 0):
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != B:
+    if not t.is_cuda or t.dtype is not torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != B:
         raise K3mlaError(f"{name} must be a CUDA bf16 [B, n] tensor with unit inner stride")
     if t.shape[1] < width:
         raise K3mlaError(f"{name} has {t.shape[1]} columns, at least {width} are read")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def absorb_q_append(q: torch.Tensor, w_kv_b: torch.Tensor, q_abs: torch.Tensor, slab: torch.Tensor, layer: int,
