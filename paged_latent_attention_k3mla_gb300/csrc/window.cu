@@ -159,7 +159,8 @@ struct WinParams {
     const int32_t *pos0, *row_start;     // chunk
     uint16_t* olat;                      // [96][R][512] f16: o_lat times a power of two per row
     float* oscale;                       // [96][R]: what undoes it; 0 for rows that see nothing
-    float* ws_o;                         // [B][nsplit][96][512] f32 partials (decode, nsplit > 1)
+    uint16_t* ws_o;                      // [B][nsplit][96][512] f16: a split's O (decode, nsplit > 1) ...
+    float* ws_oscale;                    // [B][nsplit][96]: ... and what undoes its power of two
     float2* ws_ml;                       // [B][nsplit][96]: reference max (in log2 units), sum of exp
     int32_t* dev_err;
     int B, R, max_pages, n_pages, n_layers, layer, cap;  // cap: the longest context (min of max_ctx and the table)
@@ -937,9 +938,10 @@ __device__ __forceinline__ float w_row_scale(float m, float& inverse)
 }
 
 // O [rows x 512] f32 leaves TMEM, a row a thread and half the dims a warp, each lane storing whole 32-byte sectors
-// of its own row: f16 o_lat = O / l with a power of two per row when the unit is all its rows see, else the f32
-// partial.  Reading TMEM sets the pace (some 64 bytes a clock and SM: 2.1 us for a chunk's 256 KB; eight warps
-// are no faster than four, nor are bulk stores or stores of whole lines from staged boxes), so it is read once: the
+// of its own row, as f16 with a power of two per row: o_lat = O / l when the unit is all its rows see, else the
+// split's O (f32 there would take twice the stores, 32 lines each).  Reading TMEM sets the pace (some 64 bytes a
+// clock and SM: 2.1 us for a chunk's 256 KB; eight warps are no faster than four, nor are bulk stores or stores of
+// whole lines from staged boxes), so it is read once: the
 // power of two comes from the row's first 32 entries, with room for 2^8 times their largest, and the row's
 // largest entry is found on the way.  A row that it shows to have left the range, or to lie far below it, has its
 // warps go over their rows again with the power of two that fits.
@@ -955,67 +957,52 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
     // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
     const bool mine = MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : row < C::ROWS;  // (and the row sees something)
     const int tok = MQ ? row0 + quarter : b, head = (MQ ? 32 * hb : 32 * quarter) + lane;
-    if (!single) {
-        float* out = p.ws_o + (((size_t)b * p.nsplit + s) * H + head) * LORA + 256 * half;
+    float r = 1.f, inverse = 1.f, up = 1.f;
+    // o_lat [96][R][512], or partial O [B][nsplit][96][512]; a scale each
+    const size_t at = single ? (size_t)head * p.R + tok : ((size_t)b * p.nsplit + s) * H + head;
+    uint16_t* out = (single ? p.olat : p.ws_o) + at * LORA + 256 * half;
+    if (mine && single) r = sm.u.c1.rl[singles & 1][row];
 #pragma unroll 1
-        for (int k = 0; k < 8 && mine; ++k) {
+    for (int pass = 0; pass < 2; ++pass) {  // the second only for rows whose first power of two did not fit
+        float m = 0.f;
+#pragma unroll 1
+        for (int k = pass == 0 ? -1 : 0; k < 8 && mine; ++k) {
             uint32_t v[32];
-            tmem_ld32(t_lane + 32u * (uint32_t)k, v);
+            tmem_ld32(k < 0 ? t_row : t_lane + 32u * (uint32_t)k, v);
             tmem_wait_ld();
+            float m2[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int e = 0; e < 32; ++e) m2[e & 1] = fmaxf(m2[e & 1], fabsf(__uint_as_float(v[e])));
+            m = fmaxf(m, fmaxf(m2[0], m2[1]));
+            if (k < 0) {  // the row's first entries: their largest to [2^6, 2^7)
+                up = w_row_scale(m * r * 256.f, inverse);
+                m = 0.f;
+                continue;
+            }
+            const float f = r * up;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = v[8 * i + e];
-                st_global_v8(out + 32 * k + 8 * i, w);
+                for (int e = 0; e < 8; ++e)
+                    w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
+                st_global_v8(out + 32 * k + 16 * i, w);
             }
         }
-    } else {
-        float r = 0.f, inverse = 1.f, up = 1.f;
-        uint16_t* out = p.olat + ((size_t)head * p.R + tok) * LORA + 256 * half;
-        if (mine) r = sm.u.c1.rl[singles & 1][row];
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {  // the second only for rows whose first power of two did not fit
-            float m = 0.f;
-#pragma unroll 1
-            for (int k = pass == 0 ? -1 : 0; k < 8 && mine; ++k) {
-                uint32_t v[32];
-                tmem_ld32(k < 0 ? t_row : t_lane + 32u * (uint32_t)k, v);
-                tmem_wait_ld();
-                float m2[2] = {0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 32; ++e) m2[e & 1] = fmaxf(m2[e & 1], fabsf(__uint_as_float(v[e])));
-                m = fmaxf(m, fmaxf(m2[0], m2[1]));
-                if (k < 0) {  // the row's first entries: their largest to [2^6, 2^7)
-                    up = w_row_scale(m * r * 256.f, inverse);
-                    m = 0.f;
-                    continue;
-                }
-                const float f = r * up;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
-                    st_global_v8(out + 32 * k + 16 * i, w);
-                }
-            }
-            if (pass) break;
-            if (mine) sm.u.c1.half_max[half][row] = m;
-            named_bar(WB_OUT, 32 * W_EPI);
-            if (threadIdx.x == 0) {  // the slot of 1 / l is free again
-                mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
-                mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
-            }
-            __syncwarp();
-            if (mine) m = fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r;
-            const bool fits = !mine || m == 0.f || (m * up >= 1.f && m * up < 65504.f);
-            if (__all_sync(0xFFFFFFFFu, fits)) break;
-            if (!fits) up = w_row_scale(m, inverse);
+        if (pass) break;
+        if (mine) sm.u.c1.half_max[half][row] = m;
+        named_bar(WB_OUT, 32 * W_EPI);
+        if (single && threadIdx.x == 0) {  // the slot of 1 / l is free again
+            mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
+            mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
         }
-        if (mine && half == 0) p.oscale[(size_t)head * p.R + tok] = inverse;
+        __syncwarp();
+        if (mine) m = fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r;
+        const bool fits = !mine || m == 0.f || (m * up >= 1.f && m * up < 65504.f);
+        if (__all_sync(0xFFFFFFFFu, fits)) break;
+        if (!fits) up = w_row_scale(m, inverse);
     }
+    if (mine && half == 0) (single ? p.oscale : p.ws_oscale)[at] = inverse;
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.epi_done);
@@ -1120,15 +1107,16 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
 // ---- merge of splits (decode) ---------------------------------------------------------------
 
 constexpr int WM_GROUPS = 4;
-constexpr int WM_THREADS = 128 * WM_GROUPS;
 
-// A row (slot, head) per CTA: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max), four dims a thread and
-// every fourth split a group of 128 threads, so that a long list of splits is a few loads deep; the groups
-// are added as (g0 + g1) + (g2 + g3).  The order depends on the slot's own splits only.
-__global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const WinParams p)
+// A row (slot, head) per CTA: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max), four dims a thread.
+// Split i belongs to group i mod 4; the groups' sums, each over ascending i, are added as (g0 + g1) + (g2 + g3), so
+// that the bits depend on the slot's own splits only.  G = 1: 128 threads, each with all four groups; G = 4: 512
+// threads, one group each, for long lists (a few loads deep instead of eight and more).
+template <int G> __global__ void __launch_bounds__(128 * G) k3mla_window_merge_kernel(const WinParams p)
 {
-    __shared__ float4 sum[WM_GROUPS][128];
-    __shared__ float sl[WM_GROUPS], smax[4];
+    constexpr int PER = WM_GROUPS / G;  // groups a thread
+    __shared__ float4 sum[G][128];
+    __shared__ float sl[G], smax[4];
     const int h = blockIdx.x, b = blockIdx.y, d = 4 * ((int)threadIdx.x & 127), g = (int)threadIdx.x >> 7;
     griddep_wait();
     griddep_launch_dependents();
@@ -1137,35 +1125,60 @@ __global__ void __launch_bounds__(WM_THREADS) k3mla_window_merge_kernel(const Wi
     const int all = w_pages(n, n, p.window, p.n_sink, nsp, wp0);
     const int per = slot_split(all * PAGE, p.split_tokens) / PAGE, ns = (all + per - 1) / per;
     if (ns <= 1) return;  // landed by the split itself
-    const float2* ml = p.ws_ml + (size_t)b * p.nsplit * H + h;
-    const float* o = p.ws_o + ((size_t)b * p.nsplit * H + h) * LORA + d;
+    const size_t row = (size_t)b * p.nsplit * H + h;
+    const float2* ml = p.ws_ml + row;
     float m = -INFINITY;
     for (int i = (int)lane_id(); i < ns; i += 32) m = fmaxf(m, ml[(size_t)i * H].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = g; i < ns; i += WM_GROUPS) {
-        const float2 rec = ml[(size_t)i * H];
-        const float4 v = *reinterpret_cast<const float4*>(o + (size_t)i * H * LORA);
-        const float w = ex2_approx(rec.x - m);
-        l = fmaf(w, rec.y, l);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    float l[PER];
+    float4 part[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        l[k] = 0.f;
+        part[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    sum[g][threadIdx.x & 127] = acc;
-    if (d == 0) sl[g] = l;
-    __syncthreads();
-    if (g > 0) return;
-    const float r = 1.f / ((sl[0] + sl[1]) + (sl[2] + sl[3]));
-    const float4 s1 = sum[1][threadIdx.x], s2 = sum[2][threadIdx.x], s3 = sum[3][threadIdx.x];
-    acc.x = ((acc.x + s1.x) + (s2.x + s3.x)) * r;
-    acc.y = ((acc.y + s1.y) + (s2.y + s3.y)) * r;
-    acc.z = ((acc.z + s1.z) + (s2.z + s3.z)) * r;
-    acc.w = ((acc.w + s1.w) + (s2.w + s3.w)) * r;
+#pragma unroll 2
+    for (int i0 = 0; i0 < ns; i0 += WM_GROUPS)
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const int i = i0 + (G == 1 ? k : g);
+            if (i >= ns) continue;
+            const size_t at = row + (size_t)i * H;
+            const float2 rec = p.ws_ml[at];
+            const uint2 v = *reinterpret_cast<const uint2*>(p.ws_o + at * LORA + d);
+            const float w = ex2_approx(rec.x - m), f = w * p.ws_oscale[at];
+            float x0, x1, x2, x3;
+            f16x2_parts(v.x, x0, x1);
+            f16x2_parts(v.y, x2, x3);
+            l[k] = fmaf(w, rec.y, l[k]);
+            part[k].x = fmaf(f, x0, part[k].x);
+            part[k].y = fmaf(f, x1, part[k].y);
+            part[k].z = fmaf(f, x2, part[k].z);
+            part[k].w = fmaf(f, x3, part[k].w);
+        }
+    float4 acc;
+    float ltot;
+    if constexpr (G == 1) {
+        acc.x = (part[0].x + part[1].x) + (part[2].x + part[3].x);
+        acc.y = (part[0].y + part[1].y) + (part[2].y + part[3].y);
+        acc.z = (part[0].z + part[1].z) + (part[2].z + part[3].z);
+        acc.w = (part[0].w + part[1].w) + (part[2].w + part[3].w);
+        ltot = (l[0] + l[1]) + (l[2] + l[3]);
+    } else {
+        sum[g][threadIdx.x & 127] = part[0];
+        if (d == 0) sl[g] = l[0];
+        __syncthreads();
+        if (g > 0) return;
+        const float4 s1 = sum[1][threadIdx.x], s2 = sum[2][threadIdx.x], s3 = sum[3][threadIdx.x];
+        acc.x = (part[0].x + s1.x) + (s2.x + s3.x);
+        acc.y = (part[0].y + s1.y) + (s2.y + s3.y);
+        acc.z = (part[0].z + s1.z) + (s2.z + s3.z);
+        acc.w = (part[0].w + s1.w) + (s2.w + s3.w);
+        ltot = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+    }
+    const float r = 1.f / ltot;
+    acc.x *= r, acc.y *= r, acc.z *= r, acc.w *= r;
     float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
@@ -1394,7 +1407,7 @@ static int w_nsplit(int cap, int window, int n_sink, int split_tokens)
 }
 
 struct WinWs {
-    size_t olat, scale, o, ml, total;
+    size_t olat, scale, o, oscale, ml, total;
 };
 static WinWs w_layout(long long rows, int nsplit)
 {
@@ -1402,8 +1415,10 @@ static WinWs w_layout(long long rows, int nsplit)
     w.olat = 0;
     w.scale = w_up((size_t)rows * H * LORA * 2);
     w.o = w.scale + w_up((size_t)rows * H * 4);
-    w.ml = w.o + (nsplit > 1 ? w_up((size_t)rows * nsplit * H * LORA * 4) : 0);
-    w.total = w.ml + (nsplit > 1 ? w_up((size_t)rows * nsplit * H * 8) : 0);
+    const size_t records = nsplit > 1 ? (size_t)rows * nsplit * H : 0;
+    w.oscale = w.o + w_up(records * LORA * 2);
+    w.ml = w.oscale + w_up(records * 4);
+    w.total = w.ml + w_up(records * 8);
     return w;
 }
 
@@ -1431,7 +1446,8 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     using C = WCfg<MQ>;
     p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
     p.oscale = reinterpret_cast<float*>(ws + wl.scale);
-    p.ws_o = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.o) : nullptr;
+    p.ws_o = p.nsplit > 1 ? reinterpret_cast<uint16_t*>(ws + wl.o) : nullptr;
+    p.ws_oscale = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.oscale) : nullptr;
     p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
     CUtensorMap tm_page, tm_page8, tm_q, tm_w, tm_o;
     const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
@@ -1458,7 +1474,9 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                     tm_page8, tm_q, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
-        rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(WM_THREADS), 0, st, "k3mla_window_merge_kernel", p);
+        const bool longer = p.nsplit > 8;
+        rc = launch_pdl(longer ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
+                        dim3(longer ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
     }
     WxParams x;

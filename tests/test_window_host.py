@@ -178,7 +178,8 @@ def test_window_workspaces():
         pages = min(-(-max_ctx // 64), -(-min(s, max_ctx) // 64) + (min(w, max_ctx) + 62) // 64 + 1)
         ns = -(-pages * 64 // (split or 4096))
         o_lat = r256(96 * B * 512 * 2) + r256(96 * B * 4)         # f16 rows and a scale each
-        partial = 0 if ns == 1 else r256(B * ns * 96 * 512 * 4) + r256(B * ns * 96 * 8)
+        rec = B * ns * 96                                       # f16 rows, a scale each, two f32 each
+        partial = 0 if ns == 1 else r256(rec * 512 * 2) + r256(rec * 4) + r256(rec * 8)
         assert k3mla.window_decode_workspace_bytes(B, max_ctx, w, s, split) == o_lat + partial
     assert k3mla.window_chunk_decode_workspace_bytes(2, 37, 1000) == r256(96 * 37 * 512 * 2) + r256(96 * 37 * 4)
     for bad in ((0, 1, 1, 0, 0), (1, 0, 1, 0, 0), (1, 1, 0, 0, 0), (1, 1, 1, -1, 0), (1, 1, 1, 0, 64)):

@@ -91,8 +91,9 @@ def out_tolerance(out, o, p, rows, w_kv_b, s_abs):
     """Bound of |kernel - reference| for one token row, element by element.
 
     The kernel's roundings: every p to bf16 (relative 2^-8), o_lat to f16 after a power of two that brings its
-    row's largest entry to 2^14 or more (2^-11 / 2 of the entry, or half a subnormal step, 2^-25, which is
-    2^-39 of the row's largest: both within 2^-12 |o| + 2^-38 max|o|), the output to bf16 (2^-8), f32 sums besides: each score within 640 * 2^-24 of sum |q||row| * scale
+    row's largest entry to 1 or more (2^-11 / 2 of the entry, or half a subnormal step, 2^-25, which is at most
+    2^-25 of the row's largest), the O of each split likewise when there are several (so sum_t p_t |row_t| and the
+    largest of it stand for |o|, and both count twice), the output to bf16 (2^-8), f32 sums besides: each score within 640 * 2^-24 of sum |q||row| * scale
     (s_abs, per head and token: its exponential moves by as much), the hardware exponential 2^-21, the sums over
     tokens and latent entries 2^-15 in all.  A p that is off by a factor (1 + d_t) moves o by
     sum_t p_t d_t (row_t - o): at most max|d| * sum_t p_t |row_t - o|, here taken through |W_UV|."""
@@ -102,5 +103,5 @@ def out_tolerance(out, o, p, rows, w_kv_b, s_abs):
     d = 2.0 ** -8 + 2.0 ** -19 + 640 * 2.0 ** -24 * s_abs                      # [96, T]
     spread = np.einsum("ht,tk->hk", p * d, np.abs(rows[:, :LORA])) + np.einsum("ht,hk->hk", p * d, np.abs(o))
     mass = np.einsum("ht,tk->hk", p, np.abs(rows[:, :LORA]))
-    half = 2.0 ** -12 * np.abs(o) + 2.0 ** -38 * np.abs(o).max(-1, keepdims=True)
+    half = 2 * (2.0 ** -12 * mass + 2.0 ** -25 * mass.max(-1, keepdims=True))
     return (np.einsum("hvk,hk->hv", w, spread + half + 2.0 ** -15 * mass) + 2.0 ** -8 * np.abs(out)) * 1.01 + 1e-30
