@@ -30,12 +30,11 @@
 //     (the first of them copies Q into TMEM when the last MMA of the unit before has read the old one).
 //   * PV CTA: a producer streams the pages' latents again (mostly from L2) as half pages; one thread issues
 //     O[rows x 512] += P . C; eight warps rescale O when a reference moved and, at a unit's end, take O out of
-//     TMEM; four warps clear what a page holds of unseen tokens;
+//     TMEM; four warps look unseen tokens through;
 //     one plans the units of both CTAs ahead.
-//   * Unseen tokens.  Their scores are replaced (never multiplied), and in the pages that hold some their
-//     latents are cleared in shared memory, because p = 0 times a NaN or infinity there would still be
-//     NaN.  In a chunk a token may be seen by some rows of the unit only; then just its NaNs and
-//     infinities are cleared: the rows that see it already got NaN from its score.
+//   * Unseen tokens.  Their scores are replaced (never multiplied), and in the pages that hold some, NaNs and
+//     infinities among their latents become zero in shared memory, because p = 0 times one of those would still be
+//     NaN.  In a chunk a token may be seen by some rows of the unit only: those get their NaN from its score.
 //
 // Every wait is bounded, as in decode.cu: after WAIT_NS it sets K3MLA_DEV_TIMEOUT and the roles run out.
 #include <cuda.h>
@@ -79,7 +78,7 @@ template <bool MQ> struct WCfg {
 constexpr int WN_S = 3;        // S buffers, one MMA issuer each
 constexpr int WN_HALF = 5;     // PV CTA: half-page slots
 constexpr int W_THREADS = 512;  // 128 registers a thread
-// PV CTA: the producer, the MMA issuer, four warps that clear unseen tokens, eight of the epilogue (0-3 and 10-13: a
+// PV CTA: the producer, the MMA issuer, four warps that look unseen tokens through, eight of the epilogue (0-3 and 10-13: a
 // warp reads the TMEM lanes of its own quarter), one that plans the units of both CTAs, one
 // for the rows that see nothing
 constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6, WW_EPI1 = 10, WW_PLAN = 14, WW_EMPTY = 15;
@@ -841,8 +840,8 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
     }
 }
 
-// Warps WW_CLEAR0 .. +3: in every page that not all rows of the unit see whole, the latents of tokens that no
-// row sees become zero, and so do the NaNs and infinities of those that only some rows see.  They run ahead of
+// Warps WW_CLEAR0 .. +3: in every page that not all rows of the unit see whole, the NaNs and infinities among
+// the latents of tokens that not all rows see become zero.  They run ahead of
 // the MMA issuer by up to two pages: page a is taken up once the issuer is past the waits of page a - 2, so
 // that neither the parity of a half-page slot's barrier (used again every two to three pages) nor that of the
 // two barriers they answer on in turn can be mistaken.
@@ -858,9 +857,8 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
         for (int i = 0; i < g.npg && ok; ++i) {
             const int a = gp + i, t0 = PAGE * w_logical(g, i);
             if (w_whole(p, n_lo, g.n_hi, t0)) continue;
-            // the rows' contexts are consecutive, n_lo .. n_hi: what any and what all of them see
-            const uint64_t any = w_between(p, n_lo - p.window, g.n_hi, t0), all = w_between(p, g.n_hi - p.window, n_lo, t0);
-            const uint64_t none = ~any, some = any & ~all;
+            // the rows' contexts are consecutive, n_lo .. n_hi: the tokens that not all of them see
+            const uint64_t hidden = ~w_between(p, g.n_hi - p.window, n_lo, t0);
             const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
             if (lane == 0)
                 ok = w_count<MQ>(&sm.pv_seen, a - 1) &&
@@ -868,17 +866,27 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
                      w_wait<MQ>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
+            // a warp a token: 64 pieces of 16 bytes, two a lane.  First only looked through: p = 0 times anything finite
+            // is 0 as it stands, and without a store there is no proxy fence to wait for (up to 1.5 us beside the MMAs).
+            uint64_t mine = 0;  // this warp's tokens that hold a NaN or an infinity somewhere
+#pragma unroll 4
+            for (int t = w; t < PAGE; t += 4) {
+                if (!(hidden >> t & 1ull)) continue;
+                const uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
+                const uint4 v0 = *reinterpret_cast<const uint4*>(at + (lane >> 3) * HCHUNK);
+                const uint4 v1 = *reinterpret_cast<const uint4*>(at + ((lane >> 3) + 4) * HCHUNK);
+                uint32_t m = __vmaxu2(__vmaxu2(v0.x & 0x7FFF7FFFu, v0.y & 0x7FFF7FFFu), __vmaxu2(v0.z & 0x7FFF7FFFu, v0.w & 0x7FFF7FFFu));
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v1.x & 0x7FFF7FFFu, v1.y & 0x7FFF7FFFu), __vmaxu2(v1.z & 0x7FFF7FFFu, v1.w & 0x7FFF7FFFu)));
+                if ((m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u) mine |= 1ull << t;
+            }
+            if (__any_sync(0xFFFFFFFFu, mine != 0)) {
 #pragma unroll 1
-            for (int t = w; t < PAGE; t += 4) {  // a warp a token: 64 pieces of 16 bytes, two a lane
-                const bool no = none >> t & 1ull;
-                if (!no && !(some >> t & 1ull)) continue;
-                uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
-                    if (no) {
-                        *piece = make_uint4(0u, 0u, 0u, 0u);
-                    } else {
+                for (int t = w; t < PAGE; t += 4) {
+                    if (!__any_sync(0xFFFFFFFFu, mine >> t & 1ull)) continue;
+                    uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
+#pragma unroll 1
+                    for (int x = 0; x < 2; ++x) {
+                        uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
                         uint4 v = *piece;
                         auto finite = [](uint32_t b) {  // bf16 with all exponent bits set: NaN or infinity
                             if ((b & 0x7F80u) == 0x7F80u) b &= 0xFFFF0000u;
@@ -889,9 +897,9 @@ template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const 
                         *piece = v;
                     }
                 }
+                fence_proxy_async_cta();
+                __syncwarp();
             }
-            fence_proxy_async_cta();
-            __syncwarp();
             if (lane == 0) mbar_arrive(&sm.clear_done[done & 1]);
             ++done;
         }
@@ -965,28 +973,43 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {  // the second only for rows whose first power of two did not fit
         float m = 0.f;
-#pragma unroll 1
-        for (int k = pass == 0 ? -1 : 0; k < 8 && mine; ++k) {
-            uint32_t v[32];
-            tmem_ld32(k < 0 ? t_row : t_lane + 32u * (uint32_t)k, v);
-            tmem_wait_ld();
-            float m2[2] = {0.f, 0.f};
+        auto largest = [&](const uint32_t (&v)[32]) {
+            float m2[2] = {m, 0.f};
 #pragma unroll
             for (int e = 0; e < 32; ++e) m2[e & 1] = fmaxf(m2[e & 1], fabsf(__uint_as_float(v[e])));
-            m = fmaxf(m, fmaxf(m2[0], m2[1]));
-            if (k < 0) {  // the row's first entries: their largest to [2^6, 2^7)
+            m = fmaxf(m2[0], m2[1]);
+        };
+        if (mine) {
+            uint32_t v[32];
+            if (pass == 0) {  // the row's first entries: their largest to [2^6, 2^7)
+                tmem_ld32(t_row, v);
+                tmem_wait_ld();
+                largest(v);
                 up = w_row_scale(m * r * 256.f, inverse);
                 m = 0.f;
-                continue;
             }
             const float f = r * up;
+            tmem_ld32(t_lane, v);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int k = 0; k < 8; ++k) {
+                uint32_t next[32];  // on its way while this piece is turned
+                tmem_ld32(t_lane + 32u * (uint32_t)min(k + 1, 7), next);
+                largest(v);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t w[8];
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
-                st_global_v8(out + 32 * k + 16 * i, w);
+                    for (int e = 0; e < 8; ++e)
+                        w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
+                    st_global_v8(out + 32 * k + 16 * i, w);
+                }
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    asm volatile("" : "+r"(next[e]));  // (not read before the wait)
+                    v[e] = next[e];
+                }
             }
         }
         if (pass) break;
