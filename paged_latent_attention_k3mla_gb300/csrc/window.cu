@@ -66,25 +66,26 @@ template <bool MQ> struct WCfg {
     static constexpr int NPAR = MQ ? 3 : 2;              // score CTA: softmax warps of a quarter, a page each in turn
     static constexpr int W_PROD = 4 * NPAR;              // ... behind them the producers ...
     static constexpr int W_MMA0 = W_PROD + NPROD;        // ... and three MMA issuers
-    static constexpr int NISS = MQ ? 3 : 3;
+    static constexpr int NISS = 3;
     static_assert(W_MMA0 + NISS <= 16, "the warps of a CTA");
     static constexpr int PSTAGE = RPQ * 128;             // score CTA: one softmax warp's P rows (x 64 tokens)
     static constexpr int PT_BYTES = ROWS * 128;          // P [rows][64 tokens] bf16, K-major, 128-byte swizzle
     static constexpr int META_ALPHA = PT_BYTES;          // f32 alpha[rows]
-    static constexpr int META_FLAGS = PT_BYTES + 4 * ROWS;     // u32 flags[4]: "some row of quarter w rescaled"
+    static constexpr int META_FLAGS = PT_BYTES + 4 * ROWS;     // u32 flags[4], a quarter each: F_RESCALE, F_NOT_FINITE
     static constexpr int PCOPY = PT_BYTES + 4 * ROWS + 16;     // bytes sent per page
     static constexpr int PBUF = (PCOPY + 1023) / 1024 * 1024;  // buffer pitch
 };
 constexpr int WN_S = 3;        // S buffers, one MMA issuer each
 constexpr int WN_HALF = 5;     // PV CTA: half-page slots
 constexpr int W_THREADS = 512;  // 128 registers a thread
-// PV CTA: the producer, the MMA issuer, four warps that look unseen tokens through, eight of the epilogue (0-3 and 10-13: a
-// warp reads the TMEM lanes of its own quarter), one that plans the units of both CTAs, one
-// for the rows that see nothing
-constexpr int WW_HALVES = 4, WW_PV = 5, WW_CLEAR0 = 6, WW_EPI1 = 10, WW_PLAN = 14, WW_EMPTY = 15;
+// PV CTA: the producer, the MMA issuer, eight warps of the epilogue (0-3 and 6-9: a warp reads the TMEM lanes of its own
+// quarter), one that plans the units of both CTAs, one for the rows that see nothing
+constexpr int WW_HALVES = 4, WW_PV = 5, WW_EPI1 = 6, WW_PLAN = 10, WW_EMPTY = 11;
 constexpr int W_PLANS = 8;         // planned units kept
 constexpr uint32_t WB_OUT = 1;     // named barrier of the epilogue warps
 constexpr int W_EPI = 8;
+constexpr uint32_t F_RESCALE = 1, F_NOT_FINITE = 2;  // a row's reference moved / an unseen token's score is not finite
+constexpr uint32_t E_RESCALE = 1, E_WRITE = 2, E_CLEAR = 4;  // what the epilogue warps are asked for
 
 // A unit: which rows, which pages.
 struct __align__(16) WUnit {
@@ -116,7 +117,7 @@ template <bool MQ> struct __align__(1024) WSmem {
     uint64_t s_full[WN_S], s_empty[WN_S];
     uint64_t q_free, q_ready;            // Q of the unit before is no longer read / Q of this unit is in TMEM
     uint64_t p_full[C::NPBUF], p_empty[C::NPBUF];
-    uint64_t o_done, epi_req, epi_done, clear_done[2];
+    uint64_t o_done, epi_req, epi_done;
     uint64_t l_full[2], rl_free[2];      // PV CTA's rl, by parity of the unit
     uint64_t hand[4][C::NPAR];           // a quarter's decision on a page, by turn
     uint64_t fin_full[2][4], fin_free[2][4];  // a quarter's sums of exp, by parity of the unit
@@ -128,10 +129,11 @@ template <bool MQ> struct __align__(1024) WSmem {
     int32_t copied[C::NUNIT];            // quarters that have copied their rows of the Q chunk in a ring unit
     WUnit plan[W_PLANS];                 // the units, in order
     uint64_t plan_full[W_PLANS];
-    int32_t pv_units, clear_units;       // PV CTA: units whose MMAs have been issued / that a clearing warp has left
-    int32_t pv_seen;                     // PV CTA: pages whose latents the MMA issuer has seen arrive and cleared
+    int32_t pv_units;                    // PV CTA: units whose MMAs have been issued
     uint32_t tmem_base;
-    uint32_t epi_cmd, epi_stage;         // to the epilogue warps: bit 0 rescale O, bit 1 write it out
+    uint64_t epi_hidden;                 // to the epilogue warps: the tokens of page epi_page that not all rows see
+    uint32_t epi_cmd;                    // ... and what to do, E_ bits
+    int32_t epi_page;
     int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_n0, epi_single;
     int32_t abort_flag;
     int32_t* dev_err;
@@ -358,7 +360,6 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* de
     mbar_init(&sm.o_done, 1);
     mbar_init(&sm.epi_req, 1);
     mbar_init(&sm.epi_done, W_EPI);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.clear_done[i], 4);
     for (int i = 0; i < 2; ++i) {
         mbar_init(&sm.l_full[i], 1);
         mbar_init(&sm.rl_free[i], 1);
@@ -369,7 +370,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* de
     }
     for (int i = 0; i < C::NUNIT; ++i) sm.unit_loaded[i] = sm.unit_taken[i] = sm.copied[i] = 0;
     for (int i = 0; i < W_PLANS; ++i) mbar_init(&sm.plan_full[i], 1);
-    sm.pv_seen = sm.pv_units = sm.clear_units = 0;
+    sm.pv_units = 0;
     if (rank == 1) {  // expected before anything is sent
         for (int i = 0; i < C::NPBUF; ++i) mbar_arrive_expect_tx(&sm.p_full[i], C::PCOPY);
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.l_full[i], 4 * C::ROWS);
@@ -389,7 +390,7 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
         g.npg = -1;
         if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0);
         if (g.npg == 0) continue;
-        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3) && w_count<MQ>(&sm.clear_units, 4 * (n - 6));
+        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
         if (n > 0 && g.npg > 0 && lane < g.rows)  // its queries, into L2 (the first unit's are loaded at once)
@@ -600,8 +601,13 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             tc_fence_after();
             const uint32_t t_s = t_lane + 64u * (uint32_t)r;
             const int t0 = PAGE * w_logical(g, i);
-            if (!w_whole(p, n, n, t0)) {  // unseen tokens' scores become -inf, in TMEM (a loop: short code, few pages)
+            // Unseen tokens' scores become -inf, in TMEM (a loop: short code, few pages).  Where all of them are finite, so
+            // are the tokens' latents (a NaN or an infinity times anything, 0 too, stays one in the sum), and p = 0 times
+            // those is 0: the PV CTA takes the page as it is.
+            uint32_t flags = 0;
+            if (!w_whole(p, n, n, t0)) {
                 const uint64_t seen = w_between(p, n - p.window, n, t0);
+                uint32_t most = 0;
 #pragma unroll 1
                 for (int e = 0; e < 4; ++e) {
                     uint32_t y[16];
@@ -609,10 +615,14 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
                     tmem_wait_ld();
 #pragma unroll
                     for (int q = 0; q < 16; ++q)
-                        if (!((uint32_t)(seen >> (16 * e)) >> q & 1u)) y[q] = 0xFF800000u;
+                        if (!((uint32_t)(seen >> (16 * e)) >> q & 1u)) {
+                            most = max(most, y[q] & 0x7FFFFFFFu);
+                            y[q] = 0xFF800000u;
+                        }
                     tmem_st16(t_s + 16u * (uint32_t)e, y);
                 }
                 tmem_wait_st();
+                if (__any_sync(0xFFFFFFFFu, has_row && most >= 0x7F800000u)) flags = F_NOT_FINITE;
             }
             uint32_t x[2][32];
             tmem_ld32(t_s, x[0]);
@@ -671,11 +681,11 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             if (!wait(&sm.p_empty[st], a / C::NPBUF + 1)) return;
             const uint32_t dst = recv0 + (uint32_t)(st * C::PBUF);
             const uint32_t bar = pfull0 + (uint32_t)(st * sizeof(uint64_t));
-            const uint32_t any = __ballot_sync(0xFFFFFFFFu, resc && has_row);
+            if (__any_sync(0xFFFFFFFFu, resc && has_row)) flags |= F_RESCALE;
             if (l == 0) {
                 bulk_copy_to_cluster(dst + (uint32_t)(qd * C::PSTAGE), stage, C::PSTAGE, bar);
                 bulk_commit();
-                st_async_b32(dst + C::META_FLAGS + 4 * qd, any ? 1u : 0u, bar);
+                st_async_b32(dst + C::META_FLAGS + 4 * qd, flags, bar);
             }
             if (has_row) st_async_b32(dst + C::META_ALPHA + 4 * h, __float_as_uint(alpha), bar);
         }
@@ -758,7 +768,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
     using C = WCfg<MQ>;
     // (elect_one() names the same lane every time: pending and the two counters are that lane's)
     bool ok = true, pending = false;  // pending: the epilogue has not yet taken the unit before out of TMEM
-    uint32_t epi_k = 0, clear_k = 0;
+    uint32_t epi_k = 0;
     int gp = 0;
     for (int un = 0;; ++un) {
         const WUnit g = w_next<MQ>(sm, p, un);
@@ -774,28 +784,24 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                     ok = false;
                     break;
                 }
-                if (!w_whole(p, n_lo, g.n_hi, PAGE * w_logical(g, i))) {  // its unseen tokens are cleared
-                    if (!w_wait<MQ>(&sm.clear_done[clear_k & 1u], clear_k >> 1 & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    ++clear_k;
-                }
-                *reinterpret_cast<volatile int32_t*>(&sm.pv_seen) = a + 1;
                 if (!w_wait<MQ, true>(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1))) {
                     ok = false;
                     break;
                 }
                 fence_proxy_async_cta();  // the P tile came through DSMEM copies; the MMA reads it
                 const volatile uint32_t* rf = reinterpret_cast<const volatile uint32_t*>(sm.u.c1.recv[st] + C::META_FLAGS);
-                const bool resc = i > 0 && (rf[0] | rf[1] | rf[2] | rf[3]) != 0u;
-                if (pending || resc) {
+                const uint32_t flags = rf[0] | rf[1] | rf[2] | rf[3];
+                uint32_t cmd = (flags & F_NOT_FINITE) ? E_CLEAR : 0u;
+                if (i > 0 && (flags & F_RESCALE)) cmd |= E_RESCALE;
+                if (pending || cmd) {
                     if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
                     pending = false;
-                    if (ok && resc) {
-                        umma_commit(&sm.o_done);
-                        sm.epi_cmd = 1u;
-                        sm.epi_stage = (uint32_t)st;
+                    if (ok && cmd) {
+                        if (cmd & E_RESCALE) umma_commit(&sm.o_done);
+                        sm.epi_cmd = cmd;
+                        sm.epi_page = a;
+                        // the rows' contexts are consecutive, n_lo .. n_hi: the tokens that not all of them see
+                        sm.epi_hidden = ~w_between(p, g.n_hi - p.window, n_lo, PAGE * w_logical(g, i));
                         mbar_arrive(&sm.epi_req);
                         ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
                     }
@@ -814,7 +820,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
             }
             if (ok) {  // O of the unit is complete: to be written out
                 umma_commit(&sm.o_done);
-                sm.epi_cmd = 2u;
+                sm.epi_cmd = E_WRITE;
                 sm.epi_b = g.b;
                 sm.epi_s = g.s;
                 sm.epi_hb = g.hb;
@@ -837,74 +843,6 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
         if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
         sm.epi_cmd = 0u;
         mbar_arrive(&sm.epi_req);
-    }
-}
-
-// Warps WW_CLEAR0 .. +3: in every page that not all rows of the unit see whole, the NaNs and infinities among
-// the latents of tokens that not all rows see become zero.  They run ahead of
-// the MMA issuer by up to two pages: page a is taken up once the issuer is past the waits of page a - 2, so
-// that neither the parity of a half-page slot's barrier (used again every two to three pages) nor that of the
-// two barriers they answer on in turn can be mistaken.
-template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, uint32_t warp)
-{
-    const int lane = (int)lane_id(), w = (int)warp - WW_CLEAR0;
-    bool ok = true;
-    int gp = 0, done = 0;
-    for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
-        if (g.npg < 0) break;
-        const int n_lo = w_clamp(g.n0, p.cap);
-        for (int i = 0; i < g.npg && ok; ++i) {
-            const int a = gp + i, t0 = PAGE * w_logical(g, i);
-            if (w_whole(p, n_lo, g.n_hi, t0)) continue;
-            // the rows' contexts are consecutive, n_lo .. n_hi: the tokens that not all of them see
-            const uint64_t hidden = ~w_between(p, g.n_hi - p.window, n_lo, t0);
-            const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
-            if (lane == 0)
-                ok = w_count<MQ>(&sm.pv_seen, a - 1) &&
-                     w_wait<MQ>(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u) &&
-                     w_wait<MQ>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            // a warp a token: 64 pieces of 16 bytes, two a lane.  First only looked through: p = 0 times anything finite
-            // is 0 as it stands, and without a store there is no proxy fence to wait for (up to 1.5 us beside the MMAs).
-            uint64_t mine = 0;  // this warp's tokens that hold a NaN or an infinity somewhere
-#pragma unroll 4
-            for (int t = w; t < PAGE; t += 4) {
-                if (!(hidden >> t & 1ull)) continue;
-                const uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
-                const uint4 v0 = *reinterpret_cast<const uint4*>(at + (lane >> 3) * HCHUNK);
-                const uint4 v1 = *reinterpret_cast<const uint4*>(at + ((lane >> 3) + 4) * HCHUNK);
-                uint32_t m = __vmaxu2(__vmaxu2(v0.x & 0x7FFF7FFFu, v0.y & 0x7FFF7FFFu), __vmaxu2(v0.z & 0x7FFF7FFFu, v0.w & 0x7FFF7FFFu));
-                m = __vmaxu2(m, __vmaxu2(__vmaxu2(v1.x & 0x7FFF7FFFu, v1.y & 0x7FFF7FFFu), __vmaxu2(v1.z & 0x7FFF7FFFu, v1.w & 0x7FFF7FFFu)));
-                if ((m & 0xFFFFu) >= 0x7F80u || (m >> 16) >= 0x7F80u) mine |= 1ull << t;
-            }
-            if (__any_sync(0xFFFFFFFFu, mine != 0)) {
-#pragma unroll 1
-                for (int t = w; t < PAGE; t += 4) {
-                    if (!__any_sync(0xFFFFFFFFu, mine >> t & 1ull)) continue;
-                    uint8_t* at = sm.u.c1.ring[t < HALF ? q0 : q1] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
-#pragma unroll 1
-                    for (int x = 0; x < 2; ++x) {
-                        uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
-                        uint4 v = *piece;
-                        auto finite = [](uint32_t b) {  // bf16 with all exponent bits set: NaN or infinity
-                            if ((b & 0x7F80u) == 0x7F80u) b &= 0xFFFF0000u;
-                            if ((b & 0x7F800000u) == 0x7F800000u) b &= 0x0000FFFFu;
-                            return b;
-                        };
-                        v.x = finite(v.x), v.y = finite(v.y), v.z = finite(v.z), v.w = finite(v.w);
-                        *piece = v;
-                    }
-                }
-                fence_proxy_async_cta();
-                __syncwarp();
-            }
-            if (lane == 0) mbar_arrive(&sm.clear_done[done & 1]);
-            ++done;
-        }
-        gp += g.npg;
-        if (lane == 0) atomicAdd(&sm.clear_units, 1);
     }
 }
 
@@ -1031,6 +969,33 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
     if (lane == 0) mbar_arrive(&sm.epi_done);
 }
 
+// The NaNs and infinities among the latents of page a's tokens that not all rows of the unit see become zero: the rows
+// that do not see them have p = 0 there, which only a finite latent turns into 0.  (Rare: the scores have shown that
+// there are some.  Looking every masked page through took the chunk of 1 x 1000 rows from 137 to 152 us.)
+template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, int a, uint64_t hidden, int w)
+{
+    const int lane = (int)lane_id();
+#pragma unroll 1
+    for (int t = w; t < PAGE; t += W_EPI) {  // a warp a token: 64 pieces of 16 bytes, two a lane
+        if (!(hidden >> t & 1ull)) continue;
+        const int q = (2 * a + (t >= HALF ? 1 : 0)) % WN_HALF;
+        uint8_t* at = sm.u.c1.ring[q] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+            uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
+            uint4 v = *piece;
+            auto finite = [](uint32_t b) {  // bf16 with all exponent bits set: NaN or infinity
+                if ((b & 0x7F80u) == 0x7F80u) b &= 0xFFFF0000u;
+                if ((b & 0x7F800000u) == 0x7F800000u) b &= 0x0000FFFFu;
+                return b;
+            };
+            v.x = finite(v.x), v.y = finite(v.y), v.z = finite(v.z), v.w = finite(v.w);
+            *piece = v;
+        }
+    }
+    fence_proxy_async_cta();  // the MMAs read the latents through the async proxy
+}
+
 // Epilogue warp: the TMEM lanes of its quarter, the dims of its half.
 template <bool MQ>
 __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int quarter, int half)
@@ -1047,20 +1012,22 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         const uint32_t cmd = *reinterpret_cast<volatile uint32_t*>(&sm.epi_cmd);
         if (!cmd) break;
-        got = w_wait<MQ>(&sm.o_done, od++ & 1u);
-        if ((cmd & 2u) && sm.epi_single)
+        const int page = sm.epi_page;
+        if (cmd & (E_WRITE | E_RESCALE)) got = w_wait<MQ>(&sm.o_done, od++ & 1u);
+        if ((cmd & E_WRITE) && sm.epi_single)
             got = got && w_wait<MQ, true>(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u);
         got = __all_sync(0xFFFFFFFFu, got);
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         tc_fence_after();
-        if (cmd & 2u) {
+        if (cmd & E_WRITE) {
             const bool single = sm.epi_single != 0;
             w_write_out<MQ>(sm, p, t_row, quarter, half, singles);
             singles += single;
             continue;
         }
-        const float* al = reinterpret_cast<const float*>(sm.u.c1.recv[sm.epi_stage] + C::META_ALPHA);
-        const float f = row < C::ROWS ? al[row] : 1.f;
+        if (cmd & E_CLEAR) w_clear<MQ>(sm, page, sm.epi_hidden, quarter + 4 * half);
+        const float* al = reinterpret_cast<const float*>(sm.u.c1.recv[page % C::NPBUF] + C::META_ALPHA);
+        const float f = (cmd & E_RESCALE) && row < C::ROWS ? al[row] : 1.f;
         if (__any_sync(0xFFFFFFFFu, f != 1.f)) {  // some row of this warp moved its reference
 #pragma unroll 1
             for (int cb = 0; cb < LORA / 64; ++cb) {
@@ -1116,7 +1083,6 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
             w_epilogue<MQ>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
         else if (warp == WW_HALVES) w_produce_halves<MQ>(sm, tm_page8, p);
         else if (warp == WW_PV) w_issue_pv<MQ>(sm, p, tbase);
-        else if (warp < WW_CLEAR0 + 4) w_clear<MQ>(sm, p, warp);
         else if (warp == WW_PLAN) w_plan<MQ>(sm, p);
         else if (warp == WW_EMPTY) w_empty_rows<MQ>(p);
     }
