@@ -352,7 +352,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* de
     }
     for (int i = 0; i < 4 * C::NPAR; ++i) mbar_init(&sm.hand[i / C::NPAR][i % C::NPAR], 1);
     mbar_init(&sm.q_free, C::NISS);
-    mbar_init(&sm.q_ready, 4);
+    mbar_init(&sm.q_ready, 4 * C::NPAR);
     for (int i = 0; i < C::NPBUF; ++i) {
         mbar_init(&sm.p_full[i], 1);
         mbar_init(&sm.p_empty[i], 1);
@@ -520,10 +520,11 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
     if (!ok) drain_inflight();
 }
 
-// A warp of each quarter copies its rows of Q from the ring into TMEM (lane 32 w + l <- row RPQ w + l), once the
-// score MMAs of the unit before have read the old Q.
+// The softmax warps copy Q from the ring into TMEM (lane 32 w + l <- row RPQ w + l), once the score MMAs of the unit
+// before have read the old Q: each warp its quarter's rows, of every NPAR-th ring use, when it is through with its pages
+// of the unit before.
 template <bool MQ>
-__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int base, int un)
+__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int par, int base, int un)
 {
     using C = WCfg<MQ>;
     const int lane = (int)lane_id();
@@ -532,7 +533,7 @@ __device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint
     if (!__all_sync(0xFFFFFFFFu, un == 0 || w_wait<MQ>(&sm.q_free, (uint32_t)(un - 1) & 1u))) return false;
     tc_fence_after();
 #pragma unroll 1
-    for (int j = 0; j < C::NQ; ++j) {
+    for (int j = par; j < C::NQ; j += C::NPAR) {
         const int u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
         if (!__all_sync(0xFFFFFFFFu, w_count<MQ>(&sm.unit_taken[u], k) &&
                                          w_wait<MQ>(&sm.full[u], (uint32_t)(k & 1))))
@@ -589,7 +590,7 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     for (int un = 0;; ++un) {
         const WUnit g = w_next<MQ>(sm, p, un);
         if (g.npg < 0) break;
-        if (par == 0 && !w_copy_q<MQ>(sm, p, tbase, qd, base, un)) return;
+        if (!w_copy_q<MQ>(sm, p, tbase, qd, par, base, un)) return;
         base += C::NQ + 3 * g.npg;
         const int n = MQ ? (qd < g.rows ? w_clamp(g.n0 + qd, p.cap) : 0) : g.n0;  // this quarter's context
         float m_ref = -INFINITY, lsum = 0.f;
