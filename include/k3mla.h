@@ -491,7 +491,7 @@ int k3mla_pool_truncate(k3mla_pool* pool, int slot, int new_len);
  *   cache row of position i <- cache row of position keep[l * keep_layer_stride + keep_start[b] + i]
  * The slot then holds n_b tokens (rows from n_b on keep what they held; k3mla_pool_truncate gives their
  * pages back).  Rotated keys keep the angles of their old positions.
- * keep       device int32 [n_keep], or [n_layers] lists of n_keep entries keep_layer_stride apart: per
+ * keep       device int32 [n_keep] (n_keep < 2^30), or [n_layers] lists of n_keep entries keep_layer_stride apart: per
  *            slot strictly ascending positions (>= 0).  keep_layer_stride 0: one list for every layer.
  * keep_start device int32 [B + 1], non-decreasing, within [0, n_keep]
  * slab, block_table: as for k3mla_append_latent; a source entry -1 reads as a zero row

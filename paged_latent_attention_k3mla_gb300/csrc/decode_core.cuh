@@ -65,8 +65,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, S& sm, 
 // Bounded wait until a shared counter of this CTA reaches `target` (written by another thread of
 // the CTA with a plain store); false when this CTA aborted or the wait timed out.
 template <class S>
-__device__ __noinline__ bool wait_count(const int32_t* counter, int32_t target, S& sm, int32_t* dev_err,
-                                        uint32_t sleep_ns = 32)
+__device__ __noinline__ bool wait_count(const int32_t* counter, int32_t target, S& sm, int32_t* dev_err)
 {
     const volatile int32_t* v = counter;
     if (*v >= target) return true;
@@ -78,7 +77,7 @@ __device__ __noinline__ bool wait_count(const int32_t* counter, int32_t target, 
             if (dev_err) atomicOr(dev_err, (int)K3MLA_DEV_TIMEOUT);
             return false;
         }
-        __nanosleep(sleep_ns);
+        __nanosleep(32);
     }
     return true;
 }

@@ -246,6 +246,11 @@ extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const 
         set_error("k3mla_norm_rope_append: null or misaligned pointer");
         return K3MLA_E_INVALID;
     }
+    const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(q_out);
+    if (from != to && (from < to ? to - from : from - to) < (size_t)R * H * QDIM * 2) {
+        set_error("k3mla_norm_rope_append: q_out overlaps q in part");
+        return K3MLA_E_INVALID;
+    }
     if (!device_ok()) return K3MLA_E_DEVICE;
     NormRopeParams p;
     p.q = q, p.q_out = q_out, p.wq = q_weight, p.wc = c_weight, p.wk = k_weight;

@@ -192,6 +192,7 @@ extern "C" int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, con
                                   const int32_t* keep_start, int B, int32_t* dev_err, void* stream)
 {
     if (B < 0 || n_pages <= 0 || n_layers <= 0 || max_pages_per_slot <= 0 || n_keep < 0 ||
+        n_keep > 0x3FFFFFFF ||  // (a step's positions are counted a few steps past the list)
         (keep_layer_stride != 0 && keep_layer_stride < n_keep)) {
         set_error("k3mla_compact_rows: invalid sizes");
         return K3MLA_E_INVALID;

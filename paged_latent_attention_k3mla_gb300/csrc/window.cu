@@ -27,14 +27,14 @@
 //   * Score CTA: the producers stream Q and then the page thirds through one ring of 24 KB units; three
 //     threads issue the score MMAs (A = Q from TMEM, B = the page); the softmax warps of each quarter take a page
 //     each in turn, mask, keep a lazily moved reference max, and pass bf16 p to the PV CTA by bulk DSMEM copies
-//     (the first of them copies Q into TMEM when the last MMA of the unit before has read the old one).
+//     (and copy a unit's Q into TMEM once the last MMA of the unit before has read the old one).
 //   * PV CTA: a producer streams the pages' latents again (mostly from L2) as half pages; one thread issues
 //     O[rows x 512] += P . C; eight warps rescale O when a reference moved and, at a unit's end, take O out of
-//     TMEM; four warps look unseen tokens through;
-//     one plans the units of both CTAs ahead.
-//   * Unseen tokens.  Their scores are replaced (never multiplied), and in the pages that hold some, NaNs and
-//     infinities among their latents become zero in shared memory, because p = 0 times one of those would still be
-//     NaN.  In a chunk a token may be seen by some rows of the unit only: those get their NaN from its score.
+//     TMEM; one plans the units of both CTAs ahead.
+//   * Unseen tokens.  Their scores are replaced (never multiplied).  p = 0 times a NaN or an infinity would still be
+//     NaN, so where an unseen token's score shows that its row holds one, those among the page's unseen latents
+//     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get their
+//     NaN from its score.
 //
 // Every wait is bounded, as in decode.cu: after WAIT_NS it sets K3MLA_DEV_TIMEOUT and the roles run out.
 #include <cuda.h>
@@ -1464,6 +1464,7 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                     tm_page8, tm_q, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
+        // 512 threads a row for long lists: 28.3 -> 24.1 us for a slot of 40 splits; 27.0 -> 30.6 us for 16 slots of 5
         const bool longer = p.nsplit > 8;
         rc = launch_pdl(longer ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
                         dim3(longer ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
@@ -1472,6 +1473,8 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     WxParams x;
     x.oscale = p.oscale, x.out = out, x.dev_err = p.dev_err, x.R = p.R;
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
+    // Three CTAs a head fill two rounds of the SMs where one leaves a third of them idle, but load and convert W_UV three
+    // times: 1,000 rows (16 tiles) 131.7 -> 130.0 us, 128 slots (two tiles, two CTAs) 28.7 -> 33.5 us.
     return launch_pdl(k3mla_window_expand_kernel, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st,
                       "k3mla_window_expand_kernel", tm_w, tm_o, x);
 }

@@ -62,7 +62,7 @@ def go(slab, table, keep, start):
 
 @pytest.mark.parametrize("per_layer", [False, True])
 @pytest.mark.parametrize("lens,share,L", [([1], 1.0, 1), ([200, 1, 64, 65, 0], 0.5, 3), ([1500, 700], 0.7, 2), ([900], 0.05, 4),
-                                          ([128, 129, 300], 1.0, 2)])
+                                          ([128, 129, 300], 1.0, 2), ([70, 0, 200, 33] * 10, 0.6, 4)])
 def test_kept_rows_move_to_the_front(gpu_lib, lens, share, L, per_layer):
     rng, table, slab = make(sum(lens) + L, lens, L)
     kept = [min(n, max(n > 0, int(n * share))) for n in lens]

@@ -452,3 +452,85 @@ def test_refusals_of_the_binding(gpu_lib):
     with pytest.raises(k3mla.K3mlaError):
         k3mla.window_decode(*args, split_tokens=100)
     torch.cuda.synchronize()
+
+
+def test_zero_queries_beside_unseen_infinities(gpu_lib):
+    # every score is 0, and a zero query times an unseen infinity is the NaN that gives it away
+    lens = [200, 77]
+    c = Case(61, lens, 2)
+    c.q.zero_()
+    c.poison(seen_sets(lens, 70, 3))
+    for split in (0, 128):
+        c.check(c.decode(70, 3, split), [0, 1], lens, 70, 3)
+    c = Case(62, [150], 9)
+    c.q.zero_()
+    n = [142 + r for r in range(9)]
+    c.poison([set().union(*[set(ref.visible(x, 40, 3).tolist()) for x in n])])
+    c.check(c.chunk([141], [0, 9], 40, 3), [0] * 9, n, 40, 3)
+
+
+@pytest.mark.parametrize("first,rest", [(0.0, 1.0), (2.0 ** -30, 1.0), (2.0 ** -9, 1.0), (1.0, 2.0 ** -20), (2.0 ** 12, 1.0),
+                                        (1.0, 0.0), (0.0, 0.0)])
+def test_first_dims_unlike_the_others(gpu_lib, first, rest):
+    # the power of two of a row of o_lat starts from its first 32 entries
+    lens = [400, 130, 64]
+    c = Case(63, lens, 3)
+    c.slab[..., :32] *= first
+    c.slab[..., 32:512] *= rest
+    for split in (0, 128):
+        c.check(c.decode(300, 3, split), [0, 1, 2], lens, 300, 3)
+    c = Case(64, [300], 7)
+    c.slab[..., :32] *= first
+    c.slab[..., 32:512] *= rest
+    c.check(c.chunk([293], [0, 7], 90, 3), [0] * 7, [294 + r for r in range(7)], 90, 3)
+
+
+@pytest.mark.parametrize("power", [60, -60])
+def test_large_and_small_latents(gpu_lib, power):
+    lens = [400, 100]
+    c = Case(65, lens, 2)
+    c.slab *= 2.0 ** power
+    c.q *= 2.0 ** -power
+    for split in (0, 128):
+        c.check(c.decode(300, 3, split), [0, 1], lens, 300, 3)
+
+
+def test_two_streams_at_once(gpu_lib):
+    # each call has its own workspace and output; they share the cache
+    c = Case(66, [900, 400, 1000], 3)
+    want = [c.decode(700, 5, split) for split in (0, 128)]
+    table, lens = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.lens).cuda()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros(3, H, V, dtype=torch.bfloat16, device="cuda") for _ in range(8)] for _ in range(2)]
+    ws = [torch.empty(k3mla.window_decode_workspace_bytes(3, c.max_ctx, 700, 5, split), dtype=torch.uint8, device="cuda")
+          for split in (0, 128)]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for s, split in enumerate((0, 128)):
+            k3mla.window_decode(c.q, c.slab, 1, table, lens, c.w, SCALE_BITS, outs[s][i], ws[s], c.max_ctx, 700, 5, split,
+                                stream=streams[s])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[s]) for s in range(2) for o in outs[s])
+
+
+def test_chunk_replayed_with_other_lengths(gpu_lib):
+    # a captured call reads positions and row ranges at its replay
+    c = Case(67, [300, 200], 12)
+    table = torch.from_numpy(c.table).cuda()
+    pos0 = torch.tensor([290, 198], dtype=torch.int32, device="cuda")
+    start = torch.tensor([0, 10, 12], dtype=torch.int32, device="cuda")
+    out = torch.empty(12, H, V, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(k3mla.window_chunk_decode_workspace_bytes(2, 12, c.max_ctx), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        k3mla.window_chunk_decode(c.q, c.slab, 1, table, pos0, start, c.w, SCALE_BITS, out, ws, c.max_ctx, 100, 2)
+    for p, s in (([290, 198], [0, 10, 12]), ([0, 191], [0, 3, 12]), ([100, 5], [0, 0, 7])):
+        pos0.copy_(torch.tensor(p))
+        start.copy_(torch.tensor(s))
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, c.chunk(p, s, 100, 2))
+        slot, n = rows_to(s, p, 12)
+        c.check(out, slot, n, 100, 2)

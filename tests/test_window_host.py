@@ -101,7 +101,7 @@ def norm_rope(lib, **change):
     dict(eps=-1.0), dict(eps=float("nan")), dict(B=-1), dict(R=-1), dict(start=None), dict(q=None), dict(q_out=None),
     dict(slab=None), dict(table=None), dict(pos0=None), dict(c=None), dict(k=None), dict(q=ODD), dict(q_out=ODD),
     dict(slab=ODD), dict(c=ODD), dict(k=ODD), dict(qw=ODD), dict(cw=ODD), dict(kw=ODD), dict(inv=ctypes.c_void_p(257)),
-    dict(R=2 ** 31 - 1)])
+    dict(R=2 ** 31 - 1), dict(q=ctypes.c_void_p(512)), dict(q_out=ctypes.c_void_p(256 + 3 * 96 * 192 * 2 - 16))])
 def test_norm_rope_refusals(change):
     lib = k3mla.load()
     assert norm_rope(lib, **change) == -1
@@ -119,7 +119,7 @@ def compact(lib, **change):
     return lib.k3mla_compact_rows(*a.values())
 
 
-@pytest.mark.parametrize("change", [dict(n_pages=0), dict(n_layers=0), dict(cols=0), dict(n=-1), dict(B=-1), dict(stride=4),
+@pytest.mark.parametrize("change", [dict(n_pages=0), dict(n_layers=0), dict(cols=0), dict(n=-1), dict(n=2 ** 30), dict(B=-1), dict(stride=4),
                                     dict(stride=-1), dict(slab=None), dict(slab=ODD), dict(table=None), dict(keep=None),
                                     dict(start=None)])
 def test_compact_refusals(change):
