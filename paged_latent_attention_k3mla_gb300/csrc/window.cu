@@ -884,11 +884,12 @@ __device__ __forceinline__ float w_row_scale(float m, float& inverse)
     return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
-// O [rows x 512] f32 leaves TMEM, a row a thread and half the dims a warp, each lane storing whole 32-byte sectors
-// of its own row, as f16 with a power of two per row: o_lat = O / l when the unit is all its rows see, else the
-// split's O (f32 there would take twice the stores, 32 lines each).  Reading TMEM sets the pace (some 64 bytes a
-// clock and SM: 2.1 us for a chunk's 256 KB; eight warps are no faster than four, nor are bulk stores or stores of
-// whole lines from staged boxes), so it is read once: the
+// O [rows x 512] f32 leaves TMEM, half the dims a warp, as f16 with a power of two per row: o_lat = O / l when the
+// unit is all its rows see, else the split's O (f32 there would take twice the stores).  Four lanes share a row: of 64
+// columns lane c holds 8 n + 2 c and 8 n + 2 c + 1 for n = 0 .. 7, and stores them side by side, 32 bytes, so that a
+// store instruction writes whole lines (with a row a lane, a sector each of 32 lines: 1 x 1000 rows 129 us, so 123).  The dims of
+// o_lat and of the splits' O thus lie in that order; the expansion puts W_UV into the same.
+// Reading TMEM sets the pace (some 64 bytes a clock and SM: 2.1 us for a chunk's 256 KB), so it is read once: the
 // power of two comes from the row's first 32 entries, with room for 2^8 times their largest, and the row's
 // largest entry is found on the way.  A row that it shows to have left the range, or to lie far below it, has its
 // warps go over their rows again with the power of two that fits.
@@ -899,72 +900,106 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
     using C = WCfg<MQ>;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
     const bool single = MQ || sm.epi_single != 0;
-    const int lane = (int)lane_id(), row = 32 * quarter + lane;
+    const int lane = (int)lane_id(), col = lane & 3, row = 32 * quarter + (lane >> 2);  // and row + 8, + 16, + 24
     const uint32_t t_lane = t_row + 256u * (uint32_t)half;
     // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
-    const bool mine = MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : row < C::ROWS;  // (and the row sees something)
-    const int tok = MQ ? row0 + quarter : b, head = (MQ ? 32 * hb : 32 * quarter) + lane;
-    float r = 1.f, inverse = 1.f, up = 1.f;
+    const bool mine = MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : quarter < C::ROWS / 32;  // (and sees something)
+    const int tok = MQ ? row0 + quarter : b, head = (MQ ? 32 * hb : 32 * quarter) + (lane >> 2);
     // o_lat [96][R][512], or partial O [B][nsplit][96][512]; a scale each
     const size_t at = single ? (size_t)head * p.R + tok : ((size_t)b * p.nsplit + s) * H + head;
-    uint16_t* out = (single ? p.olat : p.ws_o) + at * LORA + 256 * half;
-    if (mine && single) r = sm.u.c1.rl[singles & 1][row];
+    const size_t at8 = single ? 8 * (size_t)p.R : 8;  // eight heads on
+    uint16_t* out = (single ? p.olat : p.ws_o) + at * LORA + 256 * half + 16 * col;
+    float r[4], inverse[4], up[4], m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r[i] = mine && single ? sm.u.c1.rl[singles & 1][row + 8 * i] : 1.f;
+        inverse[i] = up[i] = 1.f;
+    }
+    auto over_lanes = [](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 1));
+        return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 2));
+    };
+    if (mine) {  // the rows' first entries: their largest to [2^6, 2^7)
+        uint32_t v[2][16];
+        tmem_ld_rows_x4(t_row, v[0]);
+        tmem_ld_rows_x4(t_row + (16u << 16), v[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                m[i] = fmaxf(m[i], fmaxf(fabsf(__uint_as_float(v[i >> 1][4 * n + 2 * (i & 1)])),
+                                         fabsf(__uint_as_float(v[i >> 1][4 * n + 2 * (i & 1) + 1]))));
+            up[i] = w_row_scale(over_lanes(m[i]) * r[i] * 256.f, inverse[i]);
+        }
+    }
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {  // the second only for rows whose first power of two did not fit
-        float m = 0.f;
-        auto largest = [&](const uint32_t (&v)[32]) {
-            float m2[2] = {m, 0.f};
-#pragma unroll
-            for (int e = 0; e < 32; ++e) m2[e & 1] = fmaxf(m2[e & 1], fabsf(__uint_as_float(v[e])));
-            m = fmaxf(m2[0], m2[1]);
-        };
         if (mine) {
-            uint32_t v[32];
-            if (pass == 0) {  // the row's first entries: their largest to [2^6, 2^7)
-                tmem_ld32(t_row, v);
-                tmem_wait_ld();
-                largest(v);
-                up = w_row_scale(m * r * 256.f, inverse);
-                m = 0.f;
-            }
-            const float f = r * up;
-            tmem_ld32(t_lane, v);
-            tmem_wait_ld();
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-                uint32_t next[32];  // on its way while this piece is turned
-                tmem_ld32(t_lane + 32u * (uint32_t)min(k + 1, 7), next);
-                largest(v);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) m[i] = 0.f;
+            auto leave = [&](const uint32_t (&v)[32], int k, int hi) {  // 64 columns of rows + 16 hi and + 16 hi + 8
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = 2 * hi + x;
+                    const float f = r[i] * up[i];
                     uint32_t w[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e] = pack_f16x2(__uint_as_float(v[16 * i + 2 * e]) * f, __uint_as_float(v[16 * i + 2 * e + 1]) * f);
-                    st_global_v8(out + 32 * k + 16 * i, w);
+                    for (int n = 0; n < 8; ++n) {
+                        const float a = __uint_as_float(v[4 * n + 2 * x]), c = __uint_as_float(v[4 * n + 2 * x + 1]);
+                        m[i] = fmaxf(m[i], fmaxf(fabsf(a), fabsf(c)));
+                        w[n] = pack_f16x2(a * f, c * f);
+                    }
+                    st_global_v8(out + (size_t)i * at8 * LORA + 64 * k, w);
                 }
+            };
+            uint32_t v[32], next[32];  // one is on its way while the other is turned
+            tmem_ld_rows_x8(t_lane, v);
+            tmem_wait_ld();
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                tmem_ld_rows_x8(t_lane + (16u << 16) + 64u * (uint32_t)k, next);
+                leave(v, k, 0);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    asm volatile("" : "+r"(next[e]));  // (not read before the wait)
-                    v[e] = next[e];
-                }
+                for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(next[e]));  // (not read before the wait)
+                tmem_ld_rows_x8(t_lane + 64u * (uint32_t)min(k + 1, 3), v);
+                leave(next, k, 1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(v[e]));
             }
         }
         if (pass) break;
-        if (mine) sm.u.c1.half_max[half][row] = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[i] = over_lanes(m[i]);
+        if (mine && col == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sm.u.c1.half_max[half][row + 8 * i] = m[i];
+        }
         named_bar(WB_OUT, 32 * W_EPI);
         if (single && threadIdx.x == 0) {  // the slot of 1 / l is free again
             mbar_arrive_expect_tx(&sm.l_full[singles & 1], 4 * C::ROWS);
             mbar_arrive_remote(mapa(smem_u32(&sm.rl_free[singles & 1]), 0));
         }
         __syncwarp();
-        if (mine) m = fmaxf(sm.u.c1.half_max[0][row], sm.u.c1.half_max[1][row]) * r;
-        const bool fits = !mine || m == 0.f || (m * up >= 1.f && m * up < 65504.f);
-        if (__all_sync(0xFFFFFFFFu, fits)) break;
-        if (!fits) up = w_row_scale(m, inverse);
+        bool fit = true;
+        if (mine) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float most = fmaxf(sm.u.c1.half_max[0][row + 8 * i], sm.u.c1.half_max[1][row + 8 * i]) * r[i];
+                if (most == 0.f || (most * up[i] >= 1.f && most * up[i] < 65504.f)) continue;
+                fit = false;
+                up[i] = w_row_scale(most, inverse[i]);
+            }
+        }
+        if (__all_sync(0xFFFFFFFFu, fit)) break;
     }
-    if (mine && half == 0) (single ? p.oscale : p.ws_oscale)[at] = inverse;
+    if (mine && half == 0 && col == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) (single ? p.oscale : p.ws_oscale)[at + i * at8] = inverse[i];
+    }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.epi_done);
@@ -1215,32 +1250,34 @@ struct WxParams {
 };
 
 // W_UV[h] in shared memory ([8 chunks][128 rows][128 B], 128-byte swizzle), bf16 -> f16 in place, every row times
-// the power of two that brings its largest entry to [2^14, 2^15).  Four threads a row, sixteen 16-byte pieces each,
-// held in registers between the row's maximum and the conversion.
+// the power of two that brings its largest entry to [2^14, 2^15), and every chunk's 64 dims in the order of the write-out:
+// 8 n + 2 j + e goes to 16 j + 2 n + e.  Four threads a row, j = 0 .. 3, the row held in registers between its maximum
+// and the conversion.
 __device__ __forceinline__ void wx_convert(uint8_t* sa, float* wscale)
 {
     const int row = (int)threadIdx.x >> 2, j = threadIdx.x & 3;
-    uint4 v[16];
+    uint32_t v[8][8];
     uint32_t m = 0;  // the largest magnitude: bf16 bit patterns of magnitudes order like the magnitudes
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int piece = 2 * j + (i & 1);
-        v[i] = *reinterpret_cast<const uint4*>(sa + (i >> 1) * (VH * 128) + row * 128 + ((piece ^ (row & 7)) << 4));
-        m = __vmaxu2(__vmaxu2(m, v[i].x & 0x7FFF7FFFu), v[i].y & 0x7FFF7FFFu);
-        m = __vmaxu2(__vmaxu2(m, v[i].z & 0x7FFF7FFFu), v[i].w & 0x7FFF7FFFu);
-    }
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            v[c][n] = *reinterpret_cast<const uint32_t*>(sa + c * (VH * 128) + row * 128 + ((n ^ (row & 7)) << 4) + 4 * j);
+            m = __vmaxu2(m, v[c][n] & 0x7FFF7FFFu);
+        }
     m = max(m & 0xFFFFu, m >> 16);
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
     m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
     float inverse;
     const float up = w_row_scale(__uint_as_float(m << 16), inverse);
     auto half2 = [&](uint32_t w) { return pack_f16x2(bf16lo_to_f32(w) * up, bf16hi_to_f32(w) * up); };
+    __syncwarp();  // the row has been read by all four
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int piece = 2 * j + (i & 1);
-        *reinterpret_cast<uint4*>(sa + (i >> 1) * (VH * 128) + row * 128 + ((piece ^ (row & 7)) << 4)) =
-            make_uint4(half2(v[i].x), half2(v[i].y), half2(v[i].z), half2(v[i].w));
-    }
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            *reinterpret_cast<uint4*>(sa + c * (VH * 128) + row * 128 + (((2 * j + x) ^ (row & 7)) << 4)) =
+                make_uint4(half2(v[c][4 * x]), half2(v[c][4 * x + 1]), half2(v[c][4 * x + 2]), half2(v[c][4 * x + 3]));
     if (j == 0) wscale[row] = inverse;
 }
 
