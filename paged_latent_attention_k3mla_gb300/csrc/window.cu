@@ -1143,12 +1143,12 @@ template <int G> __global__ void __launch_bounds__(128 * G) k3mla_window_merge_k
     __shared__ float4 sum[G][128];
     __shared__ float sl[G], smax[4];
     const int h = blockIdx.x, b = blockIdx.y, d = 4 * ((int)threadIdx.x & 127), g = (int)threadIdx.x >> 7;
-    griddep_wait();
     griddep_launch_dependents();
-    int nsp, wp0;
+    int nsp, wp0;  // a slot's length is no output of the kernel ahead, and was there before that one began
     const int n = w_clamp(p.ctx_len[b], p.cap);
     const int all = w_pages(n, n, p.window, p.n_sink, nsp, wp0);
     const int per = slot_split(all * PAGE, p.split_tokens) / PAGE, ns = (all + per - 1) / per;
+    griddep_wait();        // (every CTA: the expansion counts on this kernel's end for the splits' end too)
     if (ns <= 1) return;  // landed by the split itself
     const size_t row = (size_t)b * p.nsplit * H + h;
     const float2* ml = p.ws_ml + row;
@@ -1501,7 +1501,7 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                     tm_page8, tm_q, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
-        // 512 threads a row for long lists: 28.3 -> 24.1 us for a slot of 40 splits; 27.0 -> 30.6 us for 16 slots of 5
+        // 512 threads a row for long lists: 27.6 -> 23.2 us for a slot of 33 splits, but 26.2 -> 30.4 us for 16 slots of 3
         const bool longer = p.nsplit > 8;
         rc = launch_pdl(longer ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
                         dim3(longer ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
