@@ -1136,7 +1136,7 @@ constexpr int WM_GROUPS = 4;
 // A row (slot, head) per CTA: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max), four dims a thread.
 // Split i belongs to group i mod 4; the groups' sums, each over ascending i, are added as (g0 + g1) + (g2 + g3), so
 // that the bits depend on the slot's own splits only.  G = 1: 128 threads, each with all four groups; G = 4: 512
-// threads, one group each, for long lists (a few loads deep instead of eight and more).
+// threads, one group each, when the rows are few.
 template <int G> __global__ void __launch_bounds__(128 * G) k3mla_window_merge_kernel(const WinParams p)
 {
     constexpr int PER = WM_GROUPS / G;  // groups a thread
@@ -1501,10 +1501,11 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                     tm_page8, tm_q, p);
     if (rc) return rc;
     if (p.nsplit > 1) {
-        // 512 threads a row for long lists: 27.6 -> 23.2 us for a slot of 33 splits, but 26.2 -> 30.4 us for 16 slots of 3
-        const bool longer = p.nsplit > 8;
-        rc = launch_pdl(longer ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
-                        dim3(longer ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
+        // 512 threads a row while the rows are few: one slot of 33 splits 27.4 -> 23.3 us, four of 17 26.4 -> 25.5 us, but
+        // six of 11 26.7 -> 28.3 us, 32 of 33 120 -> 134 us
+        const bool few = (long long)H * p.B <= 3ll * sm_count();
+        rc = launch_pdl(few ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
+                        dim3(few ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
     }
     WxParams x;

@@ -125,12 +125,13 @@ def _check(rc: int, what: str):
 
 # The current stream's handle without a Stream object (3 us a call on the GPU machine's host), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -164,8 +165,8 @@ def _table(t: torch.Tensor, B: int):
 
 def _here(t: torch.Tensor, name: str):
     """The call runs on the current device: its tensors have to be there too."""
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise K3mlaError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.is_cuda and t.get_device() != _current_device():
+        raise K3mlaError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
 
 
 def absorb_q(q: torch.Tensor, w_kv_b: torch.Tensor, q_abs: torch.Tensor, stream=None) -> None:
@@ -198,10 +199,11 @@ def append_latent(slab: torch.Tensor, layer: int, block_table: torch.Tensor, pos
 
 
 def _rows(t: torch.Tensor, B: int, name: str, width: int = 0):
-    if not t.is_cuda or t.dtype is not torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] != B:
+    shape = t.shape
+    if not t.is_cuda or t.dtype is not torch.bfloat16 or len(shape) != 2 or t.stride(1) != 1 or shape[0] != B:
         raise K3mlaError(f"{name} must be a CUDA bf16 [B, n] tensor with unit inner stride")
-    if t.shape[1] < width:
-        raise K3mlaError(f"{name} has {t.shape[1]} columns, at least {width} are read")
+    if shape[1] < width:
+        raise K3mlaError(f"{name} has {shape[1]} columns, at least {width} are read")
     return t.data_ptr()
 
 
