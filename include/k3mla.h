@@ -361,8 +361,8 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  * max_ctx     upper bound of n; a larger one is clamped, as one past the table is (K3MLA_DEV_CTX)
  * workspace   device, 256-byte aligned, at least the bytes that the sizing call gives; scratch
  * others      as for k3mla_paged_decode and k3mla_chunk_decode
- * Two kernels on `stream` (three when max_ctx, window and split_tokens allow several splits), each reading
- * nothing but w_kv_b before the kernel ahead of it has completed: w_kv_b must not be written by the kernel
+ * Two kernels on `stream`, or three (some batches with several splits a slot), each reading nothing but
+ * w_kv_b before the kernel ahead of the call has completed: w_kv_b must not be written by the kernel
  * immediately before this call. */
 size_t k3mla_window_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);
 int k3mla_window_split_tokens(int B, int max_ctx, int window, int n_sink);

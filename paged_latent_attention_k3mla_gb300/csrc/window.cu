@@ -1131,88 +1131,95 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
 
 // ---- merge of splits (decode) ---------------------------------------------------------------
 
+// o_lat of a row (slot, head) = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max).  Split i belongs to group i mod 4;
+// the groups' sums, each over ascending i, are added as (g0 + g1) + (g2 + g3), so that the bits depend on the slot's
+// own splits only, whichever kernel adds them up: k3mla_window_merge_kernel, or the expansion when the rows are few.
 constexpr int WM_GROUPS = 4;
 
-// A row (slot, head) per CTA: o_lat = sum_i w_i O_i / sum_i w_i l_i with w_i = 2^(m_i - max), four dims a thread.
-// Split i belongs to group i mod 4; the groups' sums, each over ascending i, are added as (g0 + g1) + (g2 + g3), so
-// that the bits depend on the slot's own splits only.  G = 1: 128 threads, each with all four groups; G = 4: 512
-// threads, one group each, when the rows are few.
-template <int G> __global__ void __launch_bounds__(128 * G) k3mla_window_merge_kernel(const WinParams p)
+// How many splits slot b has.  (A length is no output of the kernels of this call, and was there before the first began.)
+__device__ __forceinline__ int w_splits(const WinParams& p, int b)
 {
-    constexpr int PER = WM_GROUPS / G;  // groups a thread
-    __shared__ float4 sum[G][128];
-    __shared__ float sl[G], smax[4];
-    const int h = blockIdx.x, b = blockIdx.y, d = 4 * ((int)threadIdx.x & 127), g = (int)threadIdx.x >> 7;
-    griddep_launch_dependents();
-    int nsp, wp0;  // a slot's length is no output of the kernel ahead, and was there before that one began
+    int nsp, wp0;
     const int n = w_clamp(p.ctx_len[b], p.cap);
     const int all = w_pages(n, n, p.window, p.n_sink, nsp, wp0);
-    const int per = slot_split(all * PAGE, p.split_tokens) / PAGE, ns = (all + per - 1) / per;
-    griddep_wait();        // (every CTA: the expansion counts on this kernel's end for the splits' end too)
-    if (ns <= 1) return;  // landed by the split itself
-    const size_t row = (size_t)b * p.nsplit * H + h;
-    const float2* ml = p.ws_ml + row;
+    const int per = slot_split(all * PAGE, p.split_tokens) / PAGE;
+    return (all + per - 1) / per;
+}
+
+// The largest reference max of a row's ns splits (a whole warp).
+__device__ __forceinline__ float w_max_ref(const WinParams& p, size_t row, int ns)
+{
     float m = -INFINITY;
-    for (int i = (int)lane_id(); i < ns; i += 32) m = fmaxf(m, ml[(size_t)i * H].x);
+    for (int i = (int)lane_id(); i < ns; i += 32) m = fmaxf(m, p.ws_ml[row + (size_t)i * H].x);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-    float l[PER];
-    float4 part[PER];
+    return m;
+}
+
+// Groups g0 .. g0 + PER - 1 of a row's sums: l, and D dims from d on (D / 2 registers of f16 pairs a split).
+template <int PER, int D>
+__device__ __forceinline__ void w_sum_groups(const WinParams& p, size_t row, int ns, int g0, float m, int d, float (&l)[PER],
+                                             float (&part)[PER][D])
+{
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
         l[k] = 0.f;
-        part[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < D; ++e) part[k][e] = 0.f;
     }
-#pragma unroll 2
-    for (int i0 = 0; i0 < ns; i0 += WM_GROUPS)
+#pragma unroll(PER == 1 ? 8 : 2)
+    for (int i0 = g0; i0 < ns; i0 += WM_GROUPS)
 #pragma unroll
         for (int k = 0; k < PER; ++k) {
-            const int i = i0 + (G == 1 ? k : g);
-            if (i >= ns) continue;
-            const size_t at = row + (size_t)i * H;
+            if (i0 + k >= ns) continue;
+            const size_t at = row + (size_t)(i0 + k) * H;
             const float2 rec = p.ws_ml[at];
-            const uint2 v = *reinterpret_cast<const uint2*>(p.ws_o + at * LORA + d);
+            uint32_t v[D / 2];
+#pragma unroll
+            for (int e = 0; e < D / 4; ++e) {
+                const uint2 x = reinterpret_cast<const uint2*>(p.ws_o + at * LORA + d)[e];
+                v[2 * e] = x.x, v[2 * e + 1] = x.y;
+            }
             const float w = ex2_approx(rec.x - m), f = w * p.ws_oscale[at];
-            float x0, x1, x2, x3;
-            f16x2_parts(v.x, x0, x1);
-            f16x2_parts(v.y, x2, x3);
             l[k] = fmaf(w, rec.y, l[k]);
-            part[k].x = fmaf(f, x0, part[k].x);
-            part[k].y = fmaf(f, x1, part[k].y);
-            part[k].z = fmaf(f, x2, part[k].z);
-            part[k].w = fmaf(f, x3, part[k].w);
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) {
+                float x0, x1;
+                f16x2_parts(v[e], x0, x1);
+                part[k][2 * e] = fmaf(f, x0, part[k][2 * e]);
+                part[k][2 * e + 1] = fmaf(f, x1, part[k][2 * e + 1]);
+            }
         }
-    float4 acc;
-    float ltot;
-    if constexpr (G == 1) {
-        acc.x = (part[0].x + part[1].x) + (part[2].x + part[3].x);
-        acc.y = (part[0].y + part[1].y) + (part[2].y + part[3].y);
-        acc.z = (part[0].z + part[1].z) + (part[2].z + part[3].z);
-        acc.w = (part[0].w + part[1].w) + (part[2].w + part[3].w);
-        ltot = (l[0] + l[1]) + (l[2] + l[3]);
-    } else {
-        sum[g][threadIdx.x & 127] = part[0];
-        if (d == 0) sl[g] = l[0];
-        __syncthreads();
-        if (g > 0) return;
-        const float4 s1 = sum[1][threadIdx.x], s2 = sum[2][threadIdx.x], s3 = sum[3][threadIdx.x];
-        acc.x = (part[0].x + s1.x) + (s2.x + s3.x);
-        acc.y = (part[0].y + s1.y) + (s2.y + s3.y);
-        acc.z = (part[0].z + s1.z) + (s2.z + s3.z);
-        acc.w = (part[0].w + s1.w) + (s2.w + s3.w);
-        ltot = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+}
+
+// A row per CTA of 128 threads, four dims each.
+__global__ void __launch_bounds__(128) k3mla_window_merge_kernel(const WinParams p)
+{
+    __shared__ float smax[4];
+    const int h = blockIdx.x, b = blockIdx.y, d = 4 * (int)threadIdx.x;
+    griddep_launch_dependents();
+    const int ns = w_splits(p, b);
+    griddep_wait();        // (every CTA: the expansion counts on this kernel's end for the splits' end too)
+    if (ns <= 1) return;  // landed by the split itself
+    const size_t row = (size_t)b * p.nsplit * H + h;
+    const float m = w_max_ref(p, row, ns);
+    float l[WM_GROUPS], part[WM_GROUPS][4], acc[4];
+    w_sum_groups<WM_GROUPS, 4>(p, row, ns, 0, m, d, l, part);
+    const float r = 1.f / ((l[0] + l[1]) + (l[2] + l[3]));
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        acc[e] = ((part[0][e] + part[1][e]) + (part[2][e] + part[3][e])) * r;
+        big = fmaxf(big, fabsf(acc[e]));
     }
-    const float r = 1.f / ltot;
-    acc.x *= r, acc.y *= r, acc.z *= r, acc.w *= r;
-    float big = fmaxf(fmaxf(fabsf(acc.x), fabsf(acc.y)), fmaxf(fabsf(acc.z), fabsf(acc.w)));
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
     if (lane_id() == 0) smax[threadIdx.x >> 5] = big;
-    named_bar(1, 128);
+    __syncthreads();
     float inverse;
     const float up = w_row_scale(fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3])), inverse);
     *reinterpret_cast<uint2*>(p.olat + ((size_t)h * p.B + b) * LORA + d) =
-        make_uint2(pack_f16x2(acc.x * up, acc.y * up), pack_f16x2(acc.z * up, acc.w * up));
+        make_uint2(pack_f16x2(acc[0] * up, acc[1] * up), pack_f16x2(acc[2] * up, acc[3] * up));
     if (d == 0) p.oscale[(size_t)h * p.B + b] = inverse;
 }
 
@@ -1234,6 +1241,7 @@ constexpr int WX_THREADS = 32 * (WX_EPI + 2);         // ... one loads, one issu
 static_assert(WX_SMEM <= 225 * 1024, "shared memory, beside a few hundred static bytes");
 
 struct WxSmem {
+    float merge_l[WX_EPI];    // a warp's sum of w_i l_i
     uint64_t w_full, w_ready, b_full[WX_RING], b_empty[WX_RING], d_full[2], d_empty[2];
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -1281,9 +1289,96 @@ __device__ __forceinline__ void wx_convert(uint8_t* sa, float* wscale)
     if (j == 0) wscale[row] = inverse;
 }
 
+// The rows' splits added up by the expansion itself, straight into the operand tile of head h (one tile: at most 16
+// rows): WARPS warps a row, a group each (4) or all four (1).  Saves a kernel and o_lat's way through memory.
+template <int WARPS>
+__device__ __forceinline__ void wx_merge(uint8_t* sb, WxSmem& sm, const WinParams& p, int h, int ns)
+{
+    constexpr int PER = WM_GROUPS / WARPS;
+    const int lane = (int)lane_id(), warp = (int)threadIdx.x >> 5, b = warp / WARPS, g = warp % WARPS;
+    auto place = [&](int half) {  // dims 256 half + 8 lane .. + 7 of row b
+        return reinterpret_cast<uint4*>(sb + (4 * half + (lane >> 3)) * WX_CHUNK + b * 128 + (((lane & 7) ^ (b & 7)) << 4));
+    };
+    float acc[2][8], ltot = 0.f;
+    const bool several = b < p.B && ns > 1;
+    if (several) {
+        const size_t row = (size_t)b * p.nsplit * H + h;
+        const float m = w_max_ref(p, row, ns);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float l[PER], part[PER][8];
+            w_sum_groups<PER, 8>(p, row, ns, g, m, 256 * half + 8 * lane, l, part);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                acc[half][e] = PER == 1 ? part[0][e]
+                                        : (part[0][e] + part[1 % PER][e]) + (part[2 % PER][e] + part[3 % PER][e]);
+            ltot = PER == 1 ? l[0] : (l[0] + l[1 % PER]) + (l[2 % PER] + l[3 % PER]);
+        }
+    } else if (b < p.B && g == 0) {  // landed by the split itself, or nothing seen
+        const size_t at = (size_t)h * p.B + b;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+            *place(half) = *reinterpret_cast<const uint4*>(p.olat + at * LORA + 256 * half + 8 * lane);
+        if (lane == 0) sm.rscale[0][b] = p.oscale[at];
+    }
+    if constexpr (WARPS > 1) {  // the groups meet in the row's first warp, by way of rows 8 .. 63 of the tile, which nobody has
+        auto meet = [&](int w, int k) {
+            return reinterpret_cast<float4*>(sb + (w >> 1) * WX_CHUNK + 1024 + (w & 1) * 2048) + 32 * k + lane;
+        };
+        if (several && g > 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float* a = &acc[k >> 1][4 * (k & 1)];
+                *meet(warp, k) = make_float4(a[0], a[1], a[2], a[3]);
+            }
+            if (lane == 0) sm.merge_l[warp] = ltot;
+        }
+        named_bar(1, 32 * WX_EPI);
+        if (several && g == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float* a = &acc[k >> 1][4 * (k & 1)];
+                const float4 s1 = *meet(warp + 1, k), s2 = *meet(warp + 2, k), s3 = *meet(warp + 3, k);
+                a[0] = (a[0] + s1.x) + (s2.x + s3.x);
+                a[1] = (a[1] + s1.y) + (s2.y + s3.y);
+                a[2] = (a[2] + s1.z) + (s2.z + s3.z);
+                a[3] = (a[3] + s1.w) + (s2.w + s3.w);
+            }
+            ltot = (ltot + sm.merge_l[warp + 1]) + (sm.merge_l[warp + 2] + sm.merge_l[warp + 3]);
+        }
+    }
+    if (several && g == 0) {
+        const float r = 1.f / ltot;
+        float big = 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[half][e] *= r;
+                big = fmaxf(big, fabsf(acc[half][e]));
+            }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
+        float inverse;
+        const float up = w_row_scale(big, inverse);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const float* a = acc[half];
+            *place(half) = make_uint4(pack_f16x2(a[0] * up, a[1] * up), pack_f16x2(a[2] * up, a[3] * up),
+                                      pack_f16x2(a[4] * up, a[5] * up), pack_f16x2(a[6] * up, a[7] * up));
+        }
+        if (lane == 0) sm.rscale[0][b] = inverse;
+    }
+    fence_proxy_async_cta();  // the MMAs read the tile through the async proxy
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.b_full[0]);
+}
+
+// MERGE: o_lat's rows come from memory (0), or from their splits, 1 or 4 warps a row.
+template <int MERGE>
 __global__ void __launch_bounds__(WX_THREADS, 1)
     k3mla_window_expand_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_o,
-                               const WxParams p)
+                               const WxParams p, const WinParams win)
 {
     extern __shared__ uint8_t smem_raw[];
     __shared__ WxSmem sm;
@@ -1298,7 +1393,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         mbar_init(&sm.w_full, 1);
         mbar_init(&sm.w_ready, WX_EPI);
         for (int i = 0; i < WX_RING; ++i) {
-            mbar_init(&sm.b_full[i], 1);
+            mbar_init(&sm.b_full[i], MERGE ? WX_EPI : 1);
             mbar_init(&sm.b_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -1320,7 +1415,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
     const uint32_t tbase = sm.tmem_base;
     bool ok = true;
     if (warp == WX_EPI) {
-        if (lane == 0) {
+        if (lane == 0 && !MERGE) {
             griddep_wait();
             int g = 0;
             for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y)
@@ -1344,7 +1439,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
                 ok = wait_bar(&sm.d_empty[it & 1], (uint32_t)((it >> 1) & 1) ^ 1u, sm, p.dev_err);
                 for (int c = 0; c < 8 && ok; ++c, ++g) {
                     const int s = g % WX_RING;
-                    ok = wait_bar(&sm.b_full[s], (uint32_t)((g / WX_RING) & 1), sm, p.dev_err);
+                    if (!MERGE || c == 0) ok = wait_bar(&sm.b_full[s], (uint32_t)((g / WX_RING) & 1), sm, p.dev_err);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t ad = make_sdesc(smem_u32(sa + c * (VH * 128)), 16, 1024);
@@ -1364,20 +1459,23 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         fence_proxy_async_cta();  // the MMAs read it through the async proxy
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.w_ready);
+        int ns = 0;
+        if (MERGE && warp / max(MERGE, 1) < win.B) ns = w_splits(win, warp / max(MERGE, 1));
         griddep_wait();
         griddep_launch_dependents();
+        if constexpr (MERGE != 0) wx_merge<MERGE>(sb, sm, win, h, ns);
         const int q = warp & 3, cg = warp >> 2, tid = (int)threadIdx.x, v = 32 * q + lane;
         named_bar(1, 32 * WX_EPI);  // wscale is complete
         const float ws = sm.wscale[v];
         auto scale_of = [&](int t) {  // o_lat's power of two of row tid of tile t
             const int r = t * WX_TILE + tid;
-            return tid < WX_TILE && r < p.R ? p.oscale[(size_t)h * p.R + r] : 0.f;
+            return !MERGE && tid < WX_TILE && r < p.R ? p.oscale[(size_t)h * p.R + r] : 0.f;
         };
         int it = 0;
         float next = scale_of(blockIdx.y);
         for (int t = blockIdx.y; t < tiles; t += gridDim.y, ++it) {
             const int r0 = t * WX_TILE;
-            if (tid < WX_TILE) sm.rscale[it & 1][tid] = next;
+            if (!MERGE && tid < WX_TILE) sm.rscale[it & 1][tid] = next;
             next = scale_of(t + gridDim.y);  // (a tile ahead: its latency stays off the path)
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.d_full[it & 1], (uint32_t)(it >> 1) & 1u, sm, p.dev_err));
             if (ok) {
@@ -1492,29 +1590,31 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     if (!rc) rc = make_tmap_slab_3d(&tm_w, w_kv_b, (uint64_t)H * WROWS_PER_HEAD, LORA, 8, VH, 1);
     if (!rc) rc = make_tmap_slab_3d(&tm_o, p.olat, (uint64_t)H * R, LORA, 8, WX_TILE, 1);
     if (rc) return rc;
-    static bool attr_done[64] = {}, attr_expand[64] = {};
+    static bool attr_done[64] = {}, attr_expand[3][64] = {};
     const size_t smem = sizeof(WSmem<MQ>) + 1024;
     set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
-    set_smem_attr(reinterpret_cast<const void*>(k3mla_window_expand_kernel), WX_SMEM, attr_expand);
     const int clusters = std::min(p.n_units, sm_count() / 2);
     rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
                     tm_page8, tm_q, p);
     if (rc) return rc;
-    if (p.nsplit > 1) {
-        // 512 threads a row while the rows are few: one slot of 33 splits 27.4 -> 23.3 us, four of 17 26.4 -> 25.5 us, but
-        // six of 11 26.7 -> 28.3 us, 32 of 33 120 -> 134 us
-        const bool few = (long long)H * p.B <= 3ll * sm_count();
-        rc = launch_pdl(few ? k3mla_window_merge_kernel<WM_GROUPS> : k3mla_window_merge_kernel<1>, dim3(H, p.B),
-                        dim3(few ? 128 * WM_GROUPS : 128), 0, st, "k3mla_window_merge_kernel", p);
+    // Few rows: the expansion adds the splits up itself, four warps a row (a slot of 3 splits 20.5 -> 16.9 us, of 33 27.5 ->
+    // 21.2 us, four slots of 17 26.2 -> 25.5 us) or one (16 slots of 3 26.5 -> 25.0 us, 16 of 4 38.2 -> 36.1 us; but ten of
+    // 6 26.8 -> 27.3 us, five of 11 25.8 -> 30.0 us: a warp then goes through its list in several rounds).
+    const int merge = MQ || p.nsplit == 1 ? 0 : (p.B <= WX_EPI / 4 ? 4 : (p.B <= WX_EPI && p.nsplit <= WM_GROUPS ? 1 : 0));
+    if (p.nsplit > 1 && !merge) {
+        rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(128), 0, st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
     }
     WxParams x;
     x.oscale = p.oscale, x.out = out, x.dev_err = p.dev_err, x.R = p.R;
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
+    const auto expand = MQ || merge == 0 ? k3mla_window_expand_kernel<0>
+                                         : (merge == 4 ? k3mla_window_expand_kernel<4> : k3mla_window_expand_kernel<1>);
+    set_smem_attr(reinterpret_cast<const void*>(expand), WX_SMEM, attr_expand[merge == 4 ? 2 : merge]);
     // Three CTAs a head fill two rounds of the SMs where one leaves a third of them idle, but load and convert W_UV three
     // times: 1,000 rows (16 tiles) 131.7 -> 130.0 us, 128 slots (two tiles, two CTAs) 28.7 -> 33.5 us.
-    return launch_pdl(k3mla_window_expand_kernel, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st,
-                      "k3mla_window_expand_kernel", tm_w, tm_o, x);
+    return launch_pdl(expand, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st, "k3mla_window_expand_kernel", tm_w,
+                      tm_o, x, p);
 }
 
 // What both entries ask of their common arguments; fills p.

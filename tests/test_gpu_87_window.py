@@ -211,6 +211,18 @@ def test_a_slots_bits_depend_on_the_slot_alone(gpu_lib):
         c.slab = old
 
 
+def test_a_slots_bits_do_not_depend_on_who_adds_its_splits_up(gpu_lib):
+    # alone, among 5, 16 and 17 slots and with lists of more than eight splits: the sums are one order everywhere
+    lens = [900, 65, 0, 300, 64, 1000, 1, 500, 1300, 128, 700, 20, 640, 333, 90, 1100, 800]
+    c = Case(68, lens, len(lens))
+    for window, split in ((700, 128), (1300, 128), (700, 256)):
+        whole = c.decode(window, 10, split)
+        c.check(whole, list(range(17)), lens, window, 10)
+        for some in ([5], [8, 2, 15], [0, 1, 2, 3, 4], list(range(16))):
+            got = c.decode(window, 10, split, slots=some)
+            assert torch.equal(got, whole[some])
+
+
 def test_wide_window_is_the_full_decode(gpu_lib):
     # k3mla_paged_decode lands its scores in bf16, so the two agree within those landings: each score is off by
     # 2^-8 of itself, twice, and an output by at most the largest weight error of its row
