@@ -130,6 +130,7 @@ template <bool MQ> struct __align__(1024) WSmem {
     WUnit plan[W_PLANS];                 // the units, in order
     uint64_t plan_full[W_PLANS];
     int32_t pv_units, pv_pages;          // PV CTA: units whose MMAs have been issued / pages whose P has arrived
+    int32_t ahead_units;                 // PV CTA: units that the prefetching warp is through with
     uint32_t tmem_base;
     uint64_t epi_hidden;                 // to the epilogue warps: the tokens of page epi_page that not all rows see
     uint32_t epi_cmd;                    // ... and what to do, E_ bits
@@ -370,7 +371,7 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* de
     }
     for (int i = 0; i < C::NUNIT; ++i) sm.unit_loaded[i] = sm.unit_taken[i] = sm.copied[i] = 0;
     for (int i = 0; i < W_PLANS; ++i) mbar_init(&sm.plan_full[i], 1);
-    sm.pv_units = sm.pv_pages = 0;
+    sm.pv_units = sm.pv_pages = sm.ahead_units = 0;
     if (rank == 1) {  // expected before anything is sent
         for (int i = 0; i < C::NPBUF; ++i) mbar_arrive_expect_tx(&sm.p_full[i], C::PCOPY);
         for (int i = 0; i < 2; ++i) mbar_arrive_expect_tx(&sm.l_full[i], 4 * C::ROWS);
@@ -379,7 +380,8 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* de
 
 // The planner (a warp of the PV CTA) works the cluster's units out ahead of both CTAs' roles and leaves each in
 // the shared memory of both.  At most three units ahead of the PV CTA's MMAs: the softmax warps are then no more
-// than two further units behind (their sums of exp meet in two slots), so W_PLANS = 8 slots never run over.
+// than two further units behind (their sums of exp meet in two slots), so W_PLANS = 8 slots never run over; the
+// prefetching warp, which nobody else waits for, is counted.
 template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const WinParams& p)
 {
     const int lane = (int)lane_id();
@@ -390,7 +392,7 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
         g.npg = -1;
         if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0);
         if (g.npg == 0) continue;
-        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3);
+        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3) && (MQ || w_count<MQ>(&sm.ahead_units, n - 6));
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
         if (n > 0 && g.npg > 0 && lane < g.rows)  // its queries, into L2 (the first unit's are loaded at once)
@@ -1028,6 +1030,7 @@ template <bool MQ> __device__ __forceinline__ void w_prefetch(WSmem<MQ>& sm, con
                 for (int x = 0; x < 3; ++x) tma_prefetch_3d(&tm_page, 0, y, 3 * x);
             __syncwarp();
         }
+        *reinterpret_cast<volatile int32_t*>(&sm.ahead_units) = un + 1;
         gp += g.npg;
     }
 }

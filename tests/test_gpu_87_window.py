@@ -141,6 +141,18 @@ def test_decode_more_units_than_clusters(gpu_lib):
         assert c.err.item() == 0
 
 
+def test_many_units_of_one_cluster(gpu_lib):
+    # 900 slots of one to three pages: a cluster's roles pass a dozen units, one or two pages each
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(1, 190, 900)]
+    c = Case(69, lens, len(lens))
+    got = c.decode(60, 3)
+    c.check(got, list(range(900)), lens, 60, 3, rows=range(0, 900, 19))
+    for _ in range(5):
+        assert torch.equal(c.decode(60, 3), got)
+    assert c.err.item() == 0
+
+
 def test_decode_long(gpu_lib):
     lens = [9000, 5000, 4096]
     c = Case(11, lens, 3)
