@@ -17,7 +17,7 @@
 // while the next ones are on their way -- reading ahead is always safe.  The columns, the layers and the
 // slots are independent, so even a lone slot of 24 layers fills the GPU.  Bound: HBM, 2,304 bytes a
 // moved row and layer; rows that stay in place are neither read nor written.
-// Measured: 16 slots x 24 layers, 827 MB, 155 us (5.3 TB/s, 79 % of the copy rate); one slot, 57 MB, 16 us,
+// Measured: 16 slots x 24 layers, 827 MB, 147 us (5.6 TB/s, 83 % of the copy rate); one slot, 57 MB, 16 us,
 // eighteen steps of 0.8 us behind each other.
 #include <cuda_runtime.h>
 
@@ -65,13 +65,12 @@ __global__ void __launch_bounds__(CP_THREADS) k3mla_copy_pages_kernel(uint16_t* 
     }
 }
 
-constexpr int CR_THREADS = 288;
-// COLS columns of a row, a CTA each; UNROLL rows a thread and step.
-template <int COLS, int UNROLL> struct Compact {
+// COLS columns of a row, a CTA of THREADS each; UNROLL rows a thread and step.
+template <int COLS, int UNROLL, int THREADS> struct Compact {
     static constexpr int VECS = ROW * 2 / (16 * COLS);     // 16-byte vectors of a row's column
-    static constexpr int GROUP = CR_THREADS / VECS;        // rows that the CTA's threads cover at once
+    static constexpr int GROUP = THREADS / VECS;        // rows that the CTA's threads cover at once
     static constexpr int ROWS = GROUP * UNROLL;            // rows a step
-    static_assert(COLS * VECS * 16 == ROW * 2 && GROUP * VECS == CR_THREADS, "whole columns and rows");
+    static_assert(COLS * VECS * 16 == ROW * 2 && GROUP * VECS == THREADS, "whole columns and rows");
 };
 
 struct CompactParams {
@@ -87,11 +86,11 @@ template <int UNROLL> struct CompactRows {
     int64_t src[UNROLL], dst[UNROLL];  // rows of the slab; dst -1: nothing to move, src -1: zeros
 };
 
-// grid (columns, layers, slots); block CR_THREADS.
-template <int COLS, int UNROLL>
-__global__ void __launch_bounds__(CR_THREADS) k3mla_compact_rows_kernel(const CompactParams p)
+// grid (columns, layers, slots); block THREADS.
+template <int COLS, int UNROLL, int THREADS>
+__global__ void __launch_bounds__(THREADS) k3mla_compact_rows_kernel(const CompactParams p)
 {
-    using C = Compact<COLS, UNROLL>;
+    using C = Compact<COLS, UNROLL, THREADS>;
     griddep_wait();
     griddep_launch_dependents();
     const int b = p.slot0 + (int)blockIdx.z, layer = p.layer0 + (int)blockIdx.y;
@@ -213,12 +212,12 @@ extern "C" int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, con
             const int nz = B - p.slot0 < MOST ? B - p.slot0 : MOST;
             // Few columns in all (less than eight CTAs of 128 bytes an SM): half as wide ones and two rows a thread, since
             // the steps' latency is what counts -- one slot of 24 layers 15.9 us against 24.8.  Else whole lines and one
-            // row a thread, for more CTAs an SM -- 16 slots 155 us against 164.
+            // row a thread, for more CTAs an SM -- 16 slots 147 us against 164 (eight CTAs of 256 threads fill an SM; of 288 155 us).
             int dev = 0, sms = 152;
             if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
             const bool few = 9ll * ny * nz < 8ll * sms;
-            const int rc = launch_pdl(few ? k3mla_compact_rows_kernel<18, 2> : k3mla_compact_rows_kernel<9, 1>,
-                                      dim3(few ? 18 : 9, ny, nz), dim3(CR_THREADS), 0, reinterpret_cast<cudaStream_t>(stream),
+            const int rc = launch_pdl(few ? k3mla_compact_rows_kernel<18, 2, 288> : k3mla_compact_rows_kernel<9, 1, 256>,
+                                      dim3(few ? 18 : 9, ny, nz), dim3(few ? 288 : 256), 0, reinterpret_cast<cudaStream_t>(stream),
                                       "k3mla_compact_rows_kernel", p);
             if (rc) return rc;
         }
