@@ -128,10 +128,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(_current_device())
+            return _raw_stream(_current_device() if device is None else device)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -157,16 +157,40 @@ def _opt(t, dtype, shape, name):
     return None if t is None else _dev(t, dtype, shape, name)
 
 
-def _table(t: torch.Tensor, B: int):
+def _here(slab: torch.Tensor) -> int:
+    """The device that a call runs on, the current one; its tensors have to be there (_at)."""
+    if not slab.is_cuda:
+        raise K3mlaError("slab must be a CUDA tensor")
+    return _current_device()
+
+
+def _at(device: int, t: torch.Tensor, dtype, shape, name):
+    """As _dev, and the tensor has to be on this device."""
+    try:
+        if t.get_device() == device and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, shape, name)
+    raise K3mlaError(f"{name} is on {t.device}, the call runs on cuda:{device}")
+
+
+def _opt_at(device: int, t, dtype, shape, name):
+    return None if t is None else _at(device, t, dtype, shape, name)
+
+
+def _int(x, name: str) -> int:
+    """An argument that the library takes as a C int (which would drop the upper bits of a larger one)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise K3mlaError(f"{name} = {x} does not fit 32 bits")
+    return x
+
+
+def _table(device: int, t: torch.Tensor, B: int):
     if t.dim() != 2 or t.shape[0] != B:
         raise K3mlaError(f"block_table has shape {tuple(t.shape)}, expected [{B}, max_pages]")
-    return _dev(t, torch.int32, None, "block_table")
-
-
-def _here(t: torch.Tensor, name: str):
-    """The call runs on the current device: its tensors have to be there too."""
-    if t.is_cuda and t.get_device() != _current_device():
-        raise K3mlaError(f"{name} is on {t.device}, the current device is cuda:{_current_device()}")
+    return _at(device, t, torch.int32, None, "block_table")
 
 
 def absorb_q(q: torch.Tensor, w_kv_b: torch.Tensor, q_abs: torch.Tensor, stream=None) -> None:
@@ -198,12 +222,14 @@ def append_latent(slab: torch.Tensor, layer: int, block_table: torch.Tensor, pos
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_append_latent")
 
 
-def _rows(t: torch.Tensor, B: int, name: str, width: int = 0):
+def _rows(t: torch.Tensor, B: int, name: str, width: int = 0, device: int | None = None):
     shape = t.shape
     if not t.is_cuda or t.dtype is not torch.bfloat16 or len(shape) != 2 or t.stride(1) != 1 or shape[0] != B:
         raise K3mlaError(f"{name} must be a CUDA bf16 [B, n] tensor with unit inner stride")
     if shape[1] < width:
         raise K3mlaError(f"{name} has {shape[1]} columns, at least {width} are read")
+    if device is not None and t.get_device() != device:
+        raise K3mlaError(f"{name} is on {t.device}, the call runs on cuda:{device}")
     return t.data_ptr()
 
 
@@ -271,17 +297,17 @@ def norm_rope_append(q: torch.Tensor, q_out: torch.Tensor, slab: torch.Tensor, l
     R = q.shape[0]
     B = pos0.shape[0]
     n_pages, L = slab.shape[0], slab.shape[1]
-    _here(slab, "slab")
+    dev = _here(slab)
     _check(load().k3mla_norm_rope_append(
-        _dev(q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _dev(q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
-        _opt(q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
-        _table(block_table, B), block_table.shape[1], _dev(pos0, torch.int32, (B,), "pos0"),
-        _opt(row_start, torch.int32, (B + 1,), "row_start"), _rows(c_kv, R, "c_kv", LORA), c_kv.stride(0),
-        _opt(c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE), k_rope.stride(0),
-        _opt(k_weight, torch.bfloat16, (ROPE,), "k_weight"), float(eps), _opt(inv_freq, torch.float32, (ROPE // 2,), "inv_freq"),
-        int(bool(interleaved)), B, R, _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
-        "k3mla_norm_rope_append")
+        _at(dev, q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _at(dev, q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
+        _opt_at(dev, q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"),
+        _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        _opt_at(dev, row_start, torch.int32, (B + 1,), "row_start"), _rows(c_kv, R, "c_kv", LORA, dev), c_kv.stride(0),
+        _opt_at(dev, c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE, dev), k_rope.stride(0),
+        _opt_at(dev, k_weight, torch.bfloat16, (ROPE,), "k_weight"), float(eps),
+        _opt_at(dev, inv_freq, torch.float32, (ROPE // 2,), "inv_freq"), int(bool(interleaved)), B, R,
+        _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_norm_rope_append")
 
 
 def compact_rows(slab: torch.Tensor, block_table: torch.Tensor, keep: torch.Tensor, keep_start: torch.Tensor,
@@ -294,12 +320,13 @@ def compact_rows(slab: torch.Tensor, block_table: torch.Tensor, keep: torch.Tens
     n = keep.shape[-1]
     if keep.dim() not in (1, 2) or (keep.dim() == 2 and keep.shape[0] not in (1, L)):
         raise K3mlaError(f"keep has shape {tuple(keep.shape)}, expected [n], [1, n] or [{L}, n]")
-    _here(slab, "slab")
+    dev = _here(slab)
     _check(load().k3mla_compact_rows(
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _table(block_table, B), block_table.shape[1],
-        _dev(keep, torch.int32, None, "keep"), n if keep.dim() == 2 and keep.shape[0] == L and L > 1 else 0, n,
-        _dev(keep_start, torch.int32, (B + 1,), "keep_start"), B, _opt(dev_err, torch.int32, (1,), "dev_err"),
-        _stream(stream)), "k3mla_compact_rows")
+        _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L,
+        _table(dev, block_table, B), block_table.shape[1],
+        _at(dev, keep, torch.int32, None, "keep"), n if keep.dim() == 2 and keep.shape[0] == L and L > 1 else 0, n,
+        _at(dev, keep_start, torch.int32, (B + 1,), "keep_start"), B, _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream, dev)), "k3mla_compact_rows")
 
 
 def chunk_views(block_table: torch.Tensor, pos0: torch.Tensor, row_start: torch.Tensor,
@@ -343,13 +370,16 @@ def chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tabl
 
 def window_decode_workspace_bytes(B: int, max_ctx: int, window: int, n_sink: int = 0,
                                   split_tokens: int = SPLIT_AUTO) -> int:
-    return int(load().k3mla_window_decode_workspace_bytes(B, max_ctx, window, n_sink, split_tokens))
+    return int(load().k3mla_window_decode_workspace_bytes(
+        _int(B, "B"), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _int(split_tokens, "split_tokens")))
 
 
 def window_split_tokens(B: int, max_ctx: int, window: int, n_sink: int = 0) -> int:
     """A split length for window_decode that keeps the current device busy with B slots; a slot's result
     bits then depend on it (see k3mla_window_split_tokens)."""
-    return int(load().k3mla_window_split_tokens(int(B), int(max_ctx), int(window), int(n_sink)))
+    return int(load().k3mla_window_split_tokens(_int(B, "B"), _int(max_ctx, "max_ctx"), _int(window, "window"),
+                                                _int(n_sink, "n_sink")))
 
 
 def window_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor, ctx_len: torch.Tensor,
@@ -360,18 +390,20 @@ def window_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tab
     out [B, 96, 128]; see k3mla_window_decode.  `workspace`: uint8, >= window_decode_workspace_bytes."""
     B = q_abs.shape[0]
     n_pages, L = slab.shape[0], slab.shape[1]
-    _here(slab, "slab")
+    dev = _here(slab)
     _check(load().k3mla_window_decode(
-        _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(block_table, B), block_table.shape[1], _dev(ctx_len, torch.int32, (B,), "ctx_len"),
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
-        _dev(out, torch.bfloat16, (B, H, V), "out"), _dev(workspace, torch.uint8, None, "workspace"), workspace.numel(),
-        B, int(max_ctx), int(window), int(n_sink), int(split_tokens), _opt(dev_err, torch.int32, (1,), "dev_err"),
-        _stream(stream)), "k3mla_window_decode")
+        _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1],
+        _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _int(split_tokens, "split_tokens"), _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)),
+        "k3mla_window_decode")
 
 
 def window_chunk_decode_workspace_bytes(B: int, R: int, max_ctx: int) -> int:
-    return int(load().k3mla_window_chunk_decode_workspace_bytes(B, R, max_ctx))
+    return int(load().k3mla_window_chunk_decode_workspace_bytes(_int(B, "B"), _int(R, "R"), _int(max_ctx, "max_ctx")))
 
 
 def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
@@ -384,15 +416,15 @@ def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
     R = q_abs.shape[0]
     B = pos0.shape[0]
     n_pages, L = slab.shape[0], slab.shape[1]
-    _here(slab, "slab")
+    dev = _here(slab)
     _check(load().k3mla_window_chunk_decode(
-        _dev(q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(block_table, B), block_table.shape[1], _dev(pos0, torch.int32, (B,), "pos0"),
-        _dev(row_start, torch.int32, (B + 1,), "row_start"), B, R,
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
-        _dev(out, torch.bfloat16, (R, H, V), "out"), _dev(workspace, torch.uint8, None, "workspace"), workspace.numel(),
-        int(max_ctx), int(window), int(n_sink), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
-        "k3mla_window_chunk_decode")
+        _at(dev, q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        _at(dev, row_start, torch.int32, (B + 1,), "row_start"), B, R,
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_window_chunk_decode")
 
 
 def decode_exact_workspace_bytes(B: int, max_ctx: int) -> int:
@@ -634,11 +666,12 @@ class Pool:
     def trim(self, slot: int, n_tokens: int, window: int, n_sink: int = 0) -> int:
         """Give back the pages of `slot` that no token from position n_tokens on can see (their number, or
         a negative status code)."""
-        return int(load().k3mla_pool_trim(self._h, slot, n_tokens, window, n_sink))
+        return int(load().k3mla_pool_trim(self._h, _int(slot, "slot"), _int(n_tokens, "n_tokens"), _int(window, "window"),
+                                          _int(n_sink, "n_sink")))
 
     def truncate(self, slot: int, new_len: int) -> int:
         """Give back the pages past the first new_len tokens (status code)."""
-        return int(load().k3mla_pool_truncate(self._h, slot, new_len))
+        return int(load().k3mla_pool_truncate(self._h, _int(slot, "slot"), _int(new_len, "new_len")))
 
     def refs(self, page: int) -> int:
         return int(load().k3mla_pool_page_refs(self._h, page))

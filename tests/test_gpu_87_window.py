@@ -558,3 +558,26 @@ def test_chunk_replayed_with_other_lengths(gpu_lib):
         assert torch.equal(out, c.chunk(p, s, 100, 2))
         slot, n = rows_to(s, p, 12)
         c.check(out, slot, n, 100, 2)
+
+
+def test_tensors_of_another_device_are_refused(gpu_lib, monkeypatch):
+    # (one GPU: the current device is made to look like another one)
+    c = Case(70, [100], 1)
+    out = torch.empty(1, H, V, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    table, ctx = torch.from_numpy(c.table).cuda(), torch.from_numpy(c.lens).cuda()
+    rows = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, H, 192, dtype=torch.bfloat16, device="cuda")
+    kv = torch.zeros(1, ROW, dtype=torch.bfloat16, device="cuda")
+    calls = (lambda: k3mla.window_decode(c.q, c.slab, 1, table, ctx, c.w, SCALE_BITS, out, ws, 128, 10),
+             lambda: k3mla.window_chunk_decode(c.q, c.slab, 1, table, ctx, rows, c.w, SCALE_BITS, out, ws, 128, 10),
+             lambda: k3mla.compact_rows(c.slab, table, rows, rows),
+             lambda: k3mla.norm_rope_append(q, q, c.slab, 1, table, ctx, None, kv[:, :512], kv[:, 512:]))
+    monkeypatch.setattr(k3mla, "_current_device", lambda: 1)
+    for call in calls:
+        with pytest.raises(k3mla.K3mlaError, match="is on cuda:0"):
+            call()
+    with pytest.raises(k3mla.K3mlaError, match="is on cuda:0"):
+        k3mla._rows(kv, 1, "c_kv", 512, 1)
+    with pytest.raises(k3mla.K3mlaError, match="CUDA tensor"):
+        k3mla.window_decode(c.q, c.slab.cpu(), 1, table, ctx, c.w, SCALE_BITS, out, ws, 128, 10)

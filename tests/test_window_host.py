@@ -194,3 +194,16 @@ def test_window_split_plan():
     assert k3mla.window_split_tokens(500, 4096, 1024, 0) >= 1024      # more slots than SM pairs: a split a slot
     assert k3mla.window_split_tokens(1, 32768, 4096, 4) < k3mla.window_split_tokens(16, 32768, 4096, 4)
     assert k3mla.window_split_tokens(0, 1, 1, 0) == 128
+
+
+def test_arguments_past_32_bits_are_refused():
+    for call in (lambda: k3mla.window_decode_workspace_bytes(1, 2 ** 32 + 64, 1), lambda: k3mla.window_split_tokens(1, 64, 2 ** 40),
+                 lambda: k3mla.window_chunk_decode_workspace_bytes(1, 2 ** 31, 64)):
+        with pytest.raises(k3mla.K3mlaError, match="32 bits"):
+            call()
+    pool = k3mla.Pool(n_slots=1, max_ctx=128)
+    with pytest.raises(k3mla.K3mlaError, match="32 bits"):
+        pool.trim(0, 0, 2 ** 32 + 1)
+    with pytest.raises(k3mla.K3mlaError, match="32 bits"):
+        pool.truncate(0, 2 ** 32)
+    pool.close()
