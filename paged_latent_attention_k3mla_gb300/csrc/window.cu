@@ -1268,14 +1268,13 @@ __global__ void __launch_bounds__(128) k3mla_window_merge_kernel(const WinParams
 // a tile's outputs leave while the next one's MMAs run.  The powers of two come off on the way out, W_UV's by TMEM
 // lane, o_lat's by column.
 constexpr int WX_TILE = 64;
-constexpr int WX_RING = 8;
+constexpr int WX_RING = 10;
 constexpr int WX_CHUNK = WX_TILE * 128;
 constexpr int WX_A = 8 * VH * 128;                    // W_UV[h]
-constexpr int WX_OUT = WX_TILE * VH * 2;              // a tile's bf16 outputs
-constexpr int WX_SMEM = WX_A + WX_RING * WX_CHUNK + WX_OUT + 1024;
+constexpr int WX_SMEM = WX_A + WX_RING * WX_CHUNK + 1024;
 constexpr int WX_EPI = 16;                            // warps 0..15 convert W_UV, then take the outputs
 constexpr int WX_THREADS = 32 * (WX_EPI + 2);         // ... one loads, one issues
-static_assert(WX_RING == LORA / 64, "a tile's operand fills the ring (wx_merge)");
+static_assert(WX_RING >= LORA / 64, "a whole tile's operand fits (wx_merge)");
 static_assert(WX_SMEM <= 225 * 1024, "shared memory, beside a few hundred static bytes");
 
 struct WxSmem {
@@ -1285,7 +1284,7 @@ struct WxSmem {
     int32_t abort_flag;
     uint64_t wait_ns;
     float wscale[VH];         // what undoes W_UV's powers of two
-    float rscale[2][WX_TILE]; // ... and o_lat's, by tile parity; 0: the row sees nothing, its output is 0
+    float rscale[WX_EPI];     // wx_merge: ... and o_lat's; 0: the row sees nothing, its output is 0
 };
 
 struct WxParams {
@@ -1357,7 +1356,7 @@ __device__ __forceinline__ void wx_merge(uint8_t* sb, WxSmem& sm, const WinParam
 #pragma unroll
         for (int half = 0; half < 2; ++half)
             *place(half) = *reinterpret_cast<const uint4*>(p.olat + at * LORA + 256 * half + 8 * lane);
-        if (lane == 0) sm.rscale[0][b] = p.oscale[at];
+        if (lane == 0) sm.rscale[b] = p.oscale[at];
     }
     if constexpr (WARPS > 1) {  // the groups meet in the row's first warp, by way of rows 8 .. 63 of the tile, which nobody has
         auto meet = [&](int w, int k) {
@@ -1405,7 +1404,7 @@ __device__ __forceinline__ void wx_merge(uint8_t* sb, WxSmem& sm, const WinParam
             *place(half) = make_uint4(pack_f16x2(a[0] * up, a[1] * up), pack_f16x2(a[2] * up, a[3] * up),
                                       pack_f16x2(a[4] * up, a[5] * up), pack_f16x2(a[6] * up, a[7] * up));
         }
-        if (lane == 0) sm.rscale[0][b] = inverse;
+        if (lane == 0) sm.rscale[b] = inverse;
     }
     fence_proxy_async_cta();  // the MMAs read the tile through the async proxy
     __syncwarp();
@@ -1422,7 +1421,6 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
     __shared__ WxSmem sm;
     uint8_t* sa = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sb = sa + WX_A;
-    uint16_t* so = reinterpret_cast<uint16_t*>(sb + WX_RING * WX_CHUNK);
     const int h = blockIdx.x, warp = threadIdx.x >> 5, lane = (int)lane_id();
     const int tiles = (p.R + WX_TILE - 1) / WX_TILE;
     if (threadIdx.x == 32 * WX_EPI) {
@@ -1505,43 +1503,32 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         const int q = warp & 3, cg = warp >> 2, tid = (int)threadIdx.x, v = 32 * q + lane;
         named_bar(1, 32 * WX_EPI);  // wscale is complete
         const float ws = sm.wscale[v];
-        auto scale_of = [&](int t) {  // o_lat's power of two of row tid of tile t
-            const int r = t * WX_TILE + tid;
-            return !MERGE && tid < WX_TILE && r < p.R ? p.oscale[(size_t)h * p.R + r] : 0.f;
+        auto scale_of = [&](int t) {  // undoes o_lat's power of two: lane j has row 16 cg + j of tile t
+            const int row = 16 * cg + (lane & 15), r = t * WX_TILE + row;
+            if (MERGE) return row < WX_EPI ? sm.rscale[row] : 0.f;
+            return r < p.R ? p.oscale[(size_t)h * p.R + r] : 0.f;
         };
         int it = 0;
         float next = scale_of(blockIdx.y);
         for (int t = blockIdx.y; t < tiles; t += gridDim.y, ++it) {
-            const int r0 = t * WX_TILE;
-            if (!MERGE && tid < WX_TILE) sm.rscale[it & 1][tid] = next;
+            const float rs = next;
             next = scale_of(t + gridDim.y);  // (a tile ahead: its latency stays off the path)
             if (ok) ok = __all_sync(0xFFFFFFFFu, wait_bar(&sm.d_full[it & 1], (uint32_t)(it >> 1) & 1u, sm, p.dev_err));
-            if (ok) {
-                tc_fence_after();
-                uint32_t acc[16];
-                tmem_ld16(tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(WX_TILE * (it & 1) + 16 * cg), acc);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.d_empty[it & 1]);
-                named_bar(1, 32 * WX_EPI);  // rscale is there, and the outputs of the tile before have left
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t acc[16];
+            tmem_ld16(tbase + ((uint32_t)(32 * q) << 16) + (uint32_t)(WX_TILE * (it & 1) + 16 * cg), acc);
+            tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.d_empty[it & 1]);
+            uint16_t* out = p.out + ((size_t)(t * WX_TILE + 16 * cg) * H + h) * VH + v;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float rs = sm.rscale[it & 1][16 * cg + j];
-                    const float x = rs == 0.f ? 0.f : __uint_as_float(acc[j]) * ws * rs;
-                    so[(16 * cg + j) * VH + v] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
-                }
-            } else {
-                named_bar(1, 32 * WX_EPI);
+            for (int j = 0; j < 16; ++j) {  // 64 bytes of a row a warp
+                const float s = __shfl_sync(0xFFFFFFFFu, rs, j);
+                const float x = s == 0.f ? 0.f : __uint_as_float(acc[j]) * ws * s;
+                if (t * WX_TILE + 16 * cg + j < p.R) out[(size_t)j * H * VH] = (uint16_t)(pack_bf16x2(x, 0.f) & 0xFFFFu);
             }
-            named_bar(1, 32 * WX_EPI);
-            if (ok)
-                for (int e = tid; e < WX_TILE * (VH / 8); e += 32 * WX_EPI) {
-                    const int r = e / (VH / 8), k = e % (VH / 8);
-                    if (r0 + r < p.R)
-                        reinterpret_cast<uint4*>(p.out + ((size_t)(r0 + r) * H + h) * VH)[k] =
-                            reinterpret_cast<const uint4*>(so + r * VH)[k];
-                }
         }
     }
     __syncwarp();
