@@ -1451,7 +1451,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
     const uint32_t tbase = sm.tmem_base;
     bool ok = true;
     if (warp == WX_EPI) {
-        if (lane == 0 && !MERGE) {
+        if (!MERGE && elect_one()) {
             griddep_wait();
             int g = 0;
             for (int t = blockIdx.y; t < tiles && ok; t += gridDim.y)
@@ -1466,7 +1466,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
             if (!ok) drain_inflight();
         }
     } else if (warp == WX_EPI + 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc = make_idesc_f16(128, WX_TILE);
             griddep_wait();  // (the bounded waits below start when o_lat is there)
             ok = wait_bar(&sm.w_ready, 0, sm, p.dev_err);
@@ -1500,7 +1500,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         griddep_wait();
         griddep_launch_dependents();
         if constexpr (MERGE != 0) wx_merge<MERGE>(sb, sm, win, h, ns);
-        const int q = warp & 3, cg = warp >> 2, tid = (int)threadIdx.x, v = 32 * q + lane;
+        const int q = warp & 3, cg = warp >> 2, v = 32 * q + lane;
         named_bar(1, 32 * WX_EPI);  // wscale is complete
         const float ws = sm.wscale[v];
         auto scale_of = [&](int t) {  // undoes o_lat's power of two: lane j has row 16 cg + j of tile t
@@ -1637,8 +1637,8 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                                          : (merge == 4 ? k3mla_window_expand_kernel<4> : k3mla_window_expand_kernel<1>);
     set_smem_attr(reinterpret_cast<const void*>(expand), WX_SMEM, attr_expand[merge == 4 ? 2 : merge]);
     // Three CTAs a head fill two rounds of the SMs where one leaves a third of them idle, but load and convert W_UV three
-    // times: 1,000 rows (16 tiles) 131.7 -> 130.0 us, 128 slots (two tiles, two CTAs) 28.7 -> 33.5 us.
-    return launch_pdl(expand, dim3(H, tiles >= 6 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st, "k3mla_window_expand_kernel", tm_w,
+    // times: 4,000 rows (63 tiles) 458 -> 446 us, 2,000 235 -> 231, 1,000 122.7 -> 122.2, but 600 75.0 -> 78.3, 250 37.8 -> 41.6.
+    return launch_pdl(expand, dim3(H, tiles >= 16 ? 3 : 1), dim3(WX_THREADS), WX_SMEM, st, "k3mla_window_expand_kernel", tm_w,
                       tm_o, x, p);
 }
 

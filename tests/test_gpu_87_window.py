@@ -306,6 +306,14 @@ def test_chunk_more_units_than_clusters(gpu_lib):
     assert c.err.item() == 0
 
 
+def test_chunk_of_many_tiles(gpu_lib):
+    # enough rows for several CTAs a head in the expansion, the last tile a part of one
+    c = Case(71, [1200], 1100)
+    got = c.chunk([100], [0, 1100], 30, 2)
+    c.check(got, [0] * 1100, [101 + r for r in range(1100)], 30, 2, rows=[*range(0, 1100, 61), 1023, 1024, 1087, 1088, 1099])
+    assert c.err.item() == 0
+
+
 def test_chunk_many_slots(gpu_lib):
     # more slots than one warp scans at once, most of them without new tokens
     rng = np.random.default_rng(5)
