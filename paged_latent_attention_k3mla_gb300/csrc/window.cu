@@ -38,9 +38,9 @@
 //
 // Measured, whole calls: decode of 64 slots over 4,100 seen tokens 69.7 us (324 MB, 0.68 of the copy rate), over 1,088 33.4
 // us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens 234 us (995 TFLOP/s, 0.52 of
-// the measured bf16 rate), of 1,000 rows over 300 122 us (29 of them the expansion).  Bounds: the page stream for long lists of pages (decode
-// 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which the score MMAs take 0.6), else the
-// chain through a unit and the expansion behind it (6 us).
+// the measured bf16 rate), of 1,000 rows over 300 122 us (29 of them the expansion).  Bounds: the page stream for long
+// lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which the score MMAs
+// take 0.6), else the chain through a unit and the expansion behind it (6 us).
 //
 // Every wait is bounded, as in decode.cu: after WAIT_NS it sets K3MLA_DEV_TIMEOUT and the roles run out.
 #include <cuda.h>
@@ -532,7 +532,8 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
 // before have read the old Q: each warp its quarter's rows, of every NPAR-th ring use, when it is through with its pages
 // of the unit before.
 template <bool MQ>
-__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int par, int base, int un)
+__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int par, int base,
+                                         int un)
 {
     using C = WCfg<MQ>;
     const int lane = (int)lane_id();
@@ -896,8 +897,8 @@ __device__ __forceinline__ float w_row_scale(float m, float& inverse)
 // O [rows x 512] f32 leaves TMEM, half the dims a warp, as f16 with a power of two per row: o_lat = O / l when the
 // unit is all its rows see, else the split's O (f32 there would take twice the stores).  Four lanes share a row: of 64
 // columns lane c holds 8 n + 2 c and 8 n + 2 c + 1 for n = 0 .. 7, and stores them side by side, 32 bytes, so that a
-// store instruction writes whole lines (with a row a lane, a sector each of 32 lines: 1 x 1000 rows 129 us, so 123).  The dims of
-// o_lat and of the splits' O thus lie in that order; the expansion puts W_UV into the same.
+// store instruction writes whole lines (with a row a lane, a sector each of 32 lines: 1 x 1000 rows 129 us, so 123).
+// The dims of o_lat and of the splits' O thus lie in that order; the expansion puts W_UV into the same.
 // Reading TMEM sets the pace (some 64 bytes a clock and SM: 2.1 us for a chunk's 256 KB), so it is read once: the
 // power of two comes from the row's first 32 entries, with room for 2^8 times their largest, and the row's
 // largest entry is found on the way.  A row that it shows to have left the range, or to lie far below it, has its
@@ -1032,7 +1033,8 @@ template <bool MQ> __device__ __forceinline__ void w_prefetch(WSmem<MQ>& sm, con
             const int done = gp + i - W_AHEAD + 1;  // pages whose P has to be there
             if (done <= 0) continue;  // (a cluster's first pages are loaded at once)
             if (!__all_sync(0xFFFFFFFFu, w_count<MQ>(&sm.pv_pages, done))) return;
-            if (elect_one() && y < p.n_pages * p.n_layers * PAGE && *reinterpret_cast<volatile int32_t*>(&sm.pv_pages) <= done + 2)
+            if (elect_one() && y < p.n_pages * p.n_layers * PAGE &&
+                *reinterpret_cast<volatile int32_t*>(&sm.pv_pages) <= done + 2)
                 for (int x = 0; x < 3; ++x) tma_prefetch_3d(&tm_page, 0, y, 3 * x);
             __syncwarp();
         }
@@ -1358,7 +1360,7 @@ __device__ __forceinline__ void wx_merge(uint8_t* sb, WxSmem& sm, const WinParam
             *place(half) = *reinterpret_cast<const uint4*>(p.olat + at * LORA + 256 * half + 8 * lane);
         if (lane == 0) sm.rscale[b] = p.oscale[at];
     }
-    if constexpr (WARPS > 1) {  // the groups meet in the row's first warp, by way of rows 8 .. 63 of the tile, which nobody has
+    if constexpr (WARPS > 1) {  // the groups meet in the row's first warp, by way of the tile's unused rows 8 .. 63
         auto meet = [&](int w, int k) {
             return reinterpret_cast<float4*>(sb + (w >> 1) * WX_CHUNK + 1024 + (w & 1) * 2048) + 32 * k + lane;
         };
