@@ -88,6 +88,7 @@ constexpr int W_THREADS = 512;  // 128 registers a thread
 // quarter), one that plans the units of both CTAs, one for the rows that see nothing, one that prefetches into L2 (decode)
 constexpr int WW_HALVES = 4, WW_PV = 5, WW_EPI1 = 6, WW_PLAN = 10, WW_EMPTY = 11, WW_AHEAD = 12;
 constexpr int W_PLANS = 8;         // planned units kept
+constexpr uint32_t SUSPEND_NS = 20000;  // a wait sleeps at most 20 us at a time
 constexpr uint32_t WB_OUT = 1;     // named barrier of the epilogue warps
 constexpr int W_EPI = 8;
 constexpr uint32_t F_RESCALE = 1, F_NOT_FINITE = 2;  // a row's reference moved / an unseen token's score is not finite
