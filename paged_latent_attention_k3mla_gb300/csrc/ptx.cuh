@@ -123,21 +123,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t addr, uint32_t pa
     return ok != 0;
 }
 
-// The cluster-scope wait above with a time (ns) that the thread may be suspended for before the answer is "not yet": a
-// long wait then costs few issue slots.
-__device__ __forceinline__ bool mbar_try_wait_cluster_for(uint32_t addr, uint32_t parity, uint32_t ns)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity), "r"(ns)
-        : "memory");
-    return ok != 0;
-}
-
 // ---------------------------------------------------------------- cluster
 
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank)

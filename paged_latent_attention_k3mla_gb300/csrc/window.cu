@@ -88,7 +88,6 @@ constexpr int W_THREADS = 512;  // 128 registers a thread
 // quarter), one that plans the units of both CTAs, one for the rows that see nothing, one that prefetches into L2 (decode)
 constexpr int WW_HALVES = 4, WW_PV = 5, WW_EPI1 = 6, WW_PLAN = 10, WW_EMPTY = 11, WW_AHEAD = 12;
 constexpr int W_PLANS = 8;         // planned units kept
-constexpr uint32_t SUSPEND_NS = 20000;  // a wait sleeps at most 20 us at a time
 constexpr uint32_t WB_OUT = 1;     // named barrier of the epilogue warps
 constexpr int W_EPI = 8;
 constexpr uint32_t F_RESCALE = 1, F_NOT_FINITE = 2;  // a row's reference moved / an unseen token's score is not finite
@@ -189,7 +188,8 @@ template <bool MQ> __device__ __noinline__ bool w_wait_slow(uint32_t bar, uint32
 {
     WSmem<MQ>& sm = w_smem<MQ>();
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_cluster_for(bar, parity, SUSPEND_NS)) {
+    for (uint32_t n = 1; !mbar_try_wait_cluster(bar, parity); ++n) {
+        if (n & 127u) continue;  // (the clock is slow to read: looked at every time, 1 % of the whole call)
         if (aborted(sm)) return false;
         if (globaltimer() - t0 > sm.wait_ns) {
             *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
