@@ -36,9 +36,9 @@
 //     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get their
 //     NaN from its score.
 //
-// Measured, whole calls: decode of 64 slots over 4,100 seen tokens 69.7 us (324 MB, 0.68 of the copy rate), over 1,088 33.4
-// us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens 234 us (995 TFLOP/s, 0.52 of
-// the measured bf16 rate), of 1,000 rows over 300 122 us (29 of them the expansion).  Bounds: the page stream for long
+// Measured, whole calls: decode of 64 slots over 4,100 seen tokens 69.0 us (324 MB, 0.69 of the copy rate), over 1,088 33.2
+// us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens 232 us (1,003 TFLOP/s, 0.52 of
+// the measured bf16 rate), of 1,000 rows over 300 120.5 us (29 of them the expansion).  Bounds: the page stream for long
 // lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which the score MMAs
 // take 0.6), else the chain through a unit and the expansion behind it (6 us).
 //
