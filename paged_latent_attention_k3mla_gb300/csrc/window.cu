@@ -1685,9 +1685,13 @@ extern "C" size_t k3mla_window_decode_workspace_bytes(int B, int max_ctx, int wi
 extern "C" int k3mla_window_split_tokens(int B, int max_ctx, int window, int n_sink)
 {
     if (B <= 0 || max_ctx <= 0 || window < 1 || n_sink < 0) return TILE;
-    // as many splits a slot as give every pair of SMs one, none shorter than a tile
+    // As many splits a slot as give every pair of SMs one, none shorter than a tile.  Two to four slots leave the
+    // expansion's CTAs, one a head, an SM each, where they ready W_UV meanwhile: four slots over 4,096 tokens 25.7 -> 24.6 us,
+    // over 1,000 21.4 -> 20.5, three over 4,096 24.8 -> 23.7; but one slot 21.4 -> 21.7, six over 2,000 23.7 -> 25.9, eight
+    // over 4,096 30.0 -> 34.2.
     const long long tiles = (w_max_pages(max_ctx, window, n_sink) * PAGE + TILE - 1) / TILE;
-    const long long want = std::max(1, sm_count() / 2 / B);
+    const int sms = sm_count();
+    const long long want = std::max(1, (B > 1 && B <= 4 && sms > H ? sms - H : sms) / 2 / B);
     return (int)std::min<long long>((tiles + want - 1) / want * TILE, 0x7FFFFFFF / TILE * TILE);
 }
 
