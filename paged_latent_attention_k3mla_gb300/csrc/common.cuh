@@ -22,6 +22,9 @@ constexpr int TILE = K3MLA_TILE;        // 128
 constexpr int WROWS_PER_HEAD = NOPE + VH;  // 256
 constexpr int SPLIT_MAX = K3MLA_SPLIT_MAX;  // 4096: longest split of the default rule
 
+// ceil(a / b) for a >= 0, b > 0, without the sum that leaves an int where a or b is near 2^31.
+__host__ __device__ inline int ceil_div(int a, int b) { return a / b + (a % b != 0); }
+
 // Split length of a slot whose (clamped) context is n tokens: split_tokens when positive, else the
 // default rule -- ceil(n / SPLIT_MAX) splits of equal length rounded up to the 128-token tile.  It
 // depends on n and constants only, never on the batch, the GPU or the page ids, so a slot is cut
@@ -29,20 +32,20 @@ constexpr int SPLIT_MAX = K3MLA_SPLIT_MAX;  // 4096: longest split of the defaul
 __host__ __device__ inline int slot_split(int n, int split_tokens)
 {
     if (split_tokens > 0) return split_tokens;
-    const int ns = n <= SPLIT_MAX ? 1 : (n + SPLIT_MAX - 1) / SPLIT_MAX;
-    const int per = (n + ns - 1) / ns;
+    const int ns = n <= SPLIT_MAX ? 1 : ceil_div(n, SPLIT_MAX);
+    const int per = ceil_div(n, ns);
     const int t = (per + TILE - 1) / TILE * TILE;
     return t < TILE ? TILE : t;
 }
 
 // Splits that hold tokens for a slot of n tokens cut every `split` tokens (0 for an empty context).
-__host__ __device__ inline int slot_nsplit(int n, int split) { return n <= 0 ? 0 : (n + split - 1) / split; }
+__host__ __device__ inline int slot_nsplit(int n, int split) { return n <= 0 ? 0 : ceil_div(n, split); }
 
 // Upper bound of slot_nsplit over contexts up to max_ctx: the split count of the launch's grid.
 __host__ __device__ inline int launch_nsplit(int max_ctx, int split_tokens)
 {
     const int s = split_tokens > 0 ? split_tokens : SPLIT_MAX;
-    return (max_ctx + s - 1) / s;
+    return ceil_div(max_ctx, s);
 }
 
 // Per-thread error text for k3mla_last_error().
