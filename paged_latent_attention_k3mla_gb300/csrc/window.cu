@@ -235,8 +235,15 @@ __host__ __device__ inline int w_pages(int n_lo, int n_hi, int window, int n_sin
     return nsp + (n_hi + PAGE - 1) / PAGE - wp0;
 }
 
-// Unit u (a whole warp, every lane the same answer).
-template <bool MQ> __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report)
+// Where the search for a chunk's group stands: a cluster's units come in ascending order, so each search goes on in
+// the block of 32 slots where the one before ended, and row_start is gone through once, whatever the number of slots.
+struct WScan {
+    int b0 = 0, before = 0;  // the block's first slot; the groups of the slots before it
+};
+
+// Unit u (a whole warp, every lane the same answer); npg is -1 where neither it nor a later one exists.
+template <bool MQ>
+__device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report, WScan& scan)
 {
     g.npg = 0;
     g.first = 0;
@@ -250,10 +257,9 @@ template <bool MQ> __device__ __forceinline__ void w_unit(WUnit& g, const WinPar
         // group u / 3 of up to four rows, counted slot by slot: 32 slots a step
         const int gi = u / 3, lane = (int)lane_id();
         g.hb = u % 3;
-        int before = 0;
         bool found = false;
-        for (int b0 = 0; b0 < p.B && !found; b0 += 32) {
-            const int b = b0 + lane;
+        while (scan.b0 < p.B) {
+            const int b = scan.b0 + lane;
             int lo = 0, nb = 0;
             if (b < p.B) {
                 lo = max(0, p.row_start[b]);
@@ -266,18 +272,23 @@ template <bool MQ> __device__ __forceinline__ void w_unit(WUnit& g, const WinPar
                 const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
                 if (lane >= o) upto += v;
             }
-            const unsigned past = __ballot_sync(0xFFFFFFFFu, before + upto > gi);
+            const unsigned past = __ballot_sync(0xFFFFFFFFu, scan.before + upto > gi);
             if (past) {
                 const int src = __ffs(past) - 1;
-                const int j = 4 * (gi - before - __shfl_sync(0xFFFFFFFFu, upto - mine, src));
-                g.b = b0 + src;
+                const int j = 4 * (gi - scan.before - __shfl_sync(0xFFFFFFFFu, upto - mine, src));
+                g.b = scan.b0 + src;
                 g.row0 = __shfl_sync(0xFFFFFFFFu, lo, src) + j;
                 g.rows = min(4, __shfl_sync(0xFFFFFFFFu, nb, src) - j);
                 found = true;
+                break;
             }
-            before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            scan.before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+            scan.b0 += 32;
         }
-        if (!found) return;
+        if (!found) {
+            g.npg = -1;
+            return;
+        }
         const int64_t n0 = (int64_t)p.pos0[g.b] + (g.row0 - p.row_start[g.b]) + 1;
         const int64_t n1 = n0 + g.rows - 1;
         if (report && n1 > p.cap && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
@@ -394,10 +405,11 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
     const int lane = (int)lane_id();
     bool ok = true;
     int n = 0;
+    WScan scan;
     for (int u = (int)blockIdx.x >> 1; ok; u += (int)gridDim.x >> 1) {
         WUnit g;
         g.npg = -1;
-        if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0);
+        if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0, scan);
         if (g.npg == 0) continue;
         if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3) && (MQ || w_count<MQ>(&sm.ahead_units, n - 6));
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -1766,8 +1778,9 @@ extern "C" int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* 
         return K3MLA_E_WORKSPACE;
     }
     const long long units = 3ll * (((long long)R + 3ll * B) / 4);  // sum over slots of ceil(n_b / 4), at most
-    if (units > 0x3FFFFFFFll || (long long)R * H > 0x7FFFFFFFll) {
-        set_error("k3mla_window_chunk_decode: too many rows");
+    // (the planner's one pass over 2^20 slots takes some 30 ms, far inside the bounded waits for its first unit)
+    if (units > 0x3FFFFFFFll || (long long)R * H > 0x7FFFFFFFll || B > 1 << 20) {
+        set_error("k3mla_window_chunk_decode: too many rows or slots");
         return K3MLA_E_INVALID;
     }
     if (!device_ok()) return K3MLA_E_DEVICE;

@@ -1,4 +1,5 @@
-"""The windowed operators where their arguments or values are far out: split lengths near 2^31."""
+"""The windowed operators where their arguments or values are far out: split lengths near 2^31, many idle slots, single
+infinities, waits that run out."""
 from __future__ import annotations
 
 import numpy as np
@@ -26,3 +27,30 @@ def test_a_split_as_long_as_an_int_holds_is_one_split(gpu_lib):
         k3mla.paged_decode(c.q, c.slab, 1, table, lens, c.w, SCALE_BITS, out[i], ws, c.max_ctx, split, dev_err=c.err)
     torch.cuda.synchronize()
     assert torch.equal(out[0], out[1]) and not torch.isnan(out.float()).any() and c.err.item() == 0
+
+
+def test_chunk_of_a_few_among_many_idle_slots(gpu_lib):
+    # the planner passes every slot once: without that, 60,000 slots of which four have new rows take seconds, and
+    # the waits for the units behind them run out
+    B = 60_000
+    new = np.zeros(B, np.int64)
+    new[[0, 31, 32_000, B - 1]] = (5, 1, 130, 9)
+    lens = np.where(new > 0, new + 70, 0)
+    R = int(new.sum())
+    c = Case(81, lens.tolist(), R)
+    start = np.concatenate([[0], np.cumsum(new)])
+    got = c.chunk(lens - new, start, 40, 3)
+    assert c.err.item() == 0
+    slot = np.repeat(np.arange(B), new)
+    n = [int(lens[b] - new[b] + r - start[b] + 1) for r, b in enumerate(slot)]
+    c.check(got, slot.tolist(), n, 40, 3, rows=range(0, R, 6))
+    # none at all: every row is outside every slot
+    got = c.chunk(lens - new, np.zeros(B + 1), 40, 3)
+    assert torch.all(got == 0) and c.err.item() == 0
+
+
+def test_chunk_of_more_slots_than_are_planned_is_refused(gpu_lib):
+    c = Case(82, [70], 1)
+    with pytest.raises(k3mla.K3mlaError, match="slots"):
+        c.table = np.zeros((2 ** 20 + 1, 1), np.int32)
+        c.chunk(np.zeros(2 ** 20 + 1), np.zeros(2 ** 20 + 2), 40, 3)
