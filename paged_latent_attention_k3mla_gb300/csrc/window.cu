@@ -33,8 +33,8 @@
 //     TMEM; one plans the units of both CTAs ahead.
 //   * Unseen tokens.  Their scores are replaced (never multiplied).  p = 0 times a NaN or an infinity would still be
 //     NaN, so where an unseen token's score shows that its row holds one, those among the page's unseen latents
-//     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get their
-//     NaN from its score.
+//     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get a NaN for
+//     their p of it (its score may be -inf, whose p is 0, and 0 times the latent that was there is NaN).
 //
 // Measured, whole calls: decode of 64 slots over 4,100 seen tokens 69.0 us (324 MB, 0.69 of the copy rate), over 1,088 33.2
 // us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens 232 us (1,003 TFLOP/s, 0.52 of
@@ -141,6 +141,7 @@ template <bool MQ> struct __align__(1024) WSmem {
     uint64_t epi_hidden;                 // to the epilogue warps: the tokens of page epi_page that not all rows see
     uint32_t epi_cmd;                    // ... and what to do, E_ bits
     int32_t epi_page;
+    int32_t epi_t0;                      // the first token of that page
     int32_t epi_b, epi_s, epi_hb, epi_row0, epi_rows, epi_n0, epi_single;
     int32_t abort_flag;
     int32_t* dev_err;
@@ -825,7 +826,10 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                         sm.epi_cmd = cmd;
                         sm.epi_page = a;
                         // the rows' contexts are consecutive, n_lo .. n_hi: the tokens that not all of them see
-                        sm.epi_hidden = ~w_between(p, g.n_hi - p.window, n_lo, PAGE * w_logical(g, i));
+                        sm.epi_t0 = PAGE * w_logical(g, i);
+                        sm.epi_hidden = ~w_between(p, g.n_hi - p.window, n_lo, sm.epi_t0);
+                        sm.epi_rows = g.rows;
+                        sm.epi_n0 = g.n0;
                         mbar_arrive(&sm.epi_req);
                         ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
                     }
@@ -1057,30 +1061,45 @@ template <bool MQ> __device__ __forceinline__ void w_prefetch(WSmem<MQ>& sm, con
 }
 
 // The NaNs and infinities among the latents of page a's tokens that not all rows of the unit see become zero: the rows
-// that do not see them have p = 0 there, which only a finite latent turns into 0.  (Rare: the scores have shown that
-// there are some.  Looking every masked page through took the chunk of 1 x 1000 rows from 137 to 152 us.)
-template <bool MQ> __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, int a, uint64_t hidden, int w)
+// that do not see them have p = 0 there, which only a finite latent turns into 0.  The rows of a chunk's unit that do see
+// such a token get NaN, as they would from the latent itself whatever their p (0 too), by way of that p.  (Rare: the
+// scores have shown that there are some.  Looking every masked page through took the chunk of 1 x 1000 rows from 137 to
+// 152 us.)
+template <bool MQ>
+__device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, int a, uint64_t hidden, int w)
 {
+    using C = WCfg<MQ>;
     const int lane = (int)lane_id();
 #pragma unroll 1
     for (int t = w; t < PAGE; t += W_EPI) {  // a warp a token: 64 pieces of 16 bytes, two a lane
         if (!(hidden >> t & 1ull)) continue;
         const int q = (2 * a + (t >= HALF ? 1 : 0)) % WN_HALF;
         uint8_t* at = sm.u.c1.ring[q] + (t & (HALF - 1)) * 128 + (lane & 7) * 16;
+        bool found = false;
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
             uint4* piece = reinterpret_cast<uint4*>(at + ((lane >> 3) + 4 * x) * HCHUNK);
-            uint4 v = *piece;
+            const uint4 v = *piece;
             auto finite = [](uint32_t b) {  // bf16 with all exponent bits set: NaN or infinity
                 if ((b & 0x7F80u) == 0x7F80u) b &= 0xFFFF0000u;
                 if ((b & 0x7F800000u) == 0x7F800000u) b &= 0x0000FFFFu;
                 return b;
             };
-            v.x = finite(v.x), v.y = finite(v.y), v.z = finite(v.z), v.w = finite(v.w);
-            *piece = v;
+            const uint4 f = make_uint4(finite(v.x), finite(v.y), finite(v.z), finite(v.w));
+            found = found || f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
+            *piece = f;
+        }
+        if (MQ && __any_sync(0xFFFFFFFFu, found)) {
+#pragma unroll 1
+            for (int qd = 0; qd < sm.epi_rows; ++qd) {
+                const int n = w_clamp(sm.epi_n0 + qd, p.cap);
+                if (w_between(p, n - p.window, n, sm.epi_t0) >> t & 1ull)
+                    *reinterpret_cast<uint16_t*>(sm.u.c1.recv[a % C::NPBUF] + pt_chunk_off(C::RPQ * qd + lane, t >> 3) +
+                                                 2 * (t & 7)) = 0x7FFFu;
+            }
         }
     }
-    fence_proxy_async_cta();  // the MMAs read the latents through the async proxy
+    fence_proxy_async_cta();  // the MMAs read the latents and P through the async proxy
 }
 
 // Epilogue warp: the TMEM lanes of its quarter, the dims of its half.
@@ -1112,7 +1131,7 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
             singles += single;
             continue;
         }
-        if (cmd & E_CLEAR) w_clear<MQ>(sm, page, sm.epi_hidden, quarter + 4 * half);
+        if (cmd & E_CLEAR) w_clear<MQ>(sm, p, page, sm.epi_hidden, quarter + 4 * half);
         const float* al = reinterpret_cast<const float*>(sm.u.c1.recv[page % C::NPBUF] + C::META_ALPHA);
         const float f = (cmd & E_RESCALE) && row < C::ROWS ? al[row] : 1.f;
         if (__any_sync(0xFFFFFFFFu, f != 1.f)) {  // some row of this warp moved its reference

@@ -54,3 +54,35 @@ def test_chunk_of_more_slots_than_are_planned_is_refused(gpu_lib):
     with pytest.raises(k3mla.K3mlaError, match="slots"):
         c.table = np.zeros((2 ** 20 + 1, 1), np.int32)
         c.chunk(np.zeros(2 ** 20 + 1), np.zeros(2 ** 20 + 2), 40, 3)
+
+
+def relative(a, b):
+    """Per row and head: the distance of a from b, relative to b."""
+    a, b = a.double(), b.double()
+    return (a - b).norm(dim=-1) / b.norm(dim=-1)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+@pytest.mark.parametrize("token", [200, 201, 202, 203])
+@pytest.mark.parametrize("dim", [3, 520])
+def test_one_infinite_entry_is_the_same_for_a_chunk_and_its_rows_decodes(gpu_lib, dim, token, value):
+    # Rows 0 .. 23 at positions 196 .. 219, window 6: the six rows from the token's own on see it, and by the token's
+    # place in its group of four some rows of the same group do not.  Its score is +inf or -inf by the query's sign
+    # (heads in turn).  In a latent entry (3) the infinity makes all that see it NaN, p = 0 included; in the rope part
+    # (520) it only reaches the score: +inf is NaN, -inf leaves the token out.
+    c = Case(83, [220], 24)
+    c.q[:, 0::2, dim], c.q[:, 1::2, dim] = 1.0, -1.0
+    clean = c.chunk([196], [0, 24], 6, 0)
+    c.slab[int(c.table[0, token // PAGE]), 1, token % PAGE, dim] = value
+    got = c.chunk([196], [0, 24], 6, 0)
+    one = torch.cat([c.decode(6, 0, ctx=[197 + r], q=c.q[r:r + 1]) for r in range(24)])
+    sees = torch.tensor([token in range(191 + r, 197 + r) for r in range(24)], device="cuda")
+    assert sees.sum() == 6
+    up = (c.q[..., dim].float() * value > 0) | (dim < 512)
+    want = (sees[:, None] & up)[..., None].expand(24, H, V)
+    assert torch.equal(torch.isnan(got), want) and torch.equal(torch.isnan(one), want)
+    assert torch.equal(got[~sees], clean[~sees])
+    if dim >= 512:
+        # each is within 0.01 of the definition per head (2^-8 from the output and from p each, near-orthogonal rows)
+        assert relative(got, one)[sees[:, None] & ~up].max() <= 0.02
+    assert c.err.item() == 0
