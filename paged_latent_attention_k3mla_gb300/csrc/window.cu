@@ -175,6 +175,8 @@ struct WinParams {
     int B, R, max_pages, n_pages, n_layers, layer, cap;  // cap: the longest context (min of max_ctx and the table)
     int window, n_sink, split_tokens, nsplit, n_units;
     float kscale;                        // scale * log2(e) > 0
+    uint64_t wait_ns;                    // bounded-wait limit: WAIT_NS, shorter only from the diagnostic entries
+    int32_t withhold;                    // diagnostic only, 0 otherwise: page k - 1 of a unit has its first third never loaded
 };
 
 template <bool MQ> __device__ __forceinline__ WSmem<MQ>& w_smem()
@@ -355,11 +357,11 @@ struct WLookup {
 };
 
 template <bool MQ>
-__device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, int32_t* dev_err)
+__device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, const WinParams& p)
 {
     using C = WCfg<MQ>;
-    sm.wait_ns = WAIT_NS;
-    sm.dev_err = dev_err;
+    sm.wait_ns = p.wait_ns;
+    sm.dev_err = p.dev_err;
     sm.abort_flag = 0;
 #pragma unroll 1
     for (int i = 0; i < 8; ++i) {
@@ -492,7 +494,8 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
                 for (int x = 0; x < 3 && ok; ++x) {
                     if ((base + 3 * i + x) % C::NPROD != t) continue;
                     const int u = take(base + 3 * i + x, THIRD);
-                    if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+                    if (ok && (x > 0 || i + 1 != p.withhold))  // (diagnostic: a load never issued)
+                        tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
                 }
             }
             __syncwarp();
@@ -1163,7 +1166,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     WSmem<MQ>& sm = w_smem<MQ>();
     const uint32_t rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = lane_id();
     if (threadIdx.x == 0) {
-        w_init(sm, rank, p.dev_err);
+        w_init(sm, rank, p);
         fence_mbarrier_init_cluster();
     }
     if (warp == 4) {
@@ -1193,6 +1196,9 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
         else if (warp == WW_EMPTY) w_empty_rows<MQ>(p);
         else if (!MQ && warp == WW_AHEAD) w_prefetch<MQ>(sm, tm_page, p);
     }
+    // After an abort a role leaves wherever it stands, with copies and MMAs of its own or of others still under way: they
+    // land before the CTA gives its shared memory and its TMEM back.
+    if (aborted(sm)) drain_inflight();
     __syncwarp();
     tc_fence_before();
     cluster_sync();
@@ -1700,6 +1706,7 @@ static int w_check(const char* who, const uint16_t* q_abs, const uint16_t* slab,
     p.n_pages = n_pages, p.n_layers = n_layers, p.layer = layer, p.max_pages = max_pages;
     p.cap = (int)std::min<long long>(std::min(max_ctx, 0x7FFFFF00), (long long)max_pages * PAGE);
     p.window = window, p.n_sink = n_sink, p.nsplit = 1;
+    p.wait_ns = WAIT_NS;
     return K3MLA_OK;
 }
 
@@ -1726,11 +1733,11 @@ extern "C" int k3mla_window_split_tokens(int B, int max_ctx, int window, int n_s
     return (int)std::min<long long>((tiles + want - 1) / want * TILE, 0x7FFFFFFF / TILE * TILE);
 }
 
-extern "C" int k3mla_window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
-                                   const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
-                                   const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
-                                   size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
-                                   int32_t* dev_err, void* stream)
+static int window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                         const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                         const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace, size_t ws_bytes, int B,
+                         int max_ctx, int window, int n_sink, int split_tokens, int32_t* dev_err, void* stream,
+                         uint64_t wait_ns, int withhold)
 {
     WinParams p;
     if (B < 0 || split_tokens < 0 || split_tokens % TILE != 0) {
@@ -1758,6 +1765,8 @@ extern "C" int k3mla_window_decode(const uint16_t* q_abs, const uint16_t* slab, 
     if (!device_ok()) return K3MLA_E_DEVICE;
     p.ctx_len = ctx_len;
     p.dev_err = dev_err;
+    p.wait_ns = wait_ns;
+    p.withhold = withhold;
     p.B = p.R = B;
     p.split_tokens = split_tokens;
     p.nsplit = ns;
@@ -1766,17 +1775,46 @@ extern "C" int k3mla_window_decode(const uint16_t* q_abs, const uint16_t* slab, 
                            reinterpret_cast<cudaStream_t>(stream));
 }
 
+extern "C" int k3mla_window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                                   const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                                   const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                                   size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
+                                   int32_t* dev_err, void* stream)
+{
+    return window_decode(q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, ctx_len, w_kv_b, scale_bf16, out,
+                         workspace, ws_bytes, B, max_ctx, window, n_sink, split_tokens, dev_err, stream, WAIT_NS, 0);
+}
+
+static bool w_diag_check(const char* who, int withhold_page, uint32_t wait_us)
+{
+    if (withhold_page >= 1 && withhold_page < 1 << 30 && wait_us >= 100 && wait_us <= 100000) return true;
+    set_error("%s: 1 <= withhold_page < 2^30 and 100 <= wait_us <= 100000", who);
+    return false;
+}
+
+extern "C" int k3mla_diag_window_timeout(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                                         const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                                         const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                                         size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
+                                         int withhold_page, uint32_t wait_us, int32_t* dev_err, void* stream)
+{
+    if (!w_diag_check("k3mla_diag_window_timeout", withhold_page, wait_us)) return K3MLA_E_INVALID;
+    return window_decode(q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, ctx_len, w_kv_b, scale_bf16, out,
+                         workspace, ws_bytes, B, max_ctx, window, n_sink, split_tokens, dev_err, stream,
+                         (uint64_t)wait_us * 1000ull, withhold_page + 1);
+}
+
 extern "C" size_t k3mla_window_chunk_decode_workspace_bytes(int B, int R, int max_ctx)
 {
     if (B <= 0 || R <= 0 || max_ctx <= 0) return 0;
     return w_layout(R, 1).total;
 }
 
-extern "C" int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
-                                         const int32_t* block_table, int max_pages_per_slot, const int32_t* pos0,
-                                         const int32_t* row_start, int B, int R, const uint16_t* w_kv_b,
-                                         uint16_t scale_bf16, uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx,
-                                         int window, int n_sink, int32_t* dev_err, void* stream)
+static int window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                               const int32_t* block_table, int max_pages_per_slot, const int32_t* pos0,
+                               const int32_t* row_start, int B, int R, const uint16_t* w_kv_b, uint16_t scale_bf16,
+                               uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx, int window, int n_sink,
+                               int32_t* dev_err, void* stream, uint64_t wait_ns, int withhold)
 {
     WinParams p;
     if (B < 0 || R < 0 || (B == 0 && R > 0)) {
@@ -1806,9 +1844,34 @@ extern "C" int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* 
     p.pos0 = pos0;
     p.row_start = row_start;
     p.dev_err = dev_err;
+    p.wait_ns = wait_ns;
+    p.withhold = withhold;
     p.B = B;
     p.R = R;
     p.n_units = (int)units;
     return w_launch<true>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), w_layout(R, 1), p,
                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                                         const int32_t* block_table, int max_pages_per_slot, const int32_t* pos0,
+                                         const int32_t* row_start, int B, int R, const uint16_t* w_kv_b,
+                                         uint16_t scale_bf16, uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx,
+                                         int window, int n_sink, int32_t* dev_err, void* stream)
+{
+    return window_chunk_decode(q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, pos0, row_start, B, R, w_kv_b,
+                               scale_bf16, out, workspace, ws_bytes, max_ctx, window, n_sink, dev_err, stream, WAIT_NS, 0);
+}
+
+extern "C" int k3mla_diag_window_chunk_timeout(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers,
+                                               int layer, const int32_t* block_table, int max_pages_per_slot,
+                                               const int32_t* pos0, const int32_t* row_start, int B, int R,
+                                               const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                                               size_t ws_bytes, int max_ctx, int window, int n_sink, int withhold_page,
+                                               uint32_t wait_us, int32_t* dev_err, void* stream)
+{
+    if (!w_diag_check("k3mla_diag_window_chunk_timeout", withhold_page, wait_us)) return K3MLA_E_INVALID;
+    return window_chunk_decode(q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, pos0, row_start, B, R, w_kv_b,
+                               scale_bf16, out, workspace, ws_bytes, max_ctx, window, n_sink, dev_err, stream,
+                               (uint64_t)wait_us * 1000ull, withhold_page + 1);
 }

@@ -34,6 +34,7 @@ EXPORTS = (
     "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_pool_trim",
     "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
+    "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
 )
 
 # Size of the library's built-in decode scratch (K3MLA_NOALLOC_SCRATCH_BYTES).
@@ -104,6 +105,10 @@ def load(build_if_needed: bool = True):
             "k3mla_window_decode": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
             "k3mla_window_chunk_decode_workspace_bytes": ([I, I, I], SZ),
             "k3mla_window_chunk_decode": ([P, P, I, I, I, P, I, P, P, I, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, P, P], I),
+            "k3mla_diag_window_timeout": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, I,
+                                           ctypes.c_uint32, P, P], I),
+            "k3mla_diag_window_chunk_timeout": ([P, P, I, I, I, P, I, P, P, I, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, I,
+                                                 ctypes.c_uint32, P, P], I),
             "k3mla_pool_trim": ([P, I, I, I, I], I),
             "k3mla_pool_truncate": ([P, I, I], I),
             "k3mla_compact_rows": ([P, I, I, P, I, P, I64, I, P, I, P, P], I),
@@ -596,6 +601,46 @@ def diag_decode_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
         _dev(out, torch.bfloat16, (B, H, V), "out"), None, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
         B, int(max_ctx), int(split_tokens), int(withhold_page), ctypes.c_uint32(wait_us),
         _dev(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_diag_decode_timeout")
+
+
+def diag_window_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                        ctx_len: torch.Tensor, w_kv_b: torch.Tensor, scale_bf16: int, out: torch.Tensor,
+                        workspace: torch.Tensor, max_ctx: int, window: int, n_sink: int, split_tokens: int,
+                        withhold_page: int, wait_us: int, dev_err: torch.Tensor, stream=None) -> None:
+    """Diagnostic: window_decode with page `withhold_page` of every split never loaded and every bounded wait of
+    the attention kernel limited to wait_us; see k3mla_diag_window_timeout."""
+    B = q_abs.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    dev = _here(slab)
+    _check(load().k3mla_diag_window_timeout(
+        _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1],
+        _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _int(split_tokens, "split_tokens"), _int(withhold_page, "withhold_page"), _int(wait_us, "wait_us"),
+        _at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_diag_window_timeout")
+
+
+def diag_window_chunk_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                              pos0: torch.Tensor, row_start: torch.Tensor, w_kv_b: torch.Tensor, scale_bf16: int,
+                              out: torch.Tensor, workspace: torch.Tensor, max_ctx: int, window: int, n_sink: int,
+                              withhold_page: int, wait_us: int, dev_err: torch.Tensor, stream=None) -> None:
+    """Diagnostic: the same for window_chunk_decode; see k3mla_diag_window_chunk_timeout."""
+    R = q_abs.shape[0]
+    B = pos0.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    dev = _here(slab)
+    _check(load().k3mla_diag_window_chunk_timeout(
+        _at(dev, q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        _at(dev, row_start, torch.int32, (B + 1,), "row_start"), B, R,
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _int(withhold_page, "withhold_page"), _int(wait_us, "wait_us"), _at(dev, dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream, dev)), "k3mla_diag_window_chunk_timeout")
 
 
 def diag_exact_exp(x: torch.Tensor, y: torch.Tensor, fast: torch.Tensor | None = None, stream=None) -> None:
