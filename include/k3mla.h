@@ -590,9 +590,9 @@ int k3mla_diag_decode_timeout(const uint16_t* q_abs, const uint16_t* slab, int n
                               void* workspace, size_t ws_bytes, int B, int max_ctx, int split_tokens,
                               int withhold_page, uint32_t wait_us, int32_t* dev_err, void* stream);
 
-/* The same for the windowed calls: k3mla_window_decode and k3mla_window_chunk_decode with the first third of page
- * `withhold_page` (>= 1, counted in the list of pages) of every unit of work never loaded.  A unit is one split of a slot
- * (decode) or four token rows x 32 heads (chunk). */
+/* The same for the windowed calls: k3mla_window_decode and k3mla_window_chunk_decode with the first half of page
+ * `withhold_page` (>= 1, counted in the list of pages) of every unit of work never loaded for the second contraction.  A
+ * unit is one split of a slot (decode) or four token rows x 32 heads (chunk). */
 int k3mla_diag_window_timeout(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
                               const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
                               const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
