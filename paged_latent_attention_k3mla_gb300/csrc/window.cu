@@ -1726,13 +1726,22 @@ extern "C" int k3mla_window_split_tokens(int B, int max_ctx, int window, int n_s
 {
     if (B <= 0 || max_ctx <= 0 || window < 1 || n_sink < 0) return TILE;
     // As many splits a slot as give every pair of SMs one, none shorter than a tile.  Two to four slots leave the
-    // expansion's CTAs, one a head, an SM each, where they ready W_UV meanwhile: four slots over 4,096 tokens 25.7 -> 24.6 us,
-    // over 1,000 21.4 -> 20.5, three over 4,096 24.8 -> 23.7; but one slot 21.4 -> 21.7, six over 2,000 23.7 -> 25.9, eight
-    // over 4,096 30.0 -> 34.2.
+    // expansion's CTAs, one a head, an SM each, where they ready W_UV meanwhile, unless that makes the splits longer by
+    // more than six pages, which is what the 3 us of W_UV and the fewer partials are worth.  Full plan against that one,
+    // longer by 2 pages: two slots over 3,000 tokens 23.9 -> 20.7 us, four over 1,000 21.3 -> 20.0; by 4: two over 7,000
+    // 26.1 -> 24.4, three over 4,096 24.8 -> 23.4; by 6: four over 4,096 25.4 -> 24.4, two over 10,000 27.7 -> 27.0 (but over
+    // 8,192 24.4 -> 25.2); by 8: three over 7,000 26.6 -> 27.4, four over 6,000 26.5 -> 27.7; by 24: three over 32,768 41.7 -> 58.6.
+    // One slot over 4,096 21.5 -> 21.1, but over 16,384 (6 more) 25.7 -> 27.0; five over 2,000 (4 more) 24.9 -> 26.4: their
+    // splits meet in a kernel of its own.
     const long long tiles = (w_max_pages(max_ctx, window, n_sink) * PAGE + TILE - 1) / TILE;
     const int sms = sm_count();
-    const long long want = std::max(1, (B > 1 && B <= 4 && sms > H ? sms - H : sms) / 2 / B);
-    return (int)std::min<long long>((tiles + want - 1) / want * TILE, 0x7FFFFFFF / TILE * TILE);
+    auto per = [&](int n) {  // tiles of a split when n SMs share the lists
+        const long long want = std::max(1, n / 2 / B);
+        return (tiles + want - 1) / want;
+    };
+    long long split = per(sms);
+    if (B > 1 && B <= 4 && sms > H && (per(sms - H) - split) * (TILE / PAGE) <= 6) split = per(sms - H);
+    return (int)std::min<long long>(split * TILE, 0x7FFFFFFF / TILE * TILE);
 }
 
 static int window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
