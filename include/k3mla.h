@@ -358,7 +358,7 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  * out         device [B][96][128], [R][96][128] bf16, 16-byte aligned; zeros for n <= 0 and for rows outside
  *             every slot
  * window      >= 1;  n_sink >= 0
- * scale_bf16  the softmax scale as a bf16 bit pattern, positive and finite
+ * scale_bf16  the softmax scale as a bf16 bit pattern, positive and at most 0x7F31 (2.35e38: times log2(e) it stays finite)
  * max_ctx     upper bound of n; a larger one is clamped, as one past the table is (K3MLA_DEV_CTX)
  * workspace   device, 256-byte aligned, at least the bytes that the sizing call gives; scratch
  * others      as for k3mla_paged_decode and k3mla_chunk_decode

@@ -1627,8 +1627,9 @@ static bool w_scale(uint16_t bits, float* kscale)
     float f;
     std::memcpy(&f, &u, 4);
     if (!(f > 0.f) || (bits & 0x7F80) == 0x7F80) return false;
-    *kscale = (float)((double)f * 1.4426950408889634);
-    return true;
+    const double k = (double)f * 1.4426950408889634;
+    *kscale = (float)k;
+    return k <= 3.4028234663852886e38;  // (an infinite factor would make NaN of every score of 0)
 }
 
 template <bool MQ>
