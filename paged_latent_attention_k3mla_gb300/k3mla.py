@@ -192,6 +192,14 @@ def _int(x, name: str) -> int:
     return x
 
 
+def _bits(scale) -> int:
+    """A bf16 bit pattern (the library takes 16 bits of it and would drop the others)."""
+    scale = int(scale)
+    if not 0 <= scale < 1 << 16:
+        raise K3mlaError(f"scale_bf16 = {scale} is not a bf16 bit pattern")
+    return scale
+
+
 def _table(device: int, t: torch.Tensor, B: int):
     if t.dim() != 2 or t.shape[0] != B:
         raise K3mlaError(f"block_table has shape {tuple(t.shape)}, expected [{B}, max_pages]")
@@ -220,7 +228,7 @@ def append_latent(slab: torch.Tensor, layer: int, block_table: torch.Tensor, pos
             raise K3mlaError(f"{name} must be a CUDA bf16 [B, n] tensor with unit inner stride")
     lib = load()
     _check(lib.k3mla_append_latent(
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(pos, torch.int32, (B,), "pos"), ctypes.c_void_p(c_kv.data_ptr()), c_kv.stride(0),
         ctypes.c_void_p(k_rope.data_ptr()), k_rope.stride(0), B,
@@ -250,7 +258,7 @@ def absorb_q_append(q: torch.Tensor, w_kv_b: torch.Tensor, q_abs: torch.Tensor, 
         _dev(q, torch.bfloat16, (B, H, NOPE + ROPE), "q"),
         _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"),
         _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(pos, torch.int32, (B,), "pos"), _rows(c_kv, B, "c_kv"), c_kv.stride(0),
         _rows(k_rope, B, "k_rope"), k_rope.stride(0), B,
@@ -283,10 +291,10 @@ def append_latent_rows(slab: torch.Tensor, layer: int, block_table: torch.Tensor
     R = c_kv.shape[0]
     lib = load()
     _check(lib.k3mla_append_latent_rows(
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(pos0, torch.int32, (B,), "pos0"), _dev(row_start, torch.int32, (B + 1,), "row_start"),
-        _rows(c_kv, R, "c_kv"), c_kv.stride(0), _rows(k_rope, R, "k_rope"), k_rope.stride(0), B, int(max_rows),
+        _rows(c_kv, R, "c_kv"), c_kv.stride(0), _rows(k_rope, R, "k_rope"), k_rope.stride(0), B, _int(max_rows, "max_rows"),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_append_latent_rows")
 
 
@@ -306,7 +314,7 @@ def norm_rope_append(q: torch.Tensor, q_out: torch.Tensor, slab: torch.Tensor, l
     _check(load().k3mla_norm_rope_append(
         _at(dev, q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _at(dev, q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
         _opt_at(dev, q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"),
-        _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
         _opt_at(dev, row_start, torch.int32, (B + 1,), "row_start"), _rows(c_kv, R, "c_kv", LORA, dev), c_kv.stride(0),
         _opt_at(dev, c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE, dev), k_rope.stride(0),
@@ -347,7 +355,7 @@ def chunk_views(block_table: torch.Tensor, pos0: torch.Tensor, row_start: torch.
 
 
 def chunk_decode_workspace_bytes(B: int, R: int, max_ctx: int) -> int:
-    return int(load().k3mla_chunk_decode_workspace_bytes(B, R, max_ctx))
+    return int(load().k3mla_chunk_decode_workspace_bytes(_int(B, "B"), _int(R, "R"), _int(max_ctx, "max_ctx")))
 
 
 def chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
@@ -365,11 +373,11 @@ def chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tabl
     lib = load()
     _check(lib.k3mla_chunk_decode(
         _dev(q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
+        n_pages, L, _int(layer, "layer"), _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(pos0, torch.int32, (B,), "pos0"), _dev(row_start, torch.int32, (B + 1,), "row_start"), B, R,
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), ctypes.c_uint16(scale_bf16),
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _dev(out, torch.bfloat16, (R, H, V), "out"), _opt(argmax, torch.int32, (R, H), "argmax"),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), int(max_ctx),
+        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _int(max_ctx, "max_ctx"),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_chunk_decode")
 
 
@@ -398,9 +406,9 @@ def window_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tab
     dev = _here(slab)
     _check(load().k3mla_window_decode(
         _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1],
+        n_pages, L, _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1],
         _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
-        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _int(split_tokens, "split_tokens"), _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)),
@@ -424,16 +432,16 @@ def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
     dev = _here(slab)
     _check(load().k3mla_window_chunk_decode(
         _at(dev, q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        n_pages, L, _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
         _at(dev, row_start, torch.int32, (B + 1,), "row_start"), B, R,
-        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_window_chunk_decode")
 
 
 def decode_exact_workspace_bytes(B: int, max_ctx: int) -> int:
-    return int(load().k3mla_decode_exact_workspace_bytes(B, max_ctx))
+    return int(load().k3mla_decode_exact_workspace_bytes(_int(B, "B"), _int(max_ctx, "max_ctx")))
 
 
 def decode_exact(q: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor, ctx_len: torch.Tensor,
@@ -445,16 +453,16 @@ def decode_exact(q: torch.Tensor, slab: torch.Tensor, layer: int, block_table: t
     lib = load()
     _check(lib.k3mla_decode_exact(
         _dev(q, torch.bfloat16, (B, H, NOPE + ROPE), "q"), _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
+        n_pages, L, _int(layer, "layer"), _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(ctx_len, torch.int32, (B,), "ctx_len"), _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"),
-        ctypes.c_uint16(scale_bf16), _dev(out, torch.bfloat16, (B, H, V), "out"),
+        _bits(scale_bf16), _dev(out, torch.bfloat16, (B, H, V), "out"),
         _opt(argmax, torch.int32, (B, H), "argmax"), _dev(workspace, torch.uint8, None, "workspace"),
-        workspace.numel(), B, int(max_ctx), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
+        workspace.numel(), B, _int(max_ctx, "max_ctx"), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
         "k3mla_decode_exact")
 
 
 def decode_layer_workspace_bytes(B: int, max_ctx: int) -> int:
-    return int(load().k3mla_decode_layer_workspace_bytes(B, max_ctx))
+    return int(load().k3mla_decode_layer_workspace_bytes(_int(B, "B"), _int(max_ctx, "max_ctx")))
 
 
 
@@ -471,22 +479,23 @@ def decode_layer(q: torch.Tensor, w_kv_b: torch.Tensor, slab: torch.Tensor, laye
     lib = load()
     _check(lib.k3mla_decode_layer(
         _dev(q, torch.bfloat16, (B, H, NOPE + ROPE), "q"), _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(ctx_len, torch.int32, (B,), "ctx_len"), _rows(c_kv, B, "c_kv"), c_kv.stride(0),
-        _rows(k_rope, B, "k_rope"), k_rope.stride(0), ctypes.c_uint16(scale_bf16),
+        _rows(k_rope, B, "k_rope"), k_rope.stride(0), _bits(scale_bf16),
         _dev(out, torch.bfloat16, (B, H, V), "out"), _opt(argmax, torch.int32, (B, H), "argmax"),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), B, int(max_ctx),
+        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), B, _int(max_ctx, "max_ctx"),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_decode_layer")
 
 
 def decode_workspace_bytes(B: int, max_ctx: int, split_tokens: int = SPLIT_AUTO) -> int:
-    return int(load().k3mla_decode_workspace_bytes(B, max_ctx, split_tokens))
+    return int(load().k3mla_decode_workspace_bytes(_int(B, "B"), _int(max_ctx, "max_ctx"),
+                                                   _int(split_tokens, "split_tokens")))
 
 
 def slot_split_tokens(ctx: int, split_tokens: int = SPLIT_AUTO) -> int:
     """The split length a slot of context ctx gets (k3mla_slot_split_tokens)."""
-    rc = int(load().k3mla_slot_split_tokens(int(ctx), int(split_tokens)))
+    rc = int(load().k3mla_slot_split_tokens(_int(ctx, "ctx"), _int(split_tokens, "split_tokens")))
     if rc < 0:
         _check(rc, "k3mla_slot_split_tokens")
     return rc
@@ -498,7 +507,8 @@ def batch_planned_split_tokens(ctx_len, max_ctx: int) -> int:
     k3mla_batch_planned_split_tokens.  Passing it as split_tokens makes a slot's output bits
     depend on the rest of the batch and on the GPU."""
     ctx = np.ascontiguousarray(np.asarray(ctx_len, dtype=np.int32).reshape(-1))
-    rc = int(load().k3mla_batch_planned_split_tokens(ctx.ctypes.data_as(ctypes.c_void_p), int(ctx.size), max_ctx))
+    rc = int(load().k3mla_batch_planned_split_tokens(ctx.ctypes.data_as(ctypes.c_void_p), int(ctx.size),
+                                                      _int(max_ctx, "max_ctx")))
     if rc < 0:
         _check(rc, "k3mla_batch_planned_split_tokens")
     return rc
@@ -519,12 +529,12 @@ def paged_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_tabl
     lib = load()
     _check(lib.k3mla_paged_decode(
         _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(ctx_len, torch.int32, (B,), "ctx_len"),
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _dev(out, torch.bfloat16, (B, H, V), "out"), _opt(argmax, torch.int32, (B, H), "argmax"),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), B, int(max_ctx), int(split_tokens),
+        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(split_tokens, "split_tokens"),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_paged_decode")
 
 
@@ -541,12 +551,12 @@ def paged_decode_noalloc(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, bl
     lib = load()
     _check(lib.k3mla_paged_decode_noalloc(
         _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(ctx_len, torch.int32, (B,), "ctx_len"),
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _dev(out, torch.bfloat16, (B, H, V), "out"), _opt(argmax, torch.int32, (B, H), "argmax"),
-        B, int(max_ctx), int(split_tokens), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
+        B, _int(max_ctx, "max_ctx"), _int(split_tokens, "split_tokens"), _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)),
         "k3mla_paged_decode_noalloc")
 
 
@@ -561,7 +571,7 @@ def expand_latent_cache(slab: torch.Tensor, layer: int, w_kv_b: torch.Tensor, xc
     n_pages, L = slab.shape[0], slab.shape[1]
     lib = load()
     _check(lib.k3mla_expand_latent_cache(
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"),
         _dev(xcache, torch.bfloat16, (n_pages, PAGE, H, NOPE + ROPE + V), "xcache"),
         _opt(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_expand_latent_cache")
@@ -578,8 +588,8 @@ def expanded_decode(q: torch.Tensor, xcache: torch.Tensor, block_table: torch.Te
         _dev(q, torch.bfloat16, (B, H, NOPE + ROPE), "q"),
         _dev(xcache, torch.bfloat16, (n_pages, PAGE, H, NOPE + ROPE + V), "xcache"), n_pages,
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
-        _dev(ctx_len, torch.int32, (B,), "ctx_len"), ctypes.c_uint16(scale_bf16),
-        _dev(out, torch.bfloat16, (B, H, V), "out"), B, int(max_ctx), _opt(dev_err, torch.int32, (1,), "dev_err"),
+        _dev(ctx_len, torch.int32, (B,), "ctx_len"), _bits(scale_bf16),
+        _dev(out, torch.bfloat16, (B, H, V), "out"), B, _int(max_ctx, "max_ctx"), _opt(dev_err, torch.int32, (1,), "dev_err"),
         _stream(stream)), "k3mla_expanded_decode")
 
 
@@ -594,12 +604,12 @@ def diag_decode_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
     lib = load()
     _check(lib.k3mla_diag_decode_timeout(
         _dev(q_abs, torch.bfloat16, (B, H, ROW), "q_abs"),
-        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, int(layer),
+        _dev(slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _dev(block_table, torch.int32, None, "block_table"), block_table.shape[1],
         _dev(ctx_len, torch.int32, (B,), "ctx_len"),
-        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _dev(w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _dev(out, torch.bfloat16, (B, H, V), "out"), None, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-        B, int(max_ctx), int(split_tokens), int(withhold_page), ctypes.c_uint32(wait_us),
+        B, _int(max_ctx, "max_ctx"), _int(split_tokens, "split_tokens"), int(withhold_page), ctypes.c_uint32(wait_us),
         _dev(dev_err, torch.int32, (1,), "dev_err"), _stream(stream)), "k3mla_diag_decode_timeout")
 
 
@@ -614,9 +624,9 @@ def diag_window_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
     dev = _here(slab)
     _check(load().k3mla_diag_window_timeout(
         _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1],
+        n_pages, L, _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1],
         _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
-        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _int(split_tokens, "split_tokens"), _int(withhold_page, "withhold_page"), _int(wait_us, "wait_us"),
@@ -634,9 +644,9 @@ def diag_window_chunk_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: in
     dev = _here(slab)
     _check(load().k3mla_diag_window_chunk_timeout(
         _at(dev, q_abs, torch.bfloat16, (R, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
-        n_pages, L, int(layer), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        n_pages, L, _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
         _at(dev, row_start, torch.int32, (B + 1,), "row_start"), B, R,
-        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), int(scale_bf16),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
         _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _int(withhold_page, "withhold_page"), _int(wait_us, "wait_us"), _at(dev, dev_err, torch.int32, (1,), "dev_err"),
