@@ -142,7 +142,7 @@ def _stream(stream, device=None):
 
 
 def _dev(t: torch.Tensor, dtype, shape=None, name="tensor"):
-    """The address of a dense CUDA tensor of this dtype (and shape, a tuple).  Every call checks a dozen of them, so
+    """The address of a dense CUDA tensor of this dtype (and shape).  Every call checks a dozen of them, so
     the good case is one expression; what is wrong is worked out only when something is."""
     try:
         if t.is_cuda and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
@@ -155,7 +155,9 @@ def _dev(t: torch.Tensor, dtype, shape=None, name="tensor"):
         raise K3mlaError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise K3mlaError(f"{name} must be contiguous")
-    raise K3mlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise K3mlaError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()  # (a shape that was no tuple)
 
 
 def _opt(t, dtype, shape, name):
@@ -176,8 +178,10 @@ def _at(device: int, t: torch.Tensor, dtype, shape, name):
             return t.data_ptr()
     except AttributeError:
         pass
-    _dev(t, dtype, shape, name)
-    raise K3mlaError(f"{name} is on {t.device}, the call runs on cuda:{device}")
+    at = _dev(t, dtype, shape, name)
+    if t.get_device() != device:
+        raise K3mlaError(f"{name} is on {t.device}, the call runs on cuda:{device}")
+    return at
 
 
 def _opt_at(device: int, t, dtype, shape, name):

@@ -75,3 +75,17 @@ def test_a_context_past_32_bits_is_refused():
                  lambda: k3mla.slot_split_tokens(far), lambda: k3mla.batch_planned_split_tokens([5], far)):
         with pytest.raises(k3mla.K3mlaError, match="32 bits"):
             call()
+
+
+def test_a_shape_may_be_any_sequence():
+    t = fake(2, 3)
+    for shape in ((2, 3), [2, 3], torch.Size([2, 3]), None):
+        assert k3mla._dev(t, torch.bfloat16, shape, "t") == t.data_ptr()
+        assert k3mla._at(0, t, torch.bfloat16, shape, "t") == t.data_ptr()
+        with pytest.raises(k3mla.K3mlaError, match="runs on cuda:1"):
+            k3mla._at(1, t, torch.bfloat16, shape, "t")
+    for shape in ((3, 2), [3, 2], [2], ()):
+        with pytest.raises(k3mla.K3mlaError, match="has shape"):
+            k3mla._dev(t, torch.bfloat16, shape, "t")
+        with pytest.raises(k3mla.K3mlaError, match="has shape"):
+            k3mla._at(0, t, torch.bfloat16, shape, "t")
