@@ -151,13 +151,24 @@ int k3mla_absorb_q_append(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* q
  * slab, block_table, dev_err: as for k3mla_append_latent_rows (K3MLA_DEV_UNMAPPED: that cache row is
  *            skipped, its queries are not)
  * bf16 pointers 16-byte aligned, strides multiples of 8.  One kernel on `stream`; it reads nothing before
- * the kernel ahead of it has completed. */
+ * the kernel ahead of it has completed.
+ *
+ * k3mla_norm_rope_append_at: the same with the angles' positions apart from the cache rows'.  rope_pos0 [B] device
+ * int32: token j of slot b is turned by (rope_pos0[b] + j) * inv_freq[i] (of magnitude below 2^29) and written at
+ * pos0[b] + j; NULL: as above.  For slots whose rows k3mla_compact_rows has moved: the kept keys keep the angles of
+ * their old positions, so the tokens that follow go on from there and not from the number of rows kept. */
 int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
                            int n_pages, int n_layers, int layer, const int32_t* block_table,
                            int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
                            const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
                            const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
                            const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err, void* stream);
+int k3mla_norm_rope_append_at(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
+                              int n_pages, int n_layers, int layer, const int32_t* block_table,
+                              int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                              const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
+                              const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
+                              const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err, void* stream);
 
 /* ---- exact-chain decode (PR #869, M2 commit: the certified rounding chain) ----
  * The same result as k3mla_absorb_q + k3mla_paged_decode, computed landing for
@@ -491,7 +502,8 @@ int k3mla_pool_truncate(k3mla_pool* pool, int slot, int new_len);
  * For every slot b < B, layer l < n_layers and i < n_b = keep_start[b + 1] - keep_start[b], in place:
  *   cache row of position i <- cache row of position keep[l * keep_layer_stride + keep_start[b] + i]
  * The slot then holds n_b tokens (rows from n_b on keep what they held; k3mla_pool_truncate gives their
- * pages back).  Rotated keys keep the angles of their old positions.
+ * pages back).  Rotated keys keep the angles of their old positions: k3mla_norm_rope_append_at turns the tokens
+ * that follow by positions that go on from those.
  * keep       device int32 [n_keep] (n_keep < 2^30), or [n_layers] lists of n_keep entries keep_layer_stride apart: per
  *            slot strictly ascending positions (>= 0).  keep_layer_stride 0: one list for every layer.
  * keep_start device int32 [B + 1], non-decreasing, within [0, n_keep]

@@ -7,7 +7,9 @@
 //     k'     = rot_p( k * wk / sqrt(mean_64(k^2) + eps) )
 //     cache row of p = c' | k'
 // where a null weight leaves its norm out and rot_p turns pair i of the 64 rope entries -- (i, i + 32), or
-// (2i, 2i + 1) when interleaved -- by the angle p * inv_freq[i].
+// (2i, 2i + 1) when interleaved -- by the angle p * inv_freq[i].  A slot whose rows were compacted has two counts: the row
+// goes to position p of its pages, and the angles go on from the positions its kept keys were rotated at
+// (k3mla_norm_rope_append_at).
 //
 // The angle.  p * inv_freq[i] reaches 10^6 radians in long contexts, where an f32 product is off by
 // 0.03; the product of an integer below 2^29 and an f32 is exact in f64, so the turn p * inv_freq / 2 pi
@@ -44,6 +46,7 @@ struct NormRopeParams {
     const uint16_t *wq, *wc, *wk;  // null: that norm is left out
     uint16_t* slab;
     const int32_t *table, *pos0, *row_start;  // row_start null: row r is slot r's only one
+    const int32_t* rope_pos0;                 // null: the angles' positions are pos0 as well
     const uint16_t *c_kv, *k_rope;
     int64_t c_stride, r_stride;
     const float* inv_freq;  // null: no rotation
@@ -83,6 +86,12 @@ __device__ __forceinline__ void nr_scale(float (&x)[8], float rs, const uint16_t
     nr_unpack(*reinterpret_cast<const uint4*>(w), y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= rs * y[e];
+}
+
+// The position that turns a row of slot b at position pos of its pages.
+template <bool AT> __device__ __forceinline__ int64_t nr_rope_position(const NormRopeParams& p, int b, int64_t pos)
+{
+    return AT ? p.rope_pos0[b] + (pos - p.pos0[b]) : pos;
 }
 
 // (cos, sin) of the angle pos * inv_freq.
@@ -179,7 +188,9 @@ __device__ __forceinline__ void nr_key_row(const NormRopeParams& p, int r, int b
     if (lane < 8) dst[lane + 64] = nr_pack(k);
 }
 
-// Grid: q_ctas CTAs of a row's 32 heads each, then ceil(R / 8) CTAs of eight cache rows.
+// Grid: q_ctas CTAs of a row's 32 heads each, then ceil(R / 8) CTAs of eight cache rows.  AT: with rope_pos0 (asking for
+// it in the one kernel took 5,251 rows from 61.8 to 62.3 us).
+template <bool AT>
 __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormRopeParams p)
 {
     __shared__ float2 cs[NR_WARPS][ROPE / 2];
@@ -201,7 +212,7 @@ __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormR
         int64_t pos;
         if (!row_position(p.row_start, p.pos0, p.B, r, b, pos)) return;  // left as it is (uniform in the CTA)
         if (p.inv_freq) {
-            if (warp == 0) cs[0][lane] = nr_angle(pos, p.inv_freq[lane]);
+            if (warp == 0) cs[0][lane] = nr_angle(nr_rope_position<AT>(p, b, pos), p.inv_freq[lane]);
             __syncthreads();
         }
         nr_query(p, r, part, cs[0], p.wq != nullptr, p.inv_freq != nullptr, raw);
@@ -212,7 +223,7 @@ __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormR
         int64_t pos;
         if (!row_position(p.row_start, p.pos0, p.B, r, b, pos)) return;
         if (p.inv_freq) {
-            cs[warp][lane] = nr_angle(pos, p.inv_freq[lane]);
+            cs[warp][lane] = nr_angle(nr_rope_position<AT>(p, b, pos), p.inv_freq[lane]);
             __syncwarp();
         }
         nr_key_row(p, r, b, pos, cs[warp]);
@@ -223,13 +234,13 @@ __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormR
 
 using namespace k3;
 
-extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
-                                      int n_pages, int n_layers, int layer, const int32_t* block_table,
-                                      int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
-                                      const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
-                                      const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
-                                      const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err,
-                                      void* stream)
+extern "C" int k3mla_norm_rope_append_at(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
+                                         int n_pages, int n_layers, int layer, const int32_t* block_table,
+                                         int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                                         const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride,
+                                         const uint16_t* c_weight, const uint16_t* k_rope, int64_t r_stride,
+                                         const uint16_t* k_weight, float eps, const float* inv_freq, int interleaved, int B,
+                                         int R, int32_t* dev_err, void* stream)
 {
     if (B < 0 || R < 0 || n_pages <= 0 || n_layers <= 0 || layer < 0 || layer >= n_layers || max_pages_per_slot <= 0 ||
         c_stride < LORA || r_stride < ROPE || (c_stride & 7) || (r_stride & 7) || !(eps >= 0.f) || (!row_start && R != B)) {
@@ -255,13 +266,27 @@ extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const 
     if (!device_ok()) return K3MLA_E_DEVICE;
     NormRopeParams p;
     p.q = q, p.q_out = q_out, p.wq = q_weight, p.wc = c_weight, p.wk = k_weight;
-    p.slab = slab, p.table = block_table, p.pos0 = pos0, p.row_start = row_start;
+    p.slab = slab, p.table = block_table, p.pos0 = pos0, p.row_start = row_start, p.rope_pos0 = rope_pos0;
     p.c_kv = c_kv, p.k_rope = k_rope, p.c_stride = c_stride, p.r_stride = r_stride;
     p.inv_freq = inv_freq, p.dev_err = dev_err, p.eps = eps, p.interleaved = interleaved;
     p.n_pages = n_pages, p.n_layers = n_layers, p.layer = layer, p.max_pages = max_pages_per_slot, p.B = B, p.R = R;
     const bool stays = q == q_out && !q_weight;  // entries 0..127 of every head
     p.q_nope = stays ? 0 : 1;
     p.q_ctas = stays && !inv_freq ? 0 : NR_QCTAS * R;
-    return launch_pdl(k3mla_norm_rope_kernel, dim3(p.q_ctas + (R + NR_WARPS - 1) / NR_WARPS), dim3(NR_THREADS), 0,
+    return launch_pdl(rope_pos0 ? k3mla_norm_rope_kernel<true> : k3mla_norm_rope_kernel<false>,
+                      dim3(p.q_ctas + (R + NR_WARPS - 1) / NR_WARPS), dim3(NR_THREADS), 0,
                       reinterpret_cast<cudaStream_t>(stream), "k3mla_norm_rope_kernel", p);
+}
+
+extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
+                                      int n_pages, int n_layers, int layer, const int32_t* block_table,
+                                      int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                                      const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
+                                      const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
+                                      const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err,
+                                      void* stream)
+{
+    return k3mla_norm_rope_append_at(q, q_out, q_weight, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot,
+                                     pos0, row_start, nullptr, c_kv, c_stride, c_weight, k_rope, r_stride, k_weight, eps,
+                                     inv_freq, interleaved, B, R, dev_err, stream);
 }

@@ -31,7 +31,8 @@ EXPORTS = (
     "k3mla_decode_exact_workspace_bytes", "k3mla_pool_ensure_all", "k3mla_batch_planned_split_tokens",
     "k3mla_decode_layer_workspace_bytes", "k3mla_decode_layer", "k3mla_diag_decode_timeout",
     "k3mla_expanded_cache_bytes", "k3mla_expand_latent_cache", "k3mla_expanded_decode", "k3mla_diag_exact_exp",
-    "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_pool_trim",
+    "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_norm_rope_append_at",
+    "k3mla_pool_trim",
     "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
     "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
@@ -100,6 +101,8 @@ def load(build_if_needed: bool = True):
                                    I),
             "k3mla_norm_rope_append": ([P, P, P, P, I, I, I, P, I, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I, I, I,
                                         P, P], I),
+            "k3mla_norm_rope_append_at": ([P, P, P, P, I, I, I, P, I, P, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I,
+                                           I, I, P, P], I),
             "k3mla_window_decode_workspace_bytes": ([I, I, I, I, I], SZ),
             "k3mla_window_split_tokens": ([I, I, I, I], I),
             "k3mla_window_decode": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
@@ -306,25 +309,30 @@ def norm_rope_append(q: torch.Tensor, q_out: torch.Tensor, slab: torch.Tensor, l
                      pos0: torch.Tensor, row_start: torch.Tensor | None, c_kv: torch.Tensor, k_rope: torch.Tensor,
                      q_weight: torch.Tensor | None = None, c_weight: torch.Tensor | None = None,
                      k_weight: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
-                     interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None) -> None:
+                     interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None,
+                     rope_pos0: torch.Tensor | None = None) -> None:
     """Norms of q [R, 96, 192] per head (weight [192]), of the latent c_kv [R, >=512] ([512]) and of the rope
     key k_rope [R, >=64] ([64]), rotation of the rope entries by pos * inv_freq [32] (f32), queries to q_out
     (may be q), keys into the cache rows of their positions; see k3mla_norm_rope_append.  A weight of None
-    leaves that norm out, inv_freq None the rotation; row_start None: one row per slot, at pos0."""
+    leaves that norm out, inv_freq None the rotation; row_start None: one row per slot, at pos0.  rope_pos0 [B]:
+    positions that turn the rows where these differ from the cache's (after compact_rows; k3mla_norm_rope_append_at)."""
     R = q.shape[0]
     B = pos0.shape[0]
     n_pages, L = slab.shape[0], slab.shape[1]
     dev = _here(slab)
-    _check(load().k3mla_norm_rope_append(
+    name = "k3mla_norm_rope_append" if rope_pos0 is None else "k3mla_norm_rope_append_at"
+    turned = () if rope_pos0 is None else (_at(dev, rope_pos0, torch.int32, (B,), "rope_pos0"),)
+    _check(getattr(load(), name)(
         _at(dev, q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _at(dev, q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
         _opt_at(dev, q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"),
         _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"), n_pages, L, _int(layer, "layer"),
         _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
-        _opt_at(dev, row_start, torch.int32, (B + 1,), "row_start"), _rows(c_kv, R, "c_kv", LORA, dev), c_kv.stride(0),
+        _opt_at(dev, row_start, torch.int32, (B + 1,), "row_start"), *turned,
+        _rows(c_kv, R, "c_kv", LORA, dev), c_kv.stride(0),
         _opt_at(dev, c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE, dev), k_rope.stride(0),
         _opt_at(dev, k_weight, torch.bfloat16, (ROPE,), "k_weight"), float(eps),
         _opt_at(dev, inv_freq, torch.float32, (ROPE // 2,), "inv_freq"), int(bool(interleaved)), B, R,
-        _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_norm_rope_append")
+        _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), name)
 
 
 def compact_rows(slab: torch.Tensor, block_table: torch.Tensor, keep: torch.Tensor, keep_start: torch.Tensor,
