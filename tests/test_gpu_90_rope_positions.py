@@ -55,3 +55,20 @@ def test_the_same_positions_give_the_same_bits(gpu_lib):
         slabs[i].copy_(d["slab"])
         run(d, outs[i], slabs[i], d["start"], rope, inv=False)
     assert torch.equal(outs[0], outs[1]) and torch.equal(slabs[0], slabs[1])
+
+
+def test_the_latent_norm_alone_leaves_the_queries(gpu_lib):
+    # what a layer without rotation needs: queries in place, untouched (NaN payloads too), the latent normed, the key copied
+    d = make(24, [70, 5, 300], [3, 5, 130])
+    d["q"][2, 3, 4] = float("nan")
+    before, q_in = f32(d["slab"]), d["q"].clone()
+    run(d, d["q"], d["slab"], d["start"], None, weights=(None, d["w"][1], None), inv=False)
+    assert torch.equal(d["q"].view(torch.int16), q_in.view(torch.int16))
+    cw, kv = f32(d["w"][1]), f32(d["kv"])
+    want, bound = before.astype(np.float64), np.zeros(before.shape)
+    for r, (b, p) in enumerate(ref.rows_of(d["pos0"], d["start"], d["R"])):
+        y, mag = ref.key_row(kv[r, :512], kv[r, 512:], p, cw, None, 1e-6, None, False)
+        at = (d["table"][b, p // PAGE], 1, p % PAGE)
+        want[at], bound[at] = y, 2.0 ** -8 * np.abs(y) * 1.01 + 2.0 ** -18 * mag * 1.01
+        bound[at][512:] = 0.0
+    assert np.all(np.abs(f32(d["slab"]) - want) <= bound)
