@@ -492,11 +492,15 @@ int k3mla_copy_pages(uint16_t* dst_slab, int dst_n_pages, const uint16_t* src_sl
  * behind the next token's window and past the sinks; its table entries become -1, its references
  * drop by one.  Returns the number of pages unmapped (>= 0).  K3MLA_E_INVALID for window < 1 or a
  * negative n_tokens / n_sink, K3MLA_E_CTX for n_tokens > max_ctx.  A trimmed position cannot be written
- * again (k3mla_pool_cow gives K3MLA_E_CTX), and k3mla_pool_share_prefix shares the hole as it is.
+ * again (k3mla_pool_cow gives K3MLA_E_CTX) before k3mla_pool_refill, and k3mla_pool_share_prefix shares the hole as it is.
  * k3mla_pool_truncate: unmaps the pages past the first new_len tokens (nothing if the slot maps no
- * more than those), e.g. after k3mla_compact_rows. */
+ * more than those), e.g. after k3mla_compact_rows.
+ * k3mla_pool_refill: maps a fresh page (count 1, holding whatever it held) into every hole among the slot's first
+ * n_tokens tokens, all of them or none (K3MLA_E_NO_PAGES); returns their number.  Before k3mla_compact_rows of a trimmed
+ * slot, with the number of rows it keeps: the rows move there. */
 int k3mla_pool_trim(k3mla_pool* pool, int slot, int n_tokens, int window, int n_sink);
 int k3mla_pool_truncate(k3mla_pool* pool, int slot, int new_len);
+int k3mla_pool_refill(k3mla_pool* pool, int slot, int n_tokens);
 
 /* ---- row compaction: the kept tokens of each slot move to the front of its pages --
  * For every slot b < B, layer l < n_layers and i < n_b = keep_start[b + 1] - keep_start[b], in place:
@@ -511,7 +515,9 @@ int k3mla_pool_truncate(k3mla_pool* pool, int slot, int new_len);
  * dev_err    device int32 or NULL: K3MLA_DEV_UNMAPPED where position i has no page (that row is skipped),
  *            K3MLA_DEV_BAD_PAGE for a source page outside [-1, n_pages) and K3MLA_DEV_CTX for a kept position
  *            outside the table (read as zero rows)
- * A page that receives rows must be mapped by one slot of the call only (k3mla_pool_cow un-shares it).
+ * A page that receives rows must be mapped by one slot of the call only (k3mla_pool_cow un-shares it).  A slot that
+ * k3mla_pool_trim has given holes needs k3mla_pool_refill first: kept rows whose new place is a hole are lost.  Its list
+ * then names only positions that kept their page.
  * One kernel on `stream`; it reads nothing before the kernel ahead of it has completed. */
 int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, const int32_t* block_table,
                        int max_pages_per_slot, const int32_t* keep, int64_t keep_layer_stride, int n_keep,

@@ -16,7 +16,7 @@
 //
 // Windowed attention and eviction give pages back while a slot lives: k3mla_pool_trim unmaps the pages
 // that no later token can see (holes, -1, inside the slot's mapped range), k3mla_pool_truncate those past
-// a shorter length.
+// a shorter length; k3mla_pool_refill maps fresh pages into holes, for rows that are to be moved there.
 #include <cstdint>
 #include <cstdlib>
 #include <new>
@@ -154,6 +154,26 @@ extern "C" int k3mla_pool_trim(k3mla_pool* p, int slot, int n_tokens, int window
          lp < p->mapped[slot] && (lp + 1) * K3MLA_PAGE <= first; ++lp)
         given += unmap(p, row + lp);
     return given;
+}
+
+extern "C" int k3mla_pool_refill(k3mla_pool* p, int slot, int n_tokens)
+{
+    if (!p || n_tokens < 0) return K3MLA_E_INVALID;
+    if (slot < 0 || slot >= p->n_slots) return K3MLA_E_SLOT;
+    if (n_tokens > p->max_ctx) return K3MLA_E_CTX;
+    int32_t* row = p->table.data() + (size_t)slot * p->max_pages;
+    const int most = (int)(((long long)n_tokens + K3MLA_PAGE - 1) / K3MLA_PAGE);
+    const int end = most < p->mapped[slot] ? most : p->mapped[slot];
+    int holes = 0;
+    for (int lp = 0; lp < end; ++lp) holes += row[lp] < 0;
+    if ((size_t)holes > p->free.size()) return K3MLA_E_NO_PAGES;  // all-or-nothing
+    for (int lp = 0; lp < end; ++lp)
+        if (row[lp] < 0) {
+            row[lp] = p->free.back();
+            p->free.pop_back();
+            p->refs[row[lp]] = 1;
+        }
+    return holes;
 }
 
 extern "C" int k3mla_pool_share_prefix(k3mla_pool* p, int dst_slot, int src_slot, int n_tokens)

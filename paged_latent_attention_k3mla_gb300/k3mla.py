@@ -32,7 +32,7 @@ EXPORTS = (
     "k3mla_decode_layer_workspace_bytes", "k3mla_decode_layer", "k3mla_diag_decode_timeout",
     "k3mla_expanded_cache_bytes", "k3mla_expand_latent_cache", "k3mla_expanded_decode", "k3mla_diag_exact_exp",
     "k3mla_chunk_decode_workspace_bytes", "k3mla_chunk_decode", "k3mla_norm_rope_append", "k3mla_norm_rope_append_at",
-    "k3mla_pool_trim",
+    "k3mla_pool_trim", "k3mla_pool_refill",
     "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
     "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
@@ -114,6 +114,7 @@ def load(build_if_needed: bool = True):
                                                  ctypes.c_uint32, P, P], I),
             "k3mla_pool_trim": ([P, I, I, I, I], I),
             "k3mla_pool_truncate": ([P, I, I], I),
+            "k3mla_pool_refill": ([P, I, I], I),
             "k3mla_compact_rows": ([P, I, I, P, I, P, I64, I, P, I, P, P], I),
             "k3mla_decode_exact": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, P, SZ, I, I, P, P], I),
         }
@@ -739,6 +740,11 @@ class Pool:
     def truncate(self, slot: int, new_len: int) -> int:
         """Give back the pages past the first new_len tokens (status code)."""
         return int(load().k3mla_pool_truncate(self._h, _int(slot, "slot"), _int(new_len, "new_len")))
+
+    def refill(self, slot: int, n_tokens: int) -> int:
+        """Map fresh pages into the holes among the slot's first n_tokens tokens, before compact_rows of a trimmed
+        slot (their number, or a negative status code)."""
+        return int(load().k3mla_pool_refill(self._h, _int(slot, "slot"), _int(n_tokens, "n_tokens")))
 
     def refs(self, page: int) -> int:
         return int(load().k3mla_pool_page_refs(self._h, page))
