@@ -19,6 +19,7 @@
 // a shorter length; k3mla_pool_refill maps fresh pages into holes, for rows that are to be moved there.
 #include <cstdint>
 #include <cstdlib>
+#include <exception>
 #include <new>
 #include <vector>
 
@@ -48,7 +49,7 @@ extern "C" int k3mla_pool_create(int n_pages, int n_slots, int max_ctx, uint64_t
 {
     if (!out || n_slots <= 0 || max_ctx <= 0 || n_pages < 0) return K3MLA_E_INVALID;
     *out = nullptr;
-    const int max_pages = (max_ctx + K3MLA_PAGE - 1) / K3MLA_PAGE;
+    const int max_pages = (int)(((long long)max_ctx + K3MLA_PAGE - 1) / K3MLA_PAGE);
     const long long full = (long long)n_slots * max_pages;
     if (n_pages == 0) {
         if (full > 0x7FFFFFFFll) return K3MLA_E_INVALID;
@@ -60,12 +61,17 @@ extern "C" int k3mla_pool_create(int n_pages, int n_slots, int max_ctx, uint64_t
     p->n_slots = n_slots;
     p->max_ctx = max_ctx;
     p->max_pages = max_pages;
-    p->table.assign((size_t)n_slots * max_pages, -1);
-    p->mapped.assign(n_slots, 0);
-    p->refs.assign(n_pages, 0);
+    try {
+        p->table.assign((size_t)n_slots * max_pages, -1);
+        p->mapped.assign(n_slots, 0);
+        p->refs.assign(n_pages, 0);
+        p->free.resize(n_pages);
+    } catch (const std::exception&) {  // no memory for them: none may leave a C entry
+        delete p;
+        return K3MLA_E_INVALID;
+    }
     // Free list as a stack whose top is page 0 (ids claimed in ascending order)
     // unless shuffled.
-    p->free.resize(n_pages);
     for (int i = 0; i < n_pages; ++i) p->free[i] = n_pages - 1 - i;
     if (shuffle_seed != 0) {
         uint64_t s = shuffle_seed;
@@ -85,7 +91,7 @@ extern "C" int k3mla_pool_ensure(k3mla_pool* p, int slot, int new_len)
     if (!p || new_len < 0) return K3MLA_E_INVALID;
     if (slot < 0 || slot >= p->n_slots) return K3MLA_E_SLOT;
     if (new_len > p->max_ctx) return K3MLA_E_CTX;
-    const int need = (new_len + K3MLA_PAGE - 1) / K3MLA_PAGE;
+    const int need = (int)(((long long)new_len + K3MLA_PAGE - 1) / K3MLA_PAGE);
     const int have = p->mapped[slot];
     if (need <= have) return K3MLA_OK;
     if ((size_t)(need - have) > p->free.size()) return K3MLA_E_NO_PAGES;  // all-or-nothing
@@ -181,7 +187,7 @@ extern "C" int k3mla_pool_share_prefix(k3mla_pool* p, int dst_slot, int src_slot
     if (!p || n_tokens < 0) return K3MLA_E_INVALID;
     if (dst_slot < 0 || dst_slot >= p->n_slots || src_slot < 0 || src_slot >= p->n_slots) return K3MLA_E_SLOT;
     if (n_tokens > p->max_ctx) return K3MLA_E_CTX;
-    const int need = (n_tokens + K3MLA_PAGE - 1) / K3MLA_PAGE;
+    const int need = (int)(((long long)n_tokens + K3MLA_PAGE - 1) / K3MLA_PAGE);
     if (dst_slot == src_slot || p->mapped[dst_slot] != 0 || need > p->mapped[src_slot]) return K3MLA_E_INVALID;
     const int32_t* src = p->table.data() + (size_t)src_slot * p->max_pages;
     int32_t* dst = p->table.data() + (size_t)dst_slot * p->max_pages;
