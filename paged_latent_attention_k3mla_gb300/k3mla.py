@@ -574,7 +574,7 @@ def paged_decode_noalloc(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, bl
 
 
 def expanded_cache_bytes(n_pages: int) -> int:
-    return int(load().k3mla_expanded_cache_bytes(int(n_pages)))
+    return int(load().k3mla_expanded_cache_bytes(_int(n_pages, "n_pages")))
 
 
 def expand_latent_cache(slab: torch.Tensor, layer: int, w_kv_b: torch.Tensor, xcache: torch.Tensor,
@@ -689,7 +689,8 @@ class Pool:
     def __init__(self, n_slots: int, max_ctx: int, n_pages: int = 0, shuffle_seed: int = 0):
         lib = load(build_if_needed=True)
         h = ctypes.c_void_p()
-        _check(lib.k3mla_pool_create(n_pages, n_slots, max_ctx, shuffle_seed, ctypes.byref(h)),
+        _check(lib.k3mla_pool_create(_int(n_pages, "n_pages"), _int(n_slots, "n_slots"), _int(max_ctx, "max_ctx"),
+                                     shuffle_seed, ctypes.byref(h)),
                "k3mla_pool_create")
         self._h = h
         self.n_slots = n_slots
@@ -699,7 +700,7 @@ class Pool:
 
     def ensure(self, slot: int, new_len: int) -> int:
         """Returns the status code (0 ok, negative K3MLA_E_*)."""
-        return int(load().k3mla_pool_ensure(self._h, slot, new_len))
+        return int(load().k3mla_pool_ensure(self._h, _int(slot, "slot"), _int(new_len, "new_len")))
 
     def ensure_all(self, new_len) -> int:
         """ensure(b, new_len[b]) for b = 0 .. len-1 in one call (status of the first failure, or 0)."""
@@ -707,7 +708,7 @@ class Pool:
         return int(load().k3mla_pool_ensure_all(self._h, a.ctypes.data_as(ctypes.c_void_p), a.shape[0]))
 
     def release(self, slot: int) -> int:
-        return int(load().k3mla_pool_release_slot(self._h, slot))
+        return int(load().k3mla_pool_release_slot(self._h, _int(slot, "slot")))
 
     def table(self) -> np.ndarray:
         ptr = load().k3mla_pool_host_table(self._h)
@@ -720,13 +721,14 @@ class Pool:
 
     def share_prefix(self, dst_slot: int, src_slot: int, n_tokens: int) -> int:
         """Map src_slot's first ceil(n_tokens / 64) pages into the empty dst_slot (status code)."""
-        return int(load().k3mla_pool_share_prefix(self._h, dst_slot, src_slot, n_tokens))
+        return int(load().k3mla_pool_share_prefix(self._h, _int(dst_slot, "dst_slot"), _int(src_slot, "src_slot"),
+                                                  _int(n_tokens, "n_tokens")))
 
     def cow(self, slot: int, pos: int):
         """Before writing token `pos`: None if the slot owns the page (or a negative status code),
         else the (src_page, dst_page) copy to run first."""
         s, d = ctypes.c_int32(), ctypes.c_int32()
-        rc = int(load().k3mla_pool_cow(self._h, slot, pos, ctypes.byref(s), ctypes.byref(d)))
+        rc = int(load().k3mla_pool_cow(self._h, _int(slot, "slot"), _int(pos, "pos"), ctypes.byref(s), ctypes.byref(d)))
         if rc == 1:
             return s.value, d.value
         return None if rc == 0 else rc
@@ -747,7 +749,7 @@ class Pool:
         return int(load().k3mla_pool_refill(self._h, _int(slot, "slot"), _int(n_tokens, "n_tokens")))
 
     def refs(self, page: int) -> int:
-        return int(load().k3mla_pool_page_refs(self._h, page))
+        return int(load().k3mla_pool_page_refs(self._h, _int(page, "page")))
 
     def close(self):
         if self._h:

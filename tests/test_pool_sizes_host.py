@@ -19,3 +19,16 @@ def test_contexts_as_long_as_an_int_holds():
     assert pool.ensure(0, 2 ** 31 - 1) == -2 and pool.ensure(0, 129) == 0 and pool.stats() == (3, 3)
     assert pool.trim(0, 2 ** 31 - 1, 1, 0) == 3 and pool.stats() == (3, 0)
     pool.close()
+
+
+def test_pool_arguments_past_32_bits_are_refused():
+    pool, far = k3mla.Pool(n_slots=2, max_ctx=128), 2 ** 32
+    for call in (lambda: k3mla.Pool(far + 1, 128), lambda: k3mla.Pool(1, far + 128), lambda: k3mla.Pool(1, 128, far + 1),
+                 lambda: pool.ensure(far, 64), lambda: pool.ensure(0, far + 64), lambda: pool.release(far),
+                 lambda: pool.share_prefix(far + 1, 0, 0), lambda: pool.share_prefix(1, far, 0),
+                 lambda: pool.share_prefix(1, 0, far), lambda: pool.cow(far, 0), lambda: pool.cow(0, far),
+                 lambda: pool.refs(far), lambda: k3mla.expanded_cache_bytes(far + 1)):
+        with pytest.raises(k3mla.K3mlaError, match="32 bits"):
+            call()
+    assert pool.stats() == (4, 0)
+    pool.close()
