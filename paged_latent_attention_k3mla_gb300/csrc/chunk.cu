@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace k3 {
 
@@ -65,13 +66,7 @@ __global__ void __launch_bounds__(128) k3mla_chunk_views_kernel(const int32_t* _
     griddep_wait();
     griddep_launch_dependents();
     const int r = blockIdx.x;
-    int lo = 0, hi = B;  // the last b with row_start[b] <= r (row_start is non-decreasing)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (row_start[mid] <= r) lo = mid;
-        else hi = mid;
-    }
-    const int b = lo;
+    const int b = last_slot_from(row_start, B, r);
     const bool inside = r >= row_start[b] && r < row_start[b + 1];
     if (threadIdx.x == 0) vctx[r] = inside ? pos0[b] + (r - row_start[b]) + 1 : 0;
     for (int i = threadIdx.x; i < max_pages; i += blockDim.x)

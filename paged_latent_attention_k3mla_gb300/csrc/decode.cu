@@ -73,6 +73,7 @@
 #include "common.cuh"
 #include "decode_core.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace k3 {
 
@@ -1152,12 +1153,7 @@ __global__ void __launch_bounds__(1024) k3mla_mq_prep_kernel(const int32_t* __re
     }
     for (int g = total + tid; g < g_max; g += (int)blockDim.x) groups[g] = make_int4(0, 0, 0, 0);
     for (int r = tid; r < R; r += (int)blockDim.x) {
-        int lo = 0, hi = B;  // the last slot b with row_start[b] <= r
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (row_start[mid] <= r) lo = mid;
-            else hi = mid;
-        }
+        const int lo = last_slot_from(row_start, B, r);
         int c = 0;
         if (B > 0 && r >= row_start[lo] && r < row_start[lo + 1]) {
             c = pos0[lo] + (r - row_start[lo]) + 1;

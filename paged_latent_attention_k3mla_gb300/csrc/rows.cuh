@@ -25,6 +25,18 @@ __device__ __forceinline__ int warp_count_le(const int32_t* v, int n, int x)
     return lo;
 }
 
+// The last slot b with row_start[b] <= r (slot 0 when there is none; row_start is non-decreasing), by one thread.
+__device__ __forceinline__ int last_slot_from(const int32_t* row_start, int B, int r)
+{
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (row_start[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 // Row r of the packed rows: slot b, position pos.  False when the row lies outside every slot or its
 // position is negative.  row_start null: row r is the only one of slot r.  A whole warp calls it.
 __device__ __forceinline__ bool row_position(const int32_t* row_start, const int32_t* pos0, int B, int r, int& b,

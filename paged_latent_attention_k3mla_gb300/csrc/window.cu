@@ -888,12 +888,7 @@ template <bool MQ> __device__ __forceinline__ void w_empty_rows(const WinParams&
         bool sees = true;
         if (r < p.R) {
             if constexpr (MQ) {
-                int lo = 0, hi = p.B;  // the last slot with row_start[b] <= r
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (p.row_start[mid] <= r) lo = mid;
-                    else hi = mid;
-                }
+                const int lo = last_slot_from(p.row_start, p.B, r);
                 const int first = p.row_start[lo];
                 sees = r >= first && r < p.row_start[lo + 1] && (int64_t)p.pos0[lo] + (r - first) >= 0;
             } else {
