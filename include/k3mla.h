@@ -357,7 +357,8 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  * k3mla_window_decode: one token row per slot, n = ctx_len[b].
  * k3mla_window_chunk_decode: the token rows of prefill chunks (as for k3mla_chunk_decode): row j of slot
  * b has n = pos0[b] + j + 1, so its window moves along with it; the chunk's cache rows are appended first.
- * B at most 2^20 (decode: 65,535).
+ * 1 <= B <= 2^20 where R > 0 (decode: B <= 65,535).  A split (decode) or what four neighbouring rows see (chunk) may
+ * have 2^19 pages.
  *
  * What a slot sees is cut into splits as for k3mla_paged_decode, but in its list of seen pages: split_tokens
  * (a multiple of K3MLA_TILE) counts 64 tokens a page of that list; K3MLA_SPLIT_AUTO cuts by the slot's own

@@ -1680,6 +1680,16 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                       tm_o, x, p);
 }
 
+// A unit's pages take up to 0.85 us each, and its write-out waits for all of them within WAIT_NS: half of that is allowed.
+constexpr long long W_UNIT_PAGES = 1 << 19;
+
+static bool w_unit_fits(const char* who, long long pages)
+{
+    if (pages <= W_UNIT_PAGES) return true;
+    set_error("%s: %lld pages in one unit of work, more than %lld", who, pages, W_UNIT_PAGES);
+    return false;
+}
+
 // What both entries ask of their common arguments; fills p.
 static int w_check(const char* who, const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
                    const int32_t* table, int max_pages, const uint16_t* w_kv_b, uint16_t scale_bf16, const uint16_t* out,
@@ -1765,6 +1775,8 @@ static int window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_page
         return K3MLA_E_WORKSPACE;
     }
     const int ns = w_nsplit(max_ctx, window, n_sink, split_tokens);
+    const long long longest = w_max_pages(p.cap, window, n_sink), split = (split_tokens ? split_tokens : SPLIT_MAX) / PAGE;
+    if (!w_unit_fits("k3mla_window_decode", std::min(longest, split))) return K3MLA_E_INVALID;
     if (B > 65535 || (long long)B * ns * H > 0x7FFFFFFFll) {  // the merge's grid; partial-row coordinates
         set_error("k3mla_window_decode: too many slots or splits");
         return K3MLA_E_INVALID;
@@ -1842,6 +1854,9 @@ static int window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int 
         return K3MLA_E_WORKSPACE;
     }
     const long long units = 3ll * (((long long)R + 3ll * B) / 4);  // sum over slots of ceil(n_b / 4), at most
+    // (four rows' windows reach three tokens further than one's)
+    if (!w_unit_fits("k3mla_window_chunk_decode", w_max_pages(p.cap, std::min(window, 0x7FFFFF00) + 3, n_sink)))
+        return K3MLA_E_INVALID;
     // (the planner's one pass over 2^20 slots takes some 30 ms, far inside the bounded waits for its first unit)
     if (units > 0x3FFFFFFFll || (long long)R * H > 0x7FFFFFFFll || B > 1 << 20) {
         set_error("k3mla_window_chunk_decode: too many rows or slots");

@@ -89,3 +89,14 @@ def test_a_shape_may_be_any_sequence():
             k3mla._dev(t, torch.bfloat16, shape, "t")
         with pytest.raises(k3mla.K3mlaError, match="has shape"):
             k3mla._at(0, t, torch.bfloat16, shape, "t")
+
+
+def test_a_unit_of_more_pages_than_the_waits_allow_is_refused():
+    # 2^19 pages of a list in one unit: about half a second of the one that a wait lasts
+    lib, n, cols = k3mla.load(), 2 ** 26, 2 ** 20
+    for change in (dict(split=2 ** 26), dict(split=2 ** 31 - 128), dict(split=2 ** 25 + 128, window=2 ** 25, sink=64)):
+        assert decode(lib, **{**dict(max_ctx=n, cols=cols, window=n, sink=0), **change}) == -1
+        assert b"pages in one unit" in lib.k3mla_last_error()
+    for change in (dict(window=n), dict(window=2 ** 31 - 1, sink=2 ** 31 - 1), dict(window=2 ** 25, sink=0)):
+        assert chunk(lib, **{**dict(max_ctx=n, cols=cols), **change}) == -1
+        assert b"pages in one unit" in lib.k3mla_last_error()
