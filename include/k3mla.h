@@ -350,9 +350,11 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  *   o_lat = sum_t p_t row_t[0:512],    out[h] = W_UV[h] o_lat
  * with a -1 table entry read as zero rows that take part in the softmax, as in k3mla_paged_decode.
  * Scores, maxima and sums are f32 (there is no bf16 landing of the scores here); p goes to the tensor
- * cores in bf16, o_lat in f16 with a power of two per row.  Pages that hold no seen token are neither read nor
+ * cores in bf16, o_lat in f16 with a power of two per row, and where a slot has several splits each one's sum of
+ * p_t row_t goes to the merge in f16 with a power of two per row.  Pages that hold no seen token are neither read nor
  * looked up in the table (k3mla_pool_trim frees them), and what they or the unseen tokens of other pages
- * hold, NaN and infinities included, never reaches a result.  window >= n gives full attention.
+ * hold, NaN and infinities included, never reaches a result.  A seen token with a NaN or an infinity among its
+ * latents makes the whole row NaN, its p being 0 included.  window >= n gives full attention.
  *
  * k3mla_window_decode: one token row per slot, n = ctx_len[b].
  * k3mla_window_chunk_decode: the token rows of prefill chunks (as for k3mla_chunk_decode): row j of slot
@@ -372,7 +374,8 @@ int k3mla_decode_layer(const uint16_t* q, const uint16_t* w_kv_b, uint16_t* slab
  * window      >= 1;  n_sink >= 0
  * scale_bf16  the softmax scale as a bf16 bit pattern, positive and at most 0x7F31 (2.35e38: times log2(e) it stays finite)
  * max_ctx     upper bound of n; a larger one is clamped, as one past the table is (K3MLA_DEV_CTX)
- * workspace   device, 256-byte aligned, at least the bytes that the sizing call gives; scratch
+ * workspace   device, 256-byte aligned, at least the bytes that the sizing call gives; scratch: calls that may
+ *             overlap on the GPU need one each
  * others      as for k3mla_paged_decode and k3mla_chunk_decode
  * Two kernels on `stream`, or three (some batches with several splits a slot), each reading nothing but
  * w_kv_b before the kernel ahead of the call has completed: w_kv_b must not be written by the kernel

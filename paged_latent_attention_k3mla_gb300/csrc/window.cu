@@ -7,11 +7,15 @@
 //     p     = softmax(s),  o_lat = sum_t p_t r_t[0:512],  out = W_UV[h] o_lat.
 // Decode: one token row per slot.  Chunk: several consecutive new token rows per slot.
 //
-// Numerics.  Scores, maxima, sums and o_lat are f32.  Three roundings go below that: the p of the second
-// contraction to bf16 (the tensor core's operand type; both operands have one type and the cache is bf16),
-// o_lat to f16 with a power of two per row (2^-12 of an entry; bf16 here would add as much error again as
-// the output's own rounding does), and the output to bf16.  W_UV, bf16, takes part as f16 with a power of
-// two per row of its own: exact, but for entries below 2^-29 of their row's largest.
+// Numerics.  Scores, maxima and sums are f32.  Four roundings go below that: the p of the second contraction
+// to bf16 (the tensor core's operand type; both operands have one type and the cache is bf16), a split's O,
+// where there are several, to f16 with a power of two per row on its way to the merge (f32 there would take
+// twice the stores and loads), o_lat, the operand of the expansion, to f16 likewise (bf16 here would add as
+// much error again as the output's own rounding does), and the output to bf16.  W_UV, bf16, takes part as f16
+// with a power of two per row of its own: exact, but for entries below 2^-29 of their row's largest.  What each
+// adds, relative to the output in the mean square, emulated at 64 to 4,600 seen tokens: the output's own 0.0017,
+// p 0.0009 to 0.0014, o_lat 0.0002, 17 splits' O 0.0001 to 0.0002; together 0.0019 to 0.0022, of which the
+// splits' f16 makes 0.00001.
 //
 // Structure.  A unit of work is 96 heads of one slot and one split of what it sees (decode), or 32 heads of
 // up to four consecutive token rows (chunk): a row in each of the 128 (96) TMEM lanes.  Clusters of two
@@ -36,11 +40,12 @@
 //     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get a NaN for
 //     their p of it (its score may be -inf, whose p is 0, and 0 times the latent that was there is NaN).
 //
-// Measured, whole calls: decode of 64 slots over 4,100 seen tokens 69.0 us (324 MB, 0.69 of the copy rate), over 1,088 33.2
-// us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens 232 us (1,003 TFLOP/s, 0.52 of
-// the measured bf16 rate), of 1,000 rows over 300 120.5 us (29 of them the expansion).  Bounds: the page stream for long
-// lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which the score MMAs
-// take 0.6), else the chain through a unit and the expansion behind it (6 us).
+// Measured, all kernels of a call in a graph of calls: decode of 64 slots over 4,100 seen tokens 69.1 us (324 MB, 0.69 of
+// the copy rate), over 1,088 33.2 us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens
+// 232 us (1,003 TFLOP/s, 0.52 of the measured bf16 rate), of 1,000 rows over 300 120.8 us (29 of them the expansion).
+// Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 236.8 and 122.5 us).  Bounds: the page
+// stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which
+// the score MMAs take 0.57 at their full rate), else the chain through a unit and the expansion behind it (6 us).
 //
 // Every wait is bounded, as in decode.cu: after WAIT_NS it sets K3MLA_DEV_TIMEOUT and the roles run out.
 #include <cuda.h>
