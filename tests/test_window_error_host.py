@@ -1,4 +1,4 @@
-"""The checker in window_error.py: it accepts the roundings that the windowed kernels make and rejects wrong results that
+"""The bounds of window_error.py: they accept the roundings that the windowed kernels make and reject wrong results that
 are within the bound of every element (no GPU needed)."""
 from __future__ import annotations
 
