@@ -1573,6 +1573,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
             }
         }
     }
+    if (aborted(sm)) drain_inflight();  // (as in the attention kernel)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
