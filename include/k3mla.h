@@ -60,6 +60,9 @@ extern "C" {
 #define K3MLA_SPLIT_AUTO 0     /* split_tokens: the default per-slot rule (see k3mla_paged_decode) */
 #define K3MLA_SPLIT_MAX 4096   /* longest split of the default rule, in tokens */
 
+#define K3MLA_QUANT_ROW_BYTES 640    /* the 8-bit cache: a token's row in a layer, without its scale */
+#define K3MLA_QUANT_PAGE_BYTES 41088 /* ... a page of a layer: 64 rows, then 64 scales */
+
 #define K3MLA_OK 0
 #define K3MLA_E_INVALID (-1)   /* bad pointer, size or alignment */
 #define K3MLA_E_NO_PAGES (-2)  /* pool exhausted */
@@ -393,6 +396,55 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
                               const int32_t* row_start, int B, int R, const uint16_t* w_kv_b, uint16_t scale_bf16,
                               uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx, int window, int n_sink,
                               int32_t* dev_err, void* stream);
+
+/* ---- the 8-bit latent cache ------------------------------------------------------------
+ * A second form of the cache, 642 bytes a token and layer instead of 1,152: slab [n_pages][n_layers] of blocks of
+ * K3MLA_QUANT_PAGE_BYTES, each a page of a layer: 64 rows of K3MLA_QUANT_ROW_BYTES, [512 e4m3 codes | 64 bf16 rope entries],
+ * then 64 scales, a bf16 power of two for each row.  A row stands for code_j * scale (512 latents) and rope_i * scale (the
+ * rope key).  Writing a row with latents c and rope key k:
+ *   scale  = 2^n with the smallest n that brings the largest finite |c_j| to at most 448 (0 for a row of zeros), raised
+ *            where needed to keep |k_i| / 2^n below 2^120, within [-96, 120]
+ *   code_j = e4m3(c_j / 2^n), rounded to nearest even; NaN for a NaN or an infinity
+ *   rope_i = bf16(k_i / 2^n), exact for entries of magnitude 2^(n - 126) or more
+ * A code is off by at most 2^-4 of its entry (or 2^-10 of e4m3's smallest step's 2^n where the entry is below 2^(n - 6)).
+ * Page ids, block tables and the pool (k3mla_pool_*) are those of the bf16 cache.
+ *
+ * k3mla_quant_norm_rope_append: k3mla_norm_rope_append_at with the cache rows written to the 8-bit cache, from the f32 values
+ * of the norm and the rotation (one rounding).  rope_pos0, the weights and inv_freq may be NULL; with all of them NULL and
+ * q_out == q it is an append of quantised rows.
+ * slab  device, 16-byte aligned; the other arguments as there.  Per row 640 + 2 bytes are written, in its page's block only. */
+int k3mla_quant_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint8_t* slab,
+                                 int n_pages, int n_layers, int layer, const int32_t* block_table,
+                                 int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                                 const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight,
+                                 const uint16_t* k_rope, int64_t r_stride, const uint16_t* k_weight, float eps,
+                                 const float* inv_freq, int interleaved, int B, int R, int32_t* dev_err, void* stream);
+
+/* Whole pages between the caches, all n_layers layers of page src_ids[i] of src_slab to page dst_ids[i] of dst_slab, i < n:
+ *   k3mla_quant_write_pages  bf16 -> 8 bits (adopting a prefilled sequence)
+ *   k3mla_quant_read_pages   8 bits -> bf16, the values that the rows stand for, exact but where they leave bf16's normal range (a
+ *                            latent above 3.29e38 may have become 2^128, an infinity there); a cached prefix for
+ *                            k3mla_chunk_decode or k3mla_window_chunk_decode
+ *   k3mla_quant_copy_pages   8 bits -> 8 bits (the pair k3mla_pool_cow names)
+ * Ids, their rules, dev_err and launch as for k3mla_copy_pages; slabs 16-byte aligned. */
+int k3mla_quant_write_pages(uint8_t* dst_slab, int dst_n_pages, const uint16_t* src_slab, int src_n_pages, int n_layers,
+                            const int32_t* src_ids, const int32_t* dst_ids, int n, int32_t* dev_err, void* stream);
+int k3mla_quant_read_pages(uint16_t* dst_slab, int dst_n_pages, const uint8_t* src_slab, int src_n_pages, int n_layers,
+                           const int32_t* src_ids, const int32_t* dst_ids, int n, int32_t* dev_err, void* stream);
+int k3mla_quant_copy_pages(uint8_t* dst_slab, int dst_n_pages, const uint8_t* src_slab, int src_n_pages, int n_layers,
+                           const int32_t* src_ids, const int32_t* dst_ids, int n, int32_t* dev_err, void* stream);
+
+/* k3mla_quant_decode: k3mla_window_decode over the 8-bit cache, one token row per slot: the same attention (window >=
+ * max_ctx: the whole context) over the rows that the cache stands for, the same splits, arguments, refusals and treatment of
+ * empty slots, -1 entries, unseen tokens and non-finite values.  slab 128-byte aligned.
+ * k3mla_quant_split_tokens plans a split length as k3mla_window_split_tokens does. */
+size_t k3mla_quant_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);
+int k3mla_quant_split_tokens(int B, int max_ctx, int window, int n_sink);
+int k3mla_quant_decode(const uint16_t* q_abs, const uint8_t* slab, int n_pages, int n_layers, int layer,
+                       const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                       const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                       size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
+                       int32_t* dev_err, void* stream);
 
 /* The split length a slot of context ctx gets from k3mla_paged_decode:
  * split_tokens when it is positive, else the default rule's length (at most

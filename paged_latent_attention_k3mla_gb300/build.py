@@ -18,7 +18,7 @@ LIB = os.path.join(BUILD, "libk3mla.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 SOURCES = ["host_common.cu", "decode.cu", "merge_expand.cu", "absorb_append.cu", "pages.cu", "chunk.cu", "exact.cu",
-           "expanded.cu", "norm_rope.cu", "window.cu", "pool.cpp", "plan.cpp"]
+           "expanded.cu", "norm_rope.cu", "window.cu", "quant_pages.cu", "quant_decode.cu", "pool.cpp", "plan.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

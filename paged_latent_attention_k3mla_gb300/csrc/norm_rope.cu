@@ -31,6 +31,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "quant.cuh"
 #include "rows.cuh"
 
 namespace k3 {
@@ -45,7 +46,7 @@ struct NormRopeParams {
     const uint16_t* q;
     uint16_t* q_out;  // may be q
     const uint16_t *wq, *wc, *wk;  // null: that norm is left out
-    uint16_t* slab;
+    void* slab;  // bf16 rows, or page blocks of the 8-bit cache
     const int32_t *table, *pos0, *row_start;  // row_start null: row r is slot r's only one
     const int32_t* rope_pos0;                 // null: the angles' positions are pos0 as well
     const uint16_t *c_kv, *k_rope;
@@ -57,20 +58,6 @@ struct NormRopeParams {
     int q_ctas;  // NR_QCTAS * R, or 0 when the queries stay as they are
     int q_nope;  // 0: entries 0..127 of every head stay as they are (no norm, in place)
 };
-
-__device__ __forceinline__ void nr_unpack(const uint4& v, float (&x)[8])
-{
-    x[0] = bf16lo_to_f32(v.x), x[1] = bf16hi_to_f32(v.x);
-    x[2] = bf16lo_to_f32(v.y), x[3] = bf16hi_to_f32(v.y);
-    x[4] = bf16lo_to_f32(v.z), x[5] = bf16hi_to_f32(v.z);
-    x[6] = bf16lo_to_f32(v.w), x[7] = bf16hi_to_f32(v.w);
-}
-
-__device__ __forceinline__ uint4 nr_pack(const float (&x)[8])
-{
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-}
 
 __device__ __forceinline__ float nr_sumsq(const float (&x)[8])
 {
@@ -84,7 +71,7 @@ __device__ __forceinline__ float nr_sumsq(const float (&x)[8])
 __device__ __forceinline__ void nr_scale(float (&x)[8], float rs, const uint16_t* w)
 {
     float y[8];
-    nr_unpack(*reinterpret_cast<const uint4*>(w), y);
+    unpack8(*reinterpret_cast<const uint4*>(w), y);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= rs * y[e];
 }
@@ -134,7 +121,7 @@ __device__ __forceinline__ void nr_query(const NormRopeParams& p, int r, int par
     const int g = threadIdx.x >> 3, j = threadIdx.x & 7;
     float x[3][8];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) nr_unpack(raw[k], x[k]);
+    for (int k = 0; k < 3; ++k) unpack8(raw[k], x[k]);
     if (norm) {
         float s = nr_sumsq(x[0]) + nr_sumsq(x[1]) + nr_sumsq(x[2]);
 #pragma unroll
@@ -146,21 +133,22 @@ __device__ __forceinline__ void nr_query(const NormRopeParams& p, int r, int par
     if (rot) nr_rotate(x[2], j, cs, p.interleaved != 0);
     uint4* dst = reinterpret_cast<uint4*>(p.q_out + ((size_t)r * H + part * NR_HEADS + g) * QDIM);
     if (p.q_nope) {
-        dst[j] = nr_pack(x[0]);
-        dst[j + 8] = nr_pack(x[1]);
+        dst[j] = pack8(x[0]);
+        dst[j + 8] = pack8(x[1]);
     }
-    dst[j + 16] = nr_pack(x[2]);
+    dst[j + 16] = pack8(x[2]);
 }
 
+template <bool QUANT>
 __device__ __forceinline__ void nr_key_row(const NormRopeParams& p, int r, int b, int64_t pos, const float2* cs)
 {
     const int lane = (int)lane_id();
     const uint4* sc = reinterpret_cast<const uint4*>(p.c_kv + (int64_t)r * p.c_stride);
     const uint4* sk = reinterpret_cast<const uint4*>(p.k_rope + (int64_t)r * p.r_stride);
     float c0[8], c1[8], k[8];
-    nr_unpack(sc[lane], c0);
-    nr_unpack(sc[lane + 32], c1);
-    nr_unpack(lane < 8 ? sk[lane] : make_uint4(0u, 0u, 0u, 0u), k);
+    unpack8(sc[lane], c0);
+    unpack8(sc[lane + 32], c1);
+    unpack8(lane < 8 ? sk[lane] : make_uint4(0u, 0u, 0u, 0u), k);
     if (p.wc) {
         float s = nr_sumsq(c0) + nr_sumsq(c1);
 #pragma unroll
@@ -182,16 +170,20 @@ __device__ __forceinline__ void nr_key_row(const NormRopeParams& p, int r, int b
         if (lane == 0 && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_UNMAPPED);
         return;
     }
-    const size_t row = ((size_t)id * (size_t)p.n_layers + (size_t)p.layer) * PAGE + (size_t)(pos % PAGE);
-    uint4* dst = reinterpret_cast<uint4*>(p.slab + row * ROW);
-    dst[lane] = nr_pack(c0);
-    dst[lane + 32] = nr_pack(c1);
-    if (lane < 8) dst[lane + 64] = nr_pack(k);
+    const size_t block = (size_t)id * (size_t)p.n_layers + (size_t)p.layer;
+    if constexpr (QUANT) {  // (the f32 values: one rounding to a code)
+        quant_store_row(reinterpret_cast<uint8_t*>(p.slab) + block * QPAGE, (int)(pos % PAGE), c0, c1, k);
+        return;
+    }
+    uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.slab) + (block * PAGE + (size_t)(pos % PAGE)) * ROW);
+    dst[lane] = pack8(c0);
+    dst[lane + 32] = pack8(c1);
+    if (lane < 8) dst[lane + 64] = pack8(k);
 }
 
 // Grid: q_ctas CTAs of a row's 32 heads each, then ceil(R / 8) CTAs of eight cache rows.  AT: with rope_pos0 (asking for
-// it in the one kernel took 5,251 rows from 61.8 to 62.3 us).
-template <bool AT>
+// it in the one kernel took 5,251 rows from 61.8 to 62.3 us).  QUANT: the slab is the 8-bit cache (quant.cuh).
+template <bool AT, bool QUANT>
 __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormRopeParams p)
 {
     __shared__ float2 cs[NR_WARPS][ROPE / 2];
@@ -227,7 +219,7 @@ __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormR
             cs[warp][lane] = nr_angle(nr_rope_position<AT>(p, b, pos), p.inv_freq[lane]);
             __syncwarp();
         }
-        nr_key_row(p, r, b, pos, cs[warp]);
+        nr_key_row<QUANT>(p, r, b, pos, cs[warp]);
     }
 }
 
@@ -235,33 +227,33 @@ __global__ void __launch_bounds__(NR_THREADS) k3mla_norm_rope_kernel(const NormR
 
 using namespace k3;
 
-extern "C" int k3mla_norm_rope_append_at(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
-                                         int n_pages, int n_layers, int layer, const int32_t* block_table,
-                                         int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
-                                         const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride,
-                                         const uint16_t* c_weight, const uint16_t* k_rope, int64_t r_stride,
-                                         const uint16_t* k_weight, float eps, const float* inv_freq, int interleaved, int B,
-                                         int R, int32_t* dev_err, void* stream)
+// What the calls share: the 8-bit cache (quant) or the bf16 one.
+static int norm_rope_append(const char* who, bool quant, const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight,
+                            void* slab, int n_pages, int n_layers, int layer, const int32_t* block_table,
+                            int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start, const int32_t* rope_pos0,
+                            const uint16_t* c_kv, int64_t c_stride, const uint16_t* c_weight, const uint16_t* k_rope,
+                            int64_t r_stride, const uint16_t* k_weight, float eps, const float* inv_freq, int interleaved,
+                            int B, int R, int32_t* dev_err, void* stream)
 {
     if (B < 0 || R < 0 || n_pages <= 0 || n_layers <= 0 || layer < 0 || layer >= n_layers || max_pages_per_slot <= 0 ||
         c_stride < LORA || r_stride < ROPE || (c_stride & 7) || (r_stride & 7) || !(eps >= 0.f) || (!row_start && R != B)) {
-        set_error("k3mla_norm_rope_append: invalid sizes, strides or eps");
+        set_error("%s: invalid sizes, strides or eps", who);
         return K3MLA_E_INVALID;
     }
     if (B == 0 || R == 0) return K3MLA_OK;
     if ((long long)NR_QCTAS * R + (R + NR_WARPS - 1) / NR_WARPS > 0x7FFFFFFFll) {
-        set_error("k3mla_norm_rope_append: too many rows");
+        set_error("%s: too many rows", who);
         return K3MLA_E_INVALID;
     }
     if (!q || !q_out || !slab || !block_table || !pos0 || !c_kv || !k_rope || !aligned(q, 16) || !aligned(q_out, 16) ||
         !aligned(slab, 16) || !aligned(c_kv, 16) || !aligned(k_rope, 16) || !aligned(q_weight, 16) ||
         !aligned(c_weight, 16) || !aligned(k_weight, 16) || !aligned(inv_freq, 4)) {
-        set_error("k3mla_norm_rope_append: null or misaligned pointer");
+        set_error("%s: null or misaligned pointer", who);
         return K3MLA_E_INVALID;
     }
     const uintptr_t from = reinterpret_cast<uintptr_t>(q), to = reinterpret_cast<uintptr_t>(q_out);
     if (from != to && (from < to ? to - from : from - to) < (size_t)R * H * QDIM * 2) {
-        set_error("k3mla_norm_rope_append: q_out overlaps q in part");
+        set_error("%s: q_out overlaps q in part", who);
         return K3MLA_E_INVALID;
     }
     if (!device_ok()) return K3MLA_E_DEVICE;
@@ -274,9 +266,24 @@ extern "C" int k3mla_norm_rope_append_at(const uint16_t* q, uint16_t* q_out, con
     const bool stays = q == q_out && !q_weight;  // entries 0..127 of every head
     p.q_nope = stays ? 0 : 1;
     p.q_ctas = stays && !inv_freq ? 0 : NR_QCTAS * R;
-    return launch_pdl(rope_pos0 ? k3mla_norm_rope_kernel<true> : k3mla_norm_rope_kernel<false>,
+    const auto kernel = quant ? (rope_pos0 ? k3mla_norm_rope_kernel<true, true> : k3mla_norm_rope_kernel<false, true>)
+                              : (rope_pos0 ? k3mla_norm_rope_kernel<true, false> : k3mla_norm_rope_kernel<false, false>);
+    return launch_pdl(kernel,
                       dim3(p.q_ctas + (R + NR_WARPS - 1) / NR_WARPS), dim3(NR_THREADS), 0,
                       reinterpret_cast<cudaStream_t>(stream), "k3mla_norm_rope_kernel", p);
+}
+
+extern "C" int k3mla_norm_rope_append_at(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
+                                         int n_pages, int n_layers, int layer, const int32_t* block_table,
+                                         int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                                         const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride,
+                                         const uint16_t* c_weight, const uint16_t* k_rope, int64_t r_stride,
+                                         const uint16_t* k_weight, float eps, const float* inv_freq, int interleaved, int B,
+                                         int R, int32_t* dev_err, void* stream)
+{
+    return norm_rope_append("k3mla_norm_rope_append", false, q, q_out, q_weight, slab, n_pages, n_layers, layer, block_table,
+                            max_pages_per_slot, pos0, row_start, rope_pos0, c_kv, c_stride, c_weight, k_rope, r_stride,
+                            k_weight, eps, inv_freq, interleaved, B, R, dev_err, stream);
 }
 
 extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint16_t* slab,
@@ -290,4 +297,17 @@ extern "C" int k3mla_norm_rope_append(const uint16_t* q, uint16_t* q_out, const 
     return k3mla_norm_rope_append_at(q, q_out, q_weight, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot,
                                      pos0, row_start, nullptr, c_kv, c_stride, c_weight, k_rope, r_stride, k_weight, eps,
                                      inv_freq, interleaved, B, R, dev_err, stream);
+}
+
+extern "C" int k3mla_quant_norm_rope_append(const uint16_t* q, uint16_t* q_out, const uint16_t* q_weight, uint8_t* slab,
+                                            int n_pages, int n_layers, int layer, const int32_t* block_table,
+                                            int max_pages_per_slot, const int32_t* pos0, const int32_t* row_start,
+                                            const int32_t* rope_pos0, const uint16_t* c_kv, int64_t c_stride,
+                                            const uint16_t* c_weight, const uint16_t* k_rope, int64_t r_stride,
+                                            const uint16_t* k_weight, float eps, const float* inv_freq, int interleaved,
+                                            int B, int R, int32_t* dev_err, void* stream)
+{
+    return norm_rope_append("k3mla_quant_norm_rope_append", true, q, q_out, q_weight, slab, n_pages, n_layers, layer,
+                            block_table, max_pages_per_slot, pos0, row_start, rope_pos0, c_kv, c_stride, c_weight, k_rope,
+                            r_stride, k_weight, eps, inv_freq, interleaved, B, R, dev_err, stream);
 }

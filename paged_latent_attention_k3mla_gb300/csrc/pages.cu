@@ -166,27 +166,44 @@ __global__ void __launch_bounds__(THREADS) k3mla_compact_rows_kernel(const Compa
 
 using namespace k3;
 
-extern "C" int k3mla_copy_pages(uint16_t* dst_slab, int dst_n_pages, const uint16_t* src_slab, int src_n_pages,
-                                int n_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
-                                int32_t* dev_err, void* stream)
+// Pages of n_layers * layer_bytes (a multiple of 16) each.
+static int copy_pages(const char* who, void* dst_slab, int dst_n_pages, const void* src_slab, int src_n_pages, int n_layers,
+                      size_t layer_bytes, const int32_t* src_ids, const int32_t* dst_ids, int n, int32_t* dev_err, void* stream)
 {
     if (n < 0 || n_layers <= 0 || dst_n_pages <= 0 || src_n_pages <= 0 || n > 65535) {
-        set_error("k3mla_copy_pages: invalid sizes (n must be in [0, 65535])");
+        set_error("%s: invalid sizes (n must be in [0, 65535])", who);
         return K3MLA_E_INVALID;
     }
     if (n == 0) return K3MLA_OK;
     if (!dst_slab || !src_slab || !src_ids || !dst_ids || !aligned(dst_slab, 16) || !aligned(src_slab, 16)) {
-        set_error("k3mla_copy_pages: null or misaligned pointer");
+        set_error("%s: null or misaligned pointer", who);
         return K3MLA_E_INVALID;
     }
     if (!device_ok()) return K3MLA_E_DEVICE;
-    const size_t page_vecs = (size_t)n_layers * PAGE * ROW * 2 / 16;  // 4,608 16-byte vectors per layer
+    const size_t page_vecs = (size_t)n_layers * layer_bytes / 16;  // 4,608 16-byte vectors per bf16 layer, 2,568 of the 8-bit cache
     const size_t per_cta = (size_t)CP_THREADS * CP_VEC;
     size_t chunks = (page_vecs + per_cta - 1) / per_cta;
     if (chunks > 1024) chunks = 1024;  // a grid-stride loop covers the rest of a very deep page
     return launch_pdl(k3mla_copy_pages_kernel, dim3((unsigned)chunks, (unsigned)n), dim3(CP_THREADS), 0,
-                      reinterpret_cast<cudaStream_t>(stream), "k3mla_copy_pages_kernel", dst_slab, dst_n_pages,
-                      src_slab, src_n_pages, src_ids, dst_ids, page_vecs, dev_err);
+                      reinterpret_cast<cudaStream_t>(stream), "k3mla_copy_pages_kernel",
+                      reinterpret_cast<uint16_t*>(dst_slab), dst_n_pages, reinterpret_cast<const uint16_t*>(src_slab),
+                      src_n_pages, src_ids, dst_ids, page_vecs, dev_err);
+}
+
+extern "C" int k3mla_copy_pages(uint16_t* dst_slab, int dst_n_pages, const uint16_t* src_slab, int src_n_pages,
+                                int n_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                                int32_t* dev_err, void* stream)
+{
+    return copy_pages("k3mla_copy_pages", dst_slab, dst_n_pages, src_slab, src_n_pages, n_layers, (size_t)PAGE * ROW * 2, src_ids,
+                      dst_ids, n, dev_err, stream);
+}
+
+extern "C" int k3mla_quant_copy_pages(uint8_t* dst_slab, int dst_n_pages, const uint8_t* src_slab, int src_n_pages,
+                                      int n_layers, const int32_t* src_ids, const int32_t* dst_ids, int n,
+                                      int32_t* dev_err, void* stream)
+{
+    return copy_pages("k3mla_quant_copy_pages", dst_slab, dst_n_pages, src_slab, src_n_pages, n_layers, K3MLA_QUANT_PAGE_BYTES,
+                      src_ids, dst_ids, n, dev_err, stream);
 }
 
 extern "C" int k3mla_compact_rows(uint16_t* slab, int n_pages, int n_layers, const int32_t* block_table,

@@ -59,6 +59,7 @@
 #include "decode_core.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
+#include "window.cuh"
 
 namespace k3 {
 
@@ -226,21 +227,6 @@ template <bool MQ> __device__ __forceinline__ bool w_count(const int32_t* counte
 {
     if (*reinterpret_cast<const volatile int32_t*>(counter) >= target) return true;
     return w_count_slow<MQ>(counter, target);
-}
-
-__host__ __device__ inline int w_clamp(int n, int cap) { return n < 0 ? 0 : (n > cap ? cap : n); }
-
-// The pages that the rows with contexts n_lo .. n_hi see: how many, and the two numbers of WUnit.
-__host__ __device__ inline int w_pages(int n_lo, int n_hi, int window, int n_sink, int& nsp, int& wp0)
-{
-    nsp = wp0 = 0;
-    if (n_hi <= 0) return 0;
-    const int lo = n_lo > window ? n_lo - window : 0;
-    const int sink = n_sink < n_hi ? n_sink : n_hi;
-    wp0 = lo / PAGE;
-    nsp = (sink + PAGE - 1) / PAGE;
-    if (nsp > wp0) nsp = wp0;
-    return nsp + (n_hi + PAGE - 1) / PAGE - wp0;
 }
 
 // Where the search for a chunk's group stands: a cluster's units come in ascending order, so each search goes on in
@@ -903,17 +889,6 @@ template <bool MQ> __device__ __forceinline__ void w_empty_rows(const WinParams&
         if (!sees)
             for (int h = 0; h < H; ++h) p.oscale[(size_t)h * p.R + r] = 0.f;
     }
-}
-
-// The power of two that brings a row with largest magnitude m into f16's range (to [2^14, 2^15)), and its
-// inverse; 1 for rows of zeros, infinities or NaN.
-__device__ __forceinline__ float w_row_scale(float m, float& inverse)
-{
-    const int e = (int)(__float_as_uint(m) >> 23) & 255;  // m >= 0; (f32 subnormals count as zero)
-    const bool plain = e > 0 && e < 255;
-    const int up = plain ? min(max(141 - e, -126), 126) : 0;  // 2^up m in [2^14, 2^15), or as near as f32 allows
-    inverse = __uint_as_float((uint32_t)(127 - up) << 23);
-    return __uint_as_float((uint32_t)(127 + up) << 23);
 }
 
 // O [rows x 512] f32 leaves TMEM, half the dims a warp, as f16 with a power of two per row: o_lat = O / l when the
@@ -1583,89 +1558,15 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
 
 // ---- host --------------------------------------------------------------------------------------
 
-static size_t w_up(size_t x) { return (x + 255) & ~size_t(255); }
-
-// The most pages a slot of at most cap tokens can see, and the splits that makes.
-static long long w_max_pages(int cap, int window, int n_sink)
-{
-    const long long all = ((long long)cap + PAGE - 1) / PAGE;
-    const long long sink = ((long long)std::min(n_sink, cap) + PAGE - 1) / PAGE;
-    const long long win = ((long long)std::min(window, cap) + PAGE - 2) / PAGE + 1;
-    return std::min(all, sink + win);
-}
-
-static int w_nsplit(int cap, int window, int n_sink, int split_tokens)
-{
-    return launch_nsplit((int)std::min<long long>(w_max_pages(cap, window, n_sink) * PAGE, 0x7FFFFF00), split_tokens);
-}
-
-struct WinWs {
-    size_t olat, scale, o, oscale, ml, total;
-};
-static WinWs w_layout(long long rows, int nsplit)
-{
-    WinWs w;
-    w.olat = 0;
-    w.scale = w_up((size_t)rows * H * LORA * 2);
-    w.o = w.scale + w_up((size_t)rows * H * 4);
-    const size_t records = nsplit > 1 ? (size_t)rows * nsplit * H : 0;
-    w.oscale = w.o + w_up(records * LORA * 2);
-    w.ml = w.oscale + w_up(records * 4);
-    w.total = w.ml + w_up(records * 8);
-    return w;
-}
-
-static int sm_count()
-{
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    return sms;
-}
-
-static bool w_scale(uint16_t bits, float* kscale)
-{
-    uint32_t u = (uint32_t)bits << 16;
-    float f;
-    std::memcpy(&f, &u, 4);
-    if (!(f > 0.f) || (bits & 0x7F80) == 0x7F80) return false;
-    const double k = (double)f * 1.4426950408889634;
-    *kscale = (float)k;
-    return k <= 3.4028234663852886e38;  // (an infinite factor would make NaN of every score of 0)
-}
-
+// From the splits' records, or the o_lat already landed, to the outputs; p is the attention kernel's.
 template <bool MQ>
-static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
-                    const WinWs& wl, WinParams& p, cudaStream_t st)
+static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStream_t st)
 {
-    using C = WCfg<MQ>;
-    p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
-    p.oscale = reinterpret_cast<float*>(ws + wl.scale);
-    p.ws_o = p.nsplit > 1 ? reinterpret_cast<uint16_t*>(ws + wl.o) : nullptr;
-    p.ws_oscale = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.oscale) : nullptr;
-    p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
-    CUtensorMap tm_page, tm_page8, tm_q, tm_w, tm_o;
-    const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
-    int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
-    if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
+    CUtensorMap tm_w, tm_o;
+    int rc = make_tmap_slab_3d(&tm_w, w_kv_b, (uint64_t)H * WROWS_PER_HEAD, LORA, 8, VH, 1);
+    if (!rc) rc = make_tmap_slab_3d(&tm_o, p.olat, (uint64_t)H * p.R, LORA, 8, WX_TILE, 1);
     if (rc) return rc;
-    if (MQ) {
-        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
-        const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
-        const uint32_t box[4] = {64, 32, 2, 1};
-        rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
-    } else {
-        rc = make_tmap_slab_3d(&tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
-    }
-    if (!rc) rc = make_tmap_slab_3d(&tm_w, w_kv_b, (uint64_t)H * WROWS_PER_HEAD, LORA, 8, VH, 1);
-    if (!rc) rc = make_tmap_slab_3d(&tm_o, p.olat, (uint64_t)H * R, LORA, 8, WX_TILE, 1);
-    if (rc) return rc;
-    static bool attr_done[64] = {}, attr_expand[3][64] = {};
-    const size_t smem = sizeof(WSmem<MQ>) + 1024;
-    set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
-    const int clusters = std::min(p.n_units, sm_count() / 2);
-    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
-                    tm_page8, tm_q, p);
-    if (rc) return rc;
+    static bool attr_expand[3][64] = {};
     // Few rows: the expansion adds the splits up itself, four warps a row (a slot of 3 splits 20.5 -> 16.9 us, of 33 27.5 ->
     // 21.2 us, four slots of 17 26.2 -> 25.5 us) or one (16 slots of 3 26.5 -> 25.0 us, 16 of 4 38.2 -> 36.1 us; but ten of
     // 6 26.8 -> 27.3 us, five of 11 25.8 -> 30.0 us: a warp then goes through its list in several rounds).
@@ -1686,14 +1587,38 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
                       tm_o, x, p);
 }
 
-// A unit's pages take up to 0.85 us each, and its write-out waits for all of them within WAIT_NS: half of that is allowed.
-constexpr long long W_UNIT_PAGES = 1 << 19;
-
-static bool w_unit_fits(const char* who, long long pages)
+template <bool MQ>
+static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
+                    const WinWs& wl, WinParams& p, cudaStream_t st)
 {
-    if (pages <= W_UNIT_PAGES) return true;
-    set_error("%s: %lld pages in one unit of work, more than %lld", who, pages, W_UNIT_PAGES);
-    return false;
+    using C = WCfg<MQ>;
+    p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
+    p.oscale = reinterpret_cast<float*>(ws + wl.scale);
+    p.ws_o = p.nsplit > 1 ? reinterpret_cast<uint16_t*>(ws + wl.o) : nullptr;
+    p.ws_oscale = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.oscale) : nullptr;
+    p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
+    CUtensorMap tm_page, tm_page8, tm_q;
+    const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
+    int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
+    if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
+    if (rc) return rc;
+    if (MQ) {
+        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
+        const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
+        const uint32_t box[4] = {64, 32, 2, 1};
+        rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
+    } else {
+        rc = make_tmap_slab_3d(&tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
+    }
+    if (rc) return rc;
+    static bool attr_done[64] = {};
+    const size_t smem = sizeof(WSmem<MQ>) + 1024;
+    set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
+    const int clusters = std::min(p.n_units, sm_count() / 2);
+    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
+                    tm_page8, tm_q, p);
+    if (rc) return rc;
+    return w_tail<MQ>(w_kv_b, out, p, st);
 }
 
 // What both entries ask of their common arguments; fills p.
@@ -1722,6 +1647,16 @@ static int w_check(const char* who, const uint16_t* q_abs, const uint16_t* slab,
     p.window = window, p.n_sink = n_sink, p.nsplit = 1;
     p.wait_ns = WAIT_NS;
     return K3MLA_OK;
+}
+
+int launch_window_tail(const TailArgs& t, cudaStream_t st)
+{
+    WinParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.ctx_len = t.ctx_len, p.olat = t.olat, p.oscale = t.oscale, p.ws_o = t.ws_o, p.ws_oscale = t.ws_oscale, p.ws_ml = t.ws_ml;
+    p.dev_err = t.dev_err, p.B = p.R = t.B, p.cap = t.cap, p.window = t.window, p.n_sink = t.n_sink;
+    p.split_tokens = t.split_tokens, p.nsplit = t.nsplit;
+    return w_tail<false>(t.w_kv_b, t.out, p, st);
 }
 
 }  // namespace k3

@@ -16,6 +16,7 @@ import torch
 from . import build as _build
 
 H, NOPE, ROPE, V, LORA, PAGE, ROW, TILE = 96, 128, 64, 128, 512, 64, 576, 128
+QUANT_ROW_BYTES, QUANT_PAGE_BYTES = 640, 41088   # the 8-bit cache's rows and page blocks
 SPLIT_AUTO, SPLIT_MAX = 0, 4096   # K3MLA_SPLIT_AUTO (the default per-slot rule), K3MLA_SPLIT_MAX
 
 DEV_BAD_PAGE, DEV_UNMAPPED, DEV_CTX, DEV_TIMEOUT = 1, 2, 4, 8
@@ -36,6 +37,8 @@ EXPORTS = (
     "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
     "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
+    "k3mla_quant_norm_rope_append", "k3mla_quant_write_pages", "k3mla_quant_read_pages", "k3mla_quant_copy_pages",
+    "k3mla_quant_decode_workspace_bytes", "k3mla_quant_split_tokens", "k3mla_quant_decode",
 )
 
 # Size of the library's built-in decode scratch (K3MLA_NOALLOC_SCRATCH_BYTES).
@@ -112,6 +115,14 @@ def load(build_if_needed: bool = True):
                                            ctypes.c_uint32, P, P], I),
             "k3mla_diag_window_chunk_timeout": ([P, P, I, I, I, P, I, P, P, I, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, I,
                                                  ctypes.c_uint32, P, P], I),
+            "k3mla_quant_norm_rope_append": ([P, P, P, P, I, I, I, P, I, P, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I,
+                                              I, I, P, P], I),
+            "k3mla_quant_write_pages": ([P, I, P, I, I, P, P, I, P, P], I),
+            "k3mla_quant_read_pages": ([P, I, P, I, I, P, P, I, P, P], I),
+            "k3mla_quant_copy_pages": ([P, I, P, I, I, P, P, I, P, P], I),
+            "k3mla_quant_decode_workspace_bytes": ([I, I, I, I, I], SZ),
+            "k3mla_quant_split_tokens": ([I, I, I, I], I),
+            "k3mla_quant_decode": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
             "k3mla_pool_trim": ([P, I, I, I, I], I),
             "k3mla_pool_truncate": ([P, I, I], I),
             "k3mla_pool_refill": ([P, I, I], I),
@@ -451,6 +462,109 @@ def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
         _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_window_chunk_decode")
+
+
+def _quant_slab(device: int, t: torch.Tensor, name: str = "slab"):
+    """The address of an 8-bit slab [n_pages, n_layers, QUANT_PAGE_BYTES]."""
+    if t.dim() != 3:
+        raise K3mlaError(f"{name} has shape {tuple(t.shape)}, expected [n_pages, n_layers, {QUANT_PAGE_BYTES}]")
+    return _at(device, t, torch.uint8, (t.shape[0], t.shape[1], QUANT_PAGE_BYTES), name)
+
+
+def quant_norm_rope_append(q: torch.Tensor, q_out: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                           pos0: torch.Tensor, row_start: torch.Tensor | None, c_kv: torch.Tensor, k_rope: torch.Tensor,
+                           q_weight: torch.Tensor | None = None, c_weight: torch.Tensor | None = None,
+                           k_weight: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+                           interleaved: bool = False, dev_err: torch.Tensor | None = None, stream=None,
+                           rope_pos0: torch.Tensor | None = None) -> None:
+    """norm_rope_append into the 8-bit cache: slab [n_pages, n_layers, QUANT_PAGE_BYTES] uint8; see
+    k3mla_quant_norm_rope_append."""
+    R = q.shape[0]
+    B = pos0.shape[0]
+    dev = _here(slab)
+    at = _quant_slab(dev, slab)
+    _check(load().k3mla_quant_norm_rope_append(
+        _at(dev, q, torch.bfloat16, (R, H, NOPE + ROPE), "q"), _at(dev, q_out, torch.bfloat16, (R, H, NOPE + ROPE), "q_out"),
+        _opt_at(dev, q_weight, torch.bfloat16, (NOPE + ROPE,), "q_weight"), at, slab.shape[0], slab.shape[1],
+        _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1], _at(dev, pos0, torch.int32, (B,), "pos0"),
+        _opt_at(dev, row_start, torch.int32, (B + 1,), "row_start"), _opt_at(dev, rope_pos0, torch.int32, (B,), "rope_pos0"),
+        _rows(c_kv, R, "c_kv", LORA, dev), c_kv.stride(0),
+        _opt_at(dev, c_weight, torch.bfloat16, (LORA,), "c_weight"), _rows(k_rope, R, "k_rope", ROPE, dev), k_rope.stride(0),
+        _opt_at(dev, k_weight, torch.bfloat16, (ROPE,), "k_weight"), float(eps),
+        _opt_at(dev, inv_freq, torch.float32, (ROPE // 2,), "inv_freq"), int(bool(interleaved)), B, R,
+        _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_quant_norm_rope_append")
+
+
+def _quant_pages(name: str, dst_slab, src_slab, src_ids, dst_ids, dev_err, stream) -> None:
+    dev = _here(dst_slab)
+    if src_slab.dim() < 2 or dst_slab.dim() < 2 or src_slab.shape[1] != dst_slab.shape[1]:
+        raise K3mlaError("the slabs' layer counts differ")
+    at = [_quant_slab(dev, t, who) if t.dtype == torch.uint8 else
+          _at(dev, t, torch.bfloat16, (t.shape[0], t.shape[1], PAGE, ROW), who)
+          for t, who in ((dst_slab, "dst_slab"), (src_slab, "src_slab"))]
+    n = src_ids.shape[0]
+    _check(getattr(load(), name)(
+        at[0], dst_slab.shape[0], at[1], src_slab.shape[0], dst_slab.shape[1], _at(dev, src_ids, torch.int32, (n,), "src_ids"),
+        _at(dev, dst_ids, torch.int32, (n,), "dst_ids"), n, _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream, dev)), name)
+
+
+def _typed(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
+    if t.dtype != dtype:
+        raise K3mlaError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def quant_write_pages(dst_slab: torch.Tensor, src_slab: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                      dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Pages src_ids[i] of the bf16 slab [n_pages, L, 64, 576] -> pages dst_ids[i] of the 8-bit slab
+    [n_pages, L, QUANT_PAGE_BYTES], all layers."""
+    _quant_pages("k3mla_quant_write_pages", _typed(dst_slab, torch.uint8, "dst_slab"),
+                 _typed(src_slab, torch.bfloat16, "src_slab"), src_ids, dst_ids, dev_err, stream)
+
+
+def quant_read_pages(dst_slab: torch.Tensor, src_slab: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                     dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Pages src_ids[i] of the 8-bit slab -> pages dst_ids[i] of the bf16 slab: the values that their rows stand for."""
+    _quant_pages("k3mla_quant_read_pages", _typed(dst_slab, torch.bfloat16, "dst_slab"),
+                 _typed(src_slab, torch.uint8, "src_slab"), src_ids, dst_ids, dev_err, stream)
+
+
+def quant_copy_pages(dst_slab: torch.Tensor, src_slab: torch.Tensor, src_ids: torch.Tensor, dst_ids: torch.Tensor,
+                     dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """copy_pages between 8-bit slabs (may be the same tensor)."""
+    _quant_pages("k3mla_quant_copy_pages", _typed(dst_slab, torch.uint8, "dst_slab"),
+                 _typed(src_slab, torch.uint8, "src_slab"), src_ids, dst_ids, dev_err, stream)
+
+
+def quant_decode_workspace_bytes(B: int, max_ctx: int, window: int, n_sink: int = 0, split_tokens: int = SPLIT_AUTO) -> int:
+    return int(load().k3mla_quant_decode_workspace_bytes(_int(B, "B"), _int(max_ctx, "max_ctx"), _int(window, "window"),
+                                                         _int(n_sink, "n_sink"), _int(split_tokens, "split_tokens")))
+
+
+def quant_split_tokens(B: int, max_ctx: int, window: int, n_sink: int = 0) -> int:
+    """A split length that keeps the current device busy with B slots of up to max_ctx tokens (batch-dependent)."""
+    return int(load().k3mla_quant_split_tokens(_int(B, "B"), _int(max_ctx, "max_ctx"), _int(window, "window"),
+                                               _int(n_sink, "n_sink")))
+
+
+def quant_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor, ctx_len: torch.Tensor,
+                 w_kv_b: torch.Tensor, scale_bf16: int, out: torch.Tensor, workspace: torch.Tensor, max_ctx: int,
+                 window: int | None = None, n_sink: int = 0, split_tokens: int = SPLIT_AUTO,
+                 dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """window_decode over the 8-bit slab [n_pages, n_layers, QUANT_PAGE_BYTES]; window None: the whole context.  See
+    k3mla_quant_decode.  `workspace`: uint8, >= quant_decode_workspace_bytes."""
+    B = q_abs.shape[0]
+    dev = _here(slab)
+    at = _quant_slab(dev, slab)
+    _check(load().k3mla_quant_decode(
+        _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), at, slab.shape[0], slab.shape[1], _int(layer, "layer"),
+        _table(dev, block_table, B), block_table.shape[1], _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
+        _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(max_ctx if window is None else window, "window"),
+        _int(n_sink, "n_sink"), _int(split_tokens, "split_tokens"), _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"),
+        _stream(stream, dev)), "k3mla_quant_decode")
 
 
 def decode_exact_workspace_bytes(B: int, max_ctx: int) -> int:
