@@ -679,6 +679,14 @@ int k3mla_diag_window_chunk_timeout(const uint16_t* q_abs, const uint16_t* slab,
                                     int window, int n_sink, int withhold_page, uint32_t wait_us, int32_t* dev_err,
                                     void* stream);
 
+/* The same for k3mla_quant_decode: of every unit of work (a split of a slot) the first latent chunk of tile
+ * `withhold_tile` (>= 0: two pages of the unit's list each) is never loaded. */
+int k3mla_diag_quant_timeout(const uint16_t* q_abs, const uint8_t* slab, int n_pages, int n_layers, int layer,
+                             const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                             const uint16_t* w_kv_b, uint16_t scale_bf16, uint16_t* out, void* workspace,
+                             size_t ws_bytes, int B, int max_ctx, int window, int n_sink, int split_tokens,
+                             int withhold_tile, uint32_t wait_us, int32_t* dev_err, void* stream);
+
 /* ---- diagnostic: the exact-chain mode's exponential ------------------------------
  * y[i] = the f32 nearest to e^(x[i]) as the exact-chain mode computes it (the double
  * exponential rounded once to f32 -- the chain's definition of e_t -- evaluated first in

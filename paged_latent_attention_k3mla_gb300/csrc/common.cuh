@@ -76,6 +76,10 @@ int make_tmap_slab_3d(CUtensorMap* map, const void* base, uint64_t rows, uint32_
 int make_tmap_store(CUtensorMap* map, bool f32, uint32_t rank, const void* base, const uint64_t* dims,
                     const uint64_t* strides, const uint32_t* box, bool swizzle128);
 
+// The same over bytes, 128-byte swizzle, for loads.
+int make_tmap_bytes(CUtensorMap* map, uint32_t rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box);
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Launch `kernel` on `st` with programmatic stream serialization: it may be scheduled while the

@@ -139,6 +139,32 @@ int make_tmap_store(CUtensorMap* map, bool f32, uint32_t rank, const void* base,
     return K3MLA_OK;
 }
 
+int make_tmap_bytes(CUtensorMap* map, uint32_t rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box)
+{
+    auto fn = encode_fn();
+    if (!fn) {
+        set_error("cuTensorMapEncodeTiled unavailable");
+        return K3MLA_E_CUDA;
+    }
+    cuuint64_t d[5], st[4];
+    cuuint32_t bx[5], estr[5];
+    for (uint32_t i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        bx[i] = box[i];
+        estr[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, bx, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled (byte view) failed (%d)", (int)r);
+        return K3MLA_E_CUDA;
+    }
+    return K3MLA_OK;
+}
+
 }  // namespace k3
 
 extern "C" const char* k3mla_last_error(void) { return k3::g_err; }

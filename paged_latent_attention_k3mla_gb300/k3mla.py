@@ -38,7 +38,7 @@ EXPORTS = (
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
     "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
     "k3mla_quant_norm_rope_append", "k3mla_quant_write_pages", "k3mla_quant_read_pages", "k3mla_quant_copy_pages",
-    "k3mla_quant_decode_workspace_bytes", "k3mla_quant_split_tokens", "k3mla_quant_decode",
+    "k3mla_quant_decode_workspace_bytes", "k3mla_quant_split_tokens", "k3mla_quant_decode", "k3mla_diag_quant_timeout",
 )
 
 # Size of the library's built-in decode scratch (K3MLA_NOALLOC_SCRATCH_BYTES).
@@ -123,6 +123,8 @@ def load(build_if_needed: bool = True):
             "k3mla_quant_decode_workspace_bytes": ([I, I, I, I, I], SZ),
             "k3mla_quant_split_tokens": ([I, I, I, I], I),
             "k3mla_quant_decode": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
+            "k3mla_diag_quant_timeout": ([P, P, I, I, I, P, I, P, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, I,
+                                          ctypes.c_uint32, P, P], I),
             "k3mla_pool_trim": ([P, I, I, I, I], I),
             "k3mla_pool_truncate": ([P, I, I], I),
             "k3mla_pool_refill": ([P, I, I], I),
@@ -778,6 +780,25 @@ def diag_window_chunk_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: in
         workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _int(withhold_page, "withhold_page"), _int(wait_us, "wait_us"), _at(dev, dev_err, torch.int32, (1,), "dev_err"),
         _stream(stream, dev)), "k3mla_diag_window_chunk_timeout")
+
+
+def diag_quant_timeout(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor,
+                       ctx_len: torch.Tensor, w_kv_b: torch.Tensor, scale_bf16: int, out: torch.Tensor,
+                       workspace: torch.Tensor, max_ctx: int, window: int, n_sink: int, split_tokens: int,
+                       withhold_tile: int, wait_us: int, dev_err: torch.Tensor, stream=None) -> None:
+    """Diagnostic: quant_decode with a chunk of tile `withhold_tile` of every split never loaded and every bounded wait of
+    the attention kernel limited to wait_us; see k3mla_diag_quant_timeout."""
+    B = q_abs.shape[0]
+    dev = _here(slab)
+    at = _quant_slab(dev, slab)
+    _check(load().k3mla_diag_quant_timeout(
+        _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), at, slab.shape[0], slab.shape[1], _int(layer, "layer"),
+        _table(dev, block_table, B), block_table.shape[1], _at(dev, ctx_len, torch.int32, (B,), "ctx_len"),
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
+        _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), B, _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
+        _int(split_tokens, "split_tokens"), _int(withhold_tile, "withhold_tile"), _int(wait_us, "wait_us"),
+        _at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_diag_quant_timeout")
 
 
 def diag_exact_exp(x: torch.Tensor, y: torch.Tensor, fast: torch.Tensor | None = None, stream=None) -> None:
