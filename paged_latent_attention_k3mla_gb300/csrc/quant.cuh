@@ -61,11 +61,11 @@ __device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t v)
     return r;
 }
 
-// 16 (v - part) of two pairs of f16, exact where part is v rounded to e4m3.
+// 32 (v - part) of two pairs of f16, exact where part is v rounded to e4m3.
 __device__ __forceinline__ uint32_t rest_f16x2(uint32_t v, uint32_t part)
 {
     uint32_t d;
-    asm("{\n\t.reg .b32 s;\n\tmov.b32 s, 0x4C004C00;\n\tsub.rn.f16x2 %0, %1, %2;\n\tmul.rn.f16x2 %0, %0, s;\n\t}" : "=&r"(d) : "r"(v), "r"(part));
+    asm("{\n\t.reg .b32 s;\n\tmov.b32 s, 0x50005000;\n\tsub.rn.f16x2 %0, %1, %2;\n\tmul.rn.f16x2 %0, %0, s;\n\t}" : "=&r"(d) : "r"(v), "r"(part));
     return d;
 }
 

@@ -78,21 +78,21 @@ __device__ __forceinline__ bool qd_seen(const QdParams& p, int n, int t) { retur
 // ---- shared memory, barriers ----------------------------------------------------------------
 
 constexpr int QD_HEADS = 48;                    // heads of a CTA
-constexpr int QD_HALF = 24;                     // ... of a softmax warp
+constexpr int QD_MINE = 12;                     // ... of a softmax warp
 constexpr int QD_TILE = 128;                    // tokens of a tile: two pages of the unit's list
 constexpr int QD_PAIRS = 2 * QD_HEADS;          // columns: every head twice, a first and a second e4m3 number
 constexpr int QD_CHUNK = QD_TILE * 128;         // a tile's chunk: [128 tokens][128 B]; a tile is the rope chunk, then 4 of latents
 constexpr int QD_CHUNKS = 5;
 constexpr int QD_RING = 9;
 constexpr int QD_QCHUNK = QD_PAIRS * 128;       // 128 dims of the queries' pairs
-constexpr int QD_SOFTMAX = 8;                   // warps 0 .. 7: quarter of the tile's tokens w & 3, half of the heads w >> 2
-constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10, QW_AHEAD = 11;
-constexpr int QD_THREADS = 384;
+constexpr int QD_SOFTMAX = 16;                  // warps 0 .. 15: quarter of the tile's tokens w & 3, group of the heads w >> 2
+constexpr int QW_LOAD = 16, QW_SCORE = 17, QW_PV = 18, QW_AHEAD = 19;
+constexpr int QD_THREADS = 640;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
-constexpr uint32_t QB_HALF = 1, QB_ALL = 3;     // named barriers: a half's four softmax warps (1, 2); all eight
-constexpr float QD_TAU = 1.f;                   // a reference moves when a row passes it by more than 2^TAU
-constexpr float QD_UP = 64.f;                   // p times its row's power of two is at most QD_UP 2^TAU times a scale's mantissa: 256
-constexpr float QD_LOW = 16.f;                  // the second number's units: 1 / 16
+constexpr uint32_t QB_GROUP = 1, QB_ALL = 5;    // named barriers: a group's four softmax warps (1 .. 4); all of them
+constexpr float QD_TAU = 5.f;                   // a reference moves when a row passes it by more than 2^TAU
+constexpr float QD_UP = 8.f;                    // p times its row's power of two comes to at most QD_UP 2^TAU = 256
+constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
 constexpr uint32_t QD_IDESC_ROPE = make_idesc_bf16(128, QD_HEADS, 0, 0);
 constexpr uint32_t QD_IDESC_PV = make_idesc_e4m3(128, QD_PAIRS, 1, 1);
@@ -101,13 +101,13 @@ struct __align__(1024) QdSmem {
     uint8_t q[4][QD_QCHUNK];          // K-major B of the scores: rows h (first numbers) and 48 + h (second)
     uint8_t q_rope[QD_HEADS * 128];
     uint8_t ring[QD_RING][QD_CHUNK];
-    uint8_t p[QD_TILE * 128];         // MN-major B of the second contraction: [token][half: 24 first, 24 second numbers]
+    uint8_t p[QD_TILE * 128];         // MN-major B of the second contraction: [token][group: 12 first, 12 second numbers]
     uint64_t full[QD_RING], empty[QD_RING];
     uint64_t q_ready, s_full, s_empty, p_full, pv_done;
-    float m_ref[QD_HEADS];            // the references, in log2 units
+    alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; 0 before anything was seen
+    float m_ref[QD_HEADS];            // ... as they are
     float alpha[QD_HEADS];            // what a moved reference turns the sums by
     float part[4][QD_HEADS];          // a quarter's maxima or sums
-    float up[QD_HEADS];               // the write-out's powers of two
     uint32_t most[QD_SOFTMAX][2];     // the prologue's maxima by warp: latents, rope
     uint32_t tmem_base;
     int32_t tiles_done;               // tiles whose second contraction has been issued
@@ -264,46 +264,34 @@ __device__ __forceinline__ void qd_prefetch(QdSmem& sm, const QdParams& p, const
 
 // The queries of this CTA's heads, by the softmax warps: all of them times one power of two 2^a that brings the largest finite
 // latent entry to [2^7, 2^8) (less where the rope entries would leave bf16's range), as a sum of two e4m3 numbers, the second
-// in units of 1 / 16.  A bf16 has 8 bits, the two numbers 4 each and a sign: exact down to 2^-14 of the largest, and within
-// 2^-14 below.  Returns 2^-a.
+// in units of 1 / 32.  A bf16 has 8 bits, the two numbers 4 each and a sign: exact down to 2^-14 of the largest, and within
+// 2^-15 below.  Returns 2^-a.
 __device__ __forceinline__ float qd_queries(QdSmem& sm, const QdParams& p, int b, int rank)
 {
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint16_t* src = p.q_abs + ((size_t)b * H + rank * QD_HEADS) * ROW;
-    constexpr int ITEMS = QD_HEADS * (LORA / 16) / (32 * QD_SOFTMAX);  // pieces of 16 entries a thread: 6
-    uint4 v[ITEMS][2], vr[2];
-    uint32_t most = 0, most_rope = 0;
+    constexpr int ITEMS = QD_HEADS * (LORA / 8) / (32 * QD_SOFTMAX);  // pieces of 8 entries a thread: 6
+    uint4 v[ITEMS], vr = make_uint4(0u, 0u, 0u, 0u);
     auto largest = [](uint32_t m, uint32_t w) {  // of bf16 pairs, NaN and infinities aside
         const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
         return max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     };
     auto of4 = [&](uint32_t m, const uint4& w) { return largest(largest(largest(largest(m, w.x), w.y), w.z), w.w); };
+    const int j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;  // piece j of heads h_first, + 8, ...
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int item = tid + 32 * QD_SOFTMAX * i, h = item >> 5, j = item & 31;
-        const uint4* at = reinterpret_cast<const uint4*>(src + (size_t)h * ROW + 16 * j);
-        v[i][0] = at[0];
-        v[i][1] = at[1];
-    }
+    for (int i = 0; i < ITEMS; ++i)
+        v[i] = *reinterpret_cast<const uint4*>(src + (size_t)(h_first + 8 * i) * ROW + 8 * j);
+    if (hr < QD_HEADS) vr = *reinterpret_cast<const uint4*>(src + (size_t)hr * ROW + LORA + 8 * jr);
+    uint32_t most = 0, most_rope = of4(0u, vr);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int item = tid + 32 * QD_SOFTMAX * i, h = item >> 3, j = item & 7;
-        vr[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (h < QD_HEADS) vr[i] = *reinterpret_cast<const uint4*>(src + (size_t)h * ROW + LORA + 8 * j);
-        most_rope = of4(most_rope, vr[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) most = of4(of4(most, v[i][0]), v[i][1]);
+    for (int i = 0; i < ITEMS; ++i) most = of4(most, v[i]);
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     most_rope = __reduce_max_sync(0xFFFFFFFFu, most_rope);
     if (lane == 0) sm.most[warp][0] = most, sm.most[warp][1] = most_rope;
-    if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY;
+    if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = 0.f;
     named_bar(QB_ALL, 32 * QD_SOFTMAX);
-#pragma unroll
-    for (int w = 0; w < QD_SOFTMAX; ++w) {
-        most = max(most, sm.most[w][0]);
-        most_rope = max(most_rope, sm.most[w][1]);
-    }
+    most = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane & (QD_SOFTMAX - 1)][0]);
+    most_rope = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane & (QD_SOFTMAX - 1)][1]);
     // (exponent fields: a value in [2^(e - 127), 2^(e - 126)))
     int a = most ? 134 - (int)(most >> 7) : 0;
     a = max(min(min(a, 246 - (int)(most_rope >> 7)), 100), -120);
@@ -319,24 +307,19 @@ __device__ __forceinline__ float qd_queries(QdSmem& sm, const QdParams& p, int b
     };
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-        const int item = tid + 32 * QD_SOFTMAX * i, h = item >> 5, j = item & 31;
-        uint32_t f[8], s[8];
-        two(v[i][0].x, f[0], s[0]), two(v[i][0].y, f[1], s[1]), two(v[i][0].z, f[2], s[2]), two(v[i][0].w, f[3], s[3]);
-        two(v[i][1].x, f[4], s[4]), two(v[i][1].y, f[5], s[5]), two(v[i][1].z, f[6], s[6]), two(v[i][1].w, f[7], s[7]);
-        uint8_t* at = sm.q[j >> 3] + h * 128 + (((j & 7) ^ (h & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16, f[6] | f[7] << 16);
-        *reinterpret_cast<uint4*>(at + QD_HEADS * 128) =
-            make_uint4(s[0] | s[1] << 16, s[2] | s[3] << 16, s[4] | s[5] << 16, s[6] | s[7] << 16);
+        const int h = h_first + 8 * i;
+        uint32_t f[4], s[4];
+        two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
+        uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
+        *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
+        *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int item = tid + 32 * QD_SOFTMAX * i, h = item >> 3, j = item & 7;
-        if (h >= QD_HEADS) continue;
+    if (hr < QD_HEADS) {
         float x[8];
-        unpack8(vr[i], x);
+        unpack8(vr, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= up;
-        *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((j ^ (h & 7)) << 4)) = pack8(x);
+        *reinterpret_cast<uint4*>(sm.q_rope + hr * 128 + ((jr ^ (hr & 7)) << 4)) = pack8(x);
     }
     fence_proxy_async_cta();  // the MMAs read them through the async proxy
     __syncwarp();
@@ -362,49 +345,58 @@ template <int N> __device__ __forceinline__ void qd_pin(uint32_t (&r)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// The references of this half's heads move to the largest s + k of the tile where that is larger, k a row's exponent; sums and
-// O follow.  All four warps of the half come here together.  u: the raw scores; c: what makes log2 units of them.
-__device__ __forceinline__ bool qd_move(QdSmem& sm, const QdParams& p, const float (&u)[QD_HALF], float (&l)[QD_HALF], float c,
-                                     float k, bool seen, uint32_t tbase, int quarter, int half, int i)
+// The 24 columns of a block of O that hold this group's pairs: first numbers, then second ones.
+__device__ __forceinline__ void qd_load_pairs(uint32_t at, uint32_t (&v)[2 * QD_MINE])
 {
-    const int lane = (int)lane_id(), h0 = QD_HALF * half;
+    tmem_ld16(at, reinterpret_cast<uint32_t(&)[16]>(v));
+    tmem_ld8(at + 16u, v + 16);
+}
+
+// The references of this group's heads move to the largest s + k of the tile where that is larger, k a row's exponent; sums
+// and O follow.  All four warps of the group come here together.  u: the raw scores; c: what makes log2 units of them.
+__device__ __forceinline__ bool qd_move(QdSmem& sm, const QdParams& p, const float (&u)[QD_MINE], float (&l)[QD_MINE], float c,
+                                        float k, bool seen, uint32_t tbase, int quarter, int group, int i)
+{
+    const int lane = (int)lane_id(), h0 = QD_MINE * group;
     int32_t mine = (int32_t)0x80000000;
 #pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) {
+    for (int h = 0; h < QD_MINE; ++h) {
         const int32_t m = __reduce_max_sync(0xFFFFFFFFu, seen ? qd_order(fmaf(u[h], c, k)) : (int32_t)0x80000000);
         if (lane == h) mine = m;
     }
-    if (lane < QD_HALF) sm.part[quarter][h0 + lane] = qd_unorder(mine);
-    named_bar(QB_HALF + half, 128);
-    if (quarter == 0 && lane < QD_HALF) {
+    if (lane < QD_MINE) sm.part[quarter][h0 + lane] = qd_unorder(mine);
+    named_bar(QB_GROUP + group, 128);
+    if (quarter == 0 && lane < QD_MINE) {
         const float old = sm.m_ref[h0 + lane];
         float m = old;
 #pragma unroll
         for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.part[w][h0 + lane]);
         sm.m_ref[h0 + lane] = m;
+        sm.m_neg[h0 + lane] = m == -INFINITY ? 0.f : -m;
         sm.alpha[h0 + lane] = m == old ? 1.f : ex2_approx(old - m);
     }
-    named_bar(QB_HALF + half, 128);
+    named_bar(QB_GROUP + group, 128);
+    float f[QD_MINE];
 #pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) l[h] *= sm.alpha[h0 + h];
+    for (int h = 0; h < QD_MINE; ++h) {
+        f[h] = sm.alpha[h0 + h];
+        l[h] *= f[h];
+    }
     if (i == 0) return true;
     if (!__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, i - 1))) return false;
     tc_fence_after();
     const uint32_t t0 = tbase + ((32u * (uint32_t)quarter) << 16) + 2u * (uint32_t)h0;
 #pragma unroll 1
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < 4; ++d) {
+        uint32_t v[2 * QD_MINE];
+        qd_load_pairs(t0 + (uint32_t)(QD_PAIRS * d), v);
+        tmem_wait_ld();
+        qd_pin(v);
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            uint32_t v[16];
-            const uint32_t at = t0 + (uint32_t)(QD_PAIRS * d + 16 * x);
-            tmem_ld16(at, v);
-            tmem_wait_ld();
-            qd_pin(v);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[h0 + (16 * x + e) % QD_HALF]);
-            tmem_st16(at, v);
-        }
+        for (int e = 0; e < 2 * QD_MINE; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f[e % QD_MINE]);
+        tmem_st16(t0 + (uint32_t)(QD_PAIRS * d), reinterpret_cast<uint32_t(&)[16]>(v));
+        tmem_st8(t0 + (uint32_t)(QD_PAIRS * d) + 16u, v + 16);
+    }
     tmem_wait_st();
     tc_fence_before();
     return true;
@@ -419,43 +411,44 @@ __device__ __noinline__ void qd_clear(QdSmem& sm, int i, int token)
     }
 }
 
-// Softmax warp: the tokens of its quarter, a lane each, and the heads of its half.  A token's factor is its thread's, and the
-// sums of exp stay in the thread until the end; what meets in every tile is one vote of the half's four warps, whether a row
+// Softmax warp: the tokens of its quarter, a lane each, and the heads of its group.  A token's factor is its thread's, and the
+// sums of exp stay in the thread until the end; what meets in every tile is one vote of the group's four warps, whether a row
 // has passed its reference.
 __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const QdUnit& g, int b, int s, int rank,
                                            uint32_t tbase, int tiles)
 {
-    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id(), quarter = warp & 3, half = warp >> 2, h0 = QD_HALF * half;
+    const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id(), quarter = warp & 3, group = warp >> 2, h0 = QD_MINE * group;
     const int token = 32 * quarter + lane, line = token & (PAGE - 1), page = quarter >> 1;
-    const float kq = qd_queries(sm, p, b, rank) * p.kscale;
-    const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16);
     QdLookup look;
     auto row_scale = [&](int i) {  // of this thread's token in tile i; 1 for tokens that are not there
         look(p, g, b, 2 * i, false);
         const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + page) & 31);
         return at < 0 ? (uint16_t)0x3F80u : *reinterpret_cast<const uint16_t*>(p.slab + (size_t)at * QPAGE + QSCALES + 2 * line);
     };
-    float l[QD_HALF];
-#pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) l[h] = 0.f;
     uint16_t next = row_scale(0);
+    const float kq = qd_queries(sm, p, b, rank) * p.kscale;
+    const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16);
+    float l[QD_MINE];
+#pragma unroll
+    for (int h = 0; h < QD_MINE; ++h) l[h] = 0.f;
     bool dead = false;  // a wait ran out: this warp only goes on to where the four can leave together
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
         const int e = 2 * i + page, t = PAGE * qd_logical(g, e) + line;
         const bool seen = e < g.npg && qd_seen(p, g.n, t);
         const float scale = seen ? __uint_as_float((uint32_t)next << 16) : 1.f;
-        const float k = (float)((int)(__float_as_uint(scale) >> 23) - 127), c = kq * scale;
+        const float k = (float)((int)(__float_as_uint(scale) >> 23) - 127), c = kq * scale, up = scale * QD_UP;
+        const bool whole = __all_sync(0xFFFFFFFFu, seen);
         if (i + 1 < tiles) next = row_scale(i + 1);
         dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.s_full, i));
-        float u[QD_HALF];
+        float u[QD_MINE];
         {
-            uint32_t a[QD_HALF], z[QD_HALF];
+            uint32_t a[QD_MINE], z[QD_MINE];
             tc_fence_after();
-            tmem_ld16(t_lane + QD_S_COL + (uint32_t)h0, reinterpret_cast<uint32_t(&)[16]>(a));
-            tmem_ld8(t_lane + QD_S_COL + (uint32_t)h0 + 16u, a + 16);
-            tmem_ld16(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0), reinterpret_cast<uint32_t(&)[16]>(z));
-            tmem_ld8(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0) + 16u, z + 16);
+            tmem_ld8(t_lane + QD_S_COL + (uint32_t)h0, a);
+            tmem_ld4(t_lane + QD_S_COL + (uint32_t)h0 + 8u, a + 8);
+            tmem_ld8(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0), z);
+            tmem_ld4(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0) + 8u, z + 8);
             tmem_wait_ld();
             qd_pin(a);
             qd_pin(z);
@@ -463,54 +456,63 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_empty);
 #pragma unroll
-            for (int h = 0; h < QD_HALF; ++h) u[h] = fmaf(__uint_as_float(z[h]), 1.f / QD_LOW, __uint_as_float(a[h]));
+            for (int h = 0; h < QD_MINE; h += 2)
+                f32x2_parts(fma_f32x2(f32x2(__uint_as_float(z[h]), __uint_as_float(z[h + 1])), f32x2(1.f / QD_LOW, 1.f / QD_LOW),
+                                      f32x2(__uint_as_float(a[h]), __uint_as_float(a[h + 1]))),
+                            u[h], u[h + 1]);
         }
-        float x[QD_HALF], most = -INFINITY;
+        float x[QD_MINE], most = -INFINITY;
+        auto arguments = [&]() {
 #pragma unroll
-        for (int h = 0; h < QD_HALF; ++h) {
-            x[h] = fmaf(u[h], c, -sm.m_ref[h0 + h]);
-            most = fmaxf(most, x[h]);
-        }
-        bool odd = false;
-        if (!seen) {
-#pragma unroll
-            for (int h = 0; h < QD_HALF; ++h) odd = odd || (__float_as_uint(u[h]) & 0x7F800000u) == 0x7F800000u;
-        }
-        // (the first tile's references are -inf)
-        if (named_bar_any(QB_HALF + half, 128, dead || i == 0 || (seen && !(most <= QD_TAU - k)))) {
-            if (named_bar_any(QB_HALF + half, 128, dead)) return;
-            dead = !qd_move(sm, p, u, l, c, k, seen, tbase, quarter, half, i);
-#pragma unroll
-            for (int h = 0; h < QD_HALF; ++h) {
-                const float m = sm.m_ref[h0 + h];
-                x[h] = fmaf(u[h], c, m == -INFINITY ? 0.f : -m);
+            for (int h = 0; h < QD_MINE; h += 4) {
+                const float4 m = *reinterpret_cast<const float4*>(&sm.m_neg[h0 + h]);
+                f32x2_parts(fma_f32x2(f32x2(u[h], u[h + 1]), f32x2(c, c), f32x2(m.x, m.y)), x[h], x[h + 1]);
+                f32x2_parts(fma_f32x2(f32x2(u[h + 2], u[h + 3]), f32x2(c, c), f32x2(m.z, m.w)), x[h + 2], x[h + 3]);
             }
-        }
-        if (odd) qd_clear(sm, i, token);
-        uint32_t w[QD_HALF / 2];  // 24 first numbers, 24 second ones
-        const float up = scale * QD_UP;
+        };
+        arguments();
 #pragma unroll
-        for (int y = 0; y < QD_HALF / 4; ++y) {
+        for (int h = 0; h < QD_MINE; ++h) most = fmaxf(most, x[h]);
+        // (the first tile sets the references)
+        if (named_bar_any(QB_GROUP + group, 128, dead || i == 0 || (seen && !(most <= QD_TAU - k)))) {
+            if (named_bar_any(QB_GROUP + group, 128, dead)) return;
+            dead = !qd_move(sm, p, u, l, c, k, seen, tbase, quarter, group, i);
+            arguments();
+        }
+        if (!whole) {
+            bool odd = false;
+#pragma unroll
+            for (int h = 0; h < QD_MINE; ++h) {
+                odd = odd || (__float_as_uint(u[h]) & 0x7F800000u) == 0x7F800000u;
+                if (!seen) x[h] = -INFINITY;
+            }
+            if (!seen && odd) qd_clear(sm, i, token);
+        }
+        uint32_t w[QD_MINE / 2];  // 12 first numbers, 12 second ones
+#pragma unroll
+        for (int y = 0; y < QD_MINE / 4; ++y) {
             uint32_t first[2], second[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int h = 4 * y + 2 * z;
-                float e0 = ex2_approx(x[h]), e1 = ex2_approx(x[h + 1]);
-                if (!seen) e0 = e1 = 0.f;
-                l[h] += e0;
-                l[h + 1] += e1;
-                const uint32_t v = pack_f16x2(e0 * up, e1 * up);
+                const uint64_t e2 = f32x2(ex2_approx(x[h]), ex2_approx(x[h + 1]));
+                f32x2_parts(add_f32x2(f32x2(l[h], l[h + 1]), e2), l[h], l[h + 1]);
+                float p0, p1;
+                f32x2_parts(mul_f32x2(e2, f32x2(up, up)), p0, p1);
+                const uint32_t v = pack_f16x2(p0, p1);
                 first[z] = pack_e4m3x2_f16(v);
                 second[z] = pack_e4m3x2_f16(rest_f16x2(v, e4m3x2_to_f16x2(first[z])));
             }
             w[y] = first[0] | first[1] << 16;
-            w[QD_HALF / 4 + y] = second[0] | second[1] << 16;
+            w[QD_MINE / 4 + y] = second[0] | second[1] << 16;
         }
         if (i > 0) dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, i - 1));
 #pragma unroll
-        for (int y = 0; y < 3; ++y)
-            *reinterpret_cast<uint4*>(sm.p + token * 128 + (((3 * half + y) ^ (token & 7)) << 4)) =
-                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+        for (int y = 0; y < 3; ++y) {
+            const int at = 2 * QD_MINE * group + 8 * y;  // of the token's row
+            *reinterpret_cast<uint2*>(sm.p + token * 128 + (((at >> 4) ^ (token & 7)) << 4) + (at & 8)) =
+                make_uint2(w[2 * y], w[2 * y + 1]);
+        }
         fence_proxy_async_cta();  // the MMAs read P, and what was cleared, through the async proxy
         tc_fence_before();
         __syncwarp();
@@ -519,77 +521,76 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
     // the sums of exp: over the lanes, then over the quarters
     float mine = 0.f;
 #pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) {
+    for (int h = 0; h < QD_MINE; ++h) {
         float v = l[h];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
         if (lane == h) mine = v;
     }
-    if (lane < QD_HALF) sm.part[quarter][h0 + lane] = mine;
+    if (lane < QD_MINE) sm.part[quarter][h0 + lane] = mine;
     dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, tiles - 1));
-    if (named_bar_any(QB_HALF + half, 128, dead)) return;
+    if (named_bar_any(QB_GROUP + group, 128, dead)) return;
     tc_fence_after();
     // lane h has head h0 + h of this CTA's
     float total = 1.f;
-    if (lane < QD_HALF)
+    if (lane < QD_MINE)
         total = (sm.part[0][h0 + lane] + sm.part[1][h0 + lane]) + (sm.part[2][h0 + lane] + sm.part[3][h0 + lane]);
-    const float r = (g.single ? 1.f / total : 1.f) * (1.f / QD_UP);
-    // thread = dim 128 d + 32 quarter + lane of every block d
-    float o[4][QD_HALF];
-#pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        uint32_t v[3][16];
-#pragma unroll
-        for (int y = 0; y < 3; ++y) tmem_ld16(t_lane + (uint32_t)(QD_PAIRS * d + 2 * h0 + 16 * y), v[y]);
+    float r = (g.single ? 1.f / total : 1.f) * (1.f / QD_UP);
+    // thread = dim 128 d + 32 quarter + lane of every block d; twice over O, first for the heads' largest entries
+    auto load = [&](int d, float (&o)[QD_MINE]) {
+        uint32_t v[2 * QD_MINE];
+        qd_load_pairs(t_lane + (uint32_t)(QD_PAIRS * d + 2 * h0), v);
         tmem_wait_ld();
+        qd_pin(v);
 #pragma unroll
-        for (int y = 0; y < 3; ++y) qd_pin(v[y]);
+        for (int h = 0; h < QD_MINE; ++h)
+            o[h] = fmaf(__uint_as_float(v[QD_MINE + h]), 1.f / QD_LOW, __uint_as_float(v[h]));
+    };
+    float big[QD_MINE];
 #pragma unroll
-        for (int h = 0; h < QD_HALF; ++h)
-            o[d][h] = fmaf(__uint_as_float(v[(QD_HALF + h) / 16][(QD_HALF + h) % 16]), 1.f / QD_LOW,
-                           __uint_as_float(v[h / 16][h % 16]));
+    for (int h = 0; h < QD_MINE; ++h) big[h] = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) {
+        float o[QD_MINE];
+        load(d, o);
+#pragma unroll
+        for (int h = 0; h < QD_MINE; ++h) big[h] = fmaxf(big[h], fabsf(o[h]));
     }
-    uint32_t big = 0;
+    uint32_t most = 0;
 #pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) {
-        const float f = __shfl_sync(0xFFFFFFFFu, r, h);
-        float m = 0.f;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            o[d][h] *= f;
-            m = fmaxf(m, fabsf(o[d][h]));
-        }
-        const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m));
-        if (lane == h) big = v;
+    for (int h = 0; h < QD_MINE; ++h) {
+        const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big[h]));
+        if (lane == h) most = v;
     }
-    named_bar(QB_HALF + half, 128);  // the sums have been read
-    if (lane < QD_HALF) sm.part[quarter][h0 + lane] = __uint_as_float(big);
-    named_bar(QB_HALF + half, 128);
-    float up = 1.f;
-    const int head = rank * QD_HEADS + h0 + lane;
+    named_bar(QB_GROUP + group, 128);  // the sums have been read
+    if (lane < QD_MINE) sm.part[quarter][h0 + lane] = __uint_as_float(most);
+    named_bar(QB_GROUP + group, 128);
     auto place = [&](int h) { return g.single ? (size_t)h * p.B + b : ((size_t)b * p.nsplit + s) * H + h; };
-    if (lane < QD_HALF) {
-        const float m = fmaxf(fmaxf(sm.part[0][h0 + lane], sm.part[1][h0 + lane]), fmaxf(sm.part[2][h0 + lane], sm.part[3][h0 + lane]));
+    if (lane < QD_MINE) {
+        const int h = h0 + lane;
         float inverse;
-        up = w_row_scale(m, inverse);
+        r *= w_row_scale(fmaxf(fmaxf(sm.part[0][h], sm.part[1][h]), fmaxf(sm.part[2][h], sm.part[3][h])) * r, inverse);
         if (quarter == 0) {
-            (g.single ? p.oscale : p.ws_oscale)[place(head)] = inverse;
-            if (!g.single) p.ws_ml[place(head)] = make_float2(sm.m_ref[h0 + lane], total);
+            const size_t at = place(rank * QD_HEADS + h);
+            (g.single ? p.oscale : p.ws_oscale)[at] = inverse;
+            if (!g.single) p.ws_ml[at] = make_float2(sm.m_ref[h], total);
         }
     }
     // two lanes trade, so that each has a pair of neighbouring dims of every second block
-    uint16_t* out = g.single ? p.olat : p.ws_o;
     const bool upper = lane & 1;
+    uint16_t* out = (g.single ? p.olat : p.ws_o) + place(rank * QD_HEADS + h0) * LORA;
+    const size_t step = (g.single ? (size_t)p.B : 1) * LORA;
+#pragma unroll 1
+    for (int d = 0; d < 4; d += 2) {
+        float o0[QD_MINE], o1[QD_MINE];
+        load(d, o0);
+        load(d + 1, o1);
+        uint16_t* at = out + w_dim_place(128 * (upper ? d + 1 : d) + 32 * quarter + (lane & ~1));
 #pragma unroll
-    for (int h = 0; h < QD_HALF; ++h) {
-        const float f = __shfl_sync(0xFFFFFFFFu, up, h);
-        uint16_t* row = out + place(rank * QD_HEADS + h0 + h) * LORA;
-#pragma unroll
-        for (int d = 0; d < 4; d += 2) {
-            const float mine0 = o[d][h] * f, mine1 = o[d + 1][h] * f;
+        for (int h = 0; h < QD_MINE; ++h) {
+            const float f = __shfl_sync(0xFFFFFFFFu, r, h), mine0 = o0[h] * f, mine1 = o1[h] * f;
             const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? mine0 : mine1, 1);
-            const int dim = 128 * (upper ? d + 1 : d) + 32 * quarter + (lane & ~1);
-            *reinterpret_cast<uint32_t*>(row + w_dim_place(dim)) = upper ? pack_f16x2(other, mine1) : pack_f16x2(mine0, other);
+            *reinterpret_cast<uint32_t*>(at + h * step) = upper ? pack_f16x2(other, mine1) : pack_f16x2(mine0, other);
         }
     }
 }
