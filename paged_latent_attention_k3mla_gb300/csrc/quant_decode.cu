@@ -78,20 +78,20 @@ __device__ __forceinline__ bool qd_seen(const QdParams& p, int n, int t) { retur
 // ---- shared memory, barriers ----------------------------------------------------------------
 
 constexpr int QD_HEADS = 48;                    // heads of a CTA
-constexpr int QD_MINE = 12;                     // ... of a softmax warp
+constexpr int QD_MINE = 24;                     // ... of a softmax warp
 constexpr int QD_TILE = 128;                    // tokens of a tile: two pages of the unit's list
 constexpr int QD_PAIRS = 2 * QD_HEADS;          // columns: every head twice, a first and a second e4m3 number
 constexpr int QD_CHUNK = QD_TILE * 128;         // a tile's chunk: [128 tokens][128 B]; a tile is the rope chunk, then 4 of latents
 constexpr int QD_CHUNKS = 5;
 constexpr int QD_RING = 9;
 constexpr int QD_QCHUNK = QD_PAIRS * 128;       // 128 dims of the queries' pairs
-constexpr int QD_SOFTMAX = 16;                  // warps 0 .. 15: quarter of the tile's tokens w & 3, group of the heads w >> 2
-constexpr int QW_LOAD = 16, QW_SCORE = 17, QW_PV = 18, QW_AHEAD = 19;
-constexpr int QD_THREADS = 640;
+constexpr int QD_SOFTMAX = 8;                   // warps 0 .. 7: quarter of the tile's tokens w & 3, group of the heads w >> 2
+constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10, QW_AHEAD = 11;
+constexpr int QD_THREADS = 384;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
-constexpr uint32_t QB_GROUP = 1, QB_ALL = 5;    // named barriers: a group's four softmax warps (1 .. 4); all of them
-constexpr float QD_TAU = 5.f;                   // a reference moves when a row passes it by more than 2^TAU
-constexpr float QD_UP = 8.f;                    // p times its row's power of two comes to at most QD_UP 2^TAU = 256
+constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
+constexpr float QD_TAU = 7.f;                   // a reference moves when a row passes it by more than 2^TAU
+constexpr float QD_UP = 2.f;                    // p times its row's power of two comes to at most QD_UP 2^TAU = 256
 constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
 constexpr uint32_t QD_IDESC_ROPE = make_idesc_bf16(128, QD_HEADS, 0, 0);
@@ -101,7 +101,7 @@ struct __align__(1024) QdSmem {
     uint8_t q[4][QD_QCHUNK];          // K-major B of the scores: rows h (first numbers) and 48 + h (second)
     uint8_t q_rope[QD_HEADS * 128];
     uint8_t ring[QD_RING][QD_CHUNK];
-    uint8_t p[QD_TILE * 128];         // MN-major B of the second contraction: [token][group: 12 first, 12 second numbers]
+    uint8_t p[QD_TILE * 128];         // MN-major B of the second contraction: [token][group: 24 first, 24 second numbers]
     uint64_t full[QD_RING], empty[QD_RING];
     uint64_t q_ready, s_full, s_empty, p_full, pv_done;
     alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; 0 before anything was seen
@@ -120,7 +120,7 @@ static_assert(4 * QD_PAIRS + QD_PAIRS <= 512, "TMEM columns");
 
 __device__ __forceinline__ bool qd_wait(QdSmem& sm, const QdParams& p, uint64_t* bar, int phase)
 {
-    return wait_bar(bar, (uint32_t)phase & 1u, sm, p.dev_err, true);
+    return wait_bar(bar, (uint32_t)phase & 1u, sm, p.dev_err);
 }
 
 __device__ __forceinline__ void qd_init(QdSmem& sm, const QdParams& p)
@@ -131,7 +131,7 @@ __device__ __forceinline__ void qd_init(QdSmem& sm, const QdParams& p)
 #pragma unroll 1
     for (int i = 0; i < QD_RING; ++i) {
         mbar_init(&sm.full[i], 1);
-        mbar_init(&sm.empty[i], 2);  // both CTAs have read theirs: a load writes to both
+        mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.q_ready, QD_SOFTMAX);
     mbar_init(&sm.s_full, 1);
@@ -153,16 +153,18 @@ struct QdLookup {
 
 // ---- roles --------------------------------------------------------------------------------
 
-// The producer: of every chunk this CTA's page (entry 2 i + rank of the list), into both CTAs.
+// The producer: every chunk of a tile from its two pages.
 __device__ __forceinline__ void qd_produce(QdSmem& sm, const CUtensorMap& tm_page, const QdParams& p, const QdUnit& g, int b,
-                                           int rank, int tiles)
+                                           int tiles)
 {
     bool ok = true;  // (the elected lane's)
     QdLookup look;
     const int none = p.n_pages * p.n_layers;  // past the end: read as zeros
     for (int i = 0; i < tiles; ++i) {
         look(p, g, b, 2 * i, true);
-        const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + rank) & 31);
+        int32_t at[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) at[x] = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + x) & 31);
         if (elect_one()) {
 #pragma unroll 1
             for (int c = 0; c < QD_CHUNKS && ok; ++c) {
@@ -171,9 +173,11 @@ __device__ __forceinline__ void qd_produce(QdSmem& sm, const CUtensorMap& tm_pag
                 if (!ok) break;
                 mbar_arrive_expect_tx(&sm.full[u], QD_CHUNK);
                 // (diagnostic: a load never issued)
-                if (c != 1 || i + 1 != p.withhold)
-                    tma_load_4d_mc(sm.ring[u] + rank * (PAGE * 128), &tm_page, 0, 0, c ? c - 1 : 4, at < 0 ? none : at,
-                                   &sm.full[u], 3);
+                if (c == 1 && i + 1 == p.withhold) continue;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    tma_load_4d(sm.ring[u] + x * (PAGE * 128), &tm_page, 0, 0, c ? c - 1 : 4, at[x] < 0 ? none : at[x],
+                                &sm.full[u]);
             }
         }
         __syncwarp();
@@ -208,7 +212,7 @@ __device__ __forceinline__ void qd_score(QdSmem& sm, const QdParams& p, uint32_t
                     const uint64_t r = make_sdesc(smem_u32(sm.ring[ur]), 16, 1024);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) umma_ss(tbase + QD_S_COL, r + 2u * k, qr + 2u * k, QD_IDESC_ROPE, 1u);
-                    umma_commit_mc(&sm.empty[ur], 3);
+                    umma_commit(&sm.empty[ur]);
                 }
             }
             if (ok) umma_commit(&sm.s_full);
@@ -237,7 +241,7 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_ss_8bit(tbase + (uint32_t)(QD_PAIRS * c), a + 256u * k, pd + 256u * k, QD_IDESC_PV, (i | k) != 0);
-                umma_commit_mc(&sm.empty[u], 3);
+                umma_commit(&sm.empty[u]);
             }
             if (ok) umma_commit(&sm.pv_done);
             *reinterpret_cast<volatile int32_t*>(&sm.tiles_done) = i + 1;
@@ -270,21 +274,25 @@ __device__ __forceinline__ float qd_queries(QdSmem& sm, const QdParams& p, int b
 {
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint16_t* src = p.q_abs + ((size_t)b * H + rank * QD_HEADS) * ROW;
-    constexpr int ITEMS = QD_HEADS * (LORA / 8) / (32 * QD_SOFTMAX);  // pieces of 8 entries a thread: 6
-    uint4 v[ITEMS], vr = make_uint4(0u, 0u, 0u, 0u);
+    constexpr int ITEMS = QD_HEADS * (LORA / 8) / (32 * QD_SOFTMAX);  // pieces of 8 entries a thread: 12
+    constexpr int STEP = 32 * QD_SOFTMAX / 64;
     auto largest = [](uint32_t m, uint32_t w) {  // of bf16 pairs, NaN and infinities aside
         const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
         return max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
     };
     auto of4 = [&](uint32_t m, const uint4& w) { return largest(largest(largest(largest(m, w.x), w.y), w.z), w.w); };
-    const int j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;  // piece j of heads h_first, + 8, ...
+    const int j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;  // piece j of heads h_first, + STEP, ...
+    auto piece = [&](int i) { return *reinterpret_cast<const uint4*>(src + (size_t)(h_first + STEP * i) * ROW + 8 * j); };
+    auto rope = [&](int h) { return *reinterpret_cast<const uint4*>(src + (size_t)h * ROW + LORA + 8 * jr); };
+    uint32_t most = 0, most_rope = of4(0u, rope(hr));
+    if (hr + 32 < QD_HEADS) most_rope = of4(most_rope, rope(hr + 32));
+    {
+        uint4 v[ITEMS];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
-        v[i] = *reinterpret_cast<const uint4*>(src + (size_t)(h_first + 8 * i) * ROW + 8 * j);
-    if (hr < QD_HEADS) vr = *reinterpret_cast<const uint4*>(src + (size_t)hr * ROW + LORA + 8 * jr);
-    uint32_t most = 0, most_rope = of4(0u, vr);
+        for (int i = 0; i < ITEMS; ++i) v[i] = piece(i);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) most = of4(most, v[i]);
+        for (int i = 0; i < ITEMS; ++i) most = of4(most, v[i]);
+    }
     most = __reduce_max_sync(0xFFFFFFFFu, most);
     most_rope = __reduce_max_sync(0xFFFFFFFFu, most_rope);
     if (lane == 0) sm.most[warp][0] = most, sm.most[warp][1] = most_rope;
@@ -305,21 +313,25 @@ __device__ __forceinline__ float qd_queries(QdSmem& sm, const QdParams& p, int b
         f16x2_parts(e4m3x2_to_f16x2(first), fx, fy);
         second = pack_e4m3x2((x - fx) * QD_LOW, (y - fy) * QD_LOW);
     };
-#pragma unroll
+    uint4 next = piece(0);  // (from L1; a loop: this code runs once a unit, and fetching it takes longer than running it)
+#pragma unroll 1
     for (int i = 0; i < ITEMS; ++i) {
-        const int h = h_first + 8 * i;
+        const int h = h_first + STEP * i;
+        const uint4 v = next;
+        next = piece(min(i + 1, ITEMS - 1));
         uint32_t f[4], s[4];
-        two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
+        two(v.x, f[0], s[0]), two(v.y, f[1], s[1]), two(v.z, f[2], s[2]), two(v.w, f[3], s[3]);
         uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
         *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
         *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
     }
-    if (hr < QD_HEADS) {
+#pragma unroll 1
+    for (int h = hr; h < QD_HEADS; h += 32) {
         float x[8];
-        unpack8(vr, x);
+        unpack8(rope(h), x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] *= up;
-        *reinterpret_cast<uint4*>(sm.q_rope + hr * 128 + ((jr ^ (hr & 7)) << 4)) = pack8(x);
+        *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((jr ^ (h & 7)) << 4)) = pack8(x);
     }
     fence_proxy_async_cta();  // the MMAs read them through the async proxy
     __syncwarp();
@@ -345,11 +357,11 @@ template <int N> __device__ __forceinline__ void qd_pin(uint32_t (&r)[N])
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
-// The 24 columns of a block of O that hold this group's pairs: first numbers, then second ones.
+// The 48 columns of a block of O that hold this group's pairs: first numbers, then second ones.
 __device__ __forceinline__ void qd_load_pairs(uint32_t at, uint32_t (&v)[2 * QD_MINE])
 {
-    tmem_ld16(at, reinterpret_cast<uint32_t(&)[16]>(v));
-    tmem_ld8(at + 16u, v + 16);
+    tmem_ld32(at, reinterpret_cast<uint32_t(&)[32]>(v));
+    tmem_ld16(at + 32u, reinterpret_cast<uint32_t(&)[16]>(v[32]));
 }
 
 // The references of this group's heads move to the largest s + k of the tile where that is larger, k a row's exponent; sums
@@ -394,8 +406,8 @@ __device__ __forceinline__ bool qd_move(QdSmem& sm, const QdParams& p, const flo
         qd_pin(v);
 #pragma unroll
         for (int e = 0; e < 2 * QD_MINE; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f[e % QD_MINE]);
-        tmem_st16(t0 + (uint32_t)(QD_PAIRS * d), reinterpret_cast<uint32_t(&)[16]>(v));
-        tmem_st8(t0 + (uint32_t)(QD_PAIRS * d) + 16u, v + 16);
+        tmem_st32(t0 + (uint32_t)(QD_PAIRS * d), reinterpret_cast<uint32_t(&)[32]>(v));
+        tmem_st16(t0 + (uint32_t)(QD_PAIRS * d) + 32u, reinterpret_cast<uint32_t(&)[16]>(v[32]));
     }
     tmem_wait_st();
     tc_fence_before();
@@ -437,7 +449,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
         const int e = 2 * i + page, t = PAGE * qd_logical(g, e) + line;
         const bool seen = e < g.npg && qd_seen(p, g.n, t);
         const float scale = seen ? __uint_as_float((uint32_t)next << 16) : 1.f;
-        const float k = (float)((int)(__float_as_uint(scale) >> 23) - 127), c = kq * scale, up = scale * QD_UP;
+        const float k = (float)((int)(__float_as_uint(scale) >> 23) - 127), c = kq * scale, up = scale * (QD_UP / 256.f);
         const bool whole = __all_sync(0xFFFFFFFFu, seen);
         if (i + 1 < tiles) next = row_scale(i + 1);
         dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.s_full, i));
@@ -445,10 +457,10 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
         {
             uint32_t a[QD_MINE], z[QD_MINE];
             tc_fence_after();
-            tmem_ld8(t_lane + QD_S_COL + (uint32_t)h0, a);
-            tmem_ld4(t_lane + QD_S_COL + (uint32_t)h0 + 8u, a + 8);
-            tmem_ld8(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0), z);
-            tmem_ld4(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0) + 8u, z + 8);
+            tmem_ld16(t_lane + QD_S_COL + (uint32_t)h0, reinterpret_cast<uint32_t(&)[16]>(a));
+            tmem_ld8(t_lane + QD_S_COL + (uint32_t)h0 + 16u, a + 16);
+            tmem_ld16(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0), reinterpret_cast<uint32_t(&)[16]>(z));
+            tmem_ld8(t_lane + QD_S_COL + (uint32_t)(QD_HEADS + h0) + 16u, z + 16);
             tmem_wait_ld();
             qd_pin(a);
             qd_pin(z);
@@ -488,10 +500,10 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
             }
             if (!seen && odd) qd_clear(sm, i, token);
         }
-        uint32_t w[QD_MINE / 2];  // 12 first numbers, 12 second ones
+        uint32_t w[QD_MINE / 2];  // 24 first numbers, 24 second ones
 #pragma unroll
         for (int y = 0; y < QD_MINE / 4; ++y) {
-            uint32_t first[2], second[2];
+            float a[4];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
                 const int h = 4 * y + 2 * z;
@@ -499,20 +511,23 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
                 f32x2_parts(add_f32x2(f32x2(l[h], l[h + 1]), e2), l[h], l[h + 1]);
                 float p0, p1;
                 f32x2_parts(mul_f32x2(e2, f32x2(up, up)), p0, p1);
-                const uint32_t v = pack_f16x2(p0, p1);
-                first[z] = pack_e4m3x2_f16(v);
-                second[z] = pack_e4m3x2_f16(rest_f16x2(v, e4m3x2_to_f16x2(first[z])));
+                a[z] = p0, a[z + 2] = p1;
             }
-            w[y] = first[0] | first[1] << 16;
-            w[QD_MINE / 4 + y] = second[0] | second[1] << 16;
+            // Heads 0 and 2 of the four in one register, 1 and 3 in the other.  v = p 2^-8 as an f16 has e4m3's bits, 7 higher,
+            // subnormals included: the first number is v rounded there, and no conversion (a quarter of the arithmetic's
+            // rate) is needed for it or for what is left.  (A NaN, whose bits would run over into the next head's, becomes 1: its
+            // head's sum is a NaN as well.)
+            const uint32_t va = min_f16x2(pack_f16x2(a[0], a[1]), 0x3C003C00u), vb = min_f16x2(pack_f16x2(a[2], a[3]), 0x3C003C00u);
+            const uint32_t fa = (va + 0x00400040u) & 0xFF80FF80u, fb = (vb + 0x00400040u) & 0xFF80FF80u;
+            w[y] = (fa >> 7) + (fb << 1);
+            const uint32_t sa = pack_e4m3x2_f16(rest_f16x2(va, fa)), sb = pack_e4m3x2_f16(rest_f16x2(vb, fb));
+            w[QD_MINE / 4 + y] = __byte_perm(sa, sb, 0x5140);
         }
         if (i > 0) dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, i - 1));
 #pragma unroll
-        for (int y = 0; y < 3; ++y) {
-            const int at = 2 * QD_MINE * group + 8 * y;  // of the token's row
-            *reinterpret_cast<uint2*>(sm.p + token * 128 + (((at >> 4) ^ (token & 7)) << 4) + (at & 8)) =
-                make_uint2(w[2 * y], w[2 * y + 1]);
-        }
+        for (int y = 0; y < 3; ++y)
+            *reinterpret_cast<uint4*>(sm.p + token * 128 + (((3 * group + y) ^ (token & 7)) << 4)) =
+                make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
         fence_proxy_async_cta();  // the MMAs read P, and what was cleared, through the async proxy
         tc_fence_before();
         __syncwarp();
@@ -597,13 +612,13 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
 
 // ---- the kernel ---------------------------------------------------------------------------
 
-// A cluster a unit: split s of slot b; the CTAs take 48 heads each.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(QD_THREADS, 1)
+// Two CTAs a unit, split s of slot b: 48 heads each.
+__global__ void __launch_bounds__(QD_THREADS, 1)
     k3mla_quant_decode_kernel(const __grid_constant__ CUtensorMap tm_page, const QdParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     QdSmem& sm = *reinterpret_cast<QdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int rank = (int)cluster_ctarank(), warp = (int)(threadIdx.x >> 5), unit = (int)(blockIdx.x >> 1);
+    const int rank = (int)(blockIdx.x & 1u), warp = (int)(threadIdx.x >> 5), unit = (int)(blockIdx.x >> 1);
     const int b = unit / p.nsplit, s = unit % p.nsplit;
     if (threadIdx.x == 32 * QW_LOAD) {
         qd_init(sm, p);
@@ -615,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(QD_THREADS, 1)
         tmem_relinquish();
     }
     tc_fence_before();
-    cluster_sync();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tbase = sm.tmem_base;
     griddep_wait();
@@ -625,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(QD_THREADS, 1)
     const int tiles = (g.npg + 1) / 2;
     if (tiles > 0) {
         if (warp < QD_SOFTMAX) qd_softmax(sm, p, g, b, s, rank, tbase, tiles);
-        else if (warp == QW_LOAD) qd_produce(sm, tm_page, p, g, b, rank, tiles);
+        else if (warp == QW_LOAD) qd_produce(sm, tm_page, p, g, b, tiles);
         else if (warp == QW_SCORE) qd_score(sm, p, tbase, tiles);
         else if (warp == QW_PV) qd_pv(sm, p, tbase, tiles);
         else if (warp == QW_AHEAD) qd_prefetch(sm, p, g, b, rank, tiles);
@@ -635,7 +650,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(QD_THREADS, 1)
     if (aborted(sm)) drain_inflight();
     __syncwarp();
     tc_fence_before();
-    cluster_sync();
+    __syncthreads();
     tc_fence_after();
     if (warp == QW_PV) tmem_dealloc(tbase, TMEM_COLS);
 }

@@ -102,8 +102,9 @@ def out_tolerance(q_abs, out, o, p, rows, scales, w_kv_b, scale):
     What the kernel rounds:
       * p times its row's power of two (so that it can multiply codes) to a sum of two e4m3 numbers, the second in units of
         1/32: the first is within 2^-4 of it, the rest within 2^-4 of that, 2^-8 in all, by way of an f16 (2^-12); or, where
-        the second is below its smallest step, within half a step, 2^-10 / 32 = 2^-15, when the largest of them comes to 2^3
-        at least (the reference is one of them, and they are taken to 8 at the reference): 2^-18 of it;
+        the second is below its smallest step, within half a step, 2^-10 / 32 = 2^-15, and half the f16's, 2^-17, when the
+        largest of them comes to 2 at least (the reference is one of them, and they are taken to 2 at the reference):
+        1.25 * 2^-16 of it;
       * q to a sum of two e4m3 numbers likewise: exact for entries above 2^-14 of the largest of all heads, as a bf16 has 8
         bits, else within 2^-15 where the largest comes to 2^7 at least: 2^-22 of it;
       * o_lat, and the O of each split, to f16 after a power of two (2^-12 of the entry or 2^-25 of the row's largest);
@@ -117,7 +118,7 @@ def out_tolerance(q_abs, out, o, p, rows, scales, w_kv_b, scale):
     q = np.abs(np.asarray(q_abs, np.float64))
     ds = scale * (640 * 2.0 ** -24 * q @ np.abs(rows).T + 2.0 ** -22 * q[:, :LORA].max() * np.abs(rows[:, :LORA]).sum(-1))
     size = p * scales
-    d = p * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -19 + ds) + 2.0 ** -18 * size.max(-1, keepdims=True) / scales
+    d = p * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -19 + ds) + 1.25 * 2.0 ** -16 * size.max(-1, keepdims=True) / scales
     c = np.abs(rows[:, :LORA])
     spread = d @ c + d.sum(-1)[:, None] * np.abs(o)
     mass = p @ c
