@@ -61,14 +61,6 @@ __device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t v)
     return r;
 }
 
-// The smaller of each half; the other one where one is a NaN.
-__device__ __forceinline__ uint32_t min_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t d;
-    asm("min.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // 2^13 (v - part) of two pairs of f16, exact where part is v rounded to e4m3's bits.
 __device__ __forceinline__ uint32_t rest_f16x2(uint32_t v, uint32_t part)
 {

@@ -269,75 +269,106 @@ __device__ __forceinline__ void qd_prefetch(QdSmem& sm, const QdParams& p, const
 // The queries of this CTA's heads, by the softmax warps: all of them times one power of two 2^a that brings the largest finite
 // latent entry to [2^7, 2^8) (less where the rope entries would leave bf16's range), as a sum of two e4m3 numbers, the second
 // in units of 1 / 32.  A bf16 has 8 bits, the two numbers 4 each and a sign: exact down to 2^-14 of the largest, and within
-// 2^-15 below.  Returns 2^-a.
-__device__ __forceinline__ float qd_queries(QdSmem& sm, const QdParams& p, int b, int rank)
-{
-    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint16_t* src = p.q_abs + ((size_t)b * H + rank * QD_HEADS) * ROW;
-    constexpr int ITEMS = QD_HEADS * (LORA / 8) / (32 * QD_SOFTMAX);  // pieces of 8 entries a thread: 12
-    constexpr int STEP = 32 * QD_SOFTMAX / 64;
-    auto largest = [](uint32_t m, uint32_t w) {  // of bf16 pairs, NaN and infinities aside
-        const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-        return max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
-    };
-    auto of4 = [&](uint32_t m, const uint4& w) { return largest(largest(largest(largest(m, w.x), w.y), w.z), w.w); };
-    const int j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;  // piece j of heads h_first, + STEP, ...
-    auto piece = [&](int i) { return *reinterpret_cast<const uint4*>(src + (size_t)(h_first + STEP * i) * ROW + 8 * j); };
-    auto rope = [&](int h) { return *reinterpret_cast<const uint4*>(src + (size_t)h * ROW + LORA + 8 * jr); };
-    uint32_t most = 0, most_rope = of4(0u, rope(hr));
-    if (hr + 32 < QD_HEADS) most_rope = of4(most_rope, rope(hr + 32));
+// 2^-15 below.
+struct QdQueries {
+    static constexpr int STEP = 32 * QD_SOFTMAX / 64, ITEMS = QD_HEADS / STEP, ROPES = 32 * QD_SOFTMAX / 8;
+    static_assert(STEP * ITEMS == QD_HEADS && ITEMS % 4 == 0 && 2 * ROPES >= QD_HEADS, "whole pieces");
+    const uint16_t* src;
+    int j, h_first, hr, jr;  // pieces j (8 entries) of heads h_first, + STEP, ..., pieces jr of the rope entries of hr, + ROPES
+    uint32_t most, most_rope;
+    bool odd;                // NaN or infinities among the latent entries
+
+    __device__ __forceinline__ uint4 piece(int i) const
     {
+        return *reinterpret_cast<const uint4*>(src + (size_t)(h_first + STEP * i) * ROW + 8 * j);
+    }
+    __device__ __forceinline__ uint4 rope(int h) const { return *reinterpret_cast<const uint4*>(src + (size_t)h * ROW + LORA + 8 * jr); }
+    // the largest of bf16 pairs, NaN and infinities aside
+    static __device__ __forceinline__ uint32_t of2(uint32_t m, uint32_t w, bool& odd)
+    {
+        const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+        odd = odd || max(lo, hi) >= 0x7F80u;
+        return max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+    }
+    static __device__ __forceinline__ uint32_t of8(uint32_t m, const uint4& w, bool& odd)
+    {
+        return of2(of2(of2(of2(m, w.x, odd), w.y, odd), w.z, odd), w.w, odd);
+    }
+
+    // Reads them once (before the unit's length is known: neither waits for the other).
+    __device__ __forceinline__ void read(const QdParams& p, int b, int rank)
+    {
+        const int tid = (int)threadIdx.x;
+        src = p.q_abs + ((size_t)b * H + rank * QD_HEADS) * ROW;
+        j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;
         uint4 v[ITEMS];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) v[i] = piece(i);
+        bool rope_odd = false;
+        most_rope = of8(0u, rope(hr), rope_odd);
+        if (hr + ROPES < QD_HEADS) most_rope = of8(most_rope, rope(hr + ROPES), rope_odd);
+        most = 0, odd = false;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) most = of4(most, v[i]);
+        for (int i = 0; i < ITEMS; ++i) most = of8(most, v[i], odd);
     }
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    most_rope = __reduce_max_sync(0xFFFFFFFFu, most_rope);
-    if (lane == 0) sm.most[warp][0] = most, sm.most[warp][1] = most_rope;
-    if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = 0.f;
-    named_bar(QB_ALL, 32 * QD_SOFTMAX);
-    most = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane & (QD_SOFTMAX - 1)][0]);
-    most_rope = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane & (QD_SOFTMAX - 1)][1]);
-    // (exponent fields: a value in [2^(e - 127), 2^(e - 126)))
-    int a = most ? 134 - (int)(most >> 7) : 0;
-    a = max(min(min(a, 246 - (int)(most_rope >> 7)), 100), -120);
-    const float up = __uint_as_float((uint32_t)(127 + a) << 23);
-    auto two = [&](uint32_t w, uint32_t& first, uint32_t& second) {  // a bf16 pair -> the pairs of codes
-        if ((w & 0x7F80u) == 0x7F80u) w |= 0x7Fu;
-        if ((w & 0x7F800000u) == 0x7F800000u) w |= 0x7F0000u;
-        const float x = bf16lo_to_f32(w) * up, y = bf16hi_to_f32(w) * up;
-        first = pack_e4m3x2(x, y);
-        float fx, fy;
-        f16x2_parts(e4m3x2_to_f16x2(first), fx, fy);
-        second = pack_e4m3x2((x - fx) * QD_LOW, (y - fy) * QD_LOW);
-    };
-    uint4 next = piece(0);  // (from L1; a loop: this code runs once a unit, and fetching it takes longer than running it)
+
+    // Leaves them in shared memory; returns 2^-a.
+    __device__ __forceinline__ float store(QdSmem& sm)
+    {
+        const int tid = (int)threadIdx.x, lane = tid & 31;
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        most_rope = __reduce_max_sync(0xFFFFFFFFu, most_rope);
+        odd = __any_sync(0xFFFFFFFFu, odd);
+        if (lane == 0) sm.most[tid >> 5][0] = most, sm.most[tid >> 5][1] = most_rope;
+        if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = 0.f;
+        named_bar(QB_ALL, 32 * QD_SOFTMAX);
+        most = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane % QD_SOFTMAX][0]);
+        most_rope = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane % QD_SOFTMAX][1]);
+        // (exponent fields: a value in [2^(e - 127), 2^(e - 126)))
+        int a = most ? 134 - (int)(most >> 7) : 0;
+        a = max(min(min(a, 246 - (int)(most_rope >> 7)), 100), -120);
+        const float up = __uint_as_float((uint32_t)(127 + a) << 23);
+        auto two = [&](uint32_t w, uint32_t& first, uint32_t& second) {  // a bf16 pair -> the pairs of codes
+            if (odd) {
+                if ((w & 0x7F80u) == 0x7F80u) w |= 0x7Fu;
+                if ((w & 0x7F800000u) == 0x7F800000u) w |= 0x7F0000u;
+            }
+            float x, y;
+            f32x2_parts(mul_f32x2(f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w)), f32x2(up, up)), x, y);
+            first = pack_e4m3x2(x, y);
+            float fx, fy;
+            f16x2_parts(e4m3x2_to_f16x2(first), fx, fy);
+            second = pack_e4m3x2((x - fx) * QD_LOW, (y - fy) * QD_LOW);
+        };
 #pragma unroll 1
-    for (int i = 0; i < ITEMS; ++i) {
-        const int h = h_first + STEP * i;
-        const uint4 v = next;
-        next = piece(min(i + 1, ITEMS - 1));
-        uint32_t f[4], s[4];
-        two(v.x, f[0], s[0]), two(v.y, f[1], s[1]), two(v.z, f[2], s[2]), two(v.w, f[3], s[3]);
-        uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
-        *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
-        *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
-    }
-#pragma unroll 1
-    for (int h = hr; h < QD_HEADS; h += 32) {
-        float x[8];
-        unpack8(rope(h), x);
+        for (int i0 = 0; i0 < ITEMS; i0 += 4) {  // (from L1; a loop: this code runs once a unit, and is fetched for it)
+            uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= up;
-        *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((jr ^ (h & 7)) << 4)) = pack8(x);
+            for (int i = 0; i < 4; ++i) v[i] = piece(i0 + i);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int h = h_first + STEP * (i0 + i);
+                uint32_t f[4], s[4];
+                two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
+                uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
+                *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
+                *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
+            }
+        }
+#pragma unroll 1
+        for (int h = hr; h < QD_HEADS; h += ROPES) {
+            float x[8];
+            unpack8(rope(h), x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= up;
+            *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((jr ^ (h & 7)) << 4)) = pack8(x);
+        }
+        fence_proxy_async_cta();  // the MMAs read them through the async proxy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_ready);
+        return __uint_as_float((uint32_t)(127 - a) << 23);
     }
-    fence_proxy_async_cta();  // the MMAs read them through the async proxy
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.q_ready);
-    return __uint_as_float((uint32_t)(127 - a) << 23);
-}
+};
 
 // A float as an integer that orders like it; NaN below everything.
 __device__ __forceinline__ int32_t qd_order(float x)
@@ -426,8 +457,8 @@ __device__ __noinline__ void qd_clear(QdSmem& sm, int i, int token)
 // Softmax warp: the tokens of its quarter, a lane each, and the heads of its group.  A token's factor is its thread's, and the
 // sums of exp stay in the thread until the end; what meets in every tile is one vote of the group's four warps, whether a row
 // has passed its reference.
-__device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const QdUnit& g, int b, int s, int rank,
-                                           uint32_t tbase, int tiles)
+__device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQueries& queries, const QdUnit& g, int b, int s,
+                                           int rank, uint32_t tbase, int tiles)
 {
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id(), quarter = warp & 3, group = warp >> 2, h0 = QD_MINE * group;
     const int token = 32 * quarter + lane, line = token & (PAGE - 1), page = quarter >> 1;
@@ -437,8 +468,8 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
         const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + page) & 31);
         return at < 0 ? (uint16_t)0x3F80u : *reinterpret_cast<const uint16_t*>(p.slab + (size_t)at * QPAGE + QSCALES + 2 * line);
     };
+    const float kq = queries.store(sm) * p.kscale;
     uint16_t next = row_scale(0);
-    const float kq = qd_queries(sm, p, b, rank) * p.kscale;
     const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16);
     float l[QD_MINE];
 #pragma unroll
@@ -473,7 +504,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
                                       f32x2(__uint_as_float(a[h]), __uint_as_float(a[h + 1]))),
                             u[h], u[h + 1]);
         }
-        float x[QD_MINE], most = -INFINITY;
+        float x[QD_MINE];
         auto arguments = [&]() {
 #pragma unroll
             for (int h = 0; h < QD_MINE; h += 4) {
@@ -483,8 +514,10 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
             }
         };
         arguments();
+        float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int h = 0; h < QD_MINE; ++h) most = fmaxf(most, x[h]);
+        for (int h = 4; h < QD_MINE; ++h) m4[h & 3] = fmaxf(m4[h & 3], x[h]);
+        const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // (the first tile sets the references)
         if (named_bar_any(QB_GROUP + group, 128, dead || i == 0 || (seen && !(most <= QD_TAU - k)))) {
             if (named_bar_any(QB_GROUP + group, 128, dead)) return;
@@ -515,10 +548,9 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, const 
             }
             // Heads 0 and 2 of the four in one register, 1 and 3 in the other.  v = p 2^-8 as an f16 has e4m3's bits, 7 higher,
             // subnormals included: the first number is v rounded there, and no conversion (a quarter of the arithmetic's
-            // rate) is needed for it or for what is left.  (A NaN, whose bits would run over into the next head's, becomes 1: its
-            // head's sum is a NaN as well.)
-            const uint32_t va = min_f16x2(pack_f16x2(a[0], a[1]), 0x3C003C00u), vb = min_f16x2(pack_f16x2(a[2], a[3]), 0x3C003C00u);
-            const uint32_t fa = (va + 0x00400040u) & 0xFF80FF80u, fb = (vb + 0x00400040u) & 0xFF80FF80u;
+            // rate) is needed for it or for what is left.  (Masked so that a NaN stays within its head, whose sum is one too.)
+            const uint32_t va = pack_f16x2(a[0], a[1]), vb = pack_f16x2(a[2], a[3]);
+            const uint32_t fa = (va + 0x00400040u) & 0x7F807F80u, fb = (vb + 0x00400040u) & 0x7F807F80u;
             w[y] = (fa >> 7) + (fb << 1);
             const uint32_t sa = pack_e4m3x2_f16(rest_f16x2(va, fa)), sb = pack_e4m3x2_f16(rest_f16x2(vb, fb));
             w[QD_MINE / 4 + y] = __byte_perm(sa, sb, 0x5140);
@@ -635,11 +667,13 @@ __global__ void __launch_bounds__(QD_THREADS, 1)
     const uint32_t tbase = sm.tmem_base;
     griddep_wait();
     griddep_launch_dependents();
+    QdQueries queries;
+    if (warp < QD_SOFTMAX) queries.read(p, b, rank);
     const QdUnit g = qd_unit(p, b, s, s == 0 && rank == 0 && threadIdx.x == 0);
     if (s == 0 && g.n == 0 && threadIdx.x < QD_HEADS) p.oscale[(size_t)(rank * QD_HEADS + (int)threadIdx.x) * p.B + b] = 0.f;
     const int tiles = (g.npg + 1) / 2;
     if (tiles > 0) {
-        if (warp < QD_SOFTMAX) qd_softmax(sm, p, g, b, s, rank, tbase, tiles);
+        if (warp < QD_SOFTMAX) qd_softmax(sm, p, queries, g, b, s, rank, tbase, tiles);
         else if (warp == QW_LOAD) qd_produce(sm, tm_page, p, g, b, tiles);
         else if (warp == QW_SCORE) qd_score(sm, p, tbase, tiles);
         else if (warp == QW_PV) qd_pv(sm, p, tbase, tiles);
