@@ -275,6 +275,7 @@ struct QdQueries {
     static_assert(STEP * ITEMS == QD_HEADS && ITEMS % 4 == 0 && 2 * ROPES >= QD_HEADS, "whole pieces");
     const uint16_t* src;
     int j, h_first, hr, jr;  // pieces j (8 entries) of heads h_first, + STEP, ..., pieces jr of the rope entries of hr, + ROPES
+    uint4 v[ITEMS];
     uint32_t most, most_rope;
     bool odd;                // NaN or infinities among the latent entries
 
@@ -301,7 +302,6 @@ struct QdQueries {
         const int tid = (int)threadIdx.x;
         src = p.q_abs + ((size_t)b * H + rank * QD_HEADS) * ROW;
         j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;
-        uint4 v[ITEMS];
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) v[i] = piece(i);
         bool rope_odd = false;
@@ -340,20 +340,14 @@ struct QdQueries {
             f16x2_parts(e4m3x2_to_f16x2(first), fx, fy);
             second = pack_e4m3x2((x - fx) * QD_LOW, (y - fy) * QD_LOW);
         };
-#pragma unroll 1
-        for (int i0 = 0; i0 < ITEMS; i0 += 4) {  // (from L1; a loop: this code runs once a unit, and is fetched for it)
-            uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = piece(i0 + i);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int h = h_first + STEP * (i0 + i);
-                uint32_t f[4], s[4];
-                two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
-                uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
-                *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
-                *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
-            }
+        for (int i = 0; i < ITEMS; ++i) {
+            const int h = h_first + STEP * i;
+            uint32_t f[4], s[4];
+            two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
+            uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
+            *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
+            *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
         }
 #pragma unroll 1
         for (int h = hr; h < QD_HEADS; h += ROPES) {
