@@ -397,6 +397,35 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
                               uint16_t* out, void* workspace, size_t ws_bytes, int max_ctx, int window, int n_sink,
                               int32_t* dev_err, void* stream);
 
+/* ---- attention for slots that share their first pages --------------------------------
+ * Decode of one token row per slot over its whole context (k3mla_window_decode with window >= ctx_len: the same
+ * definition, roundings, zero rows for -1, NaN for a row that sees a non-finite latent), for groups of slots whose tables
+ * begin with the same pages (k3mla_pool_share_prefix): those are looked up once, in the table of the group's first slot,
+ * and read once for four slots at a time instead of once for each slot.
+ * group_start [n_groups + 1] (non-decreasing, within [0, B]): slots group_start[g] .. group_start[g + 1] - 1 are group g's;
+ *             slots outside every group, or in one of shared_len 0, attend by themselves
+ * shared_len  [n_groups] (NULL for none): tokens that the slots of group g share.  Whole pages of them are read as shared; what is left of a
+ *             last page, like everything behind, comes from each slot's own table.  Tables are not compared.
+ * ctx_len     [B]: 0 or less (zeros), or at least 64 * (shared_len / 64); K3MLA_DEV_CTX and zeros for a slot with fewer
+ * max_shared, max_own  upper bounds of shared_len and of what a slot holds behind its group's whole shared pages (in no group:
+ *             of its ctx_len).  A longer slot is clamped and flagged (K3MLA_DEV_CTX); of a longer prefix the rest is read
+ *             by each slot for itself, within max_own.
+ * shared_split, own_split  the splits of the shared pages and of what is behind them, as split_tokens in
+ *             k3mla_window_decode; K3MLA_SPLIT_AUTO cuts by a list's own length.  A slot's result depends on its own context, its
+ *             group's shared_len and these two only.  k3mla_shared_split_tokens plans both for the current device (returns
+ *             shared_split; own_split may be NULL).
+ * q_abs, slab, block_table, w_kv_b, scale_bf16, out, dev_err as for k3mla_window_decode; B <= 65,535, n_groups <= 2^20.
+ * workspace   device, 256-byte aligned, >= k3mla_shared_decode_workspace_bytes(...) bytes; scratch, one for each call
+ *             that may overlap others.
+ * Two to four kernels on `stream`, reading nothing but w_kv_b before the kernel ahead of the call has completed: w_kv_b must not be written by the kernel immediately before this call. */
+size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int max_own, int shared_split, int own_split);
+int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split);
+int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                        const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                        const int32_t* group_start, const int32_t* shared_len, int n_groups, const uint16_t* w_kv_b,
+                        uint16_t scale_bf16, uint16_t* out, void* workspace, size_t ws_bytes, int B, int max_shared,
+                        int max_own, int shared_split, int own_split, int32_t* dev_err, void* stream);
+
 /* ---- the 8-bit latent cache ------------------------------------------------------------
  * A second form of the cache, 642 bytes a token and layer instead of 1,152: slab [n_pages][n_layers] of blocks of
  * K3MLA_QUANT_PAGE_BYTES, each a page of a layer: 64 rows of K3MLA_QUANT_ROW_BYTES, [512 e4m3 codes | 64 bf16 rope entries],

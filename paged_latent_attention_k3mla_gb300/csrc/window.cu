@@ -5,7 +5,10 @@
 // and over those, with cache rows r_t (a -1 block table entry is an all-zero row),
 //     s_t   = scale * (q_abs[h] . r_t)        (dot over 576)
 //     p     = softmax(s),  o_lat = sum_t p_t r_t[0:512],  out = W_UV[h] o_lat.
-// Decode: one token row per slot.  Chunk: several consecutive new token rows per slot.
+// Decode: one token row per slot.  Chunk: several consecutive new token rows per slot.  Shared: one token row per slot over its
+// whole context, the pages that the slots of a group share read once for four slots x 32 heads at a time (the chunk's units: all
+// 128 rows of an MMA used, and no masks), by a launch of its own; what each slot has behind them as decode's units; the
+// splits of both are added up together.
 //
 // Numerics.  Scores, maxima and sums are f32.  Four roundings go below that: the p of the second contraction
 // to bf16 (the tensor core's operand type; both operands have one type and the cache is bf16), a split's O,
@@ -63,7 +66,13 @@
 
 namespace k3 {
 
-template <bool MQ> struct WCfg {
+// What a launch attends to: one token row per slot; rows of prefill chunks; the pages that the slots of a group share, and what
+// each slot has behind them.
+constexpr int W_DECODE = 0, W_CHUNK = 1, W_SHARED = 2, W_OWN = 3;
+
+template <int MODE> struct WCfg {
+    static constexpr bool MQ = MODE == W_CHUNK || MODE == W_SHARED;  // a unit is 32 heads of up to four rows, not 96 of one
+    static constexpr bool SHARED = MODE == W_SHARED, OWN = MODE == W_OWN;
     static constexpr int RPQ = MQ ? 32 : 24;             // rows per 32-lane quarter
     static constexpr int ROWS = 4 * RPQ;                 // rows of a unit
     static constexpr int NUNIT = MQ ? 7 : 8;             // score CTA: ring of 24 KB units
@@ -111,8 +120,8 @@ struct __align__(16) WUnit {
     int n_hi;        // the last row's context
 };
 
-template <bool MQ> struct __align__(1024) WSmem {
-    using C = WCfg<MQ>;
+template <int MODE> struct __align__(1024) WSmem {
+    using C = WCfg<MODE>;
     union {
         struct {
             uint8_t ring[C::NUNIT][THIRD];
@@ -154,24 +163,26 @@ template <bool MQ> struct __align__(1024) WSmem {
     uint64_t wait_ns;
 };
 
-template <bool MQ> constexpr bool wsmem_fits()
+template <int MODE> constexpr bool wsmem_fits()
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     static_assert(C::QPIECE % 1024 == 0 && SLOT1 % 1024 == 0 && C::PBUF % 1024 == 0,
                   "operand tiles fit and start 1024-byte aligned");
     static_assert(C::NUNIT <= 8 && WN_HALF <= 8, "barrier arrays");
-    static_assert(WN_HALF * SLOT1 + (C::NPBUF - 1) * C::PBUF + 128 * 128 <= sizeof(WSmem<MQ>::u),
+    static_assert(WN_HALF * SLOT1 + (C::NPBUF - 1) * C::PBUF + 128 * 128 <= sizeof(WSmem<MODE>::u),
                   "all 128 rows of the last P buffer, read as the A operand, lie in this CTA's tile area");
-    static_assert(sizeof(WSmem<MQ>) + 1024 <= 227 * 1024, "shared memory of one CTA (with alignment slack)");
+    static_assert(sizeof(WSmem<MODE>) + 1024 <= 227 * 1024, "shared memory of one CTA (with alignment slack)");
     return true;
 }
-static_assert(wsmem_fits<false>() && wsmem_fits<true>(), "shared-memory layouts");
+static_assert(wsmem_fits<W_DECODE>() && wsmem_fits<W_CHUNK>(), "shared-memory layouts");
 
 struct WinParams {
     const uint16_t* q_abs;
     const int32_t* table;
     const int32_t* ctx_len;              // decode
     const int32_t *pos0, *row_start;     // chunk
+    const int32_t *group_start, *shared_len;  // shared and own (else null): [G + 1], [G]
+    int G, max_shared, max_own, shared_split, ns_shared;  // ns_shared: the most splits of a group's shared pages, 0: no group
     uint16_t* olat;                      // [96][R][512] f16: o_lat times a power of two per row
     float* oscale;                       // [96][R]: what undoes it; 0 for rows that see nothing
     uint16_t* ws_o;                      // [B][nsplit][96][512] f16: a split's O (decode, nsplit > 1) ...
@@ -185,17 +196,17 @@ struct WinParams {
     int32_t withhold;                    // diagnostic only, 0 otherwise: the PV CTA never loads the first half of a unit's page k - 1
 };
 
-template <bool MQ> __device__ __forceinline__ WSmem<MQ>& w_smem()
+template <int MODE> __device__ __forceinline__ WSmem<MODE>& w_smem()
 {
     extern __shared__ uint8_t smem_raw[];
-    return *reinterpret_cast<WSmem<MQ>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    return *reinterpret_cast<WSmem<MODE>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 }
 
 // Bounded wait for a phase of one of this CTA's barriers; false after an abort or when the time runs out.  The
 // test is in line (a call where it succeeds cost a fifth of the whole kernel's time), what follows is not.
-template <bool MQ> __device__ __noinline__ bool w_wait_slow(uint32_t bar, uint32_t parity)
+template <int MODE> __device__ __noinline__ bool w_wait_slow(uint32_t bar, uint32_t parity)
 {
-    WSmem<MQ>& sm = w_smem<MQ>();
+    WSmem<MODE>& sm = w_smem<MODE>();
     const uint64_t t0 = globaltimer();
     for (uint32_t n = 1; !mbar_try_wait_cluster(bar, parity); ++n) {
         if (n & 127u) continue;  // (the clock is slow to read: looked at every time, 1 % of the whole call)
@@ -209,25 +220,56 @@ template <bool MQ> __device__ __noinline__ bool w_wait_slow(uint32_t bar, uint32
     return true;
 }
 
-template <bool MQ, bool CLUSTER = false> __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity)
+template <int MODE, bool CLUSTER = false> __device__ __forceinline__ bool w_wait(uint64_t* bar, uint32_t parity)
 {
     const uint32_t a = smem_u32(bar);
     if (CLUSTER ? mbar_test_wait_cluster(a, parity) : mbar_test_wait(a, parity)) return true;
-    return w_wait_slow<MQ>(a, parity);
+    return w_wait_slow<MODE>(a, parity);
 }
 
-template <bool MQ> __device__ __noinline__ bool w_count_slow(const int32_t* counter, int32_t target)
+template <int MODE> __device__ __noinline__ bool w_count_slow(const int32_t* counter, int32_t target)
 {
-    WSmem<MQ>& sm = w_smem<MQ>();
+    WSmem<MODE>& sm = w_smem<MODE>();
     return wait_count(counter, target, sm, sm.dev_err);
 }
 
 // Bounded wait until a shared counter of this CTA reaches `target`.
-template <bool MQ> __device__ __forceinline__ bool w_count(const int32_t* counter, int32_t target)
+template <int MODE> __device__ __forceinline__ bool w_count(const int32_t* counter, int32_t target)
 {
     if (*reinterpret_cast<const volatile int32_t*>(counter) >= target) return true;
-    return w_count_slow<MQ>(counter, target);
+    return w_count_slow<MODE>(counter, target);
 }
+
+// Groups that share their first pages: how many whole pages group gi shares.
+__device__ __forceinline__ int w_shared_pages(const WinParams& p, int gi)
+{
+    return min(min(max(0, p.shared_len[gi]), p.max_shared) / PAGE, p.max_pages);
+}
+
+// A slot of such a call: the pages that its group shares (0: in no group), its tokens, clamped; none where it holds fewer than
+// it is to share.
+struct WShared {
+    int pages, n;
+};
+__device__ __forceinline__ WShared w_shared_row(const WinParams& p, int gi, int b, bool report)
+{
+    WShared s;
+    s.pages = gi < p.G && p.group_start[gi] <= b && b < p.group_start[gi + 1] ? w_shared_pages(p, gi) : 0;
+    const int n = p.ctx_len[b];
+    const int64_t most = min((int64_t)s.pages * PAGE + p.max_own, (int64_t)p.max_pages * PAGE);
+    s.n = max(0, (int)min((int64_t)n, most));
+    if (report && p.dev_err && (n > most || (n > 0 && n < s.pages * PAGE))) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
+    if (s.n < s.pages * PAGE) s.n = 0;
+    return s;
+}
+// (a whole warp, one slot)
+__device__ __forceinline__ WShared w_shared_slot(const WinParams& p, int b, bool report)
+{
+    return w_shared_row(p, warp_count_le(p.group_start + 1, p.G, b), b, report);
+}
+
+// The pages of a split of a list of `pages`.
+__device__ __forceinline__ int w_split_pages(int pages, int split_tokens) { return slot_split(pages * PAGE, split_tokens) / PAGE; }
 
 // Where the search for a chunk's group stands: a cluster's units come in ascending order, so each search goes on in
 // the block of 32 slots where the one before ended, and row_start is gone through once, whatever the number of slots.
@@ -236,9 +278,10 @@ struct WScan {
 };
 
 // Unit u (a whole warp, every lane the same answer); npg is -1 where neither it nor a later one exists.
-template <bool MQ>
+template <int MODE>
 __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool report, WScan& scan)
 {
+    using C = WCfg<MODE>;
     g.npg = 0;
     g.first = 0;
     g.s = 0;
@@ -247,17 +290,21 @@ __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool
     g.rows = 1;
     g.single = 1;
     int last;
-    if constexpr (MQ) {
-        // group u / 3 of up to four rows, counted slot by slot: 32 slots a step
-        const int gi = u / 3, lane = (int)lane_id();
+    if constexpr (C::MQ) {
+        // group u / 3 of up to four rows, counted slot by slot (shared: up to four slots, group by group): 32 slots a step
+        const int per = C::SHARED ? 3 * p.ns_shared : 3;
+        const int gi = u / per, lane = (int)lane_id();
         g.hb = u % 3;
+        g.s = u % per / 3;
+        const int32_t* starts = C::SHARED ? p.group_start : p.row_start;
+        const int count = C::SHARED ? p.G : p.B;
         bool found = false;
-        while (scan.b0 < p.B) {
+        while (scan.b0 < count) {
             const int b = scan.b0 + lane;
             int lo = 0, nb = 0;
-            if (b < p.B) {
-                lo = max(0, p.row_start[b]);
-                nb = max(0, min(p.R, p.row_start[b + 1]) - lo);
+            if (b < count) {
+                lo = max(0, starts[b]);
+                nb = max(0, min(p.R, starts[b + 1]) - lo);
             }
             const int mine = (nb + 3) / 4;
             int upto = mine;
@@ -283,11 +330,41 @@ __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool
             g.npg = -1;
             return;
         }
+        if constexpr (C::SHARED) {
+            // all pages of the unit are seen whole by its rows; n0: bit q says that row q takes part
+            const int pages = w_shared_pages(p, g.b);
+            bool in = false;
+            if (lane < g.rows) in = w_shared_row(p, g.b, g.row0 + lane, false).n > 0;
+            g.n0 = (int)__ballot_sync(0xFFFFFFFFu, in);
+            g.n_hi = pages * PAGE;
+            g.b = max(0, starts[g.b]);  // whose table names the pages
+            g.nsp = g.wp0 = 0;
+            g.single = 0;
+            const int part = w_split_pages(pages, p.shared_split);
+            g.first = g.s * part;
+            g.npg = g.n0 ? max(0, min(part, pages - g.first)) : 0;
+            return;
+        }
         const int64_t n0 = (int64_t)p.pos0[g.b] + (g.row0 - p.row_start[g.b]) + 1;
         const int64_t n1 = n0 + g.rows - 1;
         if (report && n1 > p.cap && p.dev_err) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
         g.n0 = (int)max((int64_t)-4, min(n0, (int64_t)p.cap));  // (the rows' own contexts are clamped again)
         last = (int)max((int64_t)0, min(n1, (int64_t)p.cap));
+    } else if constexpr (C::OWN) {
+        const int most = p.nsplit - p.ns_shared;
+        g.b = u / most;
+        const int s = u % most;
+        const WShared slot = w_shared_slot(p, g.b, report && s == 0);
+        const int shared = slot.n > 0 && slot.pages > 0 ? (slot.pages - 1) / w_split_pages(slot.pages, p.shared_split) + 1 : 0;
+        const int all = (slot.n + PAGE - 1) / PAGE - (slot.n ? slot.pages : 0), part = w_split_pages(all, p.split_tokens);
+        g.n0 = g.n_hi = slot.n;
+        g.nsp = 0;
+        g.wp0 = slot.pages;
+        g.first = s * part;
+        g.npg = max(0, min(part, all - g.first));
+        g.s = shared + s;
+        g.single = shared == 0 && all <= part;
+        return;
     } else {
         g.b = u / p.nsplit;
         g.s = u % p.nsplit;
@@ -297,7 +374,7 @@ __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool
     }
     g.n_hi = last;
     const int all = w_pages(max(g.n0, 0), last, p.window, p.n_sink, g.nsp, g.wp0);
-    if constexpr (MQ) {
+    if constexpr (C::MQ) {
         g.npg = all;
     } else {
         const int per = slot_split(all * PAGE, p.split_tokens) / PAGE;
@@ -347,10 +424,10 @@ struct WLookup {
     }
 };
 
-template <bool MQ>
-__device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, const WinParams& p)
+template <int MODE>
+__device__ __forceinline__ void w_init(WSmem<MODE>& sm, uint32_t rank, const WinParams& p)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     sm.wait_ns = p.wait_ns;
     sm.dev_err = p.dev_err;
     sm.abort_flag = 0;
@@ -394,8 +471,9 @@ __device__ __forceinline__ void w_init(WSmem<MQ>& sm, uint32_t rank, const WinPa
 // the shared memory of both.  At most three units ahead of the PV CTA's MMAs: the softmax warps are then no more
 // than two further units behind (their sums of exp meet in two slots), so W_PLANS = 8 slots never run over; the
 // prefetching warp, which nobody else waits for, is counted.
-template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const WinParams& p)
+template <int MODE> __device__ __forceinline__ void w_plan(WSmem<MODE>& sm, const WinParams& p)
 {
+    constexpr bool MQ = WCfg<MODE>::MQ;
     const int lane = (int)lane_id();
     bool ok = true;
     int n = 0;
@@ -403,9 +481,9 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
     for (int u = (int)blockIdx.x >> 1; ok; u += (int)gridDim.x >> 1) {
         WUnit g;
         g.npg = -1;
-        if (u < p.n_units) w_unit<MQ>(g, p, u, lane == 0, scan);
+        if (u < p.n_units) w_unit<MODE>(g, p, u, lane == 0, scan);
         if (g.npg == 0) continue;
-        if (n >= 4 && lane == 0) ok = w_count<MQ>(&sm.pv_units, n - 3) && (MQ || w_count<MQ>(&sm.ahead_units, n - 6));
+        if (n >= 4 && lane == 0) ok = w_count<MODE>(&sm.pv_units, n - 3) && (MQ || w_count<MODE>(&sm.ahead_units, n - 6));
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
         if (n > 0 && g.npg > 0 && lane < g.rows)  // its queries, into L2 (the first unit's are loaded at once)
@@ -424,10 +502,10 @@ template <bool MQ> __device__ __forceinline__ void w_plan(WSmem<MQ>& sm, const W
 }
 
 // The n-th unit; npg is -1 behind the last one, and after an abort.
-template <bool MQ> __device__ __forceinline__ WUnit w_next(WSmem<MQ>& sm, const WinParams& p, int n)
+template <int MODE> __device__ __forceinline__ WUnit w_next(WSmem<MODE>& sm, const WinParams& p, int n)
 {
     WUnit g;
-    if (__all_sync(0xFFFFFFFFu, w_wait<MQ, true>(&sm.plan_full[n % W_PLANS], (uint32_t)(n / W_PLANS) & 1u)))
+    if (__all_sync(0xFFFFFFFFu, w_wait<MODE, true>(&sm.plan_full[n % W_PLANS], (uint32_t)(n / W_PLANS) & 1u)))
         g = sm.plan[n % W_PLANS];
     else
         g.npg = -1;
@@ -438,17 +516,17 @@ template <bool MQ> __device__ __forceinline__ WUnit w_next(WSmem<MQ>& sm, const 
 
 // Producer t of NPROD: a unit's Q, then its pages in thirds, every NPROD-th use of the ring.  The uses are
 // numbered on from unit to unit; use g lies in ring unit g % NUNIT.
-template <bool MQ>
-__device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_page, const CUtensorMap& tm_q,
+template <int MODE>
+__device__ __forceinline__ void w_produce(WSmem<MODE>& sm, const CUtensorMap& tm_page, const CUtensorMap& tm_q,
                                           const WinParams& p, int t)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     bool ok = true;  // (the elected lane's)
     int base = 0;
     auto take = [&](int use, uint32_t bytes) -> int {  // the use's ring unit, ready to be loaded
         const int u = use % C::NUNIT, k = use / C::NUNIT;
-        if (C::NPROD > 1) ok = ok && w_count<MQ>(&sm.unit_loaded[u], k);
-        ok = ok && w_wait<MQ>(&sm.empty[u], (uint32_t)(k & 1) ^ 1u);
+        if (C::NPROD > 1) ok = ok && w_count<MODE>(&sm.unit_loaded[u], k);
+        ok = ok && w_wait<MODE>(&sm.empty[u], (uint32_t)(k & 1) ^ 1u);
         if (ok) {
             if (C::NPROD > 1) *reinterpret_cast<volatile int32_t*>(&sm.unit_loaded[u]) = k + 1;
             mbar_arrive_expect_tx(&sm.full[u], bytes);
@@ -456,14 +534,14 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
         return u;
     };
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
         if (elect_one()) {
             for (int j = 0; j < C::NQ && ok; ++j) {
                 if ((base + j) % C::NPROD != t) continue;
                 const int u = take(base + j, C::QPU * C::QPIECE);
                 if (!ok) break;
-                if constexpr (MQ) {
+                if constexpr (C::MQ) {
                     // piece: heads 32 hb .. of two consecutive token rows (those past the group land in lanes nobody reads)
                     for (int x = 0; x < C::QPU; ++x) {
                         const int pc = C::QPU * j + x;
@@ -497,27 +575,27 @@ __device__ __forceinline__ void w_produce(WSmem<MQ>& sm, const CUtensorMap& tm_p
 
 // Issuer r: the score MMAs of the pages a = r (mod 3), counted on from unit to unit, into S buffer r.  (One
 // thread alone issues these MMAs at 50 clocks each, the tensor core retires one every 32.)
-template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int r)
+template <int MODE> __device__ __forceinline__ void w_score(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase, int r)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     bool ok = true;
     int base = 0, gp = 0;  // ring uses and pages before this unit
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
         base += C::NQ;
         if (elect_one() && ok) {
-            ok = w_wait<MQ>(&sm.q_ready, (uint32_t)un & 1u);
+            ok = w_wait<MODE>(&sm.q_ready, (uint32_t)un & 1u);
             tc_fence_after();
 #pragma unroll 1
             for (int i = (r + C::NISS - gp % C::NISS) % C::NISS; i < g.npg && ok; i += C::NISS) {
                 const int sb = (gp + i) % WN_S, k = (gp + i) / WN_S;
-                ok = w_wait<MQ>(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u);
+                ok = w_wait<MODE>(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u);
 #pragma unroll 1
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
-                    ok = w_count<MQ>(&sm.unit_taken[u], ku) &&
-                         w_wait<MQ>(&sm.full[u], (uint32_t)(ku & 1));
+                    ok = w_count<MODE>(&sm.unit_taken[u], ku) &&
+                         w_wait<MODE>(&sm.full[u], (uint32_t)(ku & 1));
                     if (!ok) break;
                     *reinterpret_cast<volatile int32_t*>(&sm.unit_taken[u]) = ku + 1;
                     tc_fence_after();
@@ -538,21 +616,22 @@ template <bool MQ> __device__ __forceinline__ void w_score(WSmem<MQ>& sm, const 
 // The softmax warps copy Q from the ring into TMEM (lane 32 w + l <- row RPQ w + l), once the score MMAs of the unit
 // before have read the old Q: each warp its quarter's rows, of every NPAR-th ring use, when it is through with its pages
 // of the unit before.
-template <bool MQ>
-__device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int qd, int par, int base,
+template <int MODE>
+__device__ __forceinline__ bool w_copy_q(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase, int qd, int par, int base,
                                          int un)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     const int lane = (int)lane_id();
+    constexpr bool MQ = C::MQ;
     const int row = MQ ? 32 * (qd & 1) + lane : C::RPQ * qd + lane;  // of a piece
     const uint32_t taddr = tbase + ((32u * (uint32_t)qd) << 16) + Q_COL;
-    if (!__all_sync(0xFFFFFFFFu, un == 0 || w_wait<MQ>(&sm.q_free, (uint32_t)(un - 1) & 1u))) return false;
+    if (!__all_sync(0xFFFFFFFFu, un == 0 || w_wait<MODE>(&sm.q_free, (uint32_t)(un - 1) & 1u))) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int j = par; j < C::NQ; j += C::NPAR) {
         const int u = (base + j) % C::NUNIT, k = (base + j) / C::NUNIT;
-        if (!__all_sync(0xFFFFFFFFu, w_count<MQ>(&sm.unit_taken[u], k) &&
-                                         w_wait<MQ>(&sm.full[u], (uint32_t)(k & 1))))
+        if (!__all_sync(0xFFFFFFFFu, w_count<MODE>(&sm.unit_taken[u], k) &&
+                                         w_wait<MODE>(&sm.full[u], (uint32_t)(k & 1))))
             return false;
 #pragma unroll 1
         for (int x = 0; x < C::QPU; ++x) {
@@ -588,10 +667,10 @@ __device__ __forceinline__ bool w_copy_q(WSmem<MQ>& sm, const WinParams& p, uint
 // turns runs on through all units, so a turn's barrier is never a phase ahead of who waits on it.
 // (The page's code is written to be short: the SM's instruction fetch is what these kernels run short of first.
 // The scores' issue loop unrolled three times, 9 KB more, took the 16 x 64-token chunk from 328 to 358 us.)
-template <bool MQ>
-__device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
+template <int MODE>
+__device__ __forceinline__ void w_softmax(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     const int qd = (int)(warp & 3u), par = (int)(warp >> 2), l = (int)lane_id();
     const int h = C::RPQ * qd + l;
     const bool has_row = l < C::RPQ;
@@ -600,15 +679,15 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     const uint32_t pfull0 = mapa(smem_u32(&sm.p_full[0]), 1);
     const float TAU2 = TAU * 1.4426950408889634f;
     uint8_t* stage = sm.u.c0.pstage[warp];
-    auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xFFFFFFFFu, w_wait<MQ>(bar, (uint32_t)phase & 1u)); };
+    auto wait = [&](uint64_t* bar, int phase) { return __all_sync(0xFFFFFFFFu, w_wait<MODE>(bar, (uint32_t)phase & 1u)); };
     int base = 0, gp = 0, singles = 0;
 #pragma unroll 1
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
-        if (!w_copy_q<MQ>(sm, p, tbase, qd, par, base, un)) return;
+        if (!w_copy_q<MODE>(sm, p, tbase, qd, par, base, un)) return;
         base += C::NQ + 3 * g.npg;
-        const int n = MQ ? (qd < g.rows ? w_clamp(g.n0 + qd, p.cap) : 0) : g.n0;  // this quarter's context
+        const int n = C::MQ ? (qd < g.rows ? w_clamp(g.n0 + qd, p.cap) : 0) : g.n0;  // this quarter's context
         float m_ref = -INFINITY, lsum = 0.f;
         const int rel = (par + C::NPAR - gp % C::NPAR) % C::NPAR;  // this warp's first page of the unit
 #pragma unroll 1
@@ -622,7 +701,7 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             // are the tokens' latents (a NaN or an infinity times anything, 0 too, stays one in the sum), and p = 0 times
             // those is 0: the PV CTA takes the page as it is.
             uint32_t flags = 0;
-            if (!w_whole(p, n, n, t0)) {
+            if (!C::SHARED && !w_whole(p, n, n, t0)) {
                 const uint64_t seen = w_between(p, n - p.window, n, t0);
                 uint32_t most = 0;
 #pragma unroll 1
@@ -729,11 +808,14 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
             if (l == 0) mbar_arrive(&sm.fin_free[un & 1][qd]);
             if (g.single) {  // the PV CTA lands o_lat itself (a row that sees nothing has l = 0; its o_lat is not used)
                 const int sl = singles & 1;
-                if (!__all_sync(0xFFFFFFFFu, w_wait<MQ, true>(&sm.rl_free[sl], (uint32_t)((singles >> 1) + 1) & 1u))) return;
+                if (!__all_sync(0xFFFFFFFFu, w_wait<MODE, true>(&sm.rl_free[sl], (uint32_t)((singles >> 1) + 1) & 1u))) return;
                 if (has_row)
                     st_async_b32(mapa(smem_u32(&sm.u.c1.rl[sl][h]), 1), __float_as_uint(1.f / ltot),
                                  mapa(smem_u32(&sm.l_full[sl]), 1));
-            } else if (!MQ && has_row) {
+            } else if (C::SHARED) {
+                if (g.n0 >> qd & 1)
+                    p.ws_ml[((size_t)(g.row0 + qd) * p.nsplit + g.s) * H + 32 * g.hb + l] = make_float2(m_ref, ltot);
+            } else if (!C::MQ && has_row) {
                 p.ws_ml[((size_t)g.b * p.nsplit + g.s) * H + h] = make_float2(m_ref, ltot);
             }
         }
@@ -744,21 +826,21 @@ __device__ __forceinline__ void w_softmax(WSmem<MQ>& sm, const WinParams& p, uin
     if (l == 0) {
         bulk_wait<0>();
         for (int a = max(0, gp - C::NPBUF); a < gp && !aborted(sm); ++a)
-            w_wait<MQ>(&sm.p_empty[a % C::NPBUF], (uint32_t)((a / C::NPBUF) & 1));
+            w_wait<MODE>(&sm.p_empty[a % C::NPBUF], (uint32_t)((a / C::NPBUF) & 1));
     }
 }
 
 // ---- PV CTA -------------------------------------------------------------------------------
 
 // Producer: the units' pages again, their latents only, as half pages.
-template <bool MQ>
-__device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMap& tm_page8, const WinParams& p)
+template <int MODE>
+__device__ __forceinline__ void w_produce_halves(WSmem<MODE>& sm, const CUtensorMap& tm_page8, const WinParams& p)
 {
     const uint64_t pol = policy_evict_first();  // the last reader of the latent in this unit
     bool ok = true;                             // (the elected lane's)
     int e = 0;
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i, e += 2) {
@@ -767,7 +849,7 @@ __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMa
 #pragma unroll 1
                 for (int x = 0; x < 2 && ok; ++x) {
                     const int q = (e + x) % WN_HALF;
-                    ok = w_wait<MQ>(&sm.empty[q], (uint32_t)(((e + x) / WN_HALF) & 1) ^ 1u);
+                    ok = w_wait<MODE>(&sm.empty[q], (uint32_t)(((e + x) / WN_HALF) & 1) ^ 1u);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&sm.full[q], SLOT1);
                     // (diagnostic: a load never issued.  Asked here the question costs nothing that shows; in the score CTA,
@@ -782,16 +864,16 @@ __device__ __forceinline__ void w_produce_halves(WSmem<MQ>& sm, const CUtensorMa
     if (!ok) drain_inflight();
 }
 
-template <bool MQ>
-__device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase)
+template <int MODE>
+__device__ __forceinline__ void w_issue_pv(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     // (elect_one() names the same lane every time: pending and the two counters are that lane's)
     bool ok = true, pending = false;  // pending: the epilogue has not yet taken the unit before out of TMEM
     uint32_t epi_k = 0;
     int gp = 0;
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
         const int n_lo = w_clamp(g.n0, p.cap);
         if (elect_one() && ok) {
@@ -799,12 +881,12 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
             for (int i = 0; i < g.npg && ok; ++i) {
                 const int a = gp + i, st = a % C::NPBUF;
                 const int q0 = (2 * a) % WN_HALF, q1 = (2 * a + 1) % WN_HALF;
-                if (!w_wait<MQ>(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u) ||
-                    !w_wait<MQ>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u)) {
+                if (!w_wait<MODE>(&sm.full[q0], (uint32_t)(2 * a / WN_HALF) & 1u) ||
+                    !w_wait<MODE>(&sm.full[q1], (uint32_t)((2 * a + 1) / WN_HALF) & 1u)) {
                     ok = false;
                     break;
                 }
-                if (!w_wait<MQ, true>(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1))) {
+                if (!w_wait<MODE, true>(&sm.p_full[st], (uint32_t)((a / C::NPBUF) & 1))) {
                     ok = false;
                     break;
                 }
@@ -815,7 +897,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                 uint32_t cmd = (flags & F_NOT_FINITE) ? E_CLEAR : 0u;
                 if (i > 0 && (flags & F_RESCALE)) cmd |= E_RESCALE;
                 if (pending || cmd) {
-                    if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
+                    if (pending) ok = w_wait<MODE>(&sm.epi_done, epi_k++ & 1u);
                     pending = false;
                     if (ok && cmd) {
                         if (cmd & E_RESCALE) umma_commit(&sm.o_done);
@@ -827,7 +909,7 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
                         sm.epi_rows = g.rows;
                         sm.epi_n0 = g.n0;
                         mbar_arrive(&sm.epi_req);
-                        ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
+                        ok = w_wait<MODE>(&sm.epi_done, epi_k++ & 1u);
                     }
                     if (!ok) break;
                 }
@@ -864,21 +946,25 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MQ>& sm, const WinParams& p, ui
         drain_inflight();
         *reinterpret_cast<volatile int32_t*>(&sm.abort_flag) = 1;
     } else if (elect_one()) {  // the epilogue warps leave
-        if (pending) ok = w_wait<MQ>(&sm.epi_done, epi_k++ & 1u);
+        if (pending) ok = w_wait<MODE>(&sm.epi_done, epi_k++ & 1u);
         sm.epi_cmd = 0u;
         mbar_arrive(&sm.epi_req);
     }
 }
 
 // The rows that see nothing, which no unit has: their o_lat counts as zero whatever the workspace holds.
-template <bool MQ> __device__ __forceinline__ void w_empty_rows(const WinParams& p)
+template <int MODE> __device__ __forceinline__ void w_empty_rows(const WinParams& p)
 {
+    using C = WCfg<MODE>;
+    if constexpr (C::SHARED) return;  // (the launch behind has all slots)
     const int lane = (int)lane_id(), stride = 32 * ((int)gridDim.x >> 1);
     for (int r0 = 32 * ((int)blockIdx.x >> 1); r0 < p.R; r0 += stride) {
         const int r = r0 + lane;
         bool sees = true;
         if (r < p.R) {
-            if constexpr (MQ) {
+            if constexpr (C::OWN) {
+                sees = w_shared_row(p, last_slot_from(p.group_start, p.G, r), r, false).n > 0;
+            } else if constexpr (C::MQ) {
                 const int lo = last_slot_from(p.row_start, p.B, r);
                 const int first = p.row_start[lo];
                 sees = r >= first && r < p.row_start[lo + 1] && (int64_t)p.pos0[lo] + (r - first) >= 0;
@@ -900,20 +986,22 @@ template <bool MQ> __device__ __forceinline__ void w_empty_rows(const WinParams&
 // power of two comes from the row's first 32 entries, with room for 2^8 times their largest, and the row's
 // largest entry is found on the way.  A row that it shows to have left the range, or to lie far below it, has its
 // warps go over their rows again with the power of two that fits.
-template <bool MQ>
-__device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, uint32_t t_row, int quarter, int half,
+template <int MODE>
+__device__ __forceinline__ void w_write_out(WSmem<MODE>& sm, const WinParams& p, uint32_t t_row, int quarter, int half,
                                             int singles)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
+    constexpr bool MQ = C::MQ;
     const int b = sm.epi_b, s = sm.epi_s, hb = sm.epi_hb, row0 = sm.epi_row0, rows = sm.epi_rows;
-    const bool single = MQ || sm.epi_single != 0;
+    const bool single = !C::SHARED && (MQ || sm.epi_single != 0);
     const int lane = (int)lane_id(), col = lane & 3, row = 32 * quarter + (lane >> 2);  // and row + 8, + 16, + 24
     const uint32_t t_lane = t_row + 256u * (uint32_t)half;
     // a chunk's quarter holds 32 heads of token row row0 + quarter; decode's the heads 32 quarter .. of slot b
-    const bool mine = MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : quarter < C::ROWS / 32;  // (and sees something)
+    const bool mine = C::SHARED ? sm.epi_n0 >> quarter & 1
+                                : (MQ ? quarter < rows && sm.epi_n0 + quarter > 0 : quarter < C::ROWS / 32);  // (and sees something)
     const int tok = MQ ? row0 + quarter : b, head = (MQ ? 32 * hb : 32 * quarter) + (lane >> 2);
     // o_lat [96][R][512], or partial O [B][nsplit][96][512]; a scale each
-    const size_t at = single ? (size_t)head * p.R + tok : ((size_t)b * p.nsplit + s) * H + head;
+    const size_t at = single ? (size_t)head * p.R + tok : ((size_t)tok * p.nsplit + s) * H + head;
     const size_t at8 = single ? 8 * (size_t)p.R : 8;  // eight heads on
     uint16_t* out = (single ? p.olat : p.ws_o) + at * LORA + 256 * half + 16 * col;
     float r[4], inverse[4], up[4], m[4];
@@ -1018,18 +1106,18 @@ __device__ __forceinline__ void w_write_out(WSmem<MQ>& sm, const WinParams& p, u
 // 34.4, 10: 70.8 and 35.8).  A chunk's pages are in L2 for most of its units:
 // 235.5 and 123.6 us with it and without.
 constexpr int W_AHEAD = 7;
-template <bool MQ> __device__ __forceinline__ void w_prefetch(WSmem<MQ>& sm, const CUtensorMap& tm_page, const WinParams& p)
+template <int MODE> __device__ __forceinline__ void w_prefetch(WSmem<MODE>& sm, const CUtensorMap& tm_page, const WinParams& p)
 {
     int gp = 0;
     for (int un = 0;; ++un) {
-        const WUnit g = w_next<MQ>(sm, p, un);
+        const WUnit g = w_next<MODE>(sm, p, un);
         if (g.npg < 0) break;
         WLookup rows;
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
             const int done = gp + i - W_AHEAD + 1;  // pages whose P has to be there
             if (done <= 0) continue;  // (a cluster's first pages are loaded at once)
-            if (!__all_sync(0xFFFFFFFFu, w_count<MQ>(&sm.pv_pages, done))) return;
+            if (!__all_sync(0xFFFFFFFFu, w_count<MODE>(&sm.pv_pages, done))) return;
             if (elect_one() && y < p.n_pages * p.n_layers * PAGE &&
                 *reinterpret_cast<volatile int32_t*>(&sm.pv_pages) <= done + 2)
                 for (int x = 0; x < 3; ++x) tma_prefetch_3d(&tm_page, 0, y, 3 * x);
@@ -1045,10 +1133,10 @@ template <bool MQ> __device__ __forceinline__ void w_prefetch(WSmem<MQ>& sm, con
 // such a token get NaN, as they would from the latent itself whatever their p (0 too), by way of that p.  (Rare: the
 // scores have shown that there are some.  Looking every masked page through took the chunk of 1 x 1000 rows from 137 to
 // 152 us.)
-template <bool MQ>
-__device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, int a, uint64_t hidden, int w)
+template <int MODE>
+__device__ __forceinline__ void w_clear(WSmem<MODE>& sm, const WinParams& p, int a, uint64_t hidden, int w)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     const int lane = (int)lane_id();
 #pragma unroll 1
     for (int t = w; t < PAGE; t += W_EPI) {  // a warp a token: 64 pieces of 16 bytes, two a lane
@@ -1069,7 +1157,7 @@ __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, int a
             found = found || f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w;
             *piece = f;
         }
-        if (MQ && __any_sync(0xFFFFFFFFu, found)) {
+        if (C::MQ && __any_sync(0xFFFFFFFFu, found)) {
 #pragma unroll 1
             for (int qd = 0; qd < sm.epi_rows; ++qd) {
                 const int n = w_clamp(sm.epi_n0 + qd, p.cap);
@@ -1083,10 +1171,10 @@ __device__ __forceinline__ void w_clear(WSmem<MQ>& sm, const WinParams& p, int a
 }
 
 // Epilogue warp: the TMEM lanes of its quarter, the dims of its half.
-template <bool MQ>
-__device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, uint32_t tbase, int quarter, int half)
+template <int MODE>
+__device__ __forceinline__ void w_epilogue(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase, int quarter, int half)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     const int lane = (int)lane_id(), row = 32 * quarter + lane;
     const uint32_t t_row = tbase + ((32u * (uint32_t)quarter) << 16), t_lane = t_row + 256u * (uint32_t)half;
     uint32_t od = 0;
@@ -1094,24 +1182,24 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
     for (uint32_t k = 0;; ++k) {
         // (an abort may reach one warp and not another: they agree on it, so that all or none pass the
         // write-out's barriers)
-        bool got = __all_sync(0xFFFFFFFFu, w_wait<MQ>(&sm.epi_req, k & 1u));
+        bool got = __all_sync(0xFFFFFFFFu, w_wait<MODE>(&sm.epi_req, k & 1u));
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         const uint32_t cmd = *reinterpret_cast<volatile uint32_t*>(&sm.epi_cmd);
         if (!cmd) break;
         const int page = sm.epi_page;
-        if (cmd & (E_WRITE | E_RESCALE)) got = w_wait<MQ>(&sm.o_done, od++ & 1u);
+        if (cmd & (E_WRITE | E_RESCALE)) got = w_wait<MODE>(&sm.o_done, od++ & 1u);
         if ((cmd & E_WRITE) && sm.epi_single)
-            got = got && w_wait<MQ, true>(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u);
+            got = got && w_wait<MODE, true>(&sm.l_full[singles & 1], (uint32_t)(singles >> 1) & 1u);
         got = __all_sync(0xFFFFFFFFu, got);
         if (named_bar_any(WB_OUT, 32 * W_EPI, !got)) break;
         tc_fence_after();
         if (cmd & E_WRITE) {
             const bool single = sm.epi_single != 0;
-            w_write_out<MQ>(sm, p, t_row, quarter, half, singles);
+            w_write_out<MODE>(sm, p, t_row, quarter, half, singles);
             singles += single;
             continue;
         }
-        if (cmd & E_CLEAR) w_clear<MQ>(sm, p, page, sm.epi_hidden, quarter + 4 * half);
+        if (cmd & E_CLEAR) w_clear<MODE>(sm, p, page, sm.epi_hidden, quarter + 4 * half);
         const float* al = reinterpret_cast<const float*>(sm.u.c1.recv[page % C::NPBUF] + C::META_ALPHA);
         const float f = (cmd & E_RESCALE) && row < C::ROWS ? al[row] : 1.f;
         if (__any_sync(0xFFFFFFFFu, f != 1.f)) {  // some row of this warp moved its reference
@@ -1134,13 +1222,13 @@ __device__ __forceinline__ void w_epilogue(WSmem<MQ>& sm, const WinParams& p, ui
 
 // ---- the kernel ---------------------------------------------------------------------------
 
-template <bool MQ>
+template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     k3mla_window_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
                         const __grid_constant__ CUtensorMap tm_q, const WinParams p)
 {
-    using C = WCfg<MQ>;
-    WSmem<MQ>& sm = w_smem<MQ>();
+    using C = WCfg<MODE>;
+    WSmem<MODE>& sm = w_smem<MODE>();
     const uint32_t rank = cluster_ctarank(), warp = threadIdx.x >> 5, lane = lane_id();
     if (threadIdx.x == 0) {
         w_init(sm, rank, p);
@@ -1158,20 +1246,22 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     cluster_sync();
     tc_fence_after();
     const uint32_t tbase = sm.tmem_base;
-    griddep_wait();
+    // What each slot has of its own does not wait for the shared pages' kernel ahead: the two write other records, and that one
+    // began this one only when the kernel ahead of the call had completed.  It waits at its end, for those that wait for it.
+    if (!C::OWN || p.ns_shared == 0) griddep_wait();
     griddep_launch_dependents();
     if (rank == 0) {
-        if (warp < C::W_PROD) w_softmax<MQ>(sm, p, tbase, warp);
-        else if (warp < C::W_MMA0) w_produce<MQ>(sm, tm_page, tm_q, p, (int)warp - C::W_PROD);
-        else if (warp < C::W_MMA0 + C::NISS) w_score<MQ>(sm, p, tbase, (int)warp - C::W_MMA0);
+        if (warp < C::W_PROD) w_softmax<MODE>(sm, p, tbase, warp);
+        else if (warp < C::W_MMA0) w_produce<MODE>(sm, tm_page, tm_q, p, (int)warp - C::W_PROD);
+        else if (warp < C::W_MMA0 + C::NISS) w_score<MODE>(sm, p, tbase, (int)warp - C::W_MMA0);
     } else {
         if (warp < 4 || (warp >= WW_EPI1 && warp < WW_EPI1 + 4))
-            w_epilogue<MQ>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
-        else if (warp == WW_HALVES) w_produce_halves<MQ>(sm, tm_page8, p);
-        else if (warp == WW_PV) w_issue_pv<MQ>(sm, p, tbase);
-        else if (warp == WW_PLAN) w_plan<MQ>(sm, p);
-        else if (warp == WW_EMPTY) w_empty_rows<MQ>(p);
-        else if (!MQ && warp == WW_AHEAD) w_prefetch<MQ>(sm, tm_page, p);
+            w_epilogue<MODE>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
+        else if (warp == WW_HALVES) w_produce_halves<MODE>(sm, tm_page8, p);
+        else if (warp == WW_PV) w_issue_pv<MODE>(sm, p, tbase);
+        else if (warp == WW_PLAN) w_plan<MODE>(sm, p);
+        else if (warp == WW_EMPTY) w_empty_rows<MODE>(p);
+        else if (!C::MQ && warp == WW_AHEAD) w_prefetch<MODE>(sm, tm_page, p);
     }
     // After an abort a role leaves wherever it stands, with copies and MMAs of its own or of others still under way: they
     // land before the CTA gives its shared memory and its TMEM back.
@@ -1181,6 +1271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     cluster_sync();
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tbase, TMEM_COLS);
+    if (C::OWN) griddep_wait();
 }
 
 // ---- merge of splits (decode) ---------------------------------------------------------------
@@ -1190,14 +1281,24 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
 // own splits only, whichever kernel adds them up: k3mla_window_merge_kernel, or the expansion when the rows are few.
 constexpr int WM_GROUPS = 4;
 
-// How many splits slot b has.  (A length is no output of the kernels of this call, and was there before the first began.)
-__device__ __forceinline__ int w_splits(const WinParams& p, int b)
+// How many records of slot b there are to add up; 0 where its only split has landed o_lat itself (or there is none).  A whole warp.
+// (A length is no output of the kernels of this call, and was there before the first began.)
+__device__ __forceinline__ int w_records(const WinParams& p, int b)
 {
+    if (p.group_start) {
+        const WShared s = w_shared_slot(p, b, false);
+        if (s.n == 0) return 0;
+        const int own = (s.n + PAGE - 1) / PAGE - s.pages;
+        const int shared = s.pages ? (s.pages - 1) / w_split_pages(s.pages, p.shared_split) + 1 : 0;
+        const int mine = own ? (own - 1) / w_split_pages(own, p.split_tokens) + 1 : 0;
+        return shared + mine > 1 || shared ? shared + mine : 0;
+    }
     int nsp, wp0;
     const int n = w_clamp(p.ctx_len[b], p.cap);
     const int all = w_pages(n, n, p.window, p.n_sink, nsp, wp0);
     const int per = slot_split(all * PAGE, p.split_tokens) / PAGE;
-    return (all + per - 1) / per;
+    const int ns = (all + per - 1) / per;
+    return ns > 1 ? ns : 0;
 }
 
 // The largest reference max of a row's ns splits (a whole warp).
@@ -1252,9 +1353,9 @@ __global__ void __launch_bounds__(128) k3mla_window_merge_kernel(const WinParams
     __shared__ float smax[4];
     const int h = blockIdx.x, b = blockIdx.y, d = 4 * (int)threadIdx.x;
     griddep_launch_dependents();
-    const int ns = w_splits(p, b);
+    const int ns = w_records(p, b);
     griddep_wait();        // (every CTA: the expansion counts on this kernel's end for the splits' end too)
-    if (ns <= 1) return;  // landed by the split itself
+    if (ns == 0) return;  // landed by the split itself
     const size_t row = (size_t)b * p.nsplit * H + h;
     const float m = w_max_ref(p, row, ns);
     float l[WM_GROUPS], part[WM_GROUPS][4], acc[4];
@@ -1354,7 +1455,7 @@ __device__ __forceinline__ void wx_merge(uint8_t* sb, WxSmem& sm, const WinParam
         return reinterpret_cast<uint4*>(sb + (4 * half + (lane >> 3)) * WX_CHUNK + b * 128 + (((lane & 7) ^ (b & 7)) << 4));
     };
     float acc[2][8], ltot = 0.f;
-    const bool several = b < p.B && ns > 1;
+    const bool several = b < p.B && ns > 0;
     if (several) {
         const size_t row = (size_t)b * p.nsplit * H + h;
         const float m = w_max_ref(p, row, ns);
@@ -1513,7 +1614,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.w_ready);
         int ns = 0;
-        if (MERGE && warp / max(MERGE, 1) < win.B) ns = w_splits(win, warp / max(MERGE, 1));
+        if (MERGE && warp / max(MERGE, 1) < win.B) ns = w_records(win, warp / max(MERGE, 1));
         griddep_wait();
         griddep_launch_dependents();
         if constexpr (MERGE != 0) wx_merge<MERGE>(sb, sm, win, h, ns);
@@ -1559,7 +1660,7 @@ __global__ void __launch_bounds__(WX_THREADS, 1)
 // ---- host --------------------------------------------------------------------------------------
 
 // From the splits' records, or the o_lat already landed, to the outputs; p is the attention kernel's.
-template <bool MQ>
+template <int MODE>
 static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStream_t st)
 {
     CUtensorMap tm_w, tm_o;
@@ -1570,6 +1671,7 @@ static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStrea
     // Few rows: the expansion adds the splits up itself, four warps a row (a slot of 3 splits 20.5 -> 16.9 us, of 33 27.5 ->
     // 21.2 us, four slots of 17 26.2 -> 25.5 us) or one (16 slots of 3 26.5 -> 25.0 us, 16 of 4 38.2 -> 36.1 us; but ten of
     // 6 26.8 -> 27.3 us, five of 11 25.8 -> 30.0 us: a warp then goes through its list in several rounds).
+    constexpr bool MQ = WCfg<MODE>::MQ;
     const int merge = MQ || p.nsplit == 1 ? 0 : (p.B <= WX_EPI / 4 ? 4 : (p.B <= WX_EPI && p.nsplit <= WM_GROUPS ? 1 : 0));
     if (p.nsplit > 1 && !merge) {
         rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(128), 0, st, "k3mla_window_merge_kernel", p);
@@ -1587,11 +1689,11 @@ static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStrea
                       tm_o, x, p);
 }
 
-template <bool MQ>
+template <int MODE>
 static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
                     const WinWs& wl, WinParams& p, cudaStream_t st)
 {
-    using C = WCfg<MQ>;
+    using C = WCfg<MODE>;
     p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
     p.oscale = reinterpret_cast<float*>(ws + wl.scale);
     p.ws_o = p.nsplit > 1 ? reinterpret_cast<uint16_t*>(ws + wl.o) : nullptr;
@@ -1602,7 +1704,7 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
     if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
     if (rc) return rc;
-    if (MQ) {
+    if (C::MQ) {
         // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
         const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
         const uint32_t box[4] = {64, 32, 2, 1};
@@ -1612,13 +1714,13 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     }
     if (rc) return rc;
     static bool attr_done[64] = {};
-    const size_t smem = sizeof(WSmem<MQ>) + 1024;
-    set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MQ>), smem, attr_done);
+    const size_t smem = sizeof(WSmem<MODE>) + 1024;
+    set_smem_attr(reinterpret_cast<const void*>(k3mla_window_kernel<MODE>), smem, attr_done);
     const int clusters = std::min(p.n_units, sm_count() / 2);
-    rc = launch_pdl(k3mla_window_kernel<MQ>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
+    rc = launch_pdl(k3mla_window_kernel<MODE>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
                     tm_page8, tm_q, p);
     if (rc) return rc;
-    return w_tail<MQ>(w_kv_b, out, p, st);
+    return C::SHARED ? K3MLA_OK : w_tail<MODE>(w_kv_b, out, p, st);
 }
 
 // What both entries ask of their common arguments; fills p.
@@ -1656,7 +1758,7 @@ int launch_window_tail(const TailArgs& t, cudaStream_t st)
     p.ctx_len = t.ctx_len, p.olat = t.olat, p.oscale = t.oscale, p.ws_o = t.ws_o, p.ws_oscale = t.ws_oscale, p.ws_ml = t.ws_ml;
     p.dev_err = t.dev_err, p.B = p.R = t.B, p.cap = t.cap, p.window = t.window, p.n_sink = t.n_sink;
     p.split_tokens = t.split_tokens, p.nsplit = t.nsplit;
-    return w_tail<false>(t.w_kv_b, t.out, p, st);
+    return w_tail<W_DECODE>(t.w_kv_b, t.out, p, st);
 }
 
 }  // namespace k3
@@ -1731,7 +1833,7 @@ static int window_decode(const uint16_t* q_abs, const uint16_t* slab, int n_page
     p.split_tokens = split_tokens;
     p.nsplit = ns;
     p.n_units = B * ns;
-    return w_launch<false>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), w_layout(B, ns), p,
+    return w_launch<W_DECODE>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), w_layout(B, ns), p,
                            reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1812,7 +1914,7 @@ static int window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int 
     p.B = B;
     p.R = R;
     p.n_units = (int)units;
-    return w_launch<true>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), w_layout(R, 1), p,
+    return w_launch<W_CHUNK>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), w_layout(R, 1), p,
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -1837,4 +1939,108 @@ extern "C" int k3mla_diag_window_chunk_timeout(const uint16_t* q_abs, const uint
     return window_chunk_decode(q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, pos0, row_start, B, R, w_kv_b,
                                scale_bf16, out, workspace, ws_bytes, max_ctx, window, n_sink, dev_err, stream,
                                (uint64_t)wait_us * 1000ull, withhold_page + 1);
+}
+
+// ---- groups of slots that share their first pages -------------------------------------------------
+
+namespace k3 {
+
+struct SharedPlan {
+    int ns_shared, ns_own;
+};
+static bool shared_sizes_ok(int B, int max_shared, int max_own, int shared_split, int own_split)
+{
+    return B > 0 && max_shared >= 0 && max_own > 0 && shared_split >= 0 && own_split >= 0 && shared_split % TILE == 0 && own_split % TILE == 0;
+}
+static SharedPlan shared_plan(int max_shared, int max_own, int shared_split, int own_split)
+{
+    auto splits = [](int tokens, int split) {  // of a list of whole pages
+        const long long pages = ((long long)tokens + PAGE - 1) / PAGE;
+        return tokens > 0 ? launch_nsplit((int)std::min<long long>(pages * PAGE, 0x7FFFFF00), split) : 0;
+    };
+    return {splits(max_shared / PAGE * PAGE, shared_split), splits(max_own, own_split)};
+}
+
+}  // namespace k3
+
+extern "C" size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int max_own, int shared_split, int own_split)
+{
+    if (!shared_sizes_ok(B, max_shared, max_own, shared_split, own_split)) return 0;
+    const SharedPlan n = shared_plan(max_shared, max_own, shared_split, own_split);
+    return w_layout(B, n.ns_shared + n.ns_own).total;
+}
+
+extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split)
+{
+    const long long clusters = std::max(1, sm_count() / 2);
+    // The length that makes `lists` lists of up to `pages` pages take the fewest rounds of the machine: a round costs its pages and
+    // what a unit costs besides (us: 0.67 a page and 5 for four slots x 32 heads, 0.85 and 6 for a slot; a split more in the
+    // merge 0.1).
+    auto best = [&](long long lists, long long pages, double a_page, double a_unit) {
+        pages = std::max(1ll, pages);
+        long long split = pages;
+        double least = 1e30;
+        for (long long n = 1; n <= std::max(1ll, pages / 2) && n <= 4 * clusters; ++n) {  // (whole tiles: two pages)
+            const long long part = ((pages + n - 1) / n + 1) / 2 * 2, parts = (pages + part - 1) / part;
+            const double us = (double)((lists * parts + clusters - 1) / clusters) * (part * a_page + a_unit) + 0.1 * parts;
+            if (us < least) least = us, split = part;
+        }
+        return (int)std::min<long long>((split + 1) / 2 * 2 * PAGE, 0x7FFFFF00);
+    };
+    if (B <= 0 || n_groups < 0 || max_shared < 0 || max_own <= 0) {
+        if (own_split) *own_split = TILE;
+        return TILE;
+    }
+    if (own_split) *own_split = best(B, ((long long)max_own + PAGE - 1) / PAGE, 0.85, 6.0);
+    return best(3 * (((long long)B + 3ll * n_groups) / 4), max_shared / PAGE, 0.67, 5.0);
+}
+
+extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
+                                   const int32_t* block_table, int max_pages_per_slot, const int32_t* ctx_len,
+                                   const int32_t* group_start, const int32_t* shared_len, int n_groups, const uint16_t* w_kv_b,
+                                   uint16_t scale_bf16, uint16_t* out, void* workspace, size_t ws_bytes, int B, int max_shared,
+                                   int max_own, int shared_split, int own_split, int32_t* dev_err, void* stream)
+{
+    if (B == 0 && n_groups >= 0) return K3MLA_OK;
+    if (n_groups < 0 || !shared_sizes_ok(B, max_shared, max_own, shared_split, own_split)) {
+        set_error("k3mla_shared_decode: invalid sizes or splits");
+        return K3MLA_E_INVALID;
+    }
+    WinParams p;
+    int rc = w_check("k3mla_shared_decode", q_abs, slab, n_pages, n_layers, layer, block_table, max_pages_per_slot, w_kv_b,
+                     scale_bf16, out, workspace, 0x7FFFFF00, 0x7FFFFFFF, 0, p);
+    if (rc) return rc;
+    if (!ctx_len || !group_start || (!shared_len && n_groups)) {
+        set_error("k3mla_shared_decode: null or misaligned pointer");
+        return K3MLA_E_INVALID;
+    }
+    const size_t need = k3mla_shared_decode_workspace_bytes(B, max_shared, max_own, shared_split, own_split);
+    if (ws_bytes < need) {
+        set_error("k3mla_shared_decode: workspace %zu < %zu bytes", ws_bytes, need);
+        return K3MLA_E_WORKSPACE;
+    }
+    SharedPlan n = shared_plan(max_shared, max_own, shared_split, own_split);
+    if (n_groups == 0) n.ns_shared = 0;
+    const int nsplit = n.ns_shared + n.ns_own;
+    const WinWs wl = w_layout(B, nsplit);
+    auto unit = [](int tokens, int split) { return std::min<long long>(((long long)tokens + PAGE - 1) / PAGE, (split ? split : SPLIT_MAX) / PAGE); };
+    if (!w_unit_fits("k3mla_shared_decode", std::max(unit(max_shared, shared_split), unit(max_own, own_split)))) return K3MLA_E_INVALID;
+    const long long quads = ((long long)B + 3ll * n_groups) / 4;  // sum over groups of ceil(slots / 4), at most
+    if (B > 65535 || n_groups > 1 << 20 || (long long)B * nsplit * H > 0x7FFFFFFFll || 3 * quads * std::max(1, n.ns_shared) > 0x3FFFFFFFll) {
+        set_error("k3mla_shared_decode: too many slots, groups or splits");
+        return K3MLA_E_INVALID;
+    }
+    if (!device_ok()) return K3MLA_E_DEVICE;
+    p.ctx_len = ctx_len, p.group_start = group_start, p.shared_len = shared_len, p.dev_err = dev_err;
+    p.G = n_groups, p.max_shared = max_shared, p.max_own = max_own, p.shared_split = shared_split, p.split_tokens = own_split;
+    p.ns_shared = n.ns_shared, p.nsplit = nsplit;
+    p.B = p.R = B;
+    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (n.ns_shared) {
+        p.n_units = (int)(3 * quads * n.ns_shared);
+        rc = w_launch<W_SHARED>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), wl, p, st);
+        if (rc) return rc;
+    }
+    p.n_units = B * n.ns_own;
+    return w_launch<W_OWN>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), wl, p, st);
 }

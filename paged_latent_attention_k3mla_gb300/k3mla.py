@@ -37,6 +37,7 @@ EXPORTS = (
     "k3mla_pool_truncate", "k3mla_compact_rows", "k3mla_window_decode_workspace_bytes", "k3mla_window_split_tokens",
     "k3mla_window_decode", "k3mla_window_chunk_decode_workspace_bytes", "k3mla_window_chunk_decode",
     "k3mla_diag_window_timeout", "k3mla_diag_window_chunk_timeout",
+    "k3mla_shared_decode_workspace_bytes", "k3mla_shared_split_tokens", "k3mla_shared_decode",
     "k3mla_quant_norm_rope_append", "k3mla_quant_write_pages", "k3mla_quant_read_pages", "k3mla_quant_copy_pages",
     "k3mla_quant_decode_workspace_bytes", "k3mla_quant_split_tokens", "k3mla_quant_decode", "k3mla_diag_quant_timeout",
 )
@@ -115,6 +116,9 @@ def load(build_if_needed: bool = True):
                                            ctypes.c_uint32, P, P], I),
             "k3mla_diag_window_chunk_timeout": ([P, P, I, I, I, P, I, P, P, I, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, I,
                                                  ctypes.c_uint32, P, P], I),
+            "k3mla_shared_decode_workspace_bytes": ([I, I, I, I, I], SZ),
+            "k3mla_shared_split_tokens": ([I, I, I, I, ctypes.POINTER(I)], I),
+            "k3mla_shared_decode": ([P, P, I, I, I, P, I, P, P, P, I, P, ctypes.c_uint16, P, P, SZ, I, I, I, I, I, P, P], I),
             "k3mla_quant_norm_rope_append": ([P, P, P, P, I, I, I, P, I, P, P, P, P, I64, P, P, I64, P, ctypes.c_float, P, I,
                                               I, I, P, P], I),
             "k3mla_quant_write_pages": ([P, I, P, I, I, P, P, I, P, P], I),
@@ -464,6 +468,43 @@ def window_chunk_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, blo
         _at(dev, out, torch.bfloat16, (R, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
         workspace.numel(), _int(max_ctx, "max_ctx"), _int(window, "window"), _int(n_sink, "n_sink"),
         _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)), "k3mla_window_chunk_decode")
+
+
+def shared_decode_workspace_bytes(B: int, max_shared: int, max_own: int, shared_split: int = SPLIT_AUTO,
+                                  own_split: int = SPLIT_AUTO) -> int:
+    return int(load().k3mla_shared_decode_workspace_bytes(_int(B, "B"), _int(max_shared, "max_shared"), _int(max_own, "max_own"),
+                                                          _int(shared_split, "shared_split"), _int(own_split, "own_split")))
+
+
+def shared_split_tokens(B: int, n_groups: int, max_shared: int, max_own: int) -> tuple[int, int]:
+    """Split lengths (shared, own) that keep the current device busy (batch-dependent)."""
+    own = ctypes.c_int(0)
+    shared = load().k3mla_shared_split_tokens(_int(B, "B"), _int(n_groups, "n_groups"), _int(max_shared, "max_shared"),
+                                              _int(max_own, "max_own"), ctypes.byref(own))
+    return int(shared), own.value
+
+
+def shared_decode(q_abs: torch.Tensor, slab: torch.Tensor, layer: int, block_table: torch.Tensor, ctx_len: torch.Tensor,
+                  group_start: torch.Tensor, shared_len: torch.Tensor, w_kv_b: torch.Tensor, scale_bf16: int,
+                  out: torch.Tensor, workspace: torch.Tensor, max_shared: int, max_own: int, shared_split: int = SPLIT_AUTO,
+                  own_split: int = SPLIT_AUTO, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Decode of groups of slots whose tables begin with the same pages: slots group_start[g] .. group_start[g + 1] - 1
+    (int32 [G + 1]) share their first shared_len[g] tokens (int32 [G]); q_abs [B, 96, 576] -> out [B, 96, 128]; see
+    k3mla_shared_decode.  `workspace`: uint8, >= shared_decode_workspace_bytes."""
+    B = q_abs.shape[0]
+    G = shared_len.shape[0]
+    n_pages, L = slab.shape[0], slab.shape[1]
+    dev = _here(slab)
+    _check(load().k3mla_shared_decode(
+        _at(dev, q_abs, torch.bfloat16, (B, H, ROW), "q_abs"), _at(dev, slab, torch.bfloat16, (n_pages, L, PAGE, ROW), "slab"),
+        n_pages, L, _int(layer, "layer"), _table(dev, block_table, B), block_table.shape[1],
+        _at(dev, ctx_len, torch.int32, (B,), "ctx_len"), _at(dev, group_start, torch.int32, (G + 1,), "group_start"),
+        _at(dev, shared_len, torch.int32, (G,), "shared_len"), G,
+        _at(dev, w_kv_b, torch.bfloat16, (H * (NOPE + V), LORA), "w_kv_b"), _bits(scale_bf16),
+        _at(dev, out, torch.bfloat16, (B, H, V), "out"), _at(dev, workspace, torch.uint8, None, "workspace"),
+        workspace.numel(), B, _int(max_shared, "max_shared"), _int(max_own, "max_own"), _int(shared_split, "shared_split"),
+        _int(own_split, "own_split"), _opt_at(dev, dev_err, torch.int32, (1,), "dev_err"), _stream(stream, dev)),
+        "k3mla_shared_decode")
 
 
 def _quant_slab(device: int, t: torch.Tensor, name: str = "slab"):
