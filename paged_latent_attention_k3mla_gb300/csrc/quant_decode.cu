@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "decode_core.cuh"
@@ -275,25 +276,30 @@ struct QdQueries {
     static_assert(STEP * ITEMS == QD_HEADS && ITEMS % 4 == 0 && 2 * ROPES >= QD_HEADS, "whole pieces");
     const uint16_t* src;
     int j, h_first, hr, jr;  // pieces j (8 entries) of heads h_first, + STEP, ..., pieces jr of the rope entries of hr, + ROPES
-    uint4 v[ITEMS];
-    uint32_t most, most_rope;
-    bool odd;                // NaN or infinities among the latent entries
+    uint4 v[ITEMS], v_rope[2];
+    uint32_t most, most_rope;  // maxima of magnitudes, two at a time
 
     __device__ __forceinline__ uint4 piece(int i) const
     {
         return *reinterpret_cast<const uint4*>(src + (size_t)(h_first + STEP * i) * ROW + 8 * j);
     }
     __device__ __forceinline__ uint4 rope(int h) const { return *reinterpret_cast<const uint4*>(src + (size_t)h * ROW + LORA + 8 * jr); }
-    // the largest of bf16 pairs, NaN and infinities aside
-    static __device__ __forceinline__ uint32_t of2(uint32_t m, uint32_t w, bool& odd)
+    static __device__ __forceinline__ uint32_t of8(uint32_t m, const uint4& w)
     {
-        const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
-        odd = odd || max(lo, hi) >= 0x7F80u;
-        return max(m, max(lo < 0x7F80u ? lo : 0u, hi < 0x7F80u ? hi : 0u));
+        constexpr uint32_t A = 0x7FFF7FFFu;
+        return max_u16x2(max_u16x2(max_u16x2(max_u16x2(m, w.x & A), w.y & A), w.z & A), w.w & A);
     }
-    static __device__ __forceinline__ uint32_t of8(uint32_t m, const uint4& w, bool& odd)
+    static __device__ __forceinline__ uint32_t of_warp(uint32_t m) { return __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16)); }
+    // the largest in n pieces, step entries apart, NaN and infinities aside
+    static __device__ __noinline__ uint32_t finite(const uint16_t* piece, int n, int step)
     {
-        return of2(of2(of2(of2(m, w.x, odd), w.y, odd), w.z, odd), w.w, odd);
+        uint32_t m = 0;
+#pragma unroll 1
+        for (int i = 0; i < 8 * n; ++i) {
+            const uint32_t x = piece[(size_t)(i >> 3) * step + (i & 7)] & 0x7FFFu;
+            if (x < 0x7F80u) m = max(m, x);
+        }
+        return __reduce_max_sync(0xFFFFFFFFu, m);
     }
 
     // Reads them once (before the unit's length is known: neither waits for the other).
@@ -304,21 +310,22 @@ struct QdQueries {
         j = tid & 63, h_first = tid >> 6, hr = tid >> 3, jr = tid & 7;
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) v[i] = piece(i);
-        bool rope_odd = false;
-        most_rope = of8(0u, rope(hr), rope_odd);
-        if (hr + ROPES < QD_HEADS) most_rope = of8(most_rope, rope(hr + ROPES), rope_odd);
-        most = 0, odd = false;
+        v_rope[0] = rope(hr), v_rope[1] = hr + ROPES < QD_HEADS ? rope(hr + ROPES) : make_uint4(0u, 0u, 0u, 0u);
+        most_rope = of8(of8(0u, v_rope[0]), v_rope[1]);
+        most = 0;
 #pragma unroll
-        for (int i = 0; i < ITEMS; ++i) most = of8(most, v[i], odd);
+        for (int i = 0; i < ITEMS; ++i) most = of8(most, v[i]);
     }
 
     // Leaves them in shared memory; returns 2^-a.
     __device__ __forceinline__ float store(QdSmem& sm)
     {
         const int tid = (int)threadIdx.x, lane = tid & 31;
-        most = __reduce_max_sync(0xFFFFFFFFu, most);
-        most_rope = __reduce_max_sync(0xFFFFFFFFu, most_rope);
-        odd = __any_sync(0xFFFFFFFFu, odd);
+        most = of_warp(most);
+        most_rope = of_warp(most_rope);
+        const bool odd = most >= 0x7F80u;
+        if (odd) most = finite(src + (size_t)h_first * ROW + 8 * j, ITEMS, STEP * ROW);
+        if (most_rope >= 0x7F80u) most_rope = finite(src + (size_t)hr * ROW + LORA + 8 * jr, hr + ROPES < QD_HEADS ? 2 : 1, ROPES * ROW);
         if (lane == 0) sm.most[tid >> 5][0] = most, sm.most[tid >> 5][1] = most_rope;
         if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = 0.f;
         named_bar(QB_ALL, 32 * QD_SOFTMAX);
@@ -328,34 +335,43 @@ struct QdQueries {
         int a = most ? 134 - (int)(most >> 7) : 0;
         a = max(min(min(a, 246 - (int)(most_rope >> 7)), 100), -120);
         const float up = __uint_as_float((uint32_t)(127 + a) << 23);
-        auto two = [&](uint32_t w, uint32_t& first, uint32_t& second) {  // a bf16 pair -> the pairs of codes
-            if (odd) {
-                if ((w & 0x7F80u) == 0x7F80u) w |= 0x7Fu;
-                if ((w & 0x7F800000u) == 0x7F800000u) w |= 0x7F0000u;
-            }
+        const float to_f16 = up * (1.f / 256.f);  // (2^-128 at least: exact as a subnormal)
+        // A bf16 pair -> first numbers in bytes 0 and 2, second numbers in the lower half.  As with the probabilities: v, the
+        // scaled entry times 2^-8, as an f16 has e4m3's bits 7 higher, subnormals included.
+        auto two = [&](uint32_t w, uint32_t& first, uint32_t& second) {
             float x, y;
-            f32x2_parts(mul_f32x2(f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w)), f32x2(up, up)), x, y);
-            first = pack_e4m3x2(x, y);
-            float fx, fy;
-            f16x2_parts(e4m3x2_to_f16x2(first), fx, fy);
-            second = pack_e4m3x2((x - fx) * QD_LOW, (y - fy) * QD_LOW);
+            f32x2_parts(mul_f32x2(f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w)), f32x2(to_f16, to_f16)), x, y);
+            const uint32_t v = pack_f16x2(x, y), f = (v + 0x00400040u) & 0xFF80FF80u;
+            first = ((f >> 7) & 0x007F007Fu) | ((f >> 8) & ~0x007F007Fu);
+            second = pack_e4m3x2_f16(rest_f16x2(v, f));
         };
+        auto place = [&](int h) { return sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1); };
 #pragma unroll
         for (int i = 0; i < ITEMS; ++i) {
-            const int h = h_first + STEP * i;
             uint32_t f[4], s[4];
             two(v[i].x, f[0], s[0]), two(v[i].y, f[1], s[1]), two(v[i].z, f[2], s[2]), two(v[i].w, f[3], s[3]);
-            uint8_t* at = sm.q[j >> 4] + h * 128 + ((((j >> 1) & 7) ^ (h & 7)) << 4) + 8 * (j & 1);
-            *reinterpret_cast<uint2*>(at) = make_uint2(f[0] | f[1] << 16, f[2] | f[3] << 16);
+            uint8_t* at = place(h_first + STEP * i);
+            *reinterpret_cast<uint2*>(at) = make_uint2(__byte_perm(f[0], f[1], 0x6420), __byte_perm(f[2], f[3], 0x6420));
             *reinterpret_cast<uint2*>(at + QD_HEADS * 128) = make_uint2(s[0] | s[1] << 16, s[2] | s[3] << 16);
         }
+        if (odd) {  // NaN and infinities become NaN
 #pragma unroll 1
-        for (int h = hr; h < QD_HEADS; h += ROPES) {
+            for (int i = 0; i < ITEMS; ++i) {
+                const uint16_t* w = src + (size_t)(h_first + STEP * i) * ROW + 8 * j;
+                uint8_t* at = place(h_first + STEP * i);
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e)
+                    if ((w[e] & 0x7F80u) == 0x7F80u) at[e] = at[QD_HEADS * 128 + e] = 0x7Fu;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int h = hr + ROPES * i;
             float x[8];
-            unpack8(rope(h), x);
+            unpack8(v_rope[i], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= up;
-            *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((jr ^ (h & 7)) << 4)) = pack8(x);
+            if (h < QD_HEADS) *reinterpret_cast<uint4*>(sm.q_rope + h * 128 + ((jr ^ (h & 7)) << 4)) = pack8(x);
         }
         fence_proxy_async_cta();  // the MMAs read them through the async proxy
         __syncwarp();
@@ -559,16 +575,32 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full);
     }
-    // the sums of exp: over the lanes, then over the quarters
-    float mine = 0.f;
+    // The sums of exp: over the lanes -- half of the heads go to the other half of the lanes three times, so that three heads a
+    // lane are left to add up over four -- then over the quarters.
+    {
+        int first = 0;
+        auto halve = [&](auto half, int o) {
+            constexpr int n = decltype(half)::value;
+            const bool high = lane & o;
 #pragma unroll
-    for (int h = 0; h < QD_MINE; ++h) {
-        float v = l[h];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-        if (lane == h) mine = v;
+            for (int h = 0; h < n; ++h) {
+                const uint32_t lo = __float_as_uint(l[h]), hi = __float_as_uint(l[h + n]), x = high ? lo ^ hi : 0u;
+                l[h] = __uint_as_float(lo ^ x) + __uint_as_float(__shfl_xor_sync(0xFFFFFFFFu, hi ^ x, o));
+            }
+            if (high) first += n;
+        };
+        halve(std::integral_constant<int, 12>(), 16);
+        halve(std::integral_constant<int, 6>(), 8);
+        halve(std::integral_constant<int, 3>(), 4);
+        static_assert(QD_MINE == 24, "three heads a lane");
+        auto four = [](float x) {
+            x += __shfl_xor_sync(0xFFFFFFFFu, x, 2);
+            return x + __shfl_xor_sync(0xFFFFFFFFu, x, 1);
+        };
+        const float l0 = four(l[0]), l1 = four(l[1]), l2 = four(l[2]);
+        const int k = lane & 3;
+        if (k < 3) sm.part[quarter][h0 + first + k] = k == 0 ? l0 : k == 1 ? l1 : l2;
     }
-    if (lane < QD_MINE) sm.part[quarter][h0 + lane] = mine;
     dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, tiles - 1));
     if (named_bar_any(QB_GROUP + group, 128, dead)) return;
     tc_fence_after();
@@ -577,7 +609,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     if (lane < QD_MINE)
         total = (sm.part[0][h0 + lane] + sm.part[1][h0 + lane]) + (sm.part[2][h0 + lane] + sm.part[3][h0 + lane]);
     float r = (g.single ? 1.f / total : 1.f) * (1.f / QD_UP);
-    // thread = dim 128 d + 32 quarter + lane of every block d; twice over O, first for the heads' largest entries
+    // thread = dim 128 d + 32 quarter + lane of every block d; first the heads' largest entries (two blocks stay in registers)
     auto load = [&](int d, float (&o)[QD_MINE]) {
         uint32_t v[2 * QD_MINE];
         qd_load_pairs(t_lane + (uint32_t)(QD_PAIRS * d + 2 * h0), v);
@@ -587,15 +619,12 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         for (int h = 0; h < QD_MINE; ++h)
             o[h] = fmaf(__uint_as_float(v[QD_MINE + h]), 1.f / QD_LOW, __uint_as_float(v[h]));
     };
-    float big[QD_MINE];
+    float o[2][QD_MINE], big[QD_MINE];
 #pragma unroll
-    for (int h = 0; h < QD_MINE; ++h) big[h] = 0.f;
-#pragma unroll 1
-    for (int d = 0; d < 4; ++d) {
-        float o[QD_MINE];
-        load(d, o);
+    for (int d = 3; d >= 0; --d) {
+        load(d, o[d & 1]);
 #pragma unroll
-        for (int h = 0; h < QD_MINE; ++h) big[h] = fmaxf(big[h], fabsf(o[h]));
+        for (int h = 0; h < QD_MINE; ++h) big[h] = d == 3 ? fabsf(o[1][h]) : fmaxf(big[h], fabsf(o[d & 1][h]));
     }
     uint32_t most = 0;
 #pragma unroll
@@ -621,17 +650,15 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     const bool upper = lane & 1;
     uint16_t* out = (g.single ? p.olat : p.ws_o) + place(rank * QD_HEADS + h0) * LORA;
     const size_t step = (g.single ? (size_t)p.B : 1) * LORA;
-#pragma unroll 1
+#pragma unroll
     for (int d = 0; d < 4; d += 2) {
-        float o0[QD_MINE], o1[QD_MINE];
-        load(d, o0);
-        load(d + 1, o1);
-        uint16_t* at = out + w_dim_place(128 * (upper ? d + 1 : d) + 32 * quarter + (lane & ~1));
+        if (d > 0) load(d, o[0]), load(d + 1, o[1]);
+        uint16_t* to = out + w_dim_place(128 * (upper ? d + 1 : d) + 32 * quarter + (lane & ~1));
 #pragma unroll
         for (int h = 0; h < QD_MINE; ++h) {
-            const float f = __shfl_sync(0xFFFFFFFFu, r, h), mine0 = o0[h] * f, mine1 = o1[h] * f;
+            const float f = __shfl_sync(0xFFFFFFFFu, r, h), mine0 = o[0][h] * f, mine1 = o[1][h] * f;
             const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? mine0 : mine1, 1);
-            *reinterpret_cast<uint32_t*>(at + h * step) = upper ? pack_f16x2(other, mine1) : pack_f16x2(mine0, other);
+            *reinterpret_cast<uint32_t*>(to + h * step) = upper ? pack_f16x2(other, mine1) : pack_f16x2(mine0, other);
         }
     }
 }
