@@ -90,6 +90,14 @@ __device__ __forceinline__ uint32_t largest_finite(const float (&x)[8], bool& od
     return m;
 }
 
+// n for a row whose largest finite latent and rope entry have the bits m and r (of f32, without signs).
+__device__ __forceinline__ int quant_exponent(uint32_t m, uint32_t r)
+{
+    // (the exponent fields are e + 126)
+    const int n = m ? (int)(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u) : 0;
+    return min(max(max(n, (int)(r >> 23) - 246), -96), 120);
+}
+
 // A row into its place in a page block, by a whole warp: lane l has the latents 8 l .. and 256 + 8 l .., and lanes 0 .. 7 the
 // rope entries 8 l .. (the others' k is not looked at).  `block`: the page's block of the layer, line the row in it.
 __device__ __forceinline__ void quant_store_row(uint8_t* block, int line, float (&c0)[8], float (&c1)[8], const float (&k)[8])
@@ -98,9 +106,7 @@ __device__ __forceinline__ void quant_store_row(uint8_t* block, int line, float 
     bool odd = false, rope_odd = false;
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, max(largest_finite(c0, odd), largest_finite(c1, odd)));
     const uint32_t r = __reduce_max_sync(0xFFFFFFFFu, lane < 8 ? largest_finite(k, rope_odd) : 0u);
-    // (the exponent fields are e + 126)
-    int n = m ? (int)(m >> 23) - 135 + ((m & 0x7FFFFFu) > 0x600000u) : 0;
-    n = min(max(max(n, (int)(r >> 23) - 246), -96), 120);
+    const int n = quant_exponent(m, r);
     const float down = __uint_as_float((uint32_t)(127 - n) << 23);
     if (__any_sync(0xFFFFFFFFu, odd)) {
 #pragma unroll

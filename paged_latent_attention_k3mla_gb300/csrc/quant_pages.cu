@@ -27,6 +27,55 @@ struct QuantPagesParams {
     int n_pages, quant_pages, n_layers, layer0;
 };
 
+// The larger of m and x's bf16 magnitudes, NaN and infinities aside; with LATENT these become NaN.
+template <bool LATENT> __device__ __forceinline__ uint32_t qp_finite(uint32_t m, uint32_t& x)
+{
+    const uint32_t lo = x & 0x7FFFu, hi = (x >> 16) & 0x7FFFu;
+    if (lo < 0x7F80u) m = max(m, lo);
+    else if (LATENT) x |= 0x7Fu;
+    if (hi < 0x7F80u) m = max(m, hi);
+    else if (LATENT) x |= 0x7F0000u;
+    return m;
+}
+
+// quant_store_row for a row of bf16: lane l has the latents 8 l .. and 256 + 8 l .. and the rope entries 2 l, 2 l + 1.  The
+// same results in half the instructions (what bounds this direction): maxima of two magnitudes at a time, products in pairs.
+__device__ __forceinline__ void qp_store_row(uint8_t* block, int line, const uint4& c0, const uint4& c1, uint32_t k)
+{
+    const int lane = (int)lane_id();
+    uint32_t x[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    constexpr uint32_t A = 0x7FFF7FFFu;
+    uint32_t m = x[0] & A, r = k & A;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = max_u16x2(m, x[i] & A);
+    m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+    r = __reduce_max_sync(0xFFFFFFFFu, max(r & 0xFFFFu, r >> 16));
+    if (m >= 0x7F80u) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = qp_finite<true>(m, x[i]);
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+    }
+    if (r >= 0x7F80u) r = __reduce_max_sync(0xFFFFFFFFu, qp_finite<false>(0u, k));
+    const int n = quant_exponent(m << 16, r << 16);
+    const float d = __uint_as_float((uint32_t)(127 - n) << 23);
+    const uint64_t down = f32x2(d, d);
+    auto two = [&](uint32_t w, float& a, float& b) { f32x2_parts(mul_f32x2(f32x2(bf16lo_to_f32(w), bf16hi_to_f32(w)), down), a, b); };
+    float a, b;
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        two(x[i], a, b);
+        c[i] = pack_e4m3x2(a, b);
+    }
+    uint8_t* row = block + line * QROW;
+    *reinterpret_cast<uint2*>(row + 8 * lane) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    *reinterpret_cast<uint2*>(row + 256 + 8 * lane) = make_uint2(c[4] | c[5] << 16, c[6] | c[7] << 16);
+    two(k, a, b);
+    *reinterpret_cast<uint32_t*>(row + LORA + 4 * lane) = pack_bf16x2(a, b);
+    if (lane == 0) *reinterpret_cast<uint16_t*>(block + QSCALES + 2 * line) = (uint16_t)((n + 127) << 7);
+}
+
 // grid (PAGE / QP_CTA, layers, pairs).  BACK: from the 8-bit cache.
 template <bool BACK>
 __global__ void __launch_bounds__(QP_THREADS) k3mla_quant_pages_kernel(const QuantPagesParams p)
@@ -73,22 +122,17 @@ __global__ void __launch_bounds__(QP_THREADS) k3mla_quant_pages_kernel(const Qua
             }
         }
     } else {
-        uint4 v[QP_ROWS][3];
+        uint4 v[QP_ROWS][2];
+        uint32_t k[QP_ROWS];
 #pragma unroll
         for (int i = 0; i < QP_ROWS; ++i) {
             const uint4* src = reinterpret_cast<const uint4*>(rows + (size_t)i * ROW);
             v[i][0] = src[lane];
             v[i][1] = src[32 + lane];
-            v[i][2] = lane < 8 ? src[64 + lane] : make_uint4(0u, 0u, 0u, 0u);
+            k[i] = reinterpret_cast<const uint32_t*>(src + 64)[lane];
         }
 #pragma unroll
-        for (int i = 0; i < QP_ROWS; ++i) {
-            float c0[8], c1[8], k[8];
-            unpack8(v[i][0], c0);
-            unpack8(v[i][1], c1);
-            unpack8(v[i][2], k);
-            quant_store_row(block, line0 + i, c0, c1, k);
-        }
+        for (int i = 0; i < QP_ROWS; ++i) qp_store_row(block, line0 + i, v[i][0], v[i][1], k[i]);
     }
 }
 
