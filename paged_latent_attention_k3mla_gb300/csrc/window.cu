@@ -1347,35 +1347,101 @@ __device__ __forceinline__ void w_sum_groups(const WinParams& p, size_t row, int
         }
 }
 
-// A row per CTA of 128 threads, four dims each.
+// A row's sums times 1 / l, as o_lat: TEAM warps a row of the CTA's four, D dims of the row in each of N pieces a thread.
+template <int TEAM, int N, int D>
+__device__ __forceinline__ void w_merged(const WinParams& p, int b, int h, float (&acc)[N][D], const int (&d)[N])
+{
+    float big = 0.f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < D; ++e) big = fmaxf(big, fabsf(acc[n][e]));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
+    if constexpr (TEAM == 4) {
+        __shared__ float smax[4];
+        if (lane_id() == 0) smax[threadIdx.x >> 5] = big;
+        __syncthreads();
+        big = fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3]));
+    }
+    float inverse;
+    const float up = w_row_scale(big, inverse);
+    const size_t row = (size_t)h * p.B + b;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < D; e += 4)
+            *reinterpret_cast<uint2*>(p.olat + row * LORA + d[n] + e) =
+                make_uint2(pack_f16x2(acc[n][e] * up, acc[n][e + 1] * up), pack_f16x2(acc[n][e + 2] * up, acc[n][e + 3] * up));
+    if (d[0] == 0) p.oscale[row] = inverse;
+}
+
+// TEAM 4: a row a CTA of 128 threads, four dims each.  1: a row a warp, eight dims twice a lane; up to four records, all that is
+// read is asked for at once.
+template <int TEAM>
 __global__ void __launch_bounds__(128) k3mla_window_merge_kernel(const WinParams p)
 {
-    __shared__ float smax[4];
-    const int h = blockIdx.x, b = blockIdx.y, d = 4 * (int)threadIdx.x;
+    const int lane = (int)lane_id(), b = blockIdx.y, h = TEAM == 4 ? (int)blockIdx.x : 4 * (int)blockIdx.x + (int)(threadIdx.x >> 5);
     griddep_launch_dependents();
     const int ns = w_records(p, b);
     griddep_wait();        // (every CTA: the expansion counts on this kernel's end for the splits' end too)
     if (ns == 0) return;  // landed by the split itself
     const size_t row = (size_t)b * p.nsplit * H + h;
-    const float m = w_max_ref(p, row, ns);
-    float l[WM_GROUPS], part[WM_GROUPS][4], acc[4];
-    w_sum_groups<WM_GROUPS, 4>(p, row, ns, 0, m, d, l, part);
-    const float r = 1.f / ((l[0] + l[1]) + (l[2] + l[3]));
-    float big = 0.f;
+    constexpr int N = TEAM == 4 ? 1 : 2, D = TEAM == 4 ? 4 : 8;
+    int d[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        acc[e] = ((part[0][e] + part[1][e]) + (part[2][e] + part[3][e])) * r;
-        big = fmaxf(big, fabsf(acc[e]));
+    for (int n = 0; n < N; ++n) d[n] = TEAM == 4 ? 4 * (int)threadIdx.x : 256 * n + 8 * lane;
+    float acc[N][D];
+    if (TEAM == 1 && ns <= WM_GROUPS) {
+        float2 rec[WM_GROUPS];
+        float f[WM_GROUPS], l[WM_GROUPS], m = -INFINITY;
+        uint4 v[WM_GROUPS][N];
+#pragma unroll
+        for (int k = 0; k < WM_GROUPS; ++k) {
+            const bool is = k < ns;
+            const size_t at = row + (size_t)(is ? k : 0) * H;
+            rec[k] = p.ws_ml[at];
+            f[k] = p.ws_oscale[at];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                v[k][n] = is ? *reinterpret_cast<const uint4*>(p.ws_o + at * LORA + d[n]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < WM_GROUPS; ++k) m = fmaxf(m, rec[k].x);  // (those not there repeat the first)
+#pragma unroll
+        for (int k = 0; k < WM_GROUPS; ++k) {
+            const float w = k < ns ? ex2_approx(rec[k].x - m) : 0.f;
+            f[k] = k < ns ? w * f[k] : 0.f;
+            l[k] = k < ns ? fmaf(w, rec[k].y, 0.f) : 0.f;
+        }
+        const float r = 1.f / ((l[0] + l[1]) + (l[2] + l[3]));
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < D / 2; ++e) {
+                float x[WM_GROUPS][2];
+#pragma unroll
+                for (int k = 0; k < WM_GROUPS; ++k) {
+                    const uint4& u = v[k][n];
+                    f16x2_parts(e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w, x[k][0], x[k][1]);
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                    acc[n][2 * e + y] = ((fmaf(f[0], x[0][y], 0.f) + fmaf(f[1], x[1][y], 0.f)) +
+                                         (fmaf(f[2], x[2][y], 0.f) + fmaf(f[3], x[3][y], 0.f))) * r;
+            }
+    } else {
+        const float m = w_max_ref(p, row, ns);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float l[WM_GROUPS], part[WM_GROUPS][D];
+            w_sum_groups<WM_GROUPS, D>(p, row, ns, 0, m, d[n], l, part);
+            const float r = 1.f / ((l[0] + l[1]) + (l[2] + l[3]));
+#pragma unroll
+            for (int e = 0; e < D; ++e) acc[n][e] = ((part[0][e] + part[1][e]) + (part[2][e] + part[3][e])) * r;
+        }
     }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, x));
-    if (lane_id() == 0) smax[threadIdx.x >> 5] = big;
-    __syncthreads();
-    float inverse;
-    const float up = w_row_scale(fmaxf(fmaxf(smax[0], smax[1]), fmaxf(smax[2], smax[3])), inverse);
-    *reinterpret_cast<uint2*>(p.olat + ((size_t)h * p.B + b) * LORA + d) =
-        make_uint2(pack_f16x2(acc[0] * up, acc[1] * up), pack_f16x2(acc[2] * up, acc[3] * up));
-    if (d == 0) p.oscale[(size_t)h * p.B + b] = inverse;
+    w_merged<TEAM>(p, b, h, acc, d);
 }
 
 // ---- W_UV expansion ---------------------------------------------------------------------------
@@ -1674,7 +1740,12 @@ static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStrea
     constexpr bool MQ = WCfg<MODE>::MQ;
     const int merge = MQ || p.nsplit == 1 ? 0 : (p.B <= WX_EPI / 4 ? 4 : (p.B <= WX_EPI && p.nsplit <= WM_GROUPS ? 1 : 0));
     if (p.nsplit > 1 && !merge) {
-        rc = launch_pdl(k3mla_window_merge_kernel, dim3(H, p.B), dim3(128), 0, st, "k3mla_window_merge_kernel", p);
+        // A CTA a row has more of a row's records under way, a warp a row needs one round of the SMs where four warps need three:
+        // 5 slots of 11 splits 27.4 against 30.8 us, 8 of 9 65.5 / 66.7, 12 of 6 40.6 / 40.5, 16 of 4 48.1 / 48.1, 20 of 3
+        // 56.8 / 55.0, 32 of 2 49.9 / 47.4, 64 of 4 183.1 / 174.8.  The same sums in the same order.
+        const bool warps = p.B > 16;
+        rc = launch_pdl(warps ? k3mla_window_merge_kernel<1> : k3mla_window_merge_kernel<4>, dim3(warps ? H / 4 : H, p.B), dim3(128), 0,
+                        st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
     }
     WxParams x;
@@ -1970,29 +2041,62 @@ extern "C" size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int
     return w_layout(B, n.ns_shared + n.ns_own).total;
 }
 
+// When the last of S units of a us, then O units of b us, has ended, each taken by the cluster that is free first.
+static double shared_span(long long S, double a, long long O, double b, long long clusters)
+{
+    const long long q = S / clusters, r = S % clusters;  // r clusters are free after q + 1 rounds, the others after q
+    const double early = q * a, late = r ? early + a : early;
+    auto ends = [&](double base) {
+        long long lo = 0, hi = O;
+        while (lo < hi) {
+            const long long k = (lo + hi) / 2;
+            const double t = base + k * b;
+            long long room = (clusters - r) * (long long)((t - early) / b + 1e-9);
+            if (r && t >= late) room += r * (long long)((t - late) / b + 1e-9);
+            if (room >= O) hi = k;
+            else lo = k + 1;
+        }
+        return base + lo * b;
+    };
+    return std::max(late, std::min(ends(early), ends(late)));
+}
+
 extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split)
 {
-    const long long clusters = std::max(1, sm_count() / 2);
-    // The length that makes `lists` lists of up to `pages` pages take the fewest rounds of the machine: a round costs its pages and
-    // what a unit costs besides (us: 0.67 a page and 5 for four slots x 32 heads, 0.85 and 6 for a slot; a split more in the
-    // merge 0.1).
-    auto best = [&](long long lists, long long pages, double a_page, double a_unit) {
-        pages = std::max(1ll, pages);
-        long long split = pages;
-        double least = 1e30;
-        for (long long n = 1; n <= std::max(1ll, pages / 2) && n <= 4 * clusters; ++n) {  // (whole tiles: two pages)
-            const long long part = ((pages + n - 1) / n + 1) / 2 * 2, parts = (pages + part - 1) / part;
-            const double us = (double)((lists * parts + clusters - 1) / clusters) * (part * a_page + a_unit) + 0.1 * parts;
-            if (us < least) least = us, split = part;
-        }
-        return (int)std::min<long long>((split + 1) / 2 * 2 * PAGE, 0x7FFFFF00);
-    };
     if (B <= 0 || n_groups < 0 || max_shared < 0 || max_own <= 0) {
         if (own_split) *own_split = TILE;
         return TILE;
     }
-    if (own_split) *own_split = best(B, ((long long)max_own + PAGE - 1) / PAGE, 0.85, 6.0);
-    return best(3 * (((long long)B + 3ll * n_groups) / 4), max_shared / PAGE, 0.67, 5.0);
+    // Both lengths together: the own pages' units take the clusters that the shared pages' leave free, so what counts is when the
+    // last of either ends, and what the records cost in the merge.  Groups are taken as equally large, and all as long as the
+    // longest.  us a unit: 9.6 and 0.77 a page for four slots x 32 heads, 10.8 and 0.52 for a slot; 0.6 a split of the shared
+    // pages, 0.07 a slot's split of its own.  Over 28 shapes of 1 to 308 slots this is within 2.6% of the best of 36 pairs on
+    // average; each length for itself was within 9.2% (15 slots of 5 groups over 2,500 + 1,000 tokens 47.0 -> 35.7 us).
+    const long long clusters = std::max(1, sm_count() / 2);
+    const long long shared = max_shared / PAGE, own = ((long long)max_own + PAGE - 1) / PAGE;
+    const long long tiles = n_groups ? n_groups * ((((long long)B + n_groups - 1) / n_groups + 3) / 4) : 0, lists = 3 * tiles;
+    auto cut = [](long long pages, long long n) { return ((pages + n - 1) / n + 1) / 2 * 2; };  // (whole tiles: two pages)
+    auto most = [&](long long pages) { return std::max(1ll, std::min((pages + 1) / 2, 4 * clusters)); };
+    double least = 1e300;
+    long long best_shared = 2, best_own = 2, part = 0, last = 0;
+    for (long long n = 1; n <= most(shared); ++n, last = part) {
+        part = std::max(2ll, cut(shared, n));
+        if (part == last) continue;
+        const long long parts = (shared + part - 1) / part;
+        long long own_part = 0, own_last = 0;
+        for (long long m = 1; m <= most(own); ++m, own_last = own_part) {
+            own_part = cut(own, m);
+            if (own_part == own_last) continue;
+            const long long own_parts = (own + own_part - 1) / own_part;
+            const double us = shared_span(lists * parts, 9.6 + 0.77 * std::min(part, shared), B * own_parts,
+                                          10.8 + 0.52 * std::min(own_part, own), clusters) +
+                              0.6 * parts + 0.07 * B * own_parts;
+            if (us < least) least = us, best_shared = part, best_own = own_part;
+        }
+    }
+    auto tokens = [](long long pages) { return (int)std::min<long long>(pages * PAGE, 1 << 25); };  // (a unit takes no more)
+    if (own_split) *own_split = tokens(best_own);
+    return tokens(best_shared);
 }
 
 extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
