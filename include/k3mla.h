@@ -466,7 +466,8 @@ int k3mla_quant_copy_pages(uint8_t* dst_slab, int dst_n_pages, const uint8_t* sr
 /* k3mla_quant_decode: k3mla_window_decode over the 8-bit cache, one token row per slot: the same attention (window >=
  * max_ctx: the whole context) over the rows that the cache stands for, the same splits, arguments, refusals and treatment of
  * empty slots, -1 entries, unseen tokens and non-finite values.  slab 128-byte aligned.
- * k3mla_quant_split_tokens plans a split length as k3mla_window_split_tokens does. */
+ * k3mla_quant_split_tokens plans a split length, as k3mla_window_split_tokens does but for these kernels: the fewest rounds
+ * of the SMs, with what a split costs. */
 size_t k3mla_quant_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);
 int k3mla_quant_split_tokens(int B, int max_ctx, int window, int n_sink);
 int k3mla_quant_decode(const uint16_t* q_abs, const uint8_t* slab, int n_pages, int n_layers, int layer,
