@@ -92,6 +92,8 @@ constexpr int QD_THREADS = 384;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
 constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
 constexpr float QD_TAU = 7.f;                   // a reference moves when a row passes it by more than 2^TAU
+constexpr float QD_BIG = 1048576.f;             // references this large are rounded by so much that s less the reference has to be
+                                                // taken from the rounded s + k that it is one of, or none may come near it
 constexpr float QD_UP = 2.f;                    // p times its row's power of two comes to at most QD_UP 2^TAU = 256
 constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
@@ -484,6 +486,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     float l[QD_MINE];
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) l[h] = 0.f;
+    bool big = false;   // a reference of this group's heads is QD_BIG or more
     bool dead = false;  // a wait ran out: this warp only goes on to where the four can leave together
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
@@ -522,6 +525,13 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
                 f32x2_parts(fma_f32x2(f32x2(u[h], u[h + 1]), f32x2(c, c), f32x2(m.x, m.y)), x[h], x[h + 1]);
                 f32x2_parts(fma_f32x2(f32x2(u[h + 2], u[h + 3]), f32x2(c, c), f32x2(m.z, m.w)), x[h + 2], x[h + 3]);
             }
+            if (big) {
+#pragma unroll
+                for (int h = 0; h < QD_MINE; ++h) {
+                    const float m = sm.m_neg[h0 + h];
+                    if (fabsf(m) >= QD_BIG) x[h] = (fmaf(u[h], c, k) + m) - k;
+                }
+            }
         };
         arguments();
         float m4[4] = {x[0], x[1], x[2], x[3]};
@@ -532,6 +542,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         if (named_bar_any(QB_GROUP + group, 128, dead || i == 0 || (seen && !(most <= QD_TAU - k)))) {
             if (named_bar_any(QB_GROUP + group, 128, dead)) return;
             dead = !qd_move(sm, p, u, l, c, k, seen, tbase, quarter, group, i);
+            big = __any_sync(0xFFFFFFFFu, lane < QD_MINE && fabsf(sm.m_neg[h0 + min(lane, QD_MINE - 1)]) >= QD_BIG);
             arguments();
         }
         if (!whole) {
@@ -619,17 +630,17 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         for (int h = 0; h < QD_MINE; ++h)
             o[h] = fmaf(__uint_as_float(v[QD_MINE + h]), 1.f / QD_LOW, __uint_as_float(v[h]));
     };
-    float o[2][QD_MINE], big[QD_MINE];
+    float o[2][QD_MINE], top[QD_MINE];
 #pragma unroll
     for (int d = 3; d >= 0; --d) {
         load(d, o[d & 1]);
 #pragma unroll
-        for (int h = 0; h < QD_MINE; ++h) big[h] = d == 3 ? fabsf(o[1][h]) : fmaxf(big[h], fabsf(o[d & 1][h]));
+        for (int h = 0; h < QD_MINE; ++h) top[h] = d == 3 ? fabsf(o[1][h]) : fmaxf(top[h], fabsf(o[d & 1][h]));
     }
     uint32_t most = 0;
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) {
-        const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big[h]));
+        const uint32_t v = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top[h]));
         if (lane == h) most = v;
     }
     named_bar(QB_GROUP + group, 128);  // the sums have been read

@@ -106,7 +106,8 @@ def out_tolerance(q_abs, out, o, p, rows, scales, w_kv_b, scale):
         largest of them comes to 2 at least (the reference is one of them, and they are taken to 2 at the reference):
         1.25 * 2^-16 of it;
       * q to a sum of two e4m3 numbers likewise: exact for entries above 2^-14 of the largest of all heads, as a bf16 has 8
-        bits, else within 2^-15 where the largest comes to 2^7 at least: 2^-22 of it;
+        bits, else within 2^-15, and half the step of the f16 it goes through (2^-24 at 2^-8 of it: 2^-17), where the largest
+        comes to 2^7 at least: 1.25 * 2^-22 of it;
       * o_lat, and the O of each split, to f16 after a power of two (2^-12 of the entry or 2^-25 of the row's largest);
       * the output to bf16 (2^-8);
       * f32 sums besides: each score within 640 * 2^-24 of sum |q||row| * scale, the hardware exponential 2^-21, the sums
@@ -116,7 +117,7 @@ def out_tolerance(q_abs, out, o, p, rows, scales, w_kv_b, scale):
     if p.shape[1] == 0:
         return np.zeros_like(out)
     q = np.abs(np.asarray(q_abs, np.float64))
-    ds = scale * (640 * 2.0 ** -24 * q @ np.abs(rows).T + 2.0 ** -22 * q[:, :LORA].max() * np.abs(rows[:, :LORA]).sum(-1))
+    ds = scale * (640 * 2.0 ** -24 * q @ np.abs(rows).T + 1.25 * 2.0 ** -22 * q[:, :LORA].max() * np.abs(rows[:, :LORA]).sum(-1))
     size = p * scales
     d = p * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -19 + ds) + 1.25 * 2.0 ** -16 * size.max(-1, keepdims=True) / scales
     c = np.abs(rows[:, :LORA])

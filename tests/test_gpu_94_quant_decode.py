@@ -214,6 +214,39 @@ def test_a_slot_does_not_depend_on_its_batch(gpu_lib):
     assert torch.equal(c.run(k3, max_ctx=4500, slots=order), whole[order])
 
 
+def test_every_way_to_add_splits_up_gives_the_same_bits(gpu_lib):
+    """One slot in one split apart, the sums of a slot's splits are taken by the expansion (few slots) or by a kernel before it,
+    a warp or four a row, up to four records at once or in turn."""
+    k3 = gpu_lib
+    g = np.random.default_rng(14)
+    ctx = [int(x) for x in g.integers(1, 1500, 20)]
+    ctx[:3] = [512, 385, 1500]
+    c = Case(ctx, seed=14).stale()
+    whole = c.run(k3, split=128, max_ctx=1500)
+    c.check(whole)
+    for slots in (list(range(16)), [2, 0, 19, 7, 11], [4, 2, 1], [2]):
+        assert torch.equal(c.run(k3, split=128, max_ctx=1500, slots=slots), whole[slots]), slots
+    few = [b for b in range(20) if ctx[b] <= 512]
+    many = (few * 20)[:17]
+    assert torch.equal(c.run(k3, split=128, max_ctx=512, slots=many), whole[many])
+    assert torch.equal(c.run(k3, split=128, max_ctx=512, slots=many[:9]), whole[many[:9]])
+
+
+@pytest.mark.parametrize("exponent", [-130, -40, 0, 30])
+def test_queries_of_very_different_sizes(gpu_lib, exponent):
+    """Heads 2^-18 to 2^18 apart, the entries of a head too, about 2^exponent (bf16's smallest among them)."""
+    c = Case([70, 260], seed=15)
+    g = np.random.default_rng(15)
+    q = g.standard_normal((2, H, ROW)) * 2.0 ** (exponent + g.uniform(-9, 9, (2, H, 1)) + g.uniform(-9, 9, (2, H, ROW)))
+    c.q = torch.from_numpy(q.astype(np.float32)).cuda().bfloat16()
+    c.check(c.run(gpu_lib))
+
+
+def test_planned_splits(gpu_lib):
+    c = Case([900, 1, 400, 130, 257, 64] * 3, seed=16)
+    c.check(c.run(gpu_lib, split=gpu_lib.quant_split_tokens(18, 900, MOST)))
+
+
 def test_captured_and_replayed_with_new_lengths_on_another_stream(gpu_lib):
     k3 = gpu_lib
     c = Case([500, 130, 64, 0], seed=14).stale()
