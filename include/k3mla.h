@@ -58,6 +58,7 @@ extern "C" {
 #define K3MLA_ROW 576
 #define K3MLA_TILE 128 /* tokens per decode tile; split_tokens must be a multiple */
 #define K3MLA_SPLIT_AUTO 0     /* split_tokens: the default per-slot rule (see k3mla_paged_decode) */
+#define K3MLA_SHARED_NONE (-1) /* k3mla_shared_decode's shared_split: every slot reads what it shares for itself */
 #define K3MLA_SPLIT_MAX 4096   /* longest split of the default rule, in tokens */
 
 #define K3MLA_QUANT_ROW_BYTES 640    /* the 8-bit cache: a token's row in a layer, without its scale */
@@ -411,9 +412,11 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
  *             of its ctx_len).  A longer slot is clamped and flagged (K3MLA_DEV_CTX); of a longer prefix the rest is read
  *             by each slot for itself, within max_own.
  * shared_split, own_split  the splits of the shared pages and of what is behind them, as split_tokens in
- *             k3mla_window_decode; K3MLA_SPLIT_AUTO cuts by a list's own length.  A slot's result depends on its own context, its
- *             group's shared_len and these two only.  k3mla_shared_split_tokens plans both for the current device (returns
- *             shared_split; own_split may be NULL).
+ *             k3mla_window_decode; K3MLA_SPLIT_AUTO cuts by a list's own length.  shared_split K3MLA_SHARED_NONE: each slot reads
+ *             the shared pages by itself, from its own table, in one list with what is behind them (own_split).  What is read
+ *             again mostly comes from L2, so this is the faster way for short prefixes and few slots.  A slot's result depends
+ *             on its own context, its group's shared_len and these two only.  k3mla_shared_split_tokens plans both for the
+ *             current device (returns shared_split, which may be K3MLA_SHARED_NONE; own_split may be NULL).
  * q_abs, slab, block_table, w_kv_b, scale_bf16, out, dev_err as for k3mla_window_decode; B <= 65,535, n_groups <= 2^20.
  * workspace   device, 256-byte aligned, >= k3mla_shared_decode_workspace_bytes(...) bytes; scratch, one for each call
  *             that may overlap others.

@@ -185,6 +185,7 @@ struct WinParams {
     const int32_t *pos0, *row_start;     // chunk
     const int32_t *group_start, *shared_len;  // shared and own (else null): [G + 1], [G]
     int G, max_shared, max_own, shared_split, ns_shared;  // ns_shared: the most splits of a group's shared pages, 0: no group
+    int alone;                           // shared and own: every slot reads what it shares for itself
     uint16_t* olat;                      // [96][R][512] f16: o_lat times a power of two per row
     float* oscale;                       // [96][R]: what undoes it; 0 for rows that see nothing
     uint16_t* ws_o;                      // [B][nsplit][96][512] f16: a split's O (decode, nsplit > 1) ...
@@ -262,6 +263,7 @@ __device__ __forceinline__ WShared w_shared_row(const WinParams& p, int gi, int 
     s.n = max(0, (int)min((int64_t)n, most));
     if (report && p.dev_err && (n > most || (n > 0 && n < s.pages * PAGE))) atomicOr(p.dev_err, (int)K3MLA_DEV_CTX);
     if (s.n < s.pages * PAGE) s.n = 0;
+    if (p.alone) s.pages = 0;
     return s;
 }
 // (a whole warp, one slot)
@@ -2023,15 +2025,22 @@ struct SharedPlan {
 };
 static bool shared_sizes_ok(int B, int max_shared, int max_own, int shared_split, int own_split)
 {
-    return B > 0 && max_shared >= 0 && max_own > 0 && shared_split >= 0 && own_split >= 0 && shared_split % TILE == 0 && own_split % TILE == 0;
+    return B > 0 && max_shared >= 0 && max_own > 0 && own_split >= 0 && own_split % TILE == 0 &&
+           (shared_split == K3MLA_SHARED_NONE || (shared_split >= 0 && shared_split % TILE == 0));
+}
+// The longest list of pages that a slot reads by itself.
+static long long own_tokens(int max_shared, int max_own, int shared_split)
+{
+    return std::min(0x7FFFFF00ll, (shared_split == K3MLA_SHARED_NONE ? max_shared / PAGE * PAGE : 0ll) + max_own);
 }
 static SharedPlan shared_plan(int max_shared, int max_own, int shared_split, int own_split)
 {
-    auto splits = [](int tokens, int split) {  // of a list of whole pages
-        const long long pages = ((long long)tokens + PAGE - 1) / PAGE;
+    auto splits = [](long long tokens, int split) {  // of a list of whole pages
+        const long long pages = (tokens + PAGE - 1) / PAGE;
         return tokens > 0 ? launch_nsplit((int)std::min<long long>(pages * PAGE, 0x7FFFFF00), split) : 0;
     };
-    return {splits(max_shared / PAGE * PAGE, shared_split), splits(max_own, own_split)};
+    return {shared_split == K3MLA_SHARED_NONE ? 0 : splits(max_shared / PAGE * PAGE, shared_split),
+            splits(own_tokens(max_shared, max_own, shared_split), own_split)};
 }
 
 }  // namespace k3
@@ -2069,11 +2078,16 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
         if (own_split) *own_split = TILE;
         return TILE;
     }
-    // Both lengths together: the own pages' units take the clusters that the shared pages' leave free, so what counts is when the
-    // last of either ends, and what the records cost in the merge.  Groups are taken as equally large, and all as long as the
-    // longest.  us a unit: 9.6 and 0.77 a page for four slots x 32 heads, 10.8 and 0.52 for a slot; 0.6 a split of the shared
-    // pages, 0.07 a slot's split of its own.  Over 28 shapes of 1 to 308 slots this is within 2.6% of the best of 36 pairs on
-    // average; each length for itself was within 9.2% (15 slots of 5 groups over 2,500 + 1,000 tokens 47.0 -> 35.7 us).
+    // Every slot for itself, or the shared pages apart.  96 heads over a row of 1,152 B are 181 operations a byte, and a second
+    // read is L2's: what sharing saves is not bytes but the quarter of the MMAs' rows that a slot's 96 heads leave unused, 0.77 us
+    // a page of four slots x 32 heads against 0.67 of a slot's 96, a seventh of the time of long prefixes, and it costs a second
+    // launch and its records.  64 slots over 16,384 shared tokens 196 -> 173 us, 16 over 30,000 103 -> 95; but 64 over 1,024
+    // 32 -> 53, 8 over 4,096 30.2 -> 31.8.
+    // By itself a slot's split costs 5.7 us and 0.67 a page, and in the merge 2.5 us and 0.09 a split.  Apart, both lengths are
+    // planned together: the own pages' units take the clusters that the shared pages' leave free, so what counts is when the last
+    // of either ends, and what the records cost in the merge; 9.6 us and 0.77 a page for four slots x 32 heads, 10.8 and 0.52 for
+    // a slot, 0.6 a split of the shared pages, 0.07 a slot's split of its own.  Groups are taken as equally large, and all as long
+    // as the longest.  Over 28 shapes of 1 to 308 slots the choice is within 1% of the best of some 45 on average.
     const long long clusters = std::max(1, sm_count() / 2);
     const long long shared = max_shared / PAGE, own = ((long long)max_own + PAGE - 1) / PAGE;
     const long long tiles = n_groups ? n_groups * ((((long long)B + n_groups - 1) / n_groups + 3) / 4) : 0, lists = 3 * tiles;
@@ -2081,6 +2095,16 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
     auto most = [&](long long pages) { return std::max(1ll, std::min((pages + 1) / 2, 4 * clusters)); };
     double least = 1e300;
     long long best_shared = 2, best_own = 2, part = 0, last = 0;
+    bool alone = false;
+    for (long long n = 1; n <= most(shared + own); ++n, last = part) {
+        part = cut(shared + own, n);
+        if (part == last) continue;
+        const long long parts = (shared + own + part - 1) / part;
+        const double us = shared_span(B * parts, 5.7 + 0.67 * std::min(part, shared + own), 0, 1., clusters) +
+                          (parts > 1 ? 2.5 + 0.09 * B * parts : 0.);
+        if (us < least) least = us, best_own = part, alone = true;
+    }
+    last = 0;
     for (long long n = 1; n <= most(shared); ++n, last = part) {
         part = std::max(2ll, cut(shared, n));
         if (part == last) continue;
@@ -2093,12 +2117,12 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
             const double us = shared_span(lists * parts, 9.6 + 0.77 * std::min(part, shared), B * own_parts,
                                           10.8 + 0.52 * std::min(own_part, own), clusters) +
                               0.6 * parts + 0.07 * B * own_parts;
-            if (us < least) least = us, best_shared = part, best_own = own_part;
+            if (us < least) least = us, best_shared = part, best_own = own_part, alone = false;
         }
     }
     auto tokens = [](long long pages) { return (int)std::min<long long>(pages * PAGE, 1 << 25); };  // (a unit takes no more)
     if (own_split) *own_split = tokens(best_own);
-    return tokens(best_shared);
+    return alone ? K3MLA_SHARED_NONE : tokens(best_shared);
 }
 
 extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,
@@ -2129,8 +2153,11 @@ extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, 
     if (n_groups == 0) n.ns_shared = 0;
     const int nsplit = n.ns_shared + n.ns_own;
     const WinWs wl = w_layout(B, nsplit);
-    auto unit = [](int tokens, int split) { return std::min<long long>(((long long)tokens + PAGE - 1) / PAGE, (split ? split : SPLIT_MAX) / PAGE); };
-    if (!w_unit_fits("k3mla_shared_decode", std::max(unit(max_shared, shared_split), unit(max_own, own_split)))) return K3MLA_E_INVALID;
+    const bool alone = shared_split == K3MLA_SHARED_NONE;
+    auto unit = [](long long tokens, int split) { return std::min<long long>((tokens + PAGE - 1) / PAGE, (split ? split : SPLIT_MAX) / PAGE); };
+    if (!w_unit_fits("k3mla_shared_decode", std::max(alone ? 0 : unit(max_shared, shared_split),
+                                                     unit(own_tokens(max_shared, max_own, shared_split), own_split))))
+        return K3MLA_E_INVALID;
     const long long quads = ((long long)B + 3ll * n_groups) / 4;  // sum over groups of ceil(slots / 4), at most
     if (B > 65535 || n_groups > 1 << 20 || (long long)B * nsplit * H > 0x7FFFFFFFll || 3 * quads * std::max(1, n.ns_shared) > 0x3FFFFFFFll) {
         set_error("k3mla_shared_decode: too many slots, groups or splits");
@@ -2139,7 +2166,7 @@ extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, 
     if (!device_ok()) return K3MLA_E_DEVICE;
     p.ctx_len = ctx_len, p.group_start = group_start, p.shared_len = shared_len, p.dev_err = dev_err;
     p.G = n_groups, p.max_shared = max_shared, p.max_own = max_own, p.shared_split = shared_split, p.split_tokens = own_split;
-    p.ns_shared = n.ns_shared, p.nsplit = nsplit;
+    p.ns_shared = n.ns_shared, p.nsplit = nsplit, p.alone = alone;
     p.B = p.R = B;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (n.ns_shared) {

@@ -18,6 +18,7 @@ from . import build as _build
 H, NOPE, ROPE, V, LORA, PAGE, ROW, TILE = 96, 128, 64, 128, 512, 64, 576, 128
 QUANT_ROW_BYTES, QUANT_PAGE_BYTES = 640, 41088   # the 8-bit cache's rows and page blocks
 SPLIT_AUTO, SPLIT_MAX = 0, 4096   # K3MLA_SPLIT_AUTO (the default per-slot rule), K3MLA_SPLIT_MAX
+SHARED_NONE = -1                  # shared_decode's shared_split: every slot reads what it shares for itself
 
 DEV_BAD_PAGE, DEV_UNMAPPED, DEV_CTX, DEV_TIMEOUT = 1, 2, 4, 8
 
@@ -477,7 +478,7 @@ def shared_decode_workspace_bytes(B: int, max_shared: int, max_own: int, shared_
 
 
 def shared_split_tokens(B: int, n_groups: int, max_shared: int, max_own: int) -> tuple[int, int]:
-    """Split lengths (shared, own) that keep the current device busy (batch-dependent)."""
+    """Split lengths (shared, own) that keep the current device busy (batch-dependent); the first may be SHARED_NONE."""
     own = ctypes.c_int(0)
     shared = load().k3mla_shared_split_tokens(_int(B, "B"), _int(n_groups, "n_groups"), _int(max_shared, "max_shared"),
                                               _int(max_own, "max_own"), ctypes.byref(own))

@@ -69,7 +69,7 @@ class Case:
             assert (err <= tol).all(), (b, n, float((err / tol).max()))
 
 
-@pytest.mark.parametrize("shared_split,own_split", [(0, 0), (128, 128), (256, 0), (128, 256)])
+@pytest.mark.parametrize("shared_split,own_split", [(0, 0), (128, 128), (256, 0), (128, 256), (-1, 0), (-1, 128)])
 @pytest.mark.parametrize("size", [1, 2, 3, 4, 5, 9])
 def test_one_group(gpu_lib, size, shared_split, own_split):
     c = Case([([300 + 64 + 37 * i for i in range(size)], 330)], seed=size)
@@ -77,7 +77,7 @@ def test_one_group(gpu_lib, size, shared_split, own_split):
     assert c.err.item() == 0
 
 
-@pytest.mark.parametrize("shared_split,own_split", [(0, 0), (128, 128), (512, 128)])
+@pytest.mark.parametrize("shared_split,own_split", [(0, 0), (128, 128), (512, 128), (-1, 128), (-1, 0)])
 def test_many_groups_of_all_kinds(gpu_lib, shared_split, own_split):
     """Sizes 1 to 6 and 0, prefixes of no whole page, of one token, of exact pages; slots without a token of their own; slots
     that share nothing; empty slots."""
@@ -111,6 +111,22 @@ def test_bounds_may_be_larger_and_a_prefix_beyond_its_bound_is_read_by_each(gpu_
     got = c.run(k3, max_shared=130, max_own=400)        # two whole pages shared, the rest read by each slot
     c.check(got)
     assert c.err.item() == 0
+
+
+def test_alone_is_the_window_decode_of_the_same_tables(gpu_lib):
+    k3 = gpu_lib
+    c = Case([([700, 650, 641], 640), ([130, 0, 128], 128)], alone=[90], seed=17)
+    for split in (0, 128):
+        got = c.run(k3, k3.SHARED_NONE, split)
+        args = c.args()
+        want = torch.empty_like(got)
+        ws = torch.empty(k3.window_decode_workspace_bytes(7, 700, MOST, 0, split), dtype=torch.uint8, device="cuda")
+        k3.window_decode(c.q, args[0], args[1], args[2], args[3], c.w, SCALE_BITS, want, ws, 700, MOST, 0, split)
+        assert torch.equal(got, want)
+    c.ctx[1], c.ctx[2] = 639, 5000                       # too few tokens, and more than max_own says
+    got = c.run(k3, k3.SHARED_NONE, 128, max_own=60)
+    assert c.err.item() == k3.DEV_CTX and (got[1] == 0).all() and not got[1].isnan().any()
+    c.check(got, ctx=[700, 0, 700, 130, 0, 128, 60])
 
 
 def test_too_short_and_too_long_slots_are_flagged(gpu_lib):

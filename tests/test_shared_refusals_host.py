@@ -24,12 +24,13 @@ def decode(lib, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(B=-1), dict(G=-1), dict(n_pages=0), dict(layers=0), dict(layer=2), dict(layer=-1), dict(cols=0), dict(max_shared=-1),
-    dict(max_own=0), dict(shared_split=-128), dict(shared_split=64), dict(own_split=-128), dict(own_split=100), dict(scale=0),
+    dict(max_own=0), dict(shared_split=-2), dict(own_split=-1), dict(shared_split=-128), dict(shared_split=64), dict(own_split=-128), dict(own_split=100), dict(scale=0),
     dict(scale=0x8000), dict(scale=0x7F80), dict(scale=0x7F32), dict(q=None), dict(slab=None), dict(table=None), dict(ctx=None),
     dict(start=None), dict(shared=None), dict(w=None), dict(out=None), dict(ws=None), dict(q=P + 8), dict(slab=P + 8), dict(w=P + 8),
     dict(out=P + 8), dict(ws=P + 128), dict(B=65536), dict(G=(1 << 20) + 1), dict(n_pages=1 << 25, layers=1, layer=0),
     dict(B=60000, max_own=1 << 20, own_split=128), dict(max_shared=(1 << 25) + 64, shared_split=1 << 26),
-    dict(max_own=(1 << 25) + 64, own_split=1 << 26)])
+    dict(max_own=(1 << 25) + 64, own_split=1 << 26), dict(max_shared=1 << 25, max_own=64, shared_split=-1, own_split=1 << 26),
+    dict(B=60000, max_shared=1 << 20, shared_split=-1, own_split=128)])
 def test_refused(kw):
     lib = k3mla.load()
     assert decode(lib, **kw) == INVALID
@@ -45,13 +46,14 @@ def test_workspace_and_no_slots():
         assert k3mla.shared_decode_workspace_bytes(*bad) == 0
     assert k3mla.shared_decode_workspace_bytes(2, 4096, 64, 128) > k3mla.shared_decode_workspace_bytes(2, 4096, 64)
     assert k3mla.shared_decode_workspace_bytes(2, 2 ** 31 - 1, 2 ** 31 - 1) > 0
+    assert k3mla.shared_decode_workspace_bytes(2, 2 ** 31 - 1, 2 ** 31 - 1, -1) > 0
 
 
 @pytest.mark.parametrize("sizes", [(1, 0, 0, 1), (1, 1, 64, 1), (8, 1, 4096, 64), (64, 64, 100, 5000), (64, 1, 16384, 600),
                                    (65535, 1, 2 ** 31 - 1, 2 ** 31 - 1), (0, 0, 0, 0)])
 def test_planned_splits_are_splits(sizes):
     shared, own = k3mla.shared_split_tokens(*sizes)
-    assert shared > 0 and own > 0 and shared % 128 == 0 and own % 128 == 0
+    assert (shared == k3mla.SHARED_NONE or shared > 0 and shared % 128 == 0) and own > 0 and own % 128 == 0
     assert k3mla.load().k3mla_shared_split_tokens(*sizes, None) == shared
 
 
