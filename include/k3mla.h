@@ -405,8 +405,8 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
  * and read once for four slots at a time instead of once for each slot.
  * group_start [n_groups + 1] (non-decreasing, within [0, B]): slots group_start[g] .. group_start[g + 1] - 1 are group g's;
  *             slots outside every group, or in one of shared_len 0, attend by themselves
- * shared_len  [n_groups] (NULL for none): tokens that the slots of group g share.  Whole pages of them are read as shared; what is left of a
- *             last page, like everything behind, comes from each slot's own table.  Tables are not compared.
+ * shared_len  [n_groups] (NULL for none): tokens that the slots of group g share.  Whole pages of them are read as shared; what
+ *             is left of a last page, like everything behind, comes from each slot's own table.  Tables are not compared.
  * ctx_len     [B]: 0 or less (zeros), or at least 64 * (shared_len / 64); K3MLA_DEV_CTX and zeros for a slot with fewer
  * max_shared, max_own  upper bounds of shared_len and of what a slot holds behind its group's whole shared pages (in no group:
  *             of its ctx_len).  A longer slot is clamped and flagged (K3MLA_DEV_CTX); of a longer prefix the rest is read
@@ -420,7 +420,9 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
  * q_abs, slab, block_table, w_kv_b, scale_bf16, out, dev_err as for k3mla_window_decode; B <= 65,535, n_groups <= 2^20.
  * workspace   device, 256-byte aligned, >= k3mla_shared_decode_workspace_bytes(...) bytes; scratch, one for each call
  *             that may overlap others.
- * Two to four kernels on `stream`, reading nothing but w_kv_b before the kernel ahead of the call has completed: w_kv_b must not be written by the kernel immediately before this call. */
+ * Scores of magnitude 2^30 and more may give NaN, as in k3mla_window_decode: an f32 of that size has steps of 64.
+ * Two to four kernels on `stream`, reading nothing but w_kv_b before the kernel ahead of the call has completed: w_kv_b must
+ * not be written by the kernel immediately before this call. */
 size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int max_own, int shared_split, int own_split);
 int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split);
 int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, int n_pages, int n_layers, int layer,

@@ -25,6 +25,7 @@
 // CTAs of the grid, a warp each.
 // Measured, device time in a graph of calls: 5,251 rows of 16 chunks 61.8 us (6.5 TB/s, 95 % of the copy rate); 64 rows of
 // 64 slots 3.6 us, one row 2.9 us.  Called from Python, one row takes 22 us and 64 rows 26: the host's time.
+// Into the 8-bit cache (a warp's row maximum besides, and 642 B written instead of 1,152): 5,251 rows 61.1 us, one row 3.2 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

