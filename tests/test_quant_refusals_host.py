@@ -47,8 +47,8 @@ def test_decode_wants_its_workspace_and_does_nothing_for_no_slots():
     assert k3mla.quant_split_tokens(1, 32768, 1 << 30) % 128 == 0
 
 
-@pytest.mark.parametrize("sizes", [(1, 1, 1, 0), (5, 500, 500, 0), (40, 30000, 1 << 30, 0), (90, 30000, 4096, 64), (65535, 1 << 30, 1 << 30, 5),
-                                   (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("sizes", [(1, 1, 1, 0), (5, 500, 500, 0), (40, 30000, 1 << 30, 0), (90, 30000, 4096, 64),
+                                   (65535, 1 << 30, 1 << 30, 5), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1)])
 def test_planned_splits_are_splits(sizes):
     split = k3mla.quant_split_tokens(*sizes)
     assert split > 0 and split % 128 == 0 and (sizes[0] <= 4 or split <= 1 << 25)

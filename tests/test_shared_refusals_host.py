@@ -24,7 +24,8 @@ def decode(lib, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(B=-1), dict(G=-1), dict(n_pages=0), dict(layers=0), dict(layer=2), dict(layer=-1), dict(cols=0), dict(max_shared=-1),
-    dict(max_own=0), dict(shared_split=-2), dict(own_split=-1), dict(shared_split=-128), dict(shared_split=64), dict(own_split=-128), dict(own_split=100), dict(scale=0),
+    dict(max_own=0), dict(shared_split=-2), dict(own_split=-1), dict(shared_split=-128),
+    dict(shared_split=64), dict(own_split=-128), dict(own_split=100), dict(scale=0),
     dict(scale=0x8000), dict(scale=0x7F80), dict(scale=0x7F32), dict(q=None), dict(slab=None), dict(table=None), dict(ctx=None),
     dict(start=None), dict(shared=None), dict(w=None), dict(out=None), dict(ws=None), dict(q=P + 8), dict(slab=P + 8), dict(w=P + 8),
     dict(out=P + 8), dict(ws=P + 128), dict(B=65536), dict(G=(1 << 20) + 1), dict(n_pages=1 << 25, layers=1, layer=0),
