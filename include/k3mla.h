@@ -473,8 +473,8 @@ int k3mla_quant_copy_pages(uint8_t* dst_slab, int dst_n_pages, const uint8_t* sr
  * empty slots, -1 entries, unseen tokens and non-finite values.  slab 128-byte aligned.  Latent entries of the queries below
  * 2^-14 of the largest among a slot's heads 0 .. 47 (or 48 .. 95) are rounded to 2^-22 of it; a p to 2^-8 of itself, or to
  * 2^-16 of the slot's largest where that is more.
- * k3mla_quant_split_tokens plans a split length, as k3mla_window_split_tokens does but for these kernels: the fewest rounds
- * of the SMs, with what a split costs. */
+ * k3mla_quant_split_tokens plans a split length, as k3mla_window_split_tokens does but for these kernels: the one with which
+ * the last split ends first, on the current device. */
 size_t k3mla_quant_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);
 int k3mla_quant_split_tokens(int B, int max_ctx, int window, int n_sink);
 int k3mla_quant_decode(const uint16_t* q_abs, const uint8_t* slab, int n_pages, int n_layers, int layer,

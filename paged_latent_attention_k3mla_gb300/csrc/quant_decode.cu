@@ -30,7 +30,7 @@
 // chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
 // Measured: 64 slots over 4,096 tokens 69.2 us (190 MB: 2.7 TB/s, 0.40 of the copy rate; 804 TFLOP/s), 64 over 15,000 to
-// 16,384 226.4 us (2.9 TB/s, 924 TFLOP/s, 0.49 of the measured bf16 rate), one over 32,768 27.6 us, 128 of up to 256 tokens
+// 16,384 221.7 us (3.0 TB/s, 943 TFLOP/s, 0.50 of the measured bf16 rate), one over 32,768 27.6 us, 128 of up to 256 tokens
 // 30.0 us.  (The bf16 cache: 64 over 4,096 69 to 72 us.)  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each for
 // 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,200.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it
@@ -715,7 +715,7 @@ __global__ void __launch_bounds__(QD_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     QdSmem& sm = *reinterpret_cast<QdSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int rank = (int)(blockIdx.x & 1u), warp = (int)(threadIdx.x >> 5), unit = (int)(blockIdx.x >> 1);
-    const int b = unit / p.nsplit, s = unit % p.nsplit;
+    const int b = unit % p.B, s = unit / p.B;  // (first splits first: where lists are cut unevenly, the short rests come last)
     if (threadIdx.x == 32 * QW_LOAD) {
         qd_init(sm, p);
         fence_mbarrier_init_cluster();
@@ -767,20 +767,23 @@ extern "C" int k3mla_quant_split_tokens(int B, int max_ctx, int window, int n_si
 {
     // Up to four slots: the expansion adds the splits up, and window.cu's rule is within 3% of the best of up to 22 lengths.
     if (B <= 4 || max_ctx <= 0 || window < 1 || n_sink < 0) return k3mla_window_split_tokens(B, max_ctx, window, n_sink);
-    // More: whole rounds of the SMs, two CTAs a split, at 7.6 us a unit and 1.6 a tile, and 3.3 us and what the records cost for
-    // the merge.  Window.cu's rule, which fills one round, against this one: 10 slots over 500 tokens 21.2 -> 18.4 us, 26 over
-    // 30,000 214 -> 187, 40 over 10,000 145 -> 118 and over 30,000 401 -> 275, 90 over 30,000 797 -> 544; the same for 64 and 128.
+    // More: the length with which the last CTA ends first, two a split, the rests of the lists behind their full splits, at 7.6
+    // us a unit and 1.6 a tile, and 3.3 us and what the records cost for the merge.  Over 120 pairs of 6 to 220 slots and 300 to
+    // 30,000 tokens that is within 0.1% of the best of up to 40 lengths on average.  Window.cu's rule, which fills one round,
+    // against it: 10 slots over 500 tokens 21.2 -> 18.6 us, 26 over 10,000 86 -> 76, 40 over 10,000 145 -> 109 and over 30,000
+    // 401 -> 261, 64 over 4,096 the same and over 30,000 403 -> 367, 90 over 30,000 797 -> 520.
     const long long sms = sm_count(), tiles = (w_max_pages(max_ctx, window, n_sink) * PAGE + TILE - 1) / TILE;
     double least = 1e300;
-    long long split = tiles, last = 0;
-    for (long long n = 1; n <= std::min(tiles, 4 * sms); ++n) {
-        const long long part = (tiles + n - 1) / n, parts = (tiles + part - 1) / part;
-        if (part == last) continue;
-        last = part;
-        const double us = (double)((2ll * B * parts + sms - 1) / sms) * (7.6 + 1.6 * (double)part) +
+    long long split = tiles;
+    auto look = [&](long long part) {
+        const long long parts = (tiles + part - 1) / part, rest = tiles - (parts - 1) * part;
+        if (parts > 4 * sms) return;
+        const double us = units_span(2ll * B * (parts - 1), 7.6 + 1.6 * (double)part, 2ll * B, 7.6 + 1.6 * (double)rest, sms) +
                           (parts > 1 ? 3.3 + (0.21 + 0.025 * B) * (double)parts : 0.);
         if (us < least) least = us, split = part;
-    }
+    };
+    for (long long n = 1; n <= std::min(tiles, 4 * sms); ++n) look((tiles + n - 1) / n);
+    for (long long part = 1, step = 1 + tiles / 1024; part < tiles; part += step) look(part);
     return (int)std::min<long long>(split * TILE, W_UNIT_PAGES * PAGE);  // (a unit takes no more)
 }
 

@@ -2052,26 +2052,6 @@ extern "C" size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int
     return w_layout(B, n.ns_shared + n.ns_own).total;
 }
 
-// When the last of S units of a us, then O units of b us, has ended, each taken by the cluster that is free first.
-static double shared_span(long long S, double a, long long O, double b, long long clusters)
-{
-    const long long q = S / clusters, r = S % clusters;  // r clusters are free after q + 1 rounds, the others after q
-    const double early = q * a, late = r ? early + a : early;
-    auto ends = [&](double base) {
-        long long lo = 0, hi = O;
-        while (lo < hi) {
-            const long long k = (lo + hi) / 2;
-            const double t = base + k * b;
-            long long room = (clusters - r) * (long long)((t - early) / b + 1e-9);
-            if (r && t >= late) room += r * (long long)((t - late) / b + 1e-9);
-            if (room >= O) hi = k;
-            else lo = k + 1;
-        }
-        return base + lo * b;
-    };
-    return std::max(late, std::min(ends(early), ends(late)));
-}
-
 extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split)
 {
     if (B <= 0 || n_groups < 0 || max_shared < 0 || max_own <= 0) {
@@ -2100,7 +2080,7 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
         part = cut(shared + own, n);
         if (part == last) continue;
         const long long parts = (shared + own + part - 1) / part;
-        const double us = shared_span(B * parts, 5.7 + 0.67 * std::min(part, shared + own), 0, 1., clusters) +
+        const double us = units_span(B * parts, 5.7 + 0.67 * std::min(part, shared + own), 0, 1., clusters) +
                           (parts > 1 ? 2.5 + 0.09 * B * parts : 0.);
         if (us < least) least = us, best_own = part, alone = true;
     }
@@ -2114,7 +2094,7 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
             own_part = cut(own, m);
             if (own_part == own_last) continue;
             const long long own_parts = (own + own_part - 1) / own_part;
-            const double us = shared_span(lists * parts, 9.6 + 0.77 * std::min(part, shared), B * own_parts,
+            const double us = units_span(lists * parts, 9.6 + 0.77 * std::min(part, shared), B * own_parts,
                                           10.8 + 0.52 * std::min(own_part, own), clusters) +
                               0.6 * parts + 0.07 * B * own_parts;
             if (us < least) least = us, best_shared = part, best_own = own_part, alone = false;

@@ -87,6 +87,26 @@ inline bool w_scale(uint16_t bits, float* kscale)
     return k <= 3.4028234663852886e38;  // (an infinite factor would make NaN of every score of 0)
 }
 
+// When the last of S units of a us, then O units of b us, has ended, each taken by the first free of `workers`.
+inline double units_span(long long S, double a, long long O, double b, long long workers)
+{
+    const long long q = S / workers, r = S % workers;  // r workers are free after q + 1 rounds, the others after q
+    const double early = q * a, late = r ? early + a : early;
+    auto ends = [&](double base) {
+        long long lo = 0, hi = O;
+        while (lo < hi) {
+            const long long k = (lo + hi) / 2;
+            const double t = base + k * b;
+            long long room = (workers - r) * (long long)((t - early) / b + 1e-9);
+            if (r && t >= late) room += r * (long long)((t - late) / b + 1e-9);
+            if (room >= O) hi = k;
+            else lo = k + 1;
+        }
+        return base + lo * b;
+    };
+    return std::max(late, std::min(ends(early), ends(late)));
+}
+
 // A unit's pages take up to 0.85 us each, and its write-out waits for all of them within WAIT_NS: half of that is allowed.
 constexpr long long W_UNIT_PAGES = 1 << 19;
 
