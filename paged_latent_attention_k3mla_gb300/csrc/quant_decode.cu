@@ -26,12 +26,11 @@
 //
 // Structure of a CTA: eight softmax warps (a quarter of the tile's tokens x 24 heads each: a lane has a token, so a row's scale,
 // mask and sums of exp are the thread's own, and what meets every tile is one vote of four warps whether a reference has to
-// move), and one warp each that loads, issues S, issues PV, and prefetches pages into L2.  A tile is two pages; its five
+// move), and one warp each that loads, issues S and issues PV.  A tile is two pages; its five
 // chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
-// Measured: 64 slots over 4,096 tokens 69.2 us (190 MB: 2.7 TB/s, 0.40 of the copy rate; 804 TFLOP/s), 64 over 15,000 to
-// 16,384 221.7 us (3.0 TB/s, 943 TFLOP/s, 0.50 of the measured bf16 rate), one over 32,768 27.6 us, 128 of up to 256 tokens
-// 30.0 us.  (The bf16 cache: 64 over 4,096 69 to 72 us.)  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each for
+// Measured: 64 slots of up to 4,096 tokens 68.5 us (190 MB: 2.8 TB/s, 0.41 of the copy rate; 811 TFLOP/s), 64 of 15,000 to
+// 16,384 214.9 us (3.1 TB/s, 975 TFLOP/s, 0.51 of the measured bf16 rate), one of 32,768 27.6 us, 128 of up to 256 30.0 us.  (The bf16 cache: 64 over 4,096 69 to 72 us.)  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each for
 // 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,200.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it
 // frees (1,000), the last scores (600) and the softmax (1,700) of every second tile stand in one chain; the tensor pipe is 43%
@@ -117,9 +116,12 @@ constexpr int QD_CHUNKS = 5;
 constexpr int QD_RING = 9;                      // (what fits; a tenth chunk would wait for the same second contraction)
 constexpr int QD_QCHUNK = QD_PAIRS * 128;       // 128 dims of the queries' pairs
 constexpr int QD_SOFTMAX = 8;                   // warps 0 .. 7: quarter of the tile's tokens w & 3, group of the heads w >> 2
-constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10, QW_AHEAD = 11;
-constexpr int QD_THREADS = 384;
+constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10;
+constexpr int QD_THREADS = 352;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
+// A tile's pages, one each of the two CTAs, are fetched into L2 this many tiles before its scores.  64 slots x 4,096 tokens, by a
+// warp of its own: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6, without 73.9; by softmax warp 0, this many: 69.3.
+constexpr int QD_AHEAD = 3;
 constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
 constexpr float QD_TAU = 7.f;                   // a reference moves when a row passes it by more than 2^TAU
 constexpr float QD_BIG = 1048576.f;             // references this large are rounded by so much that s less the reference has to be
@@ -143,7 +145,6 @@ struct __align__(1024) QdSmem {
     float part[4][QD_HEADS];          // a quarter's maxima or sums
     uint32_t most[QD_SOFTMAX][2];     // the prologue's maxima by warp: latents, rope
     uint32_t tmem_base;
-    int32_t tiles_done;               // tiles whose second contraction has been issued
     int32_t abort_flag;
     uint64_t wait_ns;
 };
@@ -160,7 +161,6 @@ __device__ __forceinline__ void qd_init(QdSmem& sm, const QdParams& p)
 {
     sm.wait_ns = p.wait_ns;
     sm.abort_flag = 0;
-    sm.tiles_done = 0;
 #pragma unroll 1
     for (int i = 0; i < QD_RING; ++i) {
         mbar_init(&sm.full[i], 1);
@@ -279,26 +279,10 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
                 umma_commit(&sm.empty[u]);
             }
             if (ok) umma_commit(&sm.pv_done);
-            *reinterpret_cast<volatile int32_t*>(&sm.tiles_done) = i + 1;
         }
         if (!ok) drain_inflight();
     }
     __syncwarp();
-}
-
-// Page blocks into L2, QD_AHEAD tiles before their second contraction.
-constexpr int QD_AHEAD = 2;  // 64 slots x 4,096 tokens: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6; without 73.9
-__device__ __forceinline__ void qd_prefetch(QdSmem& sm, const QdParams& p, const QdUnit& g, int b, int rank, int tiles)
-{
-    QdLookup look;
-    for (int i = 0; i < tiles; ++i) {
-        look(p, g, b, 2 * i, false);
-        const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + rank) & 31);
-        if (i < 2) continue;  // (the first tiles are loaded at once)
-        if (!__all_sync(0xFFFFFFFFu, wait_count(&sm.tiles_done, i - QD_AHEAD, sm, p.dev_err))) return;
-        if (at >= 0 && elect_one()) bulk_prefetch_l2(p.slab + (size_t)at * QPAGE, QPAGE);
-        __syncwarp();
-    }
 }
 
 // The queries of this CTA's heads, by the softmax warps: all of them times one power of two 2^a that brings the largest finite
@@ -506,7 +490,8 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
 {
     const int warp = (int)(threadIdx.x >> 5), lane = (int)lane_id(), quarter = warp & 3, group = warp >> 2, h0 = QD_MINE * group;
     const int token = 32 * quarter + lane, line = token & (PAGE - 1), page = quarter >> 1;
-    QdLookup look;
+    QdLookup look, later;
+    if (warp == 0) later(p, g, b, 0, false);
     auto row_scale = [&](int i) {  // of this thread's token in tile i; 1 for tokens that are not there
         look(p, g, b, 2 * i, false);
         const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + page) & 31);
@@ -617,6 +602,12 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full);
+        if (warp == 0 && i + QD_AHEAD < tiles) {  // (a warp that waits for the next scores now)
+            const int e2 = 2 * (i + QD_AHEAD);
+            later(p, g, b, e2, false);
+            const int32_t at = __shfl_sync(0xFFFFFFFFu, later.block, (e2 + rank) & 31);
+            if (at >= 0 && lane == 0) bulk_prefetch_l2(p.slab + (size_t)at * QPAGE, QPAGE);
+        }
     }
     // The sums of exp: over the lanes -- half of the heads go to the other half of the lanes three times, so that three heads a
     // lane are left to add up over four -- then over the quarters.
@@ -741,7 +732,6 @@ __global__ void __launch_bounds__(QD_THREADS, 1)
         else if (warp == QW_LOAD) qd_produce(sm, tm_page, p, g, b, tiles);
         else if (warp == QW_SCORE) qd_score(sm, p, tbase, tiles);
         else if (warp == QW_PV) qd_pv(sm, p, tbase, tiles);
-        else if (warp == QW_AHEAD) qd_prefetch(sm, p, g, b, rank, tiles);
     }
     // After an abort a role leaves wherever it stands, with copies and MMAs under way: they land before the CTA gives its
     // shared memory and its TMEM back.
