@@ -29,7 +29,7 @@
 // move), and one warp each that loads, issues S and issues PV.  A tile is two pages; its five
 // chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
-// Measured: 64 slots of up to 4,096 tokens 68.5 us (190 MB: 2.8 TB/s, 0.41 of the copy rate; 811 TFLOP/s), 64 of 15,000 to
+// Measured: 64 slots of 4,096 tokens 68.5 us (190 MB: 2.8 TB/s, 0.41 of the copy rate; 811 TFLOP/s), 64 of 15,000 to
 // 16,384 214.9 us (3.1 TB/s, 975 TFLOP/s, 0.51 of the measured bf16 rate), one of 32,768 27.6 us, 128 of up to 256 30.0 us.  (The bf16 cache: 64 over 4,096 69 to 72 us.)  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each for
 // 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,200.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it
