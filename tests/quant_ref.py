@@ -112,16 +112,20 @@ def out_tolerance(q_abs, out, o, p, rows, scales, w_kv_b, scale):
       * the output to bf16 (2^-8);
       * f32 sums besides: each score within 640 * 2^-24 of sum |q||row| * scale, the hardware exponential 2^-21, the sums
         over tokens and latent entries 2^-15 in all.
-    A p that is off by d_t moves o by at most sum_t d_t |row_t - o|, here taken through |W_UV|."""
+    Scores that are off by e_t, |e_t| <= ds_t, multiply each weight by exp(e_t):
+        o' - o = sum_t p_t (exp(e_t) - 1) (row_t - o) / sum_t p_t exp(e_t),
+    and with weights that are off by r_t of themselves besides, exp(e_t) (1 + r_t) for exp(e_t): so with d_t = p_t (exp(ds_t)
+    (1 + r_t) - 1) it is at most sum_t d_t |row_t - o| / sum_t p_t exp(-ds_t) (1 - r_t), here taken through |W_UV|.  (For small
+    ds_t that is p_t (ds_t + r_t) over 1.)"""
     w = np.abs(np.asarray(w_kv_b, np.float64).reshape(H, NOPE + V, LORA)[:, NOPE:])
     if p.shape[1] == 0:
         return np.zeros_like(out)
     q = np.abs(np.asarray(q_abs, np.float64))
     ds = scale * (640 * 2.0 ** -24 * q @ np.abs(rows).T + 1.25 * 2.0 ** -22 * q[:, :LORA].max() * np.abs(rows[:, :LORA]).sum(-1))
-    size = p * scales
-    d = p * (2.0 ** -8 + 2.0 ** -12 + 2.0 ** -19 + ds) + 1.25 * 2.0 ** -16 * size.max(-1, keepdims=True) / scales
+    size, r, ds = p * scales, 2.0 ** -8 + 2.0 ** -12 + 2.0 ** -19, np.minimum(ds, 300)
+    d = p * (np.expm1(ds) * (1 + r) + r) + np.exp(ds) * 1.25 * 2.0 ** -16 * size.max(-1, keepdims=True) / scales
     c = np.abs(rows[:, :LORA])
-    spread = d @ c + d.sum(-1)[:, None] * np.abs(o)
+    spread = (d @ c + d.sum(-1)[:, None] * np.abs(o)) / ((p * np.exp(-ds)).sum(-1)[:, None] * (1 - r))
     mass = p @ c
     half = 2 * (2.0 ** -12 * mass + 2.0 ** -25 * mass.max(-1, keepdims=True))
     return (np.einsum("hvk,hk->hv", w, spread + half + 2.0 ** -15 * mass) + 2.0 ** -8 * np.abs(out)) * 1.01 + 1e-30
