@@ -29,9 +29,10 @@
 // move), and one warp each that loads, issues S and issues PV.  A tile is two pages; its five
 // chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
-// Measured: 64 slots of 4,096 tokens 68.5 us (190 MB: 2.8 TB/s, 0.41 of the copy rate; 811 TFLOP/s), 64 of 15,000 to
-// 16,384 214.9 us (3.1 TB/s, 975 TFLOP/s, 0.51 of the measured bf16 rate), one of 32,768 27.6 us, 128 of up to 256 30.0 us.  (The bf16 cache: 64 over 4,096 69 to 72 us.)  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each for
-// 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,200.  With S and the queries'
+// Measured: 64 slots of 4,096 tokens 65.3 us (190 MB: 2.9 TB/s, 0.43 of the copy rate; 850 TFLOP/s), 64 of 15,000 to
+// 16,384 210.5 us (3.2 TB/s, 995 TFLOP/s, 0.52 of the measured bf16 rate), one of 32,768 27.2 us, 128 of up to 256 29.3 us;
+// k3mla_window_decode over the bf16 cache takes 67 us for 64 of 4,100.  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each
+// for 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,050.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it
 // frees (1,000), the last scores (600) and the softmax (1,700) of every second tile stand in one chain; the tensor pipe is 43%
 // busy.  Small calls: 3.9 us until the queries' pairs are there, 2.2 for the write-out, and the expansion's 9.
@@ -186,7 +187,8 @@ struct QdLookup {
 
 // ---- roles --------------------------------------------------------------------------------
 
-// The producer: every chunk of a tile from its two pages.
+// The producer: every chunk of a tile from its two pages.  (This loop and the scores' are written out: what one thread does for
+// a chunk stands in the chain of a tile.  64 x 4,096 tokens 67.2 -> 65.4 us, one slot of 32,768 26.6 -> 26.9.)
 __device__ __forceinline__ void qd_produce(QdSmem& sm, const CUtensorMap& tm_page, const QdParams& p, const QdUnit& g, int b,
                                            int tiles)
 {
@@ -199,18 +201,20 @@ __device__ __forceinline__ void qd_produce(QdSmem& sm, const CUtensorMap& tm_pag
 #pragma unroll
         for (int x = 0; x < 2; ++x) at[x] = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + x) & 31);
         if (elect_one()) {
-#pragma unroll 1
+            const int32_t at0 = at[0] < 0 ? none : at[0], at1 = at[1] < 0 ? none : at[1];
+            int u = QD_CHUNKS * i % QD_RING, phase = QD_CHUNKS * i / QD_RING ^ 1;
+#pragma unroll
             for (int c = 0; c < QD_CHUNKS && ok; ++c) {
-                const int use = QD_CHUNKS * i + c, u = use % QD_RING;
-                ok = qd_wait(sm, p, &sm.empty[u], (use / QD_RING) ^ 1);
+                ok = qd_wait(sm, p, &sm.empty[u], phase);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&sm.full[u], QD_CHUNK);
                 // (diagnostic: a load never issued)
-                if (c == 1 && i + 1 == p.withhold) continue;
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    tma_load_4d(sm.ring[u] + x * (PAGE * 128), &tm_page, 0, 0, c ? c - 1 : 4, at[x] < 0 ? none : at[x],
-                                &sm.full[u]);
+                if (c != 1 || i + 1 != p.withhold) {
+                    const int z = c ? c - 1 : 4;
+                    tma_load_4d(sm.ring[u], &tm_page, 0, 0, z, at0, &sm.full[u]);
+                    tma_load_4d(sm.ring[u] + PAGE * 128, &tm_page, 0, 0, z, at1, &sm.full[u]);
+                }
+                if (++u == QD_RING) u = 0, phase ^= 1;
             }
         }
         __syncwarp();
@@ -226,17 +230,18 @@ __device__ __forceinline__ void qd_score(QdSmem& sm, const QdParams& p, uint32_t
     if (elect_one()) {
         bool ok = qd_wait(sm, p, &sm.q_ready, 0);
         const uint64_t q0 = make_sdesc(smem_u32(sm.q[0]), 16, 1024), qr = make_sdesc(smem_u32(sm.q_rope), 16, 1024);
+        const uint64_t r0 = make_sdesc(smem_u32(sm.ring[0]), 16, 1024);
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
             ok = qd_wait(sm, p, &sm.s_empty, i ^ 1);
             const int use = QD_CHUNKS * i, ur = use % QD_RING;
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < 4 && ok; ++c) {
                 const int u = (use + 1 + c) % QD_RING;
                 ok = qd_wait(sm, p, &sm.full[u], (use + 1 + c) / QD_RING);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t a = make_sdesc(smem_u32(sm.ring[u]), 16, 1024), q = q0 + (uint64_t)(c * (QD_QCHUNK >> 4));
+                const uint64_t a = r0 + (uint64_t)(u * (QD_CHUNK >> 4)), q = q0 + (uint64_t)(c * (QD_QCHUNK >> 4));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_ss_8bit(tbase + QD_S_COL, a + 2u * k, q + 2u * k, QD_IDESC_S, (c | k) != 0);
@@ -244,7 +249,7 @@ __device__ __forceinline__ void qd_score(QdSmem& sm, const QdParams& p, uint32_t
                     ok = qd_wait(sm, p, &sm.full[ur], use / QD_RING);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t r = make_sdesc(smem_u32(sm.ring[ur]), 16, 1024);
+                    const uint64_t r = r0 + (uint64_t)(ur * (QD_CHUNK >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) umma_ss(tbase + QD_S_COL, r + 2u * k, qr + 2u * k, QD_IDESC_ROPE, 1u);
                     umma_commit(&sm.empty[ur]);
@@ -262,17 +267,15 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
 {
     if (elect_one()) {
         bool ok = true;
-        const uint64_t pd = make_sdesc(smem_u32(sm.p), QD_CHUNK, 1024);
+        const uint64_t pd = make_sdesc(smem_u32(sm.p), QD_CHUNK, 1024), r0 = make_sdesc(smem_u32(sm.ring[0]), QD_CHUNK, 1024);
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
-            ok = qd_wait(sm, p, &sm.p_full, i);
+            ok = qd_wait(sm, p, &sm.p_full, i);  // (whose scores have waited for the chunks: 64 x 4,096 tokens 68.7 -> 67.4 us)
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4 && ok; ++c) {
-                const int use = QD_CHUNKS * i + 1 + c, u = use % QD_RING;
-                ok = qd_wait(sm, p, &sm.full[u], use / QD_RING);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t a = make_sdesc(smem_u32(sm.ring[u]), QD_CHUNK, 1024);
+                const int u = (QD_CHUNKS * i + 1 + c) % QD_RING;
+                const uint64_t a = r0 + (uint64_t)(u * (QD_CHUNK >> 4));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     umma_ss_8bit(tbase + (uint32_t)(QD_PAIRS * c), a + 256u * k, pd + 256u * k, QD_IDESC_PV, (i | k) != 0);
@@ -288,7 +291,7 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
 // The queries of this CTA's heads, by the softmax warps: all of them times one power of two 2^a that brings the largest finite
 // latent entry to [2^7, 2^8) (less where the rope entries would leave bf16's range), as a sum of two e4m3 numbers, the second
 // in units of 1 / 32.  A bf16 has 8 bits, the two numbers 4 each and a sign: exact down to 2^-14 of the largest, and within
-// 2^-15 below.
+// 2^-15 below, half of the second number's smallest step (and 2^-17, half an f16's on the way).
 struct QdQueries {
     static constexpr int STEP = 32 * QD_SOFTMAX / 64, ITEMS = QD_HEADS / STEP, ROPES = 32 * QD_SOFTMAX / 8;
     static_assert(STEP * ITEMS == QD_HEADS && ITEMS % 4 == 0 && 2 * ROPES >= QD_HEADS, "whole pieces");
