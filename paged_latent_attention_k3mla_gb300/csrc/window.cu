@@ -45,11 +45,11 @@
 //
 // Measured, all kernels of a call in a graph of calls: decode of 64 slots over 4,100 seen tokens 69.1 us (324 MB, 0.69 of
 // the copy rate), over 1,088 33.2 us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens
-// 232 us (1,003 TFLOP/s, 0.52 of the measured bf16 rate), of 1,000 rows over 300 120.8 us (29 of them the expansion).
+// 226 us (1,030 TFLOP/s, 0.54 of the measured bf16 rate), of 1,000 rows over 300 120.2 us (29 of them the expansion).
 // Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 173 us (1,270 TFLOP/s; 144 of them the shared pages at
 // 0.77 us a page, four slots and 32 heads, of which the score MMAs take 0.57), 5 groups of 1 to 7 over 2,500 and 1,000 35 us.
-// Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 236.8 and 122.5 us).  Bounds: the page
-// stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.67 us, of which
+// Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 230 and 122 us).  Bounds: the page
+// stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.66 us, of which
 // the score MMAs take 0.57 at their full rate), else the chain through a unit and the expansion behind it (6 us).
 //
 // Every wait is bounded, as in decode.cu: after WAIT_NS it sets K3MLA_DEV_TIMEOUT and the roles run out.
@@ -563,11 +563,27 @@ __device__ __forceinline__ void w_produce(WSmem<MODE>& sm, const CUtensorMap& tm
         for (int i = 0; i < g.npg; ++i) {
             const int32_t y = rows(p, g, i);
             if (elect_one()) {
+                if constexpr (C::NPROD == 1) {
+                    // Written out, as the issuers' loop over the thirds is: a load's wait, arming and copy keep the thread busy for
+                    // some 280 clocks, three a page, where the page's MMAs take 1,150 (16 x 64 rows 233.8 -> 225.6 us, 64 over
+                    // 16,384 tokens 202.6 -> 189.4, 64 slots over as many shared tokens 172.2 -> 169.0).
+                    int u = (base + 3 * i) % C::NUNIT;
+                    uint32_t phase = (uint32_t)((base + 3 * i) / C::NUNIT) ^ 1u;
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) {
+                        ok = ok && w_wait<MODE>(&sm.empty[u], phase & 1u);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&sm.full[u], THIRD);
+                        tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+                        if (++u == C::NUNIT) u = 0, phase ^= 1u;
+                    }
+                } else {
 #pragma unroll 1
-                for (int x = 0; x < 3 && ok; ++x) {
-                    if ((base + 3 * i + x) % C::NPROD != t) continue;
-                    const int u = take(base + 3 * i + x, THIRD);
-                    if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+                    for (int x = 0; x < 3 && ok; ++x) {
+                        if ((base + 3 * i + x) % C::NPROD != t) continue;
+                        const int u = take(base + 3 * i + x, THIRD);
+                        if (ok) tma_load_3d(sm.u.c0.ring[u], &tm_page, 0, y, 3 * x, &sm.full[u]);
+                    }
                 }
             }
             __syncwarp();
@@ -595,7 +611,7 @@ template <int MODE> __device__ __forceinline__ void w_score(WSmem<MODE>& sm, con
             for (int i = (r + C::NISS - gp % C::NISS) % C::NISS; i < g.npg && ok; i += C::NISS) {
                 const int sb = (gp + i) % WN_S, k = (gp + i) / WN_S;
                 ok = w_wait<MODE>(&sm.s_empty[sb], (uint32_t)(k & 1) ^ 1u);
-#pragma unroll 1
+#pragma unroll
                 for (int t = 0; t < 3 && ok; ++t) {
                     const int e = base + 3 * i + t, u = e % C::NUNIT, ku = e / C::NUNIT;
                     ok = w_count<MODE>(&sm.unit_taken[u], ku) &&
