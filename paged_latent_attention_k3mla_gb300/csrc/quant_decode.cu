@@ -30,7 +30,7 @@
 // chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
 // Measured: 64 slots of 4,096 tokens 65.3 us (190 MB: 2.9 TB/s, 0.43 of the copy rate; 850 TFLOP/s), 64 of 15,000 to
-// 16,384 210.5 us (3.2 TB/s, 995 TFLOP/s, 0.52 of the measured bf16 rate), one of 32,768 27.2 us, 128 of up to 256 29.3 us;
+// 16,384 205 us (3.2 TB/s, 1,020 TFLOP/s, 0.54 of the measured bf16 rate), one of 32,768 27.2 us, 128 of up to 256 29.3 us;
 // k3mla_window_decode over the bf16 cache takes 67 us for 64 of 4,100.  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each
 // for 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,050.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it

@@ -46,8 +46,8 @@
 // Measured, all kernels of a call in a graph of calls: decode of 64 slots over 4,100 seen tokens 69.1 us (324 MB, 0.69 of
 // the copy rate), over 1,088 33.2 us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens
 // 226 us (1,030 TFLOP/s, 0.54 of the measured bf16 rate), of 1,000 rows over 300 120.2 us (29 of them the expansion).
-// Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 173 us (1,270 TFLOP/s; 144 of them the shared pages at
-// 0.77 us a page, four slots and 32 heads, of which the score MMAs take 0.57), 5 groups of 1 to 7 over 2,500 and 1,000 35 us.
+// Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 171 us (1,315 TFLOP/s; 141 of them the shared pages at
+// 0.75 us a page, four slots and 32 heads, of which the score MMAs take 0.57), 5 groups of 1 to 7 over 2,500 and 1,000 35 us.
 // Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 230 and 122 us).  Bounds: the page
 // stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.66 us, of which
 // the score MMAs take 0.57 at their full rate), else the chain through a unit and the expansion behind it (6 us).
