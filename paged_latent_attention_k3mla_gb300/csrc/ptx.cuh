@@ -426,6 +426,34 @@ __device__ __forceinline__ void umma_ss_8bit(uint32_t d_tmem, uint64_t a_desc, u
         : "memory");
 }
 
+// Instruction descriptor for kind::mxf8f6f4: e4m3 x e4m3 -> f32, dense, powers of two (ue8m0) for scale factors; b_sf: which
+// byte of B's scale factors is meant, A's first.
+__host__ __device__ constexpr uint32_t make_idesc_mx_e4m3(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn, uint32_t b_sf)
+{
+    return (b_sf << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24);
+}
+
+// The same with a scale factor for every row of A and column of B (K = 32: one block).  In TMEM, row r's lies in lane r % 32
+// of each quarter, column r / 32, a byte of four.
+__device__ __forceinline__ void umma_ss_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
+                                           uint32_t b_scale, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of shared memory, 16 a lane, into four TMEM columns of all four quarters; the MMAs behind it in the same thread see
+// them.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr)
+{
+    const uint64_t d = ((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 16 | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
 // D(tmem) (+)= A(tmem) * B(smem)
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate)
@@ -530,6 +558,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_fill4(uint32_t taddr, uint32_t v)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %1, %1, %1};" ::"r"(taddr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }

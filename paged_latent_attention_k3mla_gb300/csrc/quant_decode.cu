@@ -7,27 +7,32 @@
 // Slots are cut into splits as in window.cu, and what a split leaves behind -- o_lat, or O and its reference and sum -- is what
 // window.cu's merge and expansion take.
 //
-// The codes are never converted: both contractions are kind::f8f6f4 MMAs with the codes as they lie in shared memory as the
+// The codes are never converted: both contractions are 8-bit MMAs with the codes as they lie in shared memory as the
 // operand of M, and what multiplies them is written as a sum of two e4m3 numbers, the second in units of 1 / 32, in columns of
 // their own:
 //     S^T[128 tokens x 96] = codes . (q1 | q2)^T  (+ the rope part in bf16, onto q1's columns),   raw = S1 + S2 / 32
-//     O^T[512 dims x 96]  += codes^T . (P1 | P2),                                                 O = O1 + O2 / 32
+//     O^T[512 dims x 96]  += codes^T . (P1 | P2) 2^e,                                             O = O1 + O2 / 32
+// The second is a block-scaled MMA (kind::mxf8f6f4): e is an exponent of every head and 32 tokens, K of one MMA, that brings
+// the largest P there to [2^7, 2^8).  Without it the numbers' 2^22 between their largest and their smallest step have to hold
+// all that a row weighs, and where a few tokens take most of its mass the thousands that it answers with are lost
+// together (the first of 4,096 tokens takes 0.87: the output off by 0.087 of itself, of 16,384 by 0.36; with it by 0.0017).  It
+// costs 37 shuffles a tile and warp: 64 slots of 4,096 tokens 65.3 -> 67.2 us, of 15,000 to 16,384 200 -> 209.
 // A pair has 8 bits, as a bf16 does, and two such MMAs cost what one in bf16 does (e4m3 runs at twice the rate), without the
 // 65,536 conversions a tile that a bf16 form would begin with.  96 columns are 48 heads: two CTAs a split, each with all of its
 // tokens.  Tokens on M and not heads, because 48 heads would leave half of M's 128 rows empty, and because O then fits: TMEM
-// holds O in 4 x 96 columns and S in 96, 480 of 512.
+// holds O in 4 x 96 columns and S in 96, and the exponents in 8, 488 of 512.
 //
 // Numerics.  Scores, maxima and sums are f32.  Below that: q as a pair (times a power of two for the CTA's 48 heads; exact for
-// entries down to 2^-14 of their largest, within 2^-22 of it below), P times its row's power of two as a pair (by way of an
-// f16: 2^-8 of it, as a bf16 is; within 2^-16 of the largest below that), then as in window.cu o_lat and a split's O
-// as f16 with a power of two a row, and the output as bf16.  A reference moves when a row passes it by 2^7, so that P, 2 at
-// the reference, comes to at most 256 of e4m3's 448.  Against 64 bits the outputs are off by 0.0017 to 0.0019 (relative, mean
-// square), of which 0.0017 are their own rounding.
+// entries down to 2^-14 of their largest, within 1.25 * 2^-22 of it below), p times its row's power of two as a pair (by way of
+// an f16: 2^-8 of it, as a bf16 is; within 1.25 * 2^-22 of the largest of its block below that), then as in window.cu o_lat and a
+// split's O as f16 with a power of two a row, and the output as bf16.  As the exponents carry P's size, a reference only keeps
+// the f32 sums in range: it moves when a row passes it by 2^16.  Against 64 bits the outputs are off by 0.0017 to 0.0019
+// (relative, mean square), of which 0.0017 are their own rounding.
 //
 // Structure of a CTA: eight softmax warps (a quarter of the tile's tokens x 24 heads each: a lane has a token, so a row's scale,
-// mask and sums of exp are the thread's own, and what meets every tile is one vote of four warps whether a reference has to
-// move), and one warp each that loads, issues S and issues PV.  A tile is two pages; its five
-// chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
+// mask and sums of exp are the thread's own; a block's largest P is found by 13 shuffles of a warp, and what meets every tile is
+// one vote of four warps whether a reference has to move), and one warp each that loads, issues S and issues PV.  A tile is two
+// pages; its five chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
 // Measured: 64 slots of 4,096 tokens 65.3 us (190 MB: 2.9 TB/s, 0.43 of the copy rate; 850 TFLOP/s), 64 of 15,000 to
 // 16,384 205 us (3.2 TB/s, 1,020 TFLOP/s, 0.54 of the measured bf16 rate), one of 32,768 27.2 us, 128 of up to 256 29.3 us;
@@ -120,24 +125,27 @@ constexpr int QD_SOFTMAX = 8;                   // warps 0 .. 7: quarter of the 
 constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10;
 constexpr int QD_THREADS = 352;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
+constexpr uint32_t QD_ONE_COL = 5 * QD_PAIRS, QD_SF_COL = QD_ONE_COL + 4;  // ... scale factors: the latents', 1; P's
 // A tile's pages, one each of the two CTAs, are fetched into L2 this many tiles before its scores.  64 slots x 4,096 tokens, by a
 // warp of its own: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6, without 73.9; by softmax warp 0, this many: 69.3.
 constexpr int QD_AHEAD = 3;
 constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
-constexpr float QD_TAU = 7.f;                   // a reference moves when a row passes it by more than 2^TAU
+constexpr float QD_TAU = 16.f;                  // a reference moves when a row passes it by more than 2^TAU
 constexpr float QD_BIG = 1048576.f;             // references this large are rounded by so much that s less the reference has to be
                                                 // taken from the rounded s + k that it is one of, or none may come near it
-constexpr float QD_UP = 2.f;                    // p times its row's power of two comes to at most QD_UP 2^TAU = 256
 constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
 constexpr uint32_t QD_IDESC_ROPE = make_idesc_bf16(128, QD_HEADS, 0, 0);
-constexpr uint32_t QD_IDESC_PV = make_idesc_e4m3(128, QD_PAIRS, 1, 1);
+constexpr uint32_t QD_IDESC_PV = make_idesc_mx_e4m3(128, QD_PAIRS, 1, 1, 0);
+constexpr uint32_t QD_IDESC_NEXT = 1u << 4;     // the next 32 tokens' factors
 
 struct __align__(1024) QdSmem {
     uint8_t q[4][QD_QCHUNK];          // K-major B of the scores: rows h (first numbers) and 48 + h (second)
     uint8_t q_rope[QD_HEADS * 128];
     uint8_t ring[QD_RING][QD_CHUNK];
     uint8_t p[QD_TILE * 128];         // MN-major B of the second contraction: [token][group: 24 first, 24 second numbers]
+    // P's exponents as tmem_copy_scales takes them: column n's for quarter q at 16 (n % 32) + 4 (n / 32) + q
+    alignas(128) uint8_t sf[512];
     uint64_t full[QD_RING], empty[QD_RING];
     uint64_t q_ready, s_full, s_empty, p_full, pv_done;
     alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; 0 before anything was seen
@@ -151,7 +159,7 @@ struct __align__(1024) QdSmem {
 };
 static_assert(QD_QCHUNK % 1024 == 0 && (QD_HEADS * 128) % 1024 == 0, "operand tiles start 1024-byte aligned");
 static_assert(sizeof(QdSmem) + 1024 <= 227 * 1024, "shared memory of one CTA (with alignment slack)");
-static_assert(4 * QD_PAIRS + QD_PAIRS <= 512, "TMEM columns");
+static_assert(QD_SF_COL + 4 <= 512, "TMEM columns");
 
 __device__ __forceinline__ bool qd_wait(QdSmem& sm, const QdParams& p, uint64_t* bar, int phase)
 {
@@ -268,17 +276,20 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
     if (elect_one()) {
         bool ok = true;
         const uint64_t pd = make_sdesc(smem_u32(sm.p), QD_CHUNK, 1024), r0 = make_sdesc(smem_u32(sm.ring[0]), QD_CHUNK, 1024);
+        const uint32_t one = tbase + QD_ONE_COL, sf = tbase + QD_SF_COL, sf_at = smem_u32(sm.sf);
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
             ok = qd_wait(sm, p, &sm.p_full, i);  // (whose scores have waited for the chunks: 64 x 4,096 tokens 68.7 -> 67.4 us)
             tc_fence_after();
+            tmem_copy_scales(sf, sf_at);
 #pragma unroll 1
             for (int c = 0; c < 4 && ok; ++c) {
                 const int u = (QD_CHUNKS * i + 1 + c) % QD_RING;
                 const uint64_t a = r0 + (uint64_t)(u * (QD_CHUNK >> 4));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    umma_ss_8bit(tbase + (uint32_t)(QD_PAIRS * c), a + 256u * k, pd + 256u * k, QD_IDESC_PV, (i | k) != 0);
+                    umma_ss_mx(tbase + (uint32_t)(QD_PAIRS * c), a + 256u * k, pd + 256u * k, QD_IDESC_PV + QD_IDESC_NEXT * k, one, sf,
+                               (i | k) != 0);
                 umma_commit(&sm.empty[u]);
             }
             if (ok) umma_commit(&sm.pv_done);
@@ -486,8 +497,8 @@ __device__ __noinline__ void qd_clear(QdSmem& sm, int i, int token)
 }
 
 // Softmax warp: the tokens of its quarter, a lane each, and the heads of its group.  A token's factor is its thread's, and the
-// sums of exp stay in the thread until the end; what meets in every tile is one vote of the group's four warps, whether a row
-// has passed its reference.
+// sums of exp stay in the thread until the end; what meets in every tile is the largest P of a head, within the warp, and one
+// vote of the group's four warps, whether a row has passed its reference.
 __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQueries& queries, const QdUnit& g, int b, int s,
                                            int rank, uint32_t tbase, int tiles)
 {
@@ -495,14 +506,26 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     const int token = 32 * quarter + lane, line = token & (PAGE - 1), page = quarter >> 1;
     QdLookup look, later;
     if (warp == 0) later(p, g, b, 0, false);
-    auto row_scale = [&](int i) {  // of this thread's token in tile i; 1 for tokens that are not there
+    // Of this thread's token in tile i; the smallest for tokens that are not there, zero rows that are to leave the others their
+    // exponent.
+    auto row_scale = [&](int i) {
         look(p, g, b, 2 * i, false);
         const int32_t at = __shfl_sync(0xFFFFFFFFu, look.block, (2 * i + page) & 31);
-        return at < 0 ? (uint16_t)0x3F80u : *reinterpret_cast<const uint16_t*>(p.slab + (size_t)at * QPAGE + QSCALES + 2 * line);
+        return at < 0 ? (uint16_t)0x0F80u : *reinterpret_cast<const uint16_t*>(p.slab + (size_t)at * QPAGE + QSCALES + 2 * line);
     };
     const float kq = queries.store(sm) * p.kscale;
     uint16_t next = row_scale(0);
     const uint32_t t_lane = tbase + ((32u * (uint32_t)quarter) << 16);
+    if (group == 0) {  // (seen by the second contraction as P is)
+        tmem_fill4(t_lane + QD_ONE_COL, 0x7F7F7F7Fu);
+        tmem_wait_st();
+    }
+    // The head of this warp's whose largest weight this lane finds (two lanes of eight: another's again), the lane that finds
+    // head h's, and where this one's factors lie.
+    const int mine = 12 * (lane >> 4) + 6 * (lane >> 3 & 1) + 2 * (lane & 4 ? 2 : lane >> 1 & 1) + (lane & 1);
+    const auto lane_of = [](int h) { return 16 * (h / 12) + 8 * (h / 6 & 1) + h % 6; };
+    const auto sf_place = [&](int n) { return 16 * (n & 31) + 4 * (n >> 5) + quarter; };
+    const int sf0 = sf_place(2 * h0 + mine), sf1 = sf_place(2 * h0 + QD_MINE + mine);
     float l[QD_MINE];
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) l[h] = 0.f;
@@ -512,8 +535,9 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     for (int i = 0; i < tiles; ++i) {
         const int e = 2 * i + page, t = PAGE * qd_logical(g, e) + line;
         const bool seen = e < g.npg && qd_seen(p, g.n, t);
-        const float scale = seen ? __uint_as_float((uint32_t)next << 16) : 1.f;
-        const float k = (float)((int)(__float_as_uint(scale) >> 23) - 127), c = kq * scale, up = scale * (QD_UP / 256.f);
+        const float scale = __uint_as_float(seen ? (uint32_t)next << 16 : 0x0F800000u);
+        const int field = (int)(__float_as_uint(scale) >> 23), largest = __reduce_max_sync(0xFFFFFFFFu, field);
+        const float k = (float)(field - 127), c = kq * scale, up = scale * __uint_as_float((uint32_t)max(254 - largest, 1) << 23);
         const bool whole = __all_sync(0xFFFFFFFFu, seen);
         if (i + 1 < tiles) next = row_scale(i + 1);
         dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.s_full, i));
@@ -574,19 +598,56 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
             }
             if (!seen && odd) qd_clear(sm, i, token);
         }
+        // Weights times their rows' powers of two, in units of the largest of those.
+#pragma unroll
+        for (int h = 0; h < QD_MINE; h += 2) {
+            const uint64_t e2 = f32x2(ex2_approx(x[h]), ex2_approx(x[h + 1]));
+            f32x2_parts(add_f32x2(f32x2(l[h], l[h + 1]), e2), l[h], l[h + 1]);
+            f32x2_parts(mul_f32x2(e2, f32x2(up, up)), x[h], x[h + 1]);
+        }
+        // The largest of each head over the warp's 32 tokens, a block of the second contraction: two heads a register by the
+        // upper halves of their bits (which order like them), half of the heads to the other half of the lanes twice.
+        uint32_t sf, unit;
+        {
+            uint32_t m[QD_MINE / 2];
+#pragma unroll
+            for (int h = 0; h < QD_MINE; h += 2) m[h / 2] = __byte_perm(__float_as_uint(x[h]), __float_as_uint(x[h + 1]), 0x7632);
+            auto halve = [&](auto half, int o) {
+                constexpr int n = decltype(half)::value;
+                const bool high = lane & o;
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t keep = high ? m[j + n] : m[j], give = high ? m[j] : m[j + n];
+                    m[j] = max_u16x2(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+                }
+            };
+            halve(std::integral_constant<int, 6>(), 16);
+            halve(std::integral_constant<int, 3>(), 8);
+            static_assert(QD_MINE == 24, "three registers a lane");
+            // (three: two stay with one half of the lanes, one with the other)
+            const uint32_t give = __shfl_xor_sync(0xFFFFFFFFu, lane & 4 ? m[0] : m[2], 4);
+            m[1] = max_u16x2(m[1], __shfl_xor_sync(0xFFFFFFFFu, m[1], 4));
+            m[0] = max_u16x2(lane & 4 ? m[2] : m[0], give);
+            const bool second = (lane & 6) == 2;
+            uint32_t pair = __shfl_xor_sync(0xFFFFFFFFu, (lane & 6) == 0 ? m[1] : m[0], 2);
+            pair = max_u16x2(second ? m[1] : m[0], pair);
+            pair = max_u16x2(pair, __shfl_xor_sync(0xFFFFFFFFu, pair, 1));
+            const int top = (int)((lane & 1 ? pair >> 16 : pair & 0xFFFFu) >> 7);  // the largest: in [2^(top - 127), 2^(top - 126))
+            // to [1 / 2, 1): P is 2^8 times that
+            unit = (uint32_t)(253 - min(top, 252)) << 23;
+            sf = (uint32_t)min(max(top + largest - (7 + 127), 0), 254);
+        }
         uint32_t w[QD_MINE / 2];  // 24 first numbers, 24 second ones
 #pragma unroll
         for (int y = 0; y < QD_MINE / 4; ++y) {
+            // (a shuffle each: 64 x 4,096 tokens 67.0 us, by way of shared memory 68.2)
+            auto up2 = [&](int h, float& p0, float& p1) {
+                const uint32_t f0 = __shfl_sync(0xFFFFFFFFu, unit, lane_of(h)), f1 = __shfl_sync(0xFFFFFFFFu, unit, lane_of(h + 1));
+                f32x2_parts(mul_f32x2(f32x2(x[h], x[h + 1]), f32x2(__uint_as_float(f0), __uint_as_float(f1))), p0, p1);
+            };
             float a[4];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const int h = 4 * y + 2 * z;
-                const uint64_t e2 = f32x2(ex2_approx(x[h]), ex2_approx(x[h + 1]));
-                f32x2_parts(add_f32x2(f32x2(l[h], l[h + 1]), e2), l[h], l[h + 1]);
-                float p0, p1;
-                f32x2_parts(mul_f32x2(e2, f32x2(up, up)), p0, p1);
-                a[z] = p0, a[z + 2] = p1;
-            }
+            up2(4 * y, a[0], a[2]);
+            up2(4 * y + 2, a[1], a[3]);
             // Heads 0 and 2 of the four in one register, 1 and 3 in the other.  v = p 2^-8 as an f16 has e4m3's bits, 7 higher,
             // subnormals included: the first number is v rounded there, and no conversion (a quarter of the arithmetic's
             // rate) is needed for it or for what is left.  (Masked so that a NaN stays within its head, whose sum is one too.)
@@ -601,6 +662,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         for (int y = 0; y < 3; ++y)
             *reinterpret_cast<uint4*>(sm.p + token * 128 + (((3 * group + y) ^ (token & 7)) << 4)) =
                 make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
+        sm.sf[sf0] = sm.sf[sf1] = (uint8_t)sf;
         fence_proxy_async_cta();  // the MMAs read P, and what was cleared, through the async proxy
         tc_fence_before();
         __syncwarp();
@@ -645,7 +707,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     float total = 1.f;
     if (lane < QD_MINE)
         total = (sm.part[0][h0 + lane] + sm.part[1][h0 + lane]) + (sm.part[2][h0 + lane] + sm.part[3][h0 + lane]);
-    float r = (g.single ? 1.f / total : 1.f) * (1.f / QD_UP);
+    float r = g.single ? 1.f / total : 1.f;
     // thread = dim 128 d + 32 quarter + lane of every block d; first the heads' largest entries (two blocks stay in registers)
     auto load = [&](int d, float (&o)[QD_MINE]) {
         uint32_t v[2 * QD_MINE];
