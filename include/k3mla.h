@@ -401,8 +401,9 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
 /* ---- attention for slots that share their first pages --------------------------------
  * Decode of one token row per slot over its whole context (k3mla_window_decode with window >= ctx_len: the same
  * definition, roundings, zero rows for -1, NaN for a row that sees a non-finite latent), for groups of slots whose tables
- * begin with the same pages (k3mla_pool_share_prefix): those are looked up once, in the table of the group's first slot,
- * and read once for four slots at a time instead of once for each slot.
+ * begin with the same pages (k3mla_pool_share_prefix): those are looked up once, in the table of the group's first slot
+ * that holds tokens enough to share them (so one that has ended may have lost its pages), and read once for four slots at a
+ * time instead of once for each slot.
  * group_start [n_groups + 1] (non-decreasing, within [0, B]): slots group_start[g] .. group_start[g + 1] - 1 are group g's;
  *             slots outside every group, or in one of shared_len 0, attend by themselves
  * shared_len  [n_groups] (NULL for none): tokens that the slots of group g share.  Whole pages of them are read as shared; what

@@ -341,7 +341,18 @@ __device__ __forceinline__ void w_unit(WUnit& g, const WinParams& p, int u, bool
             if (lane < g.rows) in = w_shared_row(p, g.b, g.row0 + lane, false).n > 0;
             g.n0 = (int)__ballot_sync(0xFFFFFFFFu, in);
             g.n_hi = pages * PAGE;
-            g.b = max(0, starts[g.b]);  // whose table names the pages
+            // The table of the group's first slot that takes part names the pages (one that has ended has given its own back): one
+            // before this unit's, or the first of them.
+            int owner = g.row0 + max(0, __ffs(g.n0) - 1);
+            if (g.n0)
+                for (int b0 = max(0, starts[g.b]); b0 < g.row0; b0 += 32) {
+                    const bool takes = b0 + lane < g.row0 && w_shared_row(p, g.b, b0 + lane, false).n > 0;
+                    if (const unsigned any = __ballot_sync(0xFFFFFFFFu, takes)) {
+                        owner = b0 + __ffs(any) - 1;
+                        break;
+                    }
+                }
+            g.b = owner;
             g.nsp = g.wp0 = 0;
             g.single = 0;
             const int part = w_split_pages(pages, p.shared_split);
