@@ -422,7 +422,7 @@ int k3mla_window_chunk_decode(const uint16_t* q_abs, const uint16_t* slab, int n
  * workspace   device, 256-byte aligned, >= k3mla_shared_decode_workspace_bytes(...) bytes; scratch, one for each call
  *             that may overlap others.
  * Scores of magnitude 2^30 and more may give NaN, as in k3mla_window_decode: an f32 of that size has steps of 64.
- * Two to four kernels on `stream`, reading nothing but w_kv_b before the kernel ahead of the call has completed: w_kv_b must
+ * Two or three kernels on `stream`, reading nothing but w_kv_b before the kernel ahead of the call has completed: w_kv_b must
  * not be written by the kernel immediately before this call. */
 size_t k3mla_shared_decode_workspace_bytes(int B, int max_shared, int max_own, int shared_split, int own_split);
 int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, int max_own, int* own_split);

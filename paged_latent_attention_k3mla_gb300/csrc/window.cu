@@ -7,8 +7,8 @@
 //     p     = softmax(s),  o_lat = sum_t p_t r_t[0:512],  out = W_UV[h] o_lat.
 // Decode: one token row per slot.  Chunk: several consecutive new token rows per slot.  Shared: one token row per slot over its
 // whole context, the pages that the slots of a group share read once for four slots x 32 heads at a time (the chunk's units: all
-// 128 rows of an MMA used, and no masks), by a launch of its own; what each slot has behind them as decode's units; the
-// splits of both are added up together.
+// 128 rows of an MMA used, and no masks), by clusters of their own; what each slot has behind them as decode's units, by the
+// clusters behind those in the grid; the splits of both are added up together.
 //
 // Numerics.  Scores, maxima and sums are f32.  Four roundings go below that: the p of the second contraction
 // to bf16 (the tensor core's operand type; both operands have one type and the cache is bf16), a split's O,
@@ -68,7 +68,7 @@
 
 namespace k3 {
 
-// What a launch attends to: one token row per slot; rows of prefill chunks; the pages that the slots of a group share, and what
+// What a cluster attends to: one token row per slot; rows of prefill chunks; the pages that the slots of a group share, or what
 // each slot has behind them.
 constexpr int W_DECODE = 0, W_CHUNK = 1, W_SHARED = 2, W_OWN = 3;
 
@@ -194,6 +194,7 @@ struct WinParams {
     int32_t* dev_err;
     int B, R, max_pages, n_pages, n_layers, layer, cap;  // cap: the longest context (min of max_ctx and the table)
     int window, n_sink, split_tokens, nsplit, n_units;
+    int shared_units, shared_clusters;   // shared: the grid's first clusters and their units; n_units are own's
     float kscale;                        // scale * log2(e) > 0
     uint64_t wait_ns;                    // bounded-wait limit: WAIT_NS, shorter only from the diagnostic entries
     int32_t withhold;                    // diagnostic only, 0 otherwise: the PV CTA never loads the first half of a unit's page k - 1
@@ -486,17 +487,18 @@ __device__ __forceinline__ void w_init(WSmem<MODE>& sm, uint32_t rank, const Win
 // the shared memory of both.  At most three units ahead of the PV CTA's MMAs: the softmax warps are then no more
 // than two further units behind (their sums of exp meet in two slots), so W_PLANS = 8 slots never run over; the
 // prefetching warp, which nobody else waits for, is counted.
-template <int MODE> __device__ __forceinline__ void w_plan(WSmem<MODE>& sm, const WinParams& p)
+template <int MODE> __device__ __forceinline__ void w_plan(WSmem<MODE>& sm, const WinParams& p, int cluster, int clusters)
 {
     constexpr bool MQ = WCfg<MODE>::MQ;
+    const int n_units = WCfg<MODE>::SHARED ? p.shared_units : p.n_units;
     const int lane = (int)lane_id();
     bool ok = true;
     int n = 0;
     WScan scan;
-    for (int u = (int)blockIdx.x >> 1; ok; u += (int)gridDim.x >> 1) {
+    for (int u = cluster; ok; u += clusters) {
         WUnit g;
         g.npg = -1;
-        if (u < p.n_units) w_unit<MODE>(g, p, u, lane == 0, scan);
+        if (u < n_units) w_unit<MODE>(g, p, u, lane == 0, scan);
         if (g.npg == 0) continue;
         if (n >= 4 && lane == 0) ok = w_count<MODE>(&sm.pv_units, n - 3) && (MQ || w_count<MODE>(&sm.ahead_units, n - 6));
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -984,12 +986,12 @@ __device__ __forceinline__ void w_issue_pv(WSmem<MODE>& sm, const WinParams& p, 
 }
 
 // The rows that see nothing, which no unit has: their o_lat counts as zero whatever the workspace holds.
-template <int MODE> __device__ __forceinline__ void w_empty_rows(const WinParams& p)
+template <int MODE> __device__ __forceinline__ void w_empty_rows(const WinParams& p, int cluster, int clusters)
 {
     using C = WCfg<MODE>;
-    if constexpr (C::SHARED) return;  // (the launch behind has all slots)
-    const int lane = (int)lane_id(), stride = 32 * ((int)gridDim.x >> 1);
-    for (int r0 = 32 * ((int)blockIdx.x >> 1); r0 < p.R; r0 += stride) {
+    if constexpr (C::SHARED) return;  // (own's clusters have all slots)
+    const int lane = (int)lane_id(), stride = 32 * clusters;
+    for (int r0 = 32 * cluster; r0 < p.R; r0 += stride) {
         const int r = r0 + lane;
         bool sees = true;
         if (r < p.R) {
@@ -1253,10 +1255,10 @@ __device__ __forceinline__ void w_epilogue(WSmem<MODE>& sm, const WinParams& p, 
 
 // ---- the kernel ---------------------------------------------------------------------------
 
+// The grid's cluster number `cluster` of `clusters` that share units out among them.
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
-    k3mla_window_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
-                        const __grid_constant__ CUtensorMap tm_q, const WinParams p)
+__device__ __forceinline__ void w_cluster(const CUtensorMap& tm_page, const CUtensorMap& tm_page8, const CUtensorMap& tm_q,
+                                          const WinParams& p, int cluster, int clusters)
 {
     using C = WCfg<MODE>;
     WSmem<MODE>& sm = w_smem<MODE>();
@@ -1277,9 +1279,7 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     cluster_sync();
     tc_fence_after();
     const uint32_t tbase = sm.tmem_base;
-    // What each slot has of its own does not wait for the shared pages' kernel ahead: the two write other records, and that one
-    // began this one only when the kernel ahead of the call had completed.  It waits at its end, for those that wait for it.
-    if (!C::OWN || p.ns_shared == 0) griddep_wait();
+    griddep_wait();
     griddep_launch_dependents();
     if (rank == 0) {
         if (warp < C::W_PROD) w_softmax<MODE>(sm, p, tbase, warp);
@@ -1290,8 +1290,8 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
             w_epilogue<MODE>(sm, p, tbase, (int)(warp & 3u), warp >= 4 ? 1 : 0);
         else if (warp == WW_HALVES) w_produce_halves<MODE>(sm, tm_page8, p);
         else if (warp == WW_PV) w_issue_pv<MODE>(sm, p, tbase);
-        else if (warp == WW_PLAN) w_plan<MODE>(sm, p);
-        else if (warp == WW_EMPTY) w_empty_rows<MODE>(p);
+        else if (warp == WW_PLAN) w_plan<MODE>(sm, p, cluster, clusters);
+        else if (warp == WW_EMPTY) w_empty_rows<MODE>(p, cluster, clusters);
         else if (!C::MQ && warp == WW_AHEAD) w_prefetch<MODE>(sm, tm_page, p);
     }
     // After an abort a role leaves wherever it stands, with copies and MMAs of its own or of others still under way: they
@@ -1302,7 +1302,25 @@ __global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
     cluster_sync();
     tc_fence_after();
     if (warp == 4) tmem_dealloc(tbase, TMEM_COLS);
-    if (C::OWN) griddep_wait();
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
+    k3mla_window_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
+                        const __grid_constant__ CUtensorMap tm_q, const WinParams p)
+{
+    w_cluster<MODE>(tm_page, tm_page8, tm_q, p, (int)blockIdx.x >> 1, (int)gridDim.x >> 1);
+}
+
+// Groups: the clusters of the shared pages first, then those of what each slot has of its own, which take the SMs that the
+// first leave free.  One launch, so that both wait for the kernel ahead of the call.
+__global__ void __cluster_dims__(2, 1, 1) __maxnreg__(128)
+    k3mla_shared_kernel(const __grid_constant__ CUtensorMap tm_page, const __grid_constant__ CUtensorMap tm_page8,
+                        const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q_own, const WinParams p)
+{
+    const int cluster = (int)blockIdx.x >> 1, shared = p.shared_clusters;
+    if (cluster < shared) w_cluster<W_SHARED>(tm_page, tm_page8, tm_q, p, cluster, shared);
+    else w_cluster<W_OWN>(tm_page, tm_page8, tm_q_own, p, cluster - shared, ((int)gridDim.x >> 1) - shared);
 }
 
 // ---- merge of splits (decode) ---------------------------------------------------------------
@@ -1791,29 +1809,41 @@ static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStrea
                       tm_o, x, p);
 }
 
-template <int MODE>
-static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
-                    const WinWs& wl, WinParams& p, cudaStream_t st)
+static void w_place(WinParams& p, uint8_t* ws, const WinWs& wl)
 {
-    using C = WCfg<MODE>;
     p.olat = reinterpret_cast<uint16_t*>(ws + wl.olat);
     p.oscale = reinterpret_cast<float*>(ws + wl.scale);
     p.ws_o = p.nsplit > 1 ? reinterpret_cast<uint16_t*>(ws + wl.o) : nullptr;
     p.ws_oscale = p.nsplit > 1 ? reinterpret_cast<float*>(ws + wl.oscale) : nullptr;
     p.ws_ml = p.nsplit > 1 ? reinterpret_cast<float2*>(ws + wl.ml) : nullptr;
+}
+
+static int w_page_maps(CUtensorMap* tm_page, CUtensorMap* tm_page8, const uint16_t* slab, const WinParams& p)
+{
+    const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE;
+    const int rc = make_tmap_slab_3d(tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
+    return rc ? rc : make_tmap_slab_3d(tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
+}
+
+template <int MODE> static int w_query_map(CUtensorMap* tm_q, const uint16_t* q_abs, const WinParams& p)
+{
+    using C = WCfg<MODE>;
+    const uint64_t R = (uint64_t)p.R;
+    if (!C::MQ) return make_tmap_slab_3d(tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
+    // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
+    const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
+    const uint32_t box[4] = {64, 32, 2, 1};
+    return make_tmap_store(tm_q, false, 4, q_abs, dims, strides, box, true);
+}
+
+template <int MODE>
+static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
+                    const WinWs& wl, WinParams& p, cudaStream_t st)
+{
+    w_place(p, ws, wl);
     CUtensorMap tm_page, tm_page8, tm_q;
-    const uint64_t slab_rows = (uint64_t)p.n_pages * p.n_layers * PAGE, R = (uint64_t)p.R;
-    int rc = make_tmap_slab_3d(&tm_page, slab, slab_rows, ROW, 9, PAGE, 3);
-    if (!rc) rc = make_tmap_slab_3d(&tm_page8, slab, slab_rows, ROW, 9, HALF, 8);
-    if (rc) return rc;
-    if (C::MQ) {
-        // q_abs as (64 elements, 96 heads, R rows, 9 chunks): 64 columns of 32 heads of two token rows
-        const uint64_t dims[4] = {64, H, R, 9}, strides[3] = {ROW * 2, (uint64_t)H * ROW * 2, 128};
-        const uint32_t box[4] = {64, 32, 2, 1};
-        rc = make_tmap_store(&tm_q, false, 4, q_abs, dims, strides, box, true);
-    } else {
-        rc = make_tmap_slab_3d(&tm_q, q_abs, R * H, ROW, 9, H, C::QPU);
-    }
+    int rc = w_page_maps(&tm_page, &tm_page8, slab, p);
+    if (!rc) rc = w_query_map<MODE>(&tm_q, q_abs, p);
     if (rc) return rc;
     static bool attr_done[64] = {};
     const size_t smem = sizeof(WSmem<MODE>) + 1024;
@@ -1821,8 +1851,28 @@ static int w_launch(const uint16_t* q_abs, const uint16_t* slab, const uint16_t*
     const int clusters = std::min(p.n_units, sm_count() / 2);
     rc = launch_pdl(k3mla_window_kernel<MODE>, dim3(2 * clusters), dim3(W_THREADS), smem, st, "k3mla_window_kernel", tm_page,
                     tm_page8, tm_q, p);
+    return rc ? rc : w_tail<MODE>(w_kv_b, out, p, st);
+}
+
+static int w_launch_shared(const uint16_t* q_abs, const uint16_t* slab, const uint16_t* w_kv_b, uint16_t* out, uint8_t* ws,
+                           const WinWs& wl, WinParams& p, cudaStream_t st)
+{
+    // (no shared pages: the kernel that holds one mode only is 0.6 us faster, 8 slots of 4,128 29.3 against 29.9)
+    if (p.shared_units == 0) return w_launch<W_OWN>(q_abs, slab, w_kv_b, out, ws, wl, p, st);
+    w_place(p, ws, wl);
+    CUtensorMap tm_page, tm_page8, tm_q, tm_q_own;
+    int rc = w_page_maps(&tm_page, &tm_page8, slab, p);
+    if (!rc) rc = w_query_map<W_SHARED>(&tm_q, q_abs, p);
+    if (!rc) rc = w_query_map<W_OWN>(&tm_q_own, q_abs, p);
     if (rc) return rc;
-    return C::SHARED ? K3MLA_OK : w_tail<MODE>(w_kv_b, out, p, st);
+    static bool attr_done[64] = {};
+    const size_t smem = std::max(sizeof(WSmem<W_SHARED>), sizeof(WSmem<W_OWN>)) + 1024;
+    set_smem_attr(reinterpret_cast<const void*>(k3mla_shared_kernel), smem, attr_done);
+    const int most = sm_count() / 2;
+    p.shared_clusters = std::min(p.shared_units, most);
+    rc = launch_pdl(k3mla_shared_kernel, dim3(2 * (p.shared_clusters + std::min(p.n_units, most))), dim3(W_THREADS), smem, st,
+                    "k3mla_shared_kernel", tm_page, tm_page8, tm_q, tm_q_own, p);
+    return rc ? rc : w_tail<W_OWN>(w_kv_b, out, p, st);
 }
 
 // What both entries ask of their common arguments; fills p.
@@ -2087,8 +2137,8 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
     }
     // Every slot for itself, or the shared pages apart.  96 heads over a row of 1,152 B are 181 operations a byte, and a second
     // read is L2's: what sharing saves is not bytes but the quarter of the MMAs' rows that a slot's 96 heads leave unused, 0.77 us
-    // a page of four slots x 32 heads against 0.67 of a slot's 96, a seventh of the time of long prefixes, and it costs a second
-    // launch and its records.  64 slots over 16,384 shared tokens 196 -> 173 us, 16 over 30,000 103 -> 95; but 64 over 1,024
+    // a page of four slots x 32 heads against 0.67 of a slot's 96, a seventh of the time of long prefixes, and it costs units
+    // and records of its own.  64 slots over 16,384 shared tokens 196 -> 173 us, 16 over 30,000 103 -> 95; but 64 over 1,024
     // 32 -> 53, 8 over 4,096 30.2 -> 31.8.
     // By itself a slot's split costs 5.7 us and 0.67 a page, and in the merge 2.5 us and 0.09 a split.  Apart, both lengths are
     // planned together: the own pages' units take the clusters that the shared pages' leave free, so what counts is when the last
@@ -2178,12 +2228,8 @@ extern "C" int k3mla_shared_decode(const uint16_t* q_abs, const uint16_t* slab, 
     p.G = n_groups, p.max_shared = max_shared, p.max_own = max_own, p.shared_split = shared_split, p.split_tokens = own_split;
     p.ns_shared = n.ns_shared, p.nsplit = nsplit, p.alone = alone;
     p.B = p.R = B;
-    const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (n.ns_shared) {
-        p.n_units = (int)(3 * quads * n.ns_shared);
-        rc = w_launch<W_SHARED>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), wl, p, st);
-        if (rc) return rc;
-    }
+    p.shared_units = (int)(3 * quads * n.ns_shared);
     p.n_units = B * n.ns_own;
-    return w_launch<W_OWN>(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), wl, p, st);
+    return w_launch_shared(q_abs, slab, w_kv_b, out, reinterpret_cast<uint8_t*>(workspace), wl, p,
+                           reinterpret_cast<cudaStream_t>(stream));
 }
