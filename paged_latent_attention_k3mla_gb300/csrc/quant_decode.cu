@@ -133,6 +133,7 @@ constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's fou
 constexpr float QD_TAU = 16.f;                  // a reference moves when a row passes it by more than 2^TAU
 constexpr float QD_BIG = 1048576.f;             // references this large are rounded by so much that s less the reference has to be
                                                 // taken from the rounded s + k that it is one of, or none may come near it
+constexpr float QD_NONE = 1e30f;                // makes any score that is not -inf pass a reference that is not there yet
 constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
 constexpr uint32_t QD_IDESC_ROPE = make_idesc_bf16(128, QD_HEADS, 0, 0);
@@ -148,7 +149,7 @@ struct __align__(1024) QdSmem {
     alignas(128) uint8_t sf[512];
     uint64_t full[QD_RING], empty[QD_RING];
     uint64_t q_ready, s_full, s_empty, p_full, pv_done;
-    alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; 0 before anything was seen
+    alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; QD_NONE before there is one
     float m_ref[QD_HEADS];            // ... as they are
     float alpha[QD_HEADS];            // what a moved reference turns the sums by
     float part[4][QD_HEADS];          // a quarter's maxima or sums
@@ -359,7 +360,7 @@ struct QdQueries {
         if (odd) most = finite(src + (size_t)h_first * ROW + 8 * j, ITEMS, STEP * ROW);
         if (most_rope >= 0x7F80u) most_rope = finite(src + (size_t)hr * ROW + LORA + 8 * jr, hr + ROPES < QD_HEADS ? 2 : 1, ROPES * ROW);
         if (lane == 0) sm.most[tid >> 5][0] = most, sm.most[tid >> 5][1] = most_rope;
-        if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = 0.f;
+        if (tid < QD_HEADS) sm.m_ref[tid] = -INFINITY, sm.m_neg[tid] = QD_NONE;
         named_bar(QB_ALL, 32 * QD_SOFTMAX);
         most = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane % QD_SOFTMAX][0]);
         most_rope = __reduce_max_sync(0xFFFFFFFFu, sm.most[lane % QD_SOFTMAX][1]);
@@ -457,7 +458,7 @@ __device__ __forceinline__ bool qd_move(QdSmem& sm, const QdParams& p, const flo
 #pragma unroll
         for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.part[w][h0 + lane]);
         sm.m_ref[h0 + lane] = m;
-        sm.m_neg[h0 + lane] = m == -INFINITY ? 0.f : -m;
+        sm.m_neg[h0 + lane] = m == -INFINITY ? QD_NONE : -m;
         sm.alpha[h0 + lane] = m == old ? 1.f : ex2_approx(old - m);
     }
     named_bar(QB_GROUP + group, 128);
