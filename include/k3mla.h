@@ -474,7 +474,8 @@ int k3mla_quant_copy_pages(uint8_t* dst_slab, int dst_n_pages, const uint8_t* sr
  * empty slots, -1 entries, unseen tokens and non-finite values.  slab 128-byte aligned.  Latent entries of the queries below
  * 2^-14 of the largest among a slot's heads 0 .. 47 (or 48 .. 95) are rounded to 1.25 * 2^-22 of it (a largest of 2^-93 and
  * more); a p times its row's scale to 2^-8 of itself, or to 1.25 * 2^-22 of the head's largest such product among the 32 tokens
- * of its half page where that is more.
+ * of its half page where that is more.  A p below 2^-126 of the largest among its split's first two pages counts as 0, and so
+ * may what a row adds to the output where another of its half page is 2^100 times larger.
  * k3mla_quant_split_tokens plans a split length, as k3mla_window_split_tokens does but for these kernels: the one with which
  * the last split ends first, on the current device. */
 size_t k3mla_quant_decode_workspace_bytes(int B, int max_ctx, int window, int n_sink, int split_tokens);

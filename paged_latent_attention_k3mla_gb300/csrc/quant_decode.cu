@@ -26,8 +26,11 @@
 // entries down to 2^-14 of their largest, within 1.25 * 2^-22 of it below), p times its row's power of two as a pair (by way of
 // an f16: 2^-8 of it, as a bf16 is; within 1.25 * 2^-22 of the largest of its block below that), then as in window.cu o_lat and a
 // split's O as f16 with a power of two a row, and the output as bf16.  As the exponents carry P's size, a reference only keeps
-// the f32 sums in range: it moves when a row passes it by 2^16.  Against 64 bits the outputs are off by 0.0017 to 0.0019
-// (relative, mean square), of which 0.0017 are their own rounding.
+// the f32 sums in range: a head's is the largest score at first and moves when one passes it by 2^60, as does the unit that O is
+// held in, the largest row's power of two.  Two, because rows may be as far apart as bf16's range: p alone goes into the sum of
+// exp, p times the row's size into O.  (Held to one reference, of their product, rows of 2^-20 before rows of 2^110 lost their
+// weight.)  What is lost is p below 2^-126 of the reference, and rows 2^126 times smaller than another of their block.  Against
+// 64 bits the outputs are off by 0.0017 to 0.0019 (relative, mean square), of which 0.0017 are their own rounding.
 //
 // Structure of a CTA: eight softmax warps (a quarter of the tile's tokens x 24 heads each: a lane has a token, so a row's scale,
 // mask and sums of exp are the thread's own; a block's largest P is found by 13 shuffles of a warp, and what meets every tile is
@@ -130,9 +133,9 @@ constexpr uint32_t QD_ONE_COL = 5 * QD_PAIRS, QD_SF_COL = QD_ONE_COL + 4;  // ..
 // warp of its own: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6, without 73.9; by softmax warp 0, this many: 69.3.
 constexpr int QD_AHEAD = 3;
 constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
-constexpr float QD_TAU = 16.f;                  // a reference moves when a row passes it by more than 2^TAU
-constexpr float QD_BIG = 1048576.f;             // references this large are rounded by so much that s less the reference has to be
-                                                // taken from the rounded s + k that it is one of, or none may come near it
+constexpr float QD_TAU = 60.f;                  // a reference, or O's unit, moves when something passes it by more than 2^TAU
+constexpr float QD_BIG = 1048576.f;             // scores this large are rounded by so much that s less the reference has to be taken
+                                                // from the rounded s that it is one of, or none may come near it
 constexpr float QD_NONE = 1e30f;                // makes any score that is not -inf pass a reference that is not there yet
 constexpr float QD_LOW = 32.f;                  // the second number's units are 1 / 32: half a step of the first at 256 is 8
 constexpr uint32_t QD_IDESC_S = make_idesc_e4m3(128, QD_PAIRS, 0, 0);
@@ -151,8 +154,10 @@ struct __align__(1024) QdSmem {
     uint64_t q_ready, s_full, s_empty, p_full, pv_done;
     alignas(16) float m_neg[QD_HEADS];  // the references in log2 units, negated; QD_NONE before there is one
     float m_ref[QD_HEADS];            // ... as they are
-    float alpha[QD_HEADS];            // what a moved reference turns the sums by
+    float alpha[QD_HEADS], turn[QD_HEADS];  // what a moved reference turns the sums by, and O, whose unit may have moved too
     float part[4][QD_HEADS];          // a quarter's maxima or sums
+    alignas(16) int32_t unit[2][4];   // a group's largest row exponents, by quarter
+    int32_t od[2];                    // ... and the exponent of O's unit
     uint32_t most[QD_SOFTMAX][2];     // the prologue's maxima by warp: latents, rope
     uint32_t tmem_base;
     int32_t abort_flag;
@@ -438,50 +443,66 @@ __device__ __forceinline__ void qd_load_pairs(uint32_t at, uint32_t (&v)[2 * QD_
     tmem_ld16(at + 32u, reinterpret_cast<uint32_t(&)[16]>(v[32]));
 }
 
-// The references of this group's heads move to the largest s + k of the tile where that is larger, k a row's exponent; sums
-// and O follow.  All four warps of the group come here together.  u: the raw scores; c: what makes log2 units of them.
+// x 2^n, x a power of two; 0 and 2^127 beyond what f32 has.
+__device__ __forceinline__ float qd_times_power(float x, int n)
+{
+    const int field = (int)(__float_as_uint(x) >> 23) + n;
+    return __uint_as_float(field <= 0 ? 0u : (uint32_t)min(field, 254) << 23);
+}
+
+// The references of this group's heads move to the largest score of the tile, rounded up to a whole number, and O's unit 2^od to
+// the largest row's, where those are larger; sums and O follow.  All four warps of the group come here together.  u: the raw
+// scores; c: what makes log2 units of them; largest: the exponent of the warp's largest row.
 __device__ __forceinline__ bool qd_move(QdSmem& sm, const QdParams& p, const float (&u)[QD_MINE], float (&l)[QD_MINE], float c,
-                                        float k, bool seen, uint32_t tbase, int quarter, int group, int i)
+                                        int largest, int& od, bool seen, uint32_t tbase, int quarter, int group, int i)
 {
     const int lane = (int)lane_id(), h0 = QD_MINE * group;
     int32_t mine = (int32_t)0x80000000;
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) {
-        const int32_t m = __reduce_max_sync(0xFFFFFFFFu, seen ? qd_order(fmaf(u[h], c, k)) : (int32_t)0x80000000);
+        const int32_t m = __reduce_max_sync(0xFFFFFFFFu, seen ? qd_order(__fmul_rn(u[h], c)) : (int32_t)0x80000000);
         if (lane == h) mine = m;
     }
     if (lane < QD_MINE) sm.part[quarter][h0 + lane] = qd_unorder(mine);
+    if (lane == 0) sm.unit[group][quarter] = largest;
     named_bar(QB_GROUP + group, 128);
     if (quarter == 0 && lane < QD_MINE) {
         const float old = sm.m_ref[h0 + lane];
-        float m = old;
+        float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.part[w][h0 + lane]);
+        m = fmaxf(old, ceilf(m));
         sm.m_ref[h0 + lane] = m;
         sm.m_neg[h0 + lane] = m == -INFINITY ? QD_NONE : -m;
-        sm.alpha[h0 + lane] = m == old ? 1.f : ex2_approx(old - m);
+        const int4 r = *reinterpret_cast<const int4*>(sm.unit[group]);
+        const int now = max(max(od, max(r.x, r.y)), max(r.z, r.w));
+        const float f = m == old ? 1.f : ex2_approx(old - m);
+        sm.alpha[h0 + lane] = f;
+        sm.turn[h0 + lane] = f * ex2_approx((float)(od - now));
+        if (lane == 0) sm.od[group] = now;
     }
     named_bar(QB_GROUP + group, 128);
+    od = sm.od[group];
+    if (i == 0) return true;
     float f[QD_MINE];
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) {
-        f[h] = sm.alpha[h0 + h];
-        l[h] *= f[h];
+        l[h] *= sm.alpha[h0 + h];
+        f[h] = sm.turn[h0 + h];
     }
-    if (i == 0) return true;
     if (!__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.pv_done, i - 1))) return false;
     tc_fence_after();
     const uint32_t t0 = tbase + ((32u * (uint32_t)quarter) << 16) + 2u * (uint32_t)h0;
 #pragma unroll 1
-    for (int d = 0; d < 4; ++d) {
+    for (int x = 0; x < 4; ++x) {
         uint32_t v[2 * QD_MINE];
-        qd_load_pairs(t0 + (uint32_t)(QD_PAIRS * d), v);
+        qd_load_pairs(t0 + (uint32_t)(QD_PAIRS * x), v);
         tmem_wait_ld();
         qd_pin(v);
 #pragma unroll
         for (int e = 0; e < 2 * QD_MINE; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f[e % QD_MINE]);
-        tmem_st32(t0 + (uint32_t)(QD_PAIRS * d), reinterpret_cast<uint32_t(&)[32]>(v));
-        tmem_st16(t0 + (uint32_t)(QD_PAIRS * d) + 32u, reinterpret_cast<uint32_t(&)[16]>(v[32]));
+        tmem_st32(t0 + (uint32_t)(QD_PAIRS * x), reinterpret_cast<uint32_t(&)[32]>(v));
+        tmem_st16(t0 + (uint32_t)(QD_PAIRS * x) + 32u, reinterpret_cast<uint32_t(&)[16]>(v[32]));
     }
     tmem_wait_st();
     tc_fence_before();
@@ -526,10 +547,11 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
     const int mine = 12 * (lane >> 4) + 6 * (lane >> 3 & 1) + 2 * (lane & 4 ? 2 : lane >> 1 & 1) + (lane & 1);
     const auto lane_of = [](int h) { return 16 * (h / 12) + 8 * (h / 6 & 1) + h % 6; };
     const auto sf_place = [&](int n) { return 16 * (n & 31) + 4 * (n >> 5) + quarter; };
-    const int sf0 = sf_place(2 * h0 + mine), sf1 = sf_place(2 * h0 + QD_MINE + mine);
+    const int sf_at = sf_place(2 * h0 + mine) | sf_place(2 * h0 + QD_MINE + mine) << 16;
     float l[QD_MINE];
 #pragma unroll
     for (int h = 0; h < QD_MINE; ++h) l[h] = 0.f;
+    int od = -127;      // O's unit is 2^od: the largest row's so far, or within 2^TAU of it
     bool big = false;   // a reference of this group's heads is QD_BIG or more
     bool dead = false;  // a wait ran out: this warp only goes on to where the four can leave together
 #pragma unroll 1
@@ -538,7 +560,8 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         const bool seen = e < g.npg && qd_seen(p, g.n, t);
         const float scale = __uint_as_float(seen ? (uint32_t)next << 16 : 0x0F800000u);
         const int field = (int)(__float_as_uint(scale) >> 23), largest = __reduce_max_sync(0xFFFFFFFFu, field);
-        const float k = (float)(field - 127), c = kq * scale, up = scale * __uint_as_float((uint32_t)max(254 - largest, 1) << 23);
+        const float c = kq * scale, up = scale * __uint_as_float((uint32_t)max(254 - largest, 1) << 23);
+        const float room = QD_TAU - (float)max(field - 127 - od, 0);  // for a score above its reference
         const bool whole = __all_sync(0xFFFFFFFFu, seen);
         if (i + 1 < tiles) next = row_scale(i + 1);
         dead = dead || !__all_sync(0xFFFFFFFFu, qd_wait(sm, p, &sm.s_full, i));
@@ -574,7 +597,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
 #pragma unroll
                 for (int h = 0; h < QD_MINE; ++h) {
                     const float m = sm.m_neg[h0 + h];
-                    if (fabsf(m) >= QD_BIG) x[h] = (fmaf(u[h], c, k) + m) - k;
+                    if (fabsf(m) >= QD_BIG) x[h] = __fmul_rn(u[h], c) + m;
                 }
             }
         };
@@ -583,10 +606,10 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
 #pragma unroll
         for (int h = 4; h < QD_MINE; ++h) m4[h & 3] = fmaxf(m4[h & 3], x[h]);
         const float most = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-        // (the first tile sets the references)
-        if (named_bar_any(QB_GROUP + group, 128, dead || i == 0 || (seen && !(most <= QD_TAU - k)))) {
+        // (the first tile sets the references and the unit, without a vote: 64 x 4,096 tokens 67.0 -> 66.8 us)
+        if (i == 0 || named_bar_any(QB_GROUP + group, 128, dead || (seen && !(most <= room)))) {
             if (named_bar_any(QB_GROUP + group, 128, dead)) return;
-            dead = !qd_move(sm, p, u, l, c, k, seen, tbase, quarter, group, i);
+            dead = !qd_move(sm, p, u, l, c, largest - 127, od, seen, tbase, quarter, group, i);
             big = __any_sync(0xFFFFFFFFu, lane < QD_MINE && fabsf(sm.m_neg[h0 + min(lane, QD_MINE - 1)]) >= QD_BIG);
             arguments();
         }
@@ -636,7 +659,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
             const int top = (int)((lane & 1 ? pair >> 16 : pair & 0xFFFFu) >> 7);  // the largest: in [2^(top - 127), 2^(top - 126))
             // to [1 / 2, 1): P is 2^8 times that
             unit = (uint32_t)(253 - min(top, 252)) << 23;
-            sf = (uint32_t)min(max(top + largest - (7 + 127), 0), 254);
+            sf = (uint32_t)min(max(top + largest - (7 + 127) - od, 0), 254);
         }
         uint32_t w[QD_MINE / 2];  // 24 first numbers, 24 second ones
 #pragma unroll
@@ -663,7 +686,7 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         for (int y = 0; y < 3; ++y)
             *reinterpret_cast<uint4*>(sm.p + token * 128 + (((3 * group + y) ^ (token & 7)) << 4)) =
                 make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
-        sm.sf[sf0] = sm.sf[sf1] = (uint8_t)sf;
+        sm.sf[sf_at & 0xFFFF] = sm.sf[sf_at >> 16] = (uint8_t)sf;
         fence_proxy_async_cta();  // the MMAs read P, and what was cleared, through the async proxy
         tc_fence_before();
         __syncwarp();
@@ -742,8 +765,12 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         r *= w_row_scale(fmaxf(fmaxf(sm.part[0][h], sm.part[1][h]), fmaxf(sm.part[2][h], sm.part[3][h])) * r, inverse);
         if (quarter == 0) {
             const size_t at = place(rank * QD_HEADS + h);
-            (g.single ? p.oscale : p.ws_oscale)[at] = inverse;
-            if (!g.single) p.ws_ml[at] = make_float2(sm.m_ref[h], total);
+            // A record's sum comes to [1, 2), its reference takes the power of two (exactly, below 2^22): what undoes O's is then
+            // that of a value the rows have, which f32 holds.
+            const float m = sm.m_ref[h];
+            const int e = !g.single && fabsf(m) < 4194304.f && total > 0.f && total < INFINITY ? (int)(__float_as_uint(total) >> 23) - 127 : 0;
+            (g.single ? p.oscale : p.ws_oscale)[at] = qd_times_power(inverse, od - e);
+            if (!g.single) p.ws_ml[at] = make_float2(m + (float)e, total * qd_times_power(1.f, -e));
         }
     }
     // two lanes trade, so that each has a pair of neighbouring dims of every second block

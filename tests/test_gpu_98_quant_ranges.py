@@ -61,6 +61,77 @@ def rope_query(B):
     return q
 
 
+@pytest.mark.parametrize("split", [0, 128])
+@pytest.mark.parametrize("low,high", [(-60, 60), (-80, 30), (-20, 110), (-85, -70), (100, 118)])
+def test_rows_far_apart_with_equal_scores(gpu_lib, low, high, split):
+    """Small rows before large ones and behind them: what a small row adds is lost beside the large ones, but its weight is not."""
+    r = rand(1)
+    slots = []
+    for n, first in ((512, 256), (512, 300), (200, 100)):
+        rows = r(n, ROW)
+        rows[:first, :LORA] *= 2.0 ** low
+        rows[first:, :LORA] *= 2.0 ** high
+        slots += [rope_scores(rows, 0 * rows[:, 0]), rope_scores(rows.flip(0), 0 * rows[:, 0])]
+    c = Ranges(gpu_lib, slots, rope_query(6))
+    c.q = (c.q * torch.linspace(0.5, 1.5, H, device="cuda")[:, None]).bfloat16()
+    c.check_rows(c.run(gpu_lib, split=split))
+
+
+@pytest.mark.parametrize("split", [0, 128])
+@pytest.mark.parametrize("spread", [10, 50])
+def test_rows_far_apart_whose_weights_make_up_for_it(gpu_lib, spread, split):
+    """(rows of 2^-spread to 2^spread, scores the other way round: all of them count in the output, the small ones in the sum)"""
+    r = rand(2)
+    slots = []
+    for n in (700, 130, 40):
+        rows, e = r(n, ROW), torch.rand(n, generator=torch.Generator(device="cuda").manual_seed(n), device="cuda") * 2 * spread - spread
+        rows[:, :LORA] *= torch.exp2(e)[:, None]
+        slots.append(rope_scores(rows, -e * float(np.log(2.0)) + r(n)))
+    c = Ranges(gpu_lib, slots, rope_query(3))
+    c.check_rows(c.run(gpu_lib, split=split))
+
+
+@pytest.mark.parametrize("split", [0, 128])
+@pytest.mark.parametrize("exponent", [80, 100, 118, -70])
+def test_rows_of_one_size(gpu_lib, exponent, split):
+    r = rand(3)
+    rows = r(2, 400, ROW) * 2.0 ** exponent
+    q = rope_query(2)
+    c = Ranges(gpu_lib, [rope_scores(rows[0], 3 * r(400)), rope_scores(rows[1, :70], 3 * r(70))], q)
+    c.q = (c.q * torch.linspace(-1.5, 1.5, H, device="cuda")[:, None]).bfloat16()
+    c.check_rows(c.run(gpu_lib, split=split))
+
+
+@pytest.mark.parametrize("exponent", [-100, -40, 0, 30, 60])
+def test_queries_of_very_different_sizes_with_scores_of_order_one(gpu_lib, exponent):
+    r = rand(4)
+    q = r(2, H, ROW) * 0.5 * torch.exp2(3 * torch.linspace(-1, 1, H, device="cuda"))[:, None] * 2.0 ** exponent
+    c = Ranges(gpu_lib, [r(260, ROW) * 2.0 ** -exponent, r(70, ROW) * 2.0 ** -exponent], q)
+    for split in (0, 128):
+        c.check_rows(c.run(gpu_lib, split=split))
+
+
+@pytest.mark.parametrize("exponent", [18, 22, 30, 45, 100])
+def test_scores_beyond_what_an_exponential_stands(gpu_lib, exponent):
+    """All scores 37 * 2^(exponent - 9), exact, but for one that is 2^-7 of it larger, or two: those are the answer."""
+    r = rand(5)
+    slots = []
+    for n, best in ((300, [7]), (300, [299]), (700, [130, 400]), (64, [0, 63]), (1, [0])):
+        rows = r(n, ROW)
+        rows[:, LORA:] = 0
+        rows[:, LORA] = 1
+        rows[best, LORA] = 1 + 2.0 ** -7
+        slots.append(rows)
+    q = rope_query(5)
+    q[:, :, LORA] = 2.0 ** exponent
+    c = Ranges(gpu_lib, slots, q)
+    for split in (0, 128):
+        got = c.run(gpu_lib, split=split)
+        c.check_rows(got)
+        low = c.run(gpu_lib, 100, 1, split=split)
+        c.check_rows(low, window=100, sink=1)
+
+
 def test_scores_of_minus_infinity(gpu_lib):
     """Rope keys of -inf: their tokens' weights are 0, where they fill the first tile of a split, too."""
     k3 = gpu_lib
