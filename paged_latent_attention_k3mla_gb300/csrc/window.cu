@@ -1789,10 +1789,13 @@ static int w_tail(const uint16_t* w_kv_b, uint16_t* out, WinParams& p, cudaStrea
     constexpr bool MQ = WCfg<MODE>::MQ;
     const int merge = MQ || p.nsplit == 1 ? 0 : (p.B <= WX_EPI / 4 ? 4 : (p.B <= WX_EPI && p.nsplit <= WM_GROUPS ? 1 : 0));
     if (p.nsplit > 1 && !merge) {
-        // A CTA a row has more of a row's records under way, a warp a row needs one round of the SMs where four warps need three:
-        // 5 slots of 11 splits 27.4 against 30.8 us, 8 of 9 65.5 / 66.7, 12 of 6 40.6 / 40.5, 16 of 4 48.1 / 48.1, 20 of 3
-        // 56.8 / 55.0, 32 of 2 49.9 / 47.4, 64 of 4 183.1 / 174.8.  The same sums in the same order.
-        const bool warps = p.B > 16;
+        // A CTA a row has more of a row's records under way; a warp a row needs one round of the SMs where four warps need three,
+        // and up to four records it asks for at once.  Decode of splits of 128 tokens, a CTA / a warp a row, us: 10 slots of 4
+        // splits 22.1 / 22.1, of 12 29.2 / 31.1; 17 of 4 22.5 / 21.3, of 5 26.7 / 27.6, of 32 69.0 / 85.1; 20 of 4 26.5 / 25.6, of
+        // 8 32.6 / 34.2; 24 of 5 29.3 / 28.7, of 12 43.3 / 42.9, of 16 54.1 / 54.7, of 32 88.8 / 104.8; 32 of 12 54.0 / 53.1, of 16
+        // 61.7 / 66.9; 40 of 16 76.8 / 78.4, of 32 157 / 147; 48 of 16 92.7 / 91.3, of 32 183 / 186; 64 of 4 45.7 / 38.5, of 12 96.3 /
+        // 90.7, of 32 234 / 235; 128 of 4 75.5 / 62.0, of 16 235 / 226, of 32 436 / 424.  The same sums in the same order.
+        const bool warps = p.B > (p.nsplit <= WM_GROUPS ? 16 : p.nsplit <= 12 ? 23 : 39);
         rc = launch_pdl(warps ? k3mla_window_merge_kernel<1> : k3mla_window_merge_kernel<4>, dim3(warps ? H / 4 : H, p.B), dim3(128), 0,
                         st, "k3mla_window_merge_kernel", p);
         if (rc) return rc;
