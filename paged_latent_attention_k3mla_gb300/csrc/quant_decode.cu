@@ -286,6 +286,7 @@ __device__ __forceinline__ void qd_pv(QdSmem& sm, const QdParams& p, uint32_t tb
 #pragma unroll 1
         for (int i = 0; i < tiles && ok; ++i) {
             ok = qd_wait(sm, p, &sm.p_full, i);  // (whose scores have waited for the chunks: 64 x 4,096 tokens 68.7 -> 67.4 us)
+            if (!ok) break;
             tc_fence_after();
             tmem_copy_scales(sf, sf_at);
 #pragma unroll 1
@@ -765,10 +766,10 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
         r *= w_row_scale(fmaxf(fmaxf(sm.part[0][h], sm.part[1][h]), fmaxf(sm.part[2][h], sm.part[3][h])) * r, inverse);
         if (quarter == 0) {
             const size_t at = place(rank * QD_HEADS + h);
-            // A record's sum comes to [1, 2), its reference takes the power of two (exactly, below 2^22): what undoes O's is then
-            // that of a value the rows have, which f32 holds.
+            // A record's sum comes to [2^-16, 2^-15), its reference takes the power of two (exactly, below 2^22): O is then at most
+            // that much of the rows' largest, and f32 holds what undoes its power of two, and the merge's sums.
             const float m = sm.m_ref[h];
-            const int e = !g.single && fabsf(m) < 4194304.f && total > 0.f && total < INFINITY ? (int)(__float_as_uint(total) >> 23) - 127 : 0;
+            const int e = !g.single && fabsf(m) < 4194304.f && total > 0.f && total < INFINITY ? (int)(__float_as_uint(total) >> 23) - 111 : 0;
             (g.single ? p.oscale : p.ws_oscale)[at] = qd_times_power(inverse, od - e);
             if (!g.single) p.ws_ml[at] = make_float2(m + (float)e, total * qd_times_power(1.f, -e));
         }

@@ -62,7 +62,7 @@ def rope_query(B):
 
 
 @pytest.mark.parametrize("split", [0, 128])
-@pytest.mark.parametrize("low,high", [(-60, 60), (-80, 30), (-20, 110), (-85, -70), (100, 118)])
+@pytest.mark.parametrize("low,high", [(-60, 60), (-80, 30), (-20, 110), (-85, -70), (100, 118), (-20, 125)])
 def test_rows_far_apart_with_equal_scores(gpu_lib, low, high, split):
     """Small rows before large ones and behind them: what a small row adds is lost beside the large ones, but its weight is not."""
     r = rand(1)
@@ -92,13 +92,24 @@ def test_rows_far_apart_whose_weights_make_up_for_it(gpu_lib, spread, split):
 
 
 @pytest.mark.parametrize("split", [0, 128])
-@pytest.mark.parametrize("exponent", [80, 100, 118, -70])
+@pytest.mark.parametrize("exponent", [80, 100, 118, 125, -70])
 def test_rows_of_one_size(gpu_lib, exponent, split):
     r = rand(3)
     rows = r(2, 400, ROW) * 2.0 ** exponent
     q = rope_query(2)
     c = Ranges(gpu_lib, [rope_scores(rows[0], 3 * r(400)), rope_scores(rows[1, :70], 3 * r(70))], q)
     c.q = (c.q * torch.linspace(-1.5, 1.5, H, device="cuda")[:, None]).bfloat16()
+    c.check_rows(c.run(gpu_lib, split=split))
+
+
+@pytest.mark.parametrize("split", [0, 128])
+def test_rows_near_the_largest_bf16(gpu_lib, split):
+    """Latents about 1.5 * 2^126, whose sums, not yet divided by the sum of exp, pass what f32 has.  (W_UV 2^-4 of its usual size:
+    4.5 standard deviations of the outputs would be above the largest bf16.)"""
+    r = rand(7)
+    rows = (1 + 0.1 * r(2, 700, ROW)) * 1.5 * 2.0 ** 126
+    c = Ranges(gpu_lib, [rope_scores(rows[0], 2 * r(700)), rope_scores(rows[1, :300], 2 * r(300))], rope_query(2))
+    c.w *= 2.0 ** -4
     c.check_rows(c.run(gpu_lib, split=split))
 
 
