@@ -16,7 +16,8 @@
 // the largest P there to [2^7, 2^8).  Without it the numbers' 2^22 between their largest and their smallest step have to hold
 // all that a row weighs, and where a few tokens take most of its mass the thousands that it answers with are lost
 // together (the first of 4,096 tokens takes 0.87: the output off by 0.087 of itself, of 16,384 by 0.36; with it by 0.0017).  It
-// costs 37 shuffles a tile and warp: 64 slots of 4,096 tokens 65.3 -> 67.2 us, of 15,000 to 16,384 200 -> 209.
+// costs 37 shuffles a tile and warp, and saves the moves of a reference that holds all in range: 64 slots of 4,096 tokens 65.3 ->
+// 66.7 us, with four times as large scores 73.5 -> 66.8.
 // A pair has 8 bits, as a bf16 does, and two such MMAs cost what one in bf16 does (e4m3 runs at twice the rate), without the
 // 65,536 conversions a tile that a bf16 form would begin with.  96 columns are 48 heads: two CTAs a split, each with all of its
 // tokens.  Tokens on M and not heads, because 48 heads would leave half of M's 128 rows empty, and because O then fits: TMEM
@@ -37,13 +38,14 @@
 // one vote of four warps whether a reference has to move), and one warp each that loads, issues S and issues PV.  A tile is two
 // pages; its five chunks of 128 tokens x 128 B (the rope part and four times 128 latents) go through a ring of nine.
 //
-// Measured: 64 slots of 4,096 tokens 65.3 us (190 MB: 2.9 TB/s, 0.43 of the copy rate; 850 TFLOP/s), 64 of 15,000 to
-// 16,384 205 us (3.2 TB/s, 1,020 TFLOP/s, 0.54 of the measured bf16 rate), one of 32,768 27.2 us, 128 of up to 256 29.3 us;
-// k3mla_window_decode over the bf16 cache takes 67 us for 64 of 4,100.  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each
-// for 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile 3,050.  With S and the queries'
+// Measured: 64 slots of 4,096 tokens 66.7 us (190 MB: 2.8 TB/s, 0.42 of the copy rate; 834 TFLOP/s), 64 of 15,000 to
+// 16,384 208 us (3.2 TB/s, 1,005 TFLOP/s, 0.53 of the measured bf16 rate), one of 32,768 29.2 us, 128 of up to 256 29.3 us;
+// k3mla_window_decode over the bf16 cache takes 68.2 us for 64 of 4,100.  What bounds it: a tile's MMAs take 1,990 clocks -- 56 each
+// for 128 x 96 x 32, as both operands come from shared memory at 128 B a clock -- and a tile some 3,100.  With S and the queries'
 // pairs there is room for 1.8 tiles, so the second contraction (1,700 beside S of the next tile), the loads over what it
-// frees (1,000), the last scores (600) and the softmax (1,700) of every second tile stand in one chain; the tensor pipe is 43%
-// busy.  Small calls: 3.9 us until the queries' pairs are there, 2.2 for the write-out, and the expansion's 9.
+// frees (1,000), the last scores (600) and the softmax (1,700, and the search for the blocks' largest) of every second tile stand in
+// one chain; the tensor pipe is 44% busy.  Small calls: 3.9 us until the queries' pairs are there, 2.2 for the write-out, and the
+// expansion's 9.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -129,8 +131,9 @@ constexpr int QW_LOAD = 8, QW_SCORE = 9, QW_PV = 10;
 constexpr int QD_THREADS = 352;
 constexpr uint32_t QD_S_COL = 4 * QD_PAIRS;     // TMEM: O by blocks of 128 dims at 96 d, then S
 constexpr uint32_t QD_ONE_COL = 5 * QD_PAIRS, QD_SF_COL = QD_ONE_COL + 4;  // ... scale factors: the latents', 1; P's
-// A tile's pages, one each of the two CTAs, are fetched into L2 this many tiles before its scores.  64 slots x 4,096 tokens, by a
-// warp of its own: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6, without 73.9; by softmax warp 0, this many: 69.3.
+// A tile's pages, one each of the two CTAs, are fetched into L2 this many tiles before its scores.  64 slots x 4,096 tokens, when the
+// loads' and the scores' loops were not written out yet, by a warp of its own: 1 74.3 us, 2 69.3, 3 69.7, 4 70.5, 6 71.6, without
+// 73.9; by softmax warp 0, this many: 69.3.
 constexpr int QD_AHEAD = 3;
 constexpr uint32_t QB_GROUP = 1, QB_ALL = 3;    // named barriers: a group's four softmax warps (1, 2); all of them
 constexpr float QD_TAU = 60.f;                  // a reference, or O's unit, moves when something passes it by more than 2^TAU
@@ -769,7 +772,8 @@ __device__ __forceinline__ void qd_softmax(QdSmem& sm, const QdParams& p, QdQuer
             // A record's sum comes to [2^-16, 2^-15), its reference takes the power of two (exactly, below 2^22): O is then at most
             // that much of the rows' largest, and f32 holds what undoes its power of two, and the merge's sums.
             const float m = sm.m_ref[h];
-            const int e = !g.single && fabsf(m) < 4194304.f && total > 0.f && total < INFINITY ? (int)(__float_as_uint(total) >> 23) - 111 : 0;
+            const bool turns = !g.single && fabsf(m) < 4194304.f && total > 0.f && total < INFINITY;
+            const int e = turns ? (int)(__float_as_uint(total) >> 23) - 111 : 0;
             (g.single ? p.oscale : p.ws_oscale)[at] = qd_times_power(inverse, od - e);
             if (!g.single) p.ws_ml[at] = make_float2(m + (float)e, total * qd_times_power(1.f, -e));
         }

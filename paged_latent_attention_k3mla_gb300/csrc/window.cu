@@ -43,10 +43,10 @@
 //     become zero in shared memory.  In a chunk a token may be seen by some rows of the unit only: those get a NaN for
 //     their p of it (its score may be -inf, whose p is 0, and 0 times the latent that was there is NaN).
 //
-// Measured, all kernels of a call in a graph of calls: decode of 64 slots over 4,100 seen tokens 69.1 us (324 MB, 0.69 of
+// Measured, all kernels of a call in a graph of calls: decode of 64 slots over 4,100 seen tokens 68.2 us (324 MB, 0.70 of
 // the copy rate), over 1,088 33.2 us, of one slot over 4,100 21.5 us (33 splits); chunks of 16 x 64 rows over 1,024 tokens
 // 226 us (1,030 TFLOP/s, 0.54 of the measured bf16 rate), of 1,000 rows over 300 120.2 us (29 of them the expansion).
-// Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 171 us (1,315 TFLOP/s; 141 of them the shared pages at
+// Shared: 64 slots over 16,384 shared tokens and up to 590 of their own 170 us (1,320 TFLOP/s; 141 of them the shared pages at
 // 0.75 us a page, four slots and 32 heads, of which the score MMAs take 0.57), 5 groups of 1 to 7 over 2,500 and 1,000 35 us.
 // Call after call from the host the longer ones take 1 to 4 % more (72.3, 33.4, 21.5, 230 and 122 us).  Bounds: the page
 // stream for long lists of pages (decode 0.85 us a page and cluster, 64 clusters at 5.5 TB/s; chunks 0.66 us, of which
@@ -579,7 +579,9 @@ __device__ __forceinline__ void w_produce(WSmem<MODE>& sm, const CUtensorMap& tm
                 if constexpr (C::NPROD == 1) {
                     // Written out, as the issuers' loop over the thirds is: a load's wait, arming and copy keep the thread busy for
                     // some 280 clocks, three a page, where the page's MMAs take 1,150 (16 x 64 rows 233.8 -> 225.6 us, 64 over
-                    // 16,384 tokens 202.6 -> 189.4, 64 slots over as many shared tokens 172.2 -> 169.0).
+                    // 16,384 tokens 202.6 -> 189.4, 64 slots over as many shared tokens 172.2 -> 169.0; decode, whose three
+                    // producers stay in a loop, by the issuers' alone: 1,024 slots of 600 210.7 -> 209.6, 64 of 4,096 in splits of 512
+                    // tokens 101.9 -> 101.3, but in splits of 128 227.7 -> 234.2).
                     int u = (base + 3 * i) % C::NUNIT;
                     uint32_t phase = (uint32_t)((base + 3 * i) / C::NUNIT) ^ 1u;
 #pragma unroll
@@ -698,8 +700,7 @@ __device__ __forceinline__ bool w_copy_q(WSmem<MODE>& sm, const WinParams& p, ui
 // chain through a unit's pages: the warp of each page hands its decision on to the warp of the next one; a
 // warp's sum of exp follows the reference when it comes to its own next page.  All in log2 units.  The chain of
 // turns runs on through all units, so a turn's barrier is never a phase ahead of who waits on it.
-// (The page's code is written to be short: the SM's instruction fetch is what these kernels run short of first.
-// The scores' issue loop unrolled three times, 9 KB more, took the 16 x 64-token chunk from 328 to 358 us.)
+// (The page's code is written to be short: the SM's instruction fetch is what these kernels run short of first.)
 template <int MODE>
 __device__ __forceinline__ void w_softmax(WSmem<MODE>& sm, const WinParams& p, uint32_t tbase, uint32_t warp)
 {
@@ -2139,13 +2140,14 @@ extern "C" int k3mla_shared_split_tokens(int B, int n_groups, int max_shared, in
         return TILE;
     }
     // Every slot for itself, or the shared pages apart.  96 heads over a row of 1,152 B are 181 operations a byte, and a second
-    // read is L2's: what sharing saves is not bytes but the quarter of the MMAs' rows that a slot's 96 heads leave unused, 0.77 us
+    // read is L2's: what sharing saves is not bytes but the quarter of the MMAs' rows that a slot's 96 heads leave unused, 0.75 us
     // a page of four slots x 32 heads against 0.67 of a slot's 96, a seventh of the time of long prefixes, and it costs units
-    // and records of its own.  64 slots over 16,384 shared tokens 196 -> 173 us, 16 over 30,000 103 -> 95; but 64 over 1,024
-    // 32 -> 53, 8 over 4,096 30.2 -> 31.8.
+    // and records of its own.  With the best splits of either, every slot for itself / apart: 64 slots over 16,384 shared tokens
+    // 199 / 168 us, 16 over 16,384 67 / 61, 16 over 30,000 102 / 81; but 64 over 4,096 65.7 / 70.2, 64 over 1,024 33 / 50, and 8 over
+    // 4,096 the same, 29.
     // By itself a slot's split costs 5.7 us and 0.67 a page, and in the merge 2.5 us and 0.09 a split.  Apart, both lengths are
     // planned together: the own pages' units take the clusters that the shared pages' leave free, so what counts is when the last
-    // of either ends, and what the records cost in the merge; 9.6 us and 0.77 a page for four slots x 32 heads, 10.8 and 0.52 for
+    // of either ends, and what the records cost in the merge; 9.6 us and 0.77 a page (as measured with a launch of its own) for four slots x 32 heads, 10.8 and 0.52 for
     // a slot, 0.6 a split of the shared pages, 0.07 a slot's split of its own.  Groups are taken as equally large, and all as long
     // as the longest.  Over 28 shapes of 1 to 308 slots the choice is within 1% of the best of some 45 on average.
     const long long clusters = std::max(1, sm_count() / 2);
